@@ -268,6 +268,110 @@ na_status na_rpb_grad(const void* dattn, float* drpb, int B, int ndim, const int
                       const int* kernel, const int* dilation, na_dtype dtype, void* workspace, size_t workspace_bytes,
                       void* stream);
 
+/*
+ * Around the attention.  What a block that trains or runs neighborhood attention needs next to it: the
+ * rotation of queries and keys by their positions, layer norm, and the window softmax of the unfused chain
+ * with dropout or as the difference of two maps.  The source pages do not have these operations; each is
+ * defined here.  Tensors are contiguous device memory, 16-byte aligned unless said otherwise, caller-owned;
+ * arithmetic and statistics in fp32, one rounding to the tensors' type at the end.  Sizes must be at least 1
+ * and tensors of at most 2^40 elements (else NA_ERR_UNSUPPORTED).  An output may be the very tensor of an
+ * input where its comment says so, and overlaps no other argument (else NA_ERR_INVALID_ARG).  Every
+ * result is bitwise deterministic.  Calls may be captured into a CUDA graph.
+ */
+
+typedef enum {
+    NA_ROPE_HALF = 0,        /* a block of r channels turns the pairs (i, i + r/2) */
+    NA_ROPE_INTERLEAVED = 1  /* ... the pairs (2i, 2i + 1) */
+} na_rope_layout;
+
+/*
+ * Rotary positions on a grid.  q: [B, L.., heads_q, D], k: [B, L.., heads_k, D] (heads_k = 0 and null
+ * pointers: q alone).  Axis a owns rot[a] channels (even, 0 allowed, their sum 2 .. D), blocks following one
+ * another from channel 0; the remaining channels are copied.  Pair i of axis a's block turns by
+ *   theta = (origin[a] + x_a) * freq[..], x_a the token's index along the axis,
+ *   (u, v) -> amplitude * (u cos theta - v sin theta, u sin theta + v cos theta).
+ * freq: host array of sum(rot) / 2 angular frequencies in radians per position (finite, at most 1e6 in size),
+ * axis after axis; scaled contexts are scaled frequencies.  origin: host array of ndim first positions, or
+ * null for zeros.  Both are read before the call returns.  Angles are reduced in 64-bit fixed point, so they are
+ * as exact at position 10^9 as at 1.  q_out may be q, k_out may be k.  D in {16, 32, 64, 128}.
+ */
+na_status na_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int ndim, const int* spatial,
+                  int heads_q, int heads_k, int D, const int* rot, const double* freq, const int64_t* origin,
+                  float amplitude, na_rope_layout layout, na_dtype dtype, void* stream);
+
+/* Gradients of na_rope: the rotation by -theta with the same amplitude.  dq may be dq_out, dk may be dk_out. */
+na_status na_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, int B, int ndim, const int* spatial,
+                      int heads_q, int heads_k, int D, const int* rot, const double* freq, const int64_t* origin,
+                      float amplitude, na_rope_layout layout, na_dtype dtype, void* stream);
+
+/*
+ * Layer norm of each of `rows` rows of C channels: mean = sum x / C, rstd = (sum (x - mean)^2 / C + eps)^-1/2,
+ * y = (x - mean) * rstd * w + b.  The norm per head of a [B, L.., heads, D] tensor has C = D, per token
+ * C = heads * D.  w, b: fp32 [C] whatever the tensors' type, each may be null (ones, zeros).  mean, rstd: fp32
+ * [rows], 4-byte aligned, written for the backward, or both null.  y may be x.  1 <= C <= 8192 (else
+ * NA_ERR_UNSUPPORTED); rows whose length is not a multiple of 16 bytes are read element by element.
+ */
+na_status na_layernorm(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd, int64_t rows,
+                       int C, float eps, na_dtype dtype, void* stream);
+
+/* Bytes of device workspace na_layernorm_bwd needs for dw and db (0 on invalid arguments). */
+size_t na_layernorm_bwd_workspace_size(int64_t rows, int C, na_dtype dtype);
+
+/*
+ * Gradients of na_layernorm from dy, x and the saved statistics, with h = (x - mean) * rstd and g = dy * w:
+ *   dx = rstd * (g - sum g / C - h * sum (g h) / C),  dw = sum over rows of dy * h,  db = sum over rows of dy.
+ * dw, db: fp32 [C], overwritten, or both null.  dx may be dy or x.  Workspace as for na_rpb_grad: null, or at
+ * least na_layernorm_bwd_workspace_size bytes; unused without dw and db.
+ */
+na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const float* mean, const float* rstd, void* dx,
+                           float* dw, float* db, int64_t rows, int C, na_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout.  p in [0, 1] is the probability of a zero.  Whether element i (index in memory order) is kept is a
+ * function of i and of the generator's state rng = {seed, offset}, two 64-bit integers in DEVICE memory, 8-byte
+ * aligned: the seven-round Philox4x32 block at counter (i / 8, offset) and key seed (low 32-bit words first)
+ * holds eight 16-bit fields (low half of word 0 first), and the element is kept when field i % 8 is below
+ * round((1 - p) 2^16); kept elements are multiplied by 2^16 / round((1 - p) 2^16).  No mask is stored: the
+ * backward of a call takes the same state.  Calls that shall draw apart take states that differ, which the
+ * caller advances (a captured graph reads the state anew at every replay).  rng may be null where
+ * round((1 - p) 2^16) is 2^16 (p = 0).
+ */
+
+/* y = dropout(x) over n elements; y may be x.  Its own gradient: call it on dy with the same state. */
+na_status na_dropout(const void* x, void* y, int64_t n, double p, const void* rng, na_dtype dtype, void* stream);
+
+/* y = dropout(softmax(x)) over the K window weights of every (batch, token, head) row, the layout of
+ * na_softmax.  A row of -inf alone gives zeros.  y may be x. */
+na_status na_softmax_dropout(const void* x, void* y, int B, int ndim, const int* spatial, int heads, const int* kernel,
+                             double p, const void* rng, na_dtype dtype, void* stream);
+
+/* Gradient of na_softmax_dropout from the logits x (the weights are computed again, nothing is stored):
+ * s = softmax(x), g = dropout(dy), dx = s * (g - sum s g).  A place of weight zero (a logit of -inf) has gradient
+ * zero whatever dy holds there.  dx may be x or dy. */
+na_status na_softmax_dropout_bwd(const void* x, const void* dy, void* dx, int B, int ndim, const int* spatial, int heads,
+                                 const int* kernel, double p, const void* rng, na_dtype dtype, void* stream);
+
+/* Differential attention weights: y = dropout(softmax(x1) - lam * softmax(x2)) over the K window weights of every
+ * row, the layout of na_softmax.  lam: fp32, 4-byte aligned: [heads], or with lam_per_row = 1 [B, L.., heads].  A row
+ * of -inf alone counts as zeros.  y may be x1 or x2. */
+na_status na_diff_softmax(const void* x1, const void* x2, const float* lam, int lam_per_row, void* y, int B, int ndim,
+                          const int* spatial, int heads, const int* kernel, double p, const void* rng, na_dtype dtype,
+                          void* stream);
+
+/* Bytes of device workspace na_diff_softmax_bwd needs for a lam per head (0 on invalid arguments). */
+size_t na_diff_softmax_bwd_workspace_size(int B, int ndim, const int* spatial, int heads, const int* kernel);
+
+/* Gradients of na_diff_softmax from the logits: s_m = softmax(x_m), g = dropout(dy), r_m = sum s_m g,
+ * dx1 = s_1 (g - r_1), dx2 = -lam s_2 (g - r_2), dlam = -r_2 per row, summed over batch and tokens for a lam per
+ * head (two stages through the workspace in a fixed order, no atomics).  dlam has the layout of lam.  Places of
+ * weight zero as for na_softmax_dropout_bwd.  dx1 and dx2 may each be one of x1, x2, dy, but not the same one.
+ * Workspace as for na_rpb_grad; unused with lam_per_row. */
+na_status na_diff_softmax_bwd(const void* x1, const void* x2, const float* lam, int lam_per_row, const void* dy,
+                              void* dx1, void* dx2, float* dlam, int B, int ndim, const int* spatial, int heads,
+                              const int* kernel, double p, const void* rng, na_dtype dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

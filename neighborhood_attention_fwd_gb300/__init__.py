@@ -9,10 +9,13 @@ library raises.
 Tensors are contiguous [B, L_1, .., L_n, heads, D] (n = 1..3); lse/delta are fp32 [B, L.., heads].
 The unfused operations (na_qk, na_softmax, na_av and their gradients) keep the attention weights
 as [B, L.., heads, K], K = the product of the kernel sizes, window offsets first axis outermost.
+Around the attention: rotary positions (na_rope), layer norm (na_layernorm), and the window softmax with
+dropout or as the difference of two maps (na_softmax_dropout, na_diff_softmax, na_dropout).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -24,6 +27,9 @@ __all__ = [
     "na_bwd_workspace_size", "na_device_status", "na_strerror", "na_plan_info", "library_path",
     "na_qk", "na_av", "na_softmax", "na_softmax_bwd", "na_qk_bwd", "na_av_bwd", "na_rpb_grad",
     "na_rpb_grad_workspace_size", "na_mask_window", "na_debug_wait_hook",
+    "RopeFreqs", "na_rope", "na_rope_bwd", "na_layernorm", "na_layernorm_bwd", "na_layernorm_bwd_workspace_size",
+    "na_dropout", "na_softmax_dropout", "na_softmax_dropout_bwd", "na_diff_softmax", "na_diff_softmax_bwd",
+    "na_diff_softmax_bwd_workspace_size",
 ]
 
 NA_BF16, NA_FP32, NA_FP16 = 0, 1, 2
@@ -79,6 +85,24 @@ def load(path: str | None = None):
     lib.na_softmax_bwd.argtypes = [P, P, P] + geo_nd + [IP, I, P]
     lib.na_qk_bwd.argtypes = [P, P, P, P, P] + geo + kd + [I, P]
     lib.na_av_bwd.argtypes = [P, P, P, P, P] + geo + [IP, IP, I, P]
+    L, Z, DB = ctypes.c_int64, ctypes.c_size_t, ctypes.c_double
+    rope = [P, P, P, P, I, I, IP, I, I, I, IP, ctypes.POINTER(DB), ctypes.POINTER(L), F, I, I, P]
+    lib.na_rope.argtypes = lib.na_rope_bwd.argtypes = rope
+    lib.na_layernorm.argtypes = [P, P, P, P, P, P, L, I, F, I, P]
+    lib.na_layernorm_bwd.argtypes = [P] * 8 + [L, I, I, P, Z, P]
+    lib.na_layernorm_bwd_workspace_size.argtypes = [L, I, I]
+    lib.na_layernorm_bwd_workspace_size.restype = Z
+    drop = [IP, DB, P, I]                    # kernel, p, rng, dtype
+    lib.na_dropout.argtypes = [P, P, L, DB, P, I, P]
+    lib.na_softmax_dropout.argtypes = [P, P] + geo_nd + drop + [P]
+    lib.na_softmax_dropout_bwd.argtypes = [P, P, P] + geo_nd + drop + [P]
+    lib.na_diff_softmax.argtypes = [P, P, P, I, P] + geo_nd + drop + [P]
+    lib.na_diff_softmax_bwd.argtypes = [P, P, P, I, P, P, P, P] + geo_nd + drop + [P, Z, P]
+    lib.na_diff_softmax_bwd_workspace_size.argtypes = [I, I, IP, I, IP]
+    lib.na_diff_softmax_bwd_workspace_size.restype = Z
+    for f in ("na_rope", "na_rope_bwd", "na_layernorm", "na_layernorm_bwd", "na_dropout", "na_softmax_dropout",
+              "na_softmax_dropout_bwd", "na_diff_softmax", "na_diff_softmax_bwd"):
+        getattr(lib, f).restype = I
     for f in ("na_fwd", "na_bwd", "na_bwd_delta", "na_bwd_dq", "na_bwd_dkdv", "na_device_status", "na_plan_info",
               "na_qk", "na_av", "na_softmax", "na_softmax_bwd", "na_qk_bwd", "na_av_bwd", "na_rpb_grad",
               "na_mask_window"):
@@ -389,3 +413,249 @@ def na_mask_window(attn, sizes, kernel, dilation=None, stream=None):
         flat.record_stream(stream)
     elif stream is not None:
         torch.cuda.ExternalStream(int(stream)).synchronize()
+
+
+# ---------------------------------------------------------------------------------------------
+# Around the attention: rotary positions, layer norm, dropout, differential weights
+# ---------------------------------------------------------------------------------------------
+
+def _on_device(*tensors):
+    """Every tensor on the current CUDA device (kernels are launched on its stream)."""
+    here = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.device.index != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+class RopeFreqs:
+    """Frequencies of na_rope: freqs[a][i] = radians per position of pair i of axis a (axis a owns
+    2 len(freqs[a]) channels), the amplitude that scales the rotated channels, and the pairs' layout, "half" or
+    "interleaved".  A program makes one per configuration and keeps it."""
+
+    def __init__(self, freqs, amplitude: float = 1.0, layout: str = "half"):
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        self.freqs = tuple(tuple(float(f) for f in axis) for axis in freqs)
+        self.amplitude = float(amplitude)
+        self.layout = layout
+        flat = [f for axis in self.freqs for f in axis]
+        self._rot = (ctypes.c_int * len(self.freqs))(*[2 * len(axis) for axis in self.freqs])
+        self._freq = (ctypes.c_double * max(1, len(flat)))(*flat)
+        self._code = 0 if layout == "half" else 1
+
+    @classmethod
+    def scaled(cls, rot, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, trained: int | None = None,
+               fast: float = 32.0, slow: float = 1.0, amplitude: float | None = None, layout: str = "half"):
+        """The usual frequencies base^(-2i/r) of rot[a] = r channels per axis, and their scalings for grids or
+        sequences `factor` times as long as the trained ones:
+          "linear": every frequency divided by factor (positions interpolated);
+          "ntk":    base * factor^(r/(r-2)), which divides the lowest frequency by factor and keeps the highest;
+          "yarn":   divided by factor where a pair makes at most `slow` turns over the `trained` positions, kept
+                    where it makes at least `fast`, blended linearly in the turns between, and the amplitude
+                    0.1 ln(factor) + 1 unless one is given."""
+        if scaling not in ("none", "linear", "ntk", "yarn"):
+            raise ValueError("scaling must be 'none', 'linear', 'ntk' or 'yarn'")
+        if not (base > 0 and factor > 0):
+            raise ValueError("base and factor must be positive")
+        if scaling == "yarn" and (trained is None or trained < 1 or not fast > slow):
+            raise ValueError("yarn needs the trained length, and fast > slow")
+        axes = []
+        for r in rot:
+            r = int(r)
+            if r < 0 or r % 2:
+                raise ValueError("rot must be even")
+            b = base * factor ** (r / (r - 2)) if scaling == "ntk" and r > 2 else base
+            f = [b ** (-2.0 * i / r) for i in range(r // 2)]
+            if scaling == "linear":
+                f = [x / factor for x in f]
+            elif scaling == "yarn":
+                keep = [min(1.0, max(0.0, (trained * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+                f = [x / factor * (1 - g) + x * g for x, g in zip(f, keep)]
+            axes.append(f)
+        if amplitude is None:
+            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+        return cls(axes, amplitude, layout)
+
+
+def _rope(call, what, q, k, q_out, k_out, freqs, origin, stream):
+    B, ndim, spatial, heads, D = _geometry(q)
+    if len(freqs._rot) != ndim:
+        raise ValueError("the frequencies need one entry per spatial axis")
+    _check(q, q.shape, q.dtype, "q")
+    _check(q_out, q.shape, q.dtype, "q_out")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    heads_k = 0
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError("k must have the axes of q")
+        heads_k = int(k.shape[-2])
+        _check(k, tuple(q.shape[:-2]) + (heads_k, D), q.dtype, "k")
+        _check(k_out, k.shape, q.dtype, "k_out")
+    _on_device(q, k, q_out, k_out)
+    if isinstance(origin, int):
+        origin = (origin,) * ndim
+    if origin is not None:
+        if len(origin) != ndim:
+            raise ValueError("origin needs one entry per spatial axis")
+        origin = (ctypes.c_int64 * ndim)(*[int(x) for x in origin])
+    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, ndim, _ints(spatial), heads, heads_k, D, freqs._rot,
+              freqs._freq, origin, freqs.amplitude, freqs._code, _dtype_code(q), _stream(stream))
+    _ok(st, what)
+
+
+def na_rope(q, k, q_out, k_out, freqs: RopeFreqs, origin=None, stream=None):
+    """Rotary positions of q [B, L.., heads, D] and k (the same with its own head count, or None), written
+    into q_out and k_out, which may be q and k.  origin: the grid's first position, one per axis or one for all."""
+    _rope(load().na_rope, "na_rope", q, k, q_out, k_out, freqs, origin, stream)
+
+
+def na_rope_bwd(dq_out, dk_out, dq, dk, freqs: RopeFreqs, origin=None, stream=None):
+    """dq, dk of na_rope given its outputs' gradients (dq may be dq_out, dk may be dk_out)."""
+    _rope(load().na_rope_bwd, "na_rope_bwd", dq_out, dk_out, dq, dk, freqs, origin, stream)
+
+
+def _rows(x):
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError("expected [.., C] with at least one element")
+    C = int(x.shape[-1])
+    return x.numel() // C, C
+
+
+def na_layernorm(x, w, b, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """y = (x - mean) * rstd * w + b over the last axis of x [.., C] (per head: [B, L.., heads, D]; per token:
+    [B, L.., heads * D]).  w, b: fp32 [C] or None; mean, rstd: fp32 x.shape[:-1] for the backward, or None."""
+    rows, C = _rows(x)
+    _check(x, x.shape, x.dtype, "x")
+    _check(y, x.shape, x.dtype, "y")
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _check(t, (C,), torch.float32, name)
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd go together")
+    if mean is not None:
+        _check(mean, x.shape[:-1], torch.float32, "mean")
+        _check(rstd, x.shape[:-1], torch.float32, "rstd")
+    _on_device(x, w, b, y, mean, rstd)
+    st = load().na_layernorm(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, float(eps),
+                             _dtype_code(x), _stream(stream))
+    _ok(st, "na_layernorm")
+
+
+def na_layernorm_bwd_workspace_size(rows: int, C: int, dtype=torch.bfloat16) -> int:
+    code = _dtype_code(torch.empty(0, dtype=dtype))
+    return int(load().na_layernorm_bwd_workspace_size(int(rows), int(C), code))
+
+
+def na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw=None, db=None, workspace=None, stream=None):
+    """dx (may be dy or x) and, when given, dw and db (fp32 [C]) of na_layernorm."""
+    rows, C = _rows(x)
+    for name, t in (("x", x), ("dy", dy), ("dx", dx)):
+        _check(t, x.shape, x.dtype, name)
+    for name, t in (("w", w), ("dw", dw), ("db", db)):
+        if t is not None:
+            _check(t, (C,), torch.float32, name)
+    if (dw is None) != (db is None):
+        raise ValueError("dw and db go together")
+    _check(mean, x.shape[:-1], torch.float32, "mean")
+    _check(rstd, x.shape[:-1], torch.float32, "rstd")
+    _on_device(dy, x, w, mean, rstd, dx, dw, db, workspace)
+    st = load().na_layernorm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+                                 _ptr(dw), _ptr(db), rows, C, _dtype_code(x), *_workspace(workspace), _stream(stream))
+    _ok(st, "na_layernorm_bwd")
+
+
+def _rng(rng):
+    if rng is not None:
+        _check(rng, (2,), torch.int64, "rng")
+    return _ptr(rng)
+
+
+def na_dropout(x, y, p: float, rng, stream=None):
+    """y = dropout(x) (y may be x): each element zero with probability p, else scaled.  rng: int64 CUDA tensor
+    (seed, offset); the same state keeps the same elements, so the gradient is na_dropout(dy, dx, p, rng)."""
+    _check(x, x.shape, x.dtype, "x")
+    _check(y, x.shape, x.dtype, "y")
+    state = _rng(rng)
+    _on_device(x, y, rng)
+    st = load().na_dropout(x.data_ptr(), y.data_ptr(), x.numel(), float(p), state, _dtype_code(x), _stream(stream))
+    _ok(st, "na_dropout")
+
+
+def na_softmax_dropout(x, y, kernel, p: float, rng, stream=None):
+    """y = dropout(softmax(x)) over each row's K window weights (y may be x; keep x for the gradient)."""
+    B, ndim, spatial, heads, kernel = _attn_geometry(x, kernel)
+    _check(x, x.shape, x.dtype, "x")
+    _check(y, x.shape, x.dtype, "y")
+    state = _rng(rng)
+    _on_device(x, y, rng)
+    st = load().na_softmax_dropout(x.data_ptr(), y.data_ptr(), B, ndim, _ints(spatial), heads, _ints(kernel), float(p),
+                                   state, _dtype_code(x), _stream(stream))
+    _ok(st, "na_softmax_dropout")
+
+
+def na_softmax_dropout_bwd(x, dy, dx, kernel, p: float, rng, stream=None):
+    """dx of na_softmax_dropout given its logits x, dy and the forward's p and rng (dx may be x or dy)."""
+    B, ndim, spatial, heads, kernel = _attn_geometry(x, kernel)
+    for name, t in (("x", x), ("dy", dy), ("dx", dx)):
+        _check(t, x.shape, x.dtype, name)
+    state = _rng(rng)
+    _on_device(x, dy, dx, rng)
+    st = load().na_softmax_dropout_bwd(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), B, ndim, _ints(spatial), heads,
+                                       _ints(kernel), float(p), state, _dtype_code(x), _stream(stream))
+    _ok(st, "na_softmax_dropout_bwd")
+
+
+def _lam_rows(lam, rows_shape, heads):
+    """0 for a weight per head ([heads]), 1 for one per row ([B, L.., heads])."""
+    per_row = lam.dim() != 1
+    _check(lam, rows_shape if per_row else (heads,), torch.float32, "lam")
+    return int(per_row)
+
+
+def na_diff_softmax(x1, x2, lam, y, kernel, p: float = 0.0, rng=None, stream=None):
+    """y = dropout(softmax(x1) - lam * softmax(x2)) over each row's K window weights.  lam: fp32 [heads] or
+    [B, L.., heads].  y may be x1 or x2 (keep the logits for the gradient)."""
+    B, ndim, spatial, heads, kernel = _attn_geometry(x1, kernel)
+    for name, t in (("x1", x1), ("x2", x2), ("y", y)):
+        _check(t, x1.shape, x1.dtype, name)
+    per_row = _lam_rows(lam, x1.shape[:-1], heads)
+    state = _rng(rng)
+    _on_device(x1, x2, lam, y, rng)
+    st = load().na_diff_softmax(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, y.data_ptr(), B, ndim,
+                                _ints(spatial), heads, _ints(kernel), float(p), state, _dtype_code(x1), _stream(stream))
+    _ok(st, "na_diff_softmax")
+
+
+def na_diff_softmax_bwd_workspace_size(B, spatial, heads, kernel) -> int:
+    kernel = (kernel,) * len(spatial) if isinstance(kernel, int) else tuple(kernel)
+    return int(load().na_diff_softmax_bwd_workspace_size(int(B), len(spatial), _ints(spatial), int(heads), _ints(kernel)))
+
+
+def na_diff_softmax_bwd(x1, x2, lam, dy, dx1, dx2, dlam, kernel, p: float = 0.0, rng=None, workspace=None, stream=None):
+    """dx1, dx2, dlam (the shape of lam) of na_diff_softmax given its logits, dy and the forward's p and rng."""
+    B, ndim, spatial, heads, kernel = _attn_geometry(x1, kernel)
+    for name, t in (("x1", x1), ("x2", x2), ("dy", dy), ("dx1", dx1), ("dx2", dx2)):
+        _check(t, x1.shape, x1.dtype, name)
+    per_row = _lam_rows(lam, x1.shape[:-1], heads)
+    _check(dlam, lam.shape, torch.float32, "dlam")
+    state = _rng(rng)
+    _on_device(x1, x2, lam, dy, dx1, dx2, dlam, rng, workspace)
+    st = load().na_diff_softmax_bwd(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, dy.data_ptr(), dx1.data_ptr(),
+                                    dx2.data_ptr(), dlam.data_ptr(), B, ndim, _ints(spatial), heads, _ints(kernel),
+                                    float(p), state, _dtype_code(x1), *_workspace(workspace), _stream(stream))
+    _ok(st, "na_diff_softmax_bwd")

@@ -17,6 +17,8 @@
 #include "na_internal.h"
 
 namespace na {
+na_status device_status_word(unsigned** out);
+unsigned long long wait_limit_ns();
 uint32_t tc_smem_bytes(int which, const TilePlan& pl, int D);
 int tc_tmem_cols(int which, int D);
 int tc_max_nc(int which, int D, int sbufs);
@@ -545,6 +547,11 @@ void unfused_tma_maps(na::UnfParams& p, int B, const void* src, const void* w, n
     p.tma = 1;
 }
 }  // namespace
+
+namespace na {
+na_status device_status_word(unsigned** out) { return status_ptr(out); }
+unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
+}  // namespace na
 
 extern "C" {
 

@@ -1,0 +1,164 @@
+// na_block.cuh -- what the operators around the attention (na_rope.cu, na_norm.cu, na_winsoft.cu) share:
+// argument checks on the host, cache-streaming 16-byte accesses and the dropout generator.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/na.h"
+#include "na_elem.cuh"
+#include "na_internal.h"
+
+namespace na {
+
+// Device status word of the current device, and the time limit of one bounded wait (na_api.cu).
+na_status device_status_word(unsigned** out);
+unsigned long long wait_limit_ns();
+
+// ---------------------------------------------------------------------------------------------
+// Host: argument checks
+// ---------------------------------------------------------------------------------------------
+
+struct Span {
+    const void* p;
+    long long bytes;
+};
+
+inline bool spans_overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// An output may be one of the tensors in `same` (the very same memory) and overlaps nothing else.
+inline bool output_clear(const Span& out, std::initializer_list<Span> same, std::initializer_list<Span> apart) {
+    for (const Span& s : same)
+        if (spans_overlap(out, s) && (out.p != s.p || out.bytes != s.bytes)) return false;
+    for (const Span& s : apart)
+        if (spans_overlap(out, s)) return false;
+    return true;
+}
+
+inline bool ptr_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+inline bool known_dtype(na_dtype dt) { return dt == NA_BF16 || dt == NA_FP16 || dt == NA_FP32; }
+inline int elem_bytes(na_dtype dt) { return dt == NA_FP32 ? 4 : 2; }
+
+// Tokens (B times the grid) of a [B, L_1 .., heads, width] tensor, with the size limits of the attention
+// entry points (2^31 grid positions, 2^40 elements); L receives the grid as 3 axes, outermost first.
+inline na_status grid_tokens(int B, int ndim, const int* spatial, int heads, long long width, int (&L)[3], long long& tokens) {
+    if (ndim < 1 || ndim > 3 || !spatial || B < 1 || heads < 1 || width < 1) return NA_ERR_INVALID_ARG;
+    for (int a = 0; a < ndim; ++a)
+        if (spatial[a] < 1) return NA_ERR_INVALID_ARG;
+    for (int a = 0; a < 3; ++a) L[a] = 1;
+    long long n = 1;
+    for (int a = 0; a < ndim; ++a) {
+        L[3 - ndim + a] = spatial[a];
+        n *= spatial[a];
+        if (n > (1LL << 31)) return NA_ERR_UNSUPPORTED;
+    }
+    tokens = n * B;
+    if (tokens > (1LL << 40) / heads || tokens * heads > (1LL << 40) / width) return NA_ERR_UNSUPPORTED;
+    return NA_OK;
+}
+
+constexpr int kSms = 152;   // multiprocessors of a GB300: grids are sized for them
+
+inline na_status launch_result() { return cudaGetLastError() == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
+
+// ---------------------------------------------------------------------------------------------
+// Device: 16-byte accesses.  The operators read and write every byte once, so they leave L1 alone.
+// Not the read-only path: an output may be the input's tensor.
+// ---------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_stream(void* p, const uint4& v) {
+    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------------------------
+// Dropout: which elements are kept is a function of (seed, offset, element index) alone, so no mask is
+// stored: the backward pass computes it again.  Generator: Philox4x32 (Salmon, Moraes, Dror and Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", 2011) with seven rounds, the fewest that the paper
+// reports as passing all of BigCrush; it costs 0.7 of the default ten.  One block of 128 bits serves
+// eight elements of 16 bits each: block i / 8 of element i sits at counter (i / 8, offset) under key
+// seed, and field i % 8 is compared with the number of steps kept.  Sixteen bits make the keep
+// probability a multiple of 2^-16; the gain is the inverse of that multiple, so the mean is exact.
+// ---------------------------------------------------------------------------------------------
+
+struct Dropout {
+    const unsigned long long* state;  // device: {seed, offset}; null: nothing is dropped
+    uint32_t steps;                   // fields below it are kept, 0 .. 65535 with a state
+    float gain;                       // 65536 / steps (0 when steps is 0)
+};
+
+// false for a probability outside [0, 1] or a missing generator state.
+inline bool make_dropout(double p, const void* state, Dropout& d) {
+    if (!(p >= 0.0 && p <= 1.0)) return false;
+    d.steps = static_cast<uint32_t>(std::floor((1.0 - p) * 65536.0 + 0.5));
+    d.gain = d.steps ? static_cast<float>(65536.0 / d.steps) : 0.f;
+    d.state = d.steps == 65536u ? nullptr : static_cast<const unsigned long long*>(state);
+    return d.steps == 65536u || state != nullptr;
+}
+
+struct RngState {
+    uint32_t k0, k1, o0, o1;
+};
+
+__device__ __forceinline__ RngState rng_load(const unsigned long long* s) {
+    const unsigned long long seed = s[0], off = s[1];
+    return RngState{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(off),
+                    static_cast<uint32_t>(off >> 32)};
+}
+
+// Keep masks of the eight elements of one block: word j holds 0xffff in the half of each kept element
+// 2 j (low half) and 2 j + 1 (high half).
+__device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long long block, uint32_t steps) {
+    uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32), c2 = s.o0, c3 = s.o1;
+    uint32_t k0 = s.k0, k1 = s.k1;
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+        const unsigned long long a = static_cast<unsigned long long>(c0) * 0xD2511F53u;
+        const unsigned long long b = static_cast<unsigned long long>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(b);
+        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(a);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    // whole words below steps << 16 are those whose high field is below steps
+    const uint32_t lim = steps << 16;
+    auto masks = [lim](uint32_t w) { return (w < lim ? 0xffff0000u : 0u) | ((w << 16) < lim ? 0x0000ffffu : 0u); };
+    return make_uint4(masks(c0), masks(c1), masks(c2), masks(c3));
+}
+
+__device__ __forceinline__ bool keep_of(const uint4& m, int i) {
+    const uint32_t w = i < 2 ? m.x : (i < 4 ? m.y : (i < 6 ? m.z : m.w));
+    return ((w >> (16 * (i & 1))) & 1u) != 0u;
+}
+
+__device__ __forceinline__ uint4 and4(const uint4& a, const uint4& m) {
+    return make_uint4(a.x & m.x, a.y & m.y, a.z & m.z, a.w & m.w);
+}
+
+// The mask of eight 16-bit elements widened to the two chunks of eight 32-bit elements.
+__device__ __forceinline__ void widen_masks(const uint4& m, uint4& a, uint4& b) {
+    auto lo = [](uint32_t w) { return static_cast<uint32_t>(static_cast<int32_t>(w << 16) >> 16); };
+    auto hi = [](uint32_t w) { return static_cast<uint32_t>(static_cast<int32_t>(w) >> 16); };
+    a = make_uint4(lo(m.x), hi(m.x), lo(m.y), hi(m.y));
+    b = make_uint4(lo(m.z), hi(m.z), lo(m.w), hi(m.w));
+}
+
+}  // namespace na

@@ -17,6 +17,7 @@ namespace dev {
 // Wait sites recorded in the status word (0x5000 | site) when a bounded wait runs out.
 enum WaitSite : unsigned {
     kSiteQ = 1, kSiteKV = 2, kSiteS = 3, kSiteP = 4, kSitePV = 5, kSiteEmpty = 6, kSiteFinal = 7, kSiteSt = 8,
+    kSiteWin = 9,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // default limit of one wait: 2 s
