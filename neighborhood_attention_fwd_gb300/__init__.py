@@ -437,8 +437,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _workspace(ws, stream, nbytes, device):
+    """(tensor, pointer, bytes) of a call's workspace.  Without one from the caller, a call on the current stream
+    takes it from torch's allocator, which keeps freed memory at hand; a call on another stream leaves it to the
+    library, which allocates on that stream."""
+    if ws is None and stream is None:
+        ws = torch.empty(nbytes(), dtype=torch.uint8, device=device)
+    return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 class RopeFreqs:
@@ -574,8 +579,11 @@ def na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw=None, db=None, workspace=None,
     _check(mean, x.shape[:-1], torch.float32, "mean")
     _check(rstd, x.shape[:-1], torch.float32, "rstd")
     _on_device(dy, x, w, mean, rstd, dx, dw, db, workspace)
+    code = _dtype_code(x)
+    need = lambda: load().na_layernorm_bwd_workspace_size(rows, C, code)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if dw is None else _workspace(workspace, stream, need, x.device)
     st = load().na_layernorm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-                                 _ptr(dw), _ptr(db), rows, C, _dtype_code(x), *_workspace(workspace), _stream(stream))
+                                 _ptr(dw), _ptr(db), rows, C, code, ws_ptr, ws_bytes, _stream(stream))
     _ok(st, "na_layernorm_bwd")
 
 
@@ -655,7 +663,10 @@ def na_diff_softmax_bwd(x1, x2, lam, dy, dx1, dx2, dlam, kernel, p: float = 0.0,
     _check(dlam, lam.shape, torch.float32, "dlam")
     state = _rng(rng)
     _on_device(x1, x2, lam, dy, dx1, dx2, dlam, rng, workspace)
+    L, k = _ints(spatial), _ints(kernel)
+    need = lambda: load().na_diff_softmax_bwd_workspace_size(B, ndim, L, heads, k)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if per_row else _workspace(workspace, stream, need, x1.device)
     st = load().na_diff_softmax_bwd(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, dy.data_ptr(), dx1.data_ptr(),
-                                    dx2.data_ptr(), dlam.data_ptr(), B, ndim, _ints(spatial), heads, _ints(kernel),
-                                    float(p), state, _dtype_code(x1), *_workspace(workspace), _stream(stream))
+                                    dx2.data_ptr(), dlam.data_ptr(), B, ndim, L, heads, k, float(p), state,
+                                    _dtype_code(x1), ws_ptr, ws_bytes, _stream(stream))
     _ok(st, "na_diff_softmax_bwd")

@@ -122,9 +122,8 @@ __device__ __forceinline__ RngState rng_load(const unsigned long long* s) {
                     static_cast<uint32_t>(off >> 32)};
 }
 
-// Keep masks of the eight elements of one block: word j holds 0xffff in the half of each kept element
-// 2 j (low half) and 2 j + 1 (high half).
-__device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long long block, uint32_t steps) {
+// The 128 random bits of a block.
+__device__ __forceinline__ uint4 rng_block(const RngState& s, unsigned long long block) {
     uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32), c2 = s.o0, c3 = s.o1;
     uint32_t k0 = s.k0, k1 = s.k1;
 #pragma unroll
@@ -138,10 +137,19 @@ __device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long lon
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    // whole words below steps << 16 are those whose high field is below steps
-    const uint32_t lim = steps << 16;
-    auto masks = [lim](uint32_t w) { return (w < lim ? 0xffff0000u : 0u) | ((w << 16) < lim ? 0x0000ffffu : 0u); };
-    return make_uint4(masks(c0), masks(c1), masks(c2), masks(c3));
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// Whole words below steps << 16 are those whose high field is below steps (steps < 65536).
+__device__ __forceinline__ bool keep_high(uint32_t w, uint32_t steps) { return w < (steps << 16); }
+__device__ __forceinline__ bool keep_low(uint32_t w, uint32_t steps) { return (w << 16) < (steps << 16); }
+
+// Keep masks of the eight elements of one block: word j holds 0xffff in the half of each kept element
+// 2 j (low half) and 2 j + 1 (high half).
+__device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long long block, uint32_t steps) {
+    const uint4 w = rng_block(s, block);
+    auto masks = [steps](uint32_t v) { return (keep_high(v, steps) ? 0xffff0000u : 0u) | (keep_low(v, steps) ? 0x0000ffffu : 0u); };
+    return make_uint4(masks(w.x), masks(w.y), masks(w.z), masks(w.w));
 }
 
 __device__ __forceinline__ bool keep_of(const uint4& m, int i) {
@@ -149,16 +157,28 @@ __device__ __forceinline__ bool keep_of(const uint4& m, int i) {
     return ((w >> (16 * (i & 1))) & 1u) != 0u;
 }
 
-__device__ __forceinline__ uint4 and4(const uint4& a, const uint4& m) {
-    return make_uint4(a.x & m.x, a.y & m.y, a.z & m.z, a.w & m.w);
+// Zeros the dropped elements of an octet: eight 16-bit elements, or eight 32-bit ones in two chunks.
+__device__ __forceinline__ void drop_octet(uint4& d, const RngState& s, unsigned long long block, uint32_t steps) {
+    const uint4 w = rng_block(s, block);
+    auto drop = [steps](uint32_t& v, uint32_t r) {
+        if (!keep_high(r, steps)) v &= 0x0000ffffu;
+        if (!keep_low(r, steps)) v &= 0xffff0000u;
+    };
+    drop(d.x, w.x);
+    drop(d.y, w.y);
+    drop(d.z, w.z);
+    drop(d.w, w.w);
 }
-
-// The mask of eight 16-bit elements widened to the two chunks of eight 32-bit elements.
-__device__ __forceinline__ void widen_masks(const uint4& m, uint4& a, uint4& b) {
-    auto lo = [](uint32_t w) { return static_cast<uint32_t>(static_cast<int32_t>(w << 16) >> 16); };
-    auto hi = [](uint32_t w) { return static_cast<uint32_t>(static_cast<int32_t>(w) >> 16); };
-    a = make_uint4(lo(m.x), hi(m.x), lo(m.y), hi(m.y));
-    b = make_uint4(lo(m.z), hi(m.z), lo(m.w), hi(m.w));
+__device__ __forceinline__ void drop_octet(uint4& a, uint4& b, const RngState& s, unsigned long long block, uint32_t steps) {
+    const uint4 w = rng_block(s, block);
+    auto drop = [steps](uint32_t& lo, uint32_t& hi, uint32_t r) {
+        if (!keep_low(r, steps)) lo = 0u;
+        if (!keep_high(r, steps)) hi = 0u;
+    };
+    drop(a.x, a.y, w.x);
+    drop(a.z, a.w, w.y);
+    drop(b.x, b.y, w.z);
+    drop(b.z, b.w, w.w);
 }
 
 }  // namespace na
