@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libna.so")
 SOURCES = ["na_api.cu", "na_fma.cu", "na_tc.cu", "na_tc_f16.cu", "na_tc_sb3.cu", "na_unfused.cu",
-           "na_rope.cu", "na_norm.cu", "na_winsoft.cu", "na_win_bf16.cu", "na_win_f16.cu", "na_win_f32.cu"]
+           "na_rope.cu", "na_norm.cu", "na_winsoft.cu"]
+SOURCES += [f"na_win_{form}_{way}_{t}.cu" for form in ("soft", "diff") for way in ("fwd", "bwd") for t in ("bf16", "f16", "f32")]
 HEADERS = ["na_internal.h", "na_device.cuh", "na_tc_impl.cuh", "na_elem.cuh", "na_block.cuh",
            "na_win.h", "na_win_impl.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

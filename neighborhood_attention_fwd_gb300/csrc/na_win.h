@@ -5,7 +5,7 @@
 
 namespace na {
 
-constexpr int kWinThreads = 256;
+constexpr int kWinThreads = 128;
 
 struct WinParams {
     const void* x1;
@@ -17,19 +17,26 @@ struct WinParams {
     float* dlam;           // backward: -r_2 of every row
     long long rows, tiles;
     int K, heads;
-    int lanes, log_lanes;  // lanes per row (a power of two)
     int tile;              // rows per tile (a multiple of 8)
     int stages;            // tiles of a block's ring
-    uint32_t lam_rows, rows32;
-    FastDiv fd_heads;
+    uint32_t lam_rows;
     Dropout drop;
     unsigned* err;         // device status word
     unsigned long long wait_ns;
 };
 
-// One instance per type: `diff` the difference of two maps, `bwd` the gradients.
-na_status launch_win_bf16(WinParams& p, bool diff, bool bwd, cudaStream_t s);
-na_status launch_win_f16(WinParams& p, bool diff, bool bwd, cudaStream_t s);
-na_status launch_win_f32(WinParams& p, bool diff, bool bwd, cudaStream_t s);
+// Kernels of one type and form: `diff` the difference of two maps, `bwd` the gradients.
+na_status launch_soft_fwd_bf16(WinParams& p, cudaStream_t s);
+na_status launch_soft_fwd_f16(WinParams& p, cudaStream_t s);
+na_status launch_soft_fwd_f32(WinParams& p, cudaStream_t s);
+na_status launch_soft_bwd_bf16(WinParams& p, cudaStream_t s);
+na_status launch_soft_bwd_f16(WinParams& p, cudaStream_t s);
+na_status launch_soft_bwd_f32(WinParams& p, cudaStream_t s);
+na_status launch_diff_fwd_bf16(WinParams& p, cudaStream_t s);
+na_status launch_diff_fwd_f16(WinParams& p, cudaStream_t s);
+na_status launch_diff_fwd_f32(WinParams& p, cudaStream_t s);
+na_status launch_diff_bwd_bf16(WinParams& p, cudaStream_t s);
+na_status launch_diff_bwd_f16(WinParams& p, cudaStream_t s);
+na_status launch_diff_bwd_f32(WinParams& p, cudaStream_t s);
 
 }  // namespace na

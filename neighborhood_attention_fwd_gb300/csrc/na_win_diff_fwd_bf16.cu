@@ -1,0 +1,6 @@
+// na_win_diff_fwd_bf16.cu -- differential window softmax, forward, bf16: kernel instances.
+#include "na_win_impl.cuh"
+
+namespace na {
+na_status launch_diff_fwd_bf16(WinParams& p, cudaStream_t s) { return launch_win_rows<__nv_bfloat16, true, false>(p, s); }
+}  // namespace na

@@ -29,7 +29,9 @@ using namespace dev;
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
+constexpr int kTileBytes = 12 * 1024;
+constexpr int kLongThreads = 256;   // block of a row that no tile holds
 
 // A row's words: 4 bytes, one or two weights.
 template <typename T>
@@ -85,36 +87,33 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// The place of a lane in its row.  Lane l holds words l, l + lanes, .., J of them; the row has (K + 1) / 2 words (K is
+// The place of a lane in its row.  Lane l of L holds words l, l + L, .., J of them; the row has (K + 1) / 2 words (K is
 // odd) and fills all but the last of every lane's: only word 0 (`head`: its low half is the row before's) and the
 // last words (`last` 0: past the row, 1: the low half alone, 2: whole) need care.
 struct Place {
-    uint32_t* s;     // the lane's first word of the first tensor's tile
-    int lanes;
+    uint32_t at;     // the lane's first word, in words from the tile's start
     bool head;
     int last;
 };
 
-template <typename T, int J>
-__device__ __forceinline__ void row_load(uint32_t (&r)[J], const Place& a, uint32_t shift, uint32_t fill) {
-    const uint32_t* s = a.s + shift;
+template <typename T, int L, int J>
+__device__ __forceinline__ void row_load(uint32_t (&r)[J], const uint32_t* s, const Place& a, uint32_t fill) {
 #pragma unroll
-    for (int j = 0; j < J - 1; ++j) r[j] = s[a.lanes * j];
-    r[J - 1] = a.last ? s[a.lanes * (J - 1)] : fill;
+    for (int j = 0; j < J - 1; ++j) r[j] = s[L * j];
+    r[J - 1] = a.last ? s[L * (J - 1)] : fill;
     if (Words<T>::N == 2) {
         if (a.last == 1) r[J - 1] = (r[J - 1] & 0xffffu) | (fill & 0xffff0000u);
         if (a.head) r[0] = (r[0] & 0xffff0000u) | (fill & 0xffffu);
     }
 }
 
-template <typename T, int J>
-__device__ __forceinline__ void row_store(const float (&v)[J * Words<T>::N], const Place& a, uint32_t shift) {
+template <typename T, int L, int J>
+__device__ __forceinline__ void row_store(const float (&v)[J * Words<T>::N], uint32_t* s, const Place& a) {
     constexpr int N = Words<T>::N;
-    uint32_t* s = a.s + shift;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const uint32_t u = Words<T>::put(v + j * N);
-        uint32_t* to = s + a.lanes * j;
+        uint32_t* to = s + L * j;
         if (N == 2 && j == 0 && a.head) {   // the low half is the row before's
             if (J > 1 || a.last == 2) reinterpret_cast<uint16_t*>(to)[1] = static_cast<uint16_t>(u >> 16);
         } else if (j < J - 1 || a.last == 2) {
@@ -125,17 +124,17 @@ __device__ __forceinline__ void row_store(const float (&v)[J * Words<T>::N], con
     }
 }
 
-__device__ __forceinline__ float lanes_max(float v, int lanes) {
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        if (m < lanes) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    for (int m = L / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
     return v;
 }
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        if (m < lanes) v += __shfl_xor_sync(0xffffffffu, v, m);
+    for (int m = L / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     return v;
 }
 
@@ -149,15 +148,15 @@ __device__ __forceinline__ float row_top(float m, bool& far) {
 }
 
 // v = exp(x - max) of a row, and its sum over the lanes (0 for an empty row).
-template <typename T, int J>
-__device__ __forceinline__ float row_exp(const uint32_t (&r)[J], float (&v)[J * Words<T>::N], int lanes) {
+template <typename T, int L, int J>
+__device__ __forceinline__ float row_exp(const uint32_t (&r)[J], float (&v)[J * Words<T>::N]) {
     constexpr int N = Words<T>::N, NV = J * N;
     uint32_t mw = r[0];
 #pragma unroll
     for (int j = 1; j < J; ++j) mw = Words<T>::max(mw, r[j]);
     // a NaN in mw loses to any number, and is none where it is alone: its exponential is NaN all the same
     bool far;
-    float m = row_top(lanes_max(fmaxf(Words<T>::top(mw), -INFINITY), lanes), far);
+    float m = row_top(lanes_max<L>(fmaxf(Words<T>::top(mw), -INFINITY)), far);
 #pragma unroll
     for (int j = 0; j < J; ++j) Words<T>::get(r[j], v + j * N);
     if (far) {
@@ -183,7 +182,7 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[J], float (&v)[J * 
         v[NV - 1] = fast_exp2(fmaf(v[NV - 1], kLog2e, ml2));
         a += v[NV - 1];
     }
-    return lanes_sum(a, lanes);
+    return lanes_sum<L>(a);
 }
 
 // 1 / l of a row's sum: at least 1 (its largest term), 0 for an empty row, or NaN.
@@ -210,8 +209,8 @@ __device__ __forceinline__ void row_axpy(float (&v)[NV], const float (&u)[NV], f
 }
 
 // sum v g over the lanes.
-template <int NV>
-__device__ __forceinline__ float row_dot(const float (&v)[NV], const float (&g)[NV], int lanes) {
+template <int L, int NV>
+__device__ __forceinline__ float row_dot(const float (&v)[NV], const float (&g)[NV]) {
     uint64_t t = 0;
 #pragma unroll
     for (int i = 0; i + 1 < NV; i += 2) t = fma2(pack2(v[i], v[i + 1]), pack2(g[i], g[i + 1]), t);
@@ -219,7 +218,7 @@ __device__ __forceinline__ float row_dot(const float (&v)[NV], const float (&g)[
     split2(t, a, b);
     a += b;
     if (NV % 2) a = fmaf(v[NV - 1], g[NV - 1], a);
-    return lanes_sum(a, lanes);
+    return lanes_sum<L>(a);
 }
 
 // v = v a (g - q), pairwise.
@@ -263,20 +262,25 @@ __device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, 
     }
 }
 
-template <typename T, bool DIFF, bool BWD, int J>
-__global__ void __launch_bounds__(kWinThreads) win_kernel(const __grid_constant__ WinParams p) {
+// Blocks per multiprocessor that the registers leave room for: the backward holds a row's weights and gradients.
+template <bool DIFF, bool BWD, int J>
+constexpr int win_blocks() { return BWD || DIFF ? 6 : 8; }
+
+template <typename T, bool DIFF, bool BWD, int L, int J>
+__global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_kernel(const __grid_constant__ WinParams p) {
     constexpr int N = Words<T>::N, NV = J * N, NB = (DIFF ? 2 : 1) + (BWD ? 1 : 0), NO = DIFF && BWD ? 2 : 1;
+    constexpr int kRows = kWinThreads / L;   // rows of a pass: even, so a lane's place in its row is the same in every pass
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxStages];
+    __shared__ int issued, lost;   // thread 0's: tiles loaded; the first one whose copy did not land in time (-1: none)
     const uint32_t buf = static_cast<uint32_t>(p.tile) * p.K * sizeof(T);   // a multiple of 16
     const uint32_t stage = NB * buf;
     const WaitGuard guard{p.err, p.wait_ns};
-    // bytes of tile t
-    auto tile_bytes = [&](long long t) {
-        return static_cast<uint32_t>(min(static_cast<long long>(p.tile), p.rows - t * p.tile)) * p.K * static_cast<uint32_t>(sizeof(T));
-    };
-    auto load = [&](long long t, int s) {   // one thread
-        const uint32_t bulk = tile_bytes(t) & ~15u;
+    const long long last_tile = p.tiles - 1;
+    const int last_rows = static_cast<int>(p.rows - last_tile * p.tile);
+    auto load = [&](long long t, int s) {   // thread 0
+        ++issued;
+        const uint32_t bulk = t == last_tile ? (static_cast<uint32_t>(last_rows) * p.K * sizeof(T)) & ~15u : buf;
         const long long off = t * static_cast<long long>(buf);
         unsigned char* to = smem + s * stage;
         mbar_arrive_expect_tx(&full[s], NB * bulk);
@@ -289,24 +293,43 @@ __global__ void __launch_bounds__(kWinThreads) win_kernel(const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         fence_barrier_init();
+        issued = 0;
+        lost = -1;
         long long t = blockIdx.x;
         for (int s = 0; s < p.stages - 1 && t < p.tiles; ++s, t += gridDim.x) load(t, s);
     }
     RngState rng{};
     const bool dropping = p.drop.state != nullptr;
     if (dropping) rng = rng_load(p.drop.state);
-    const int l = threadIdx.x & (p.lanes - 1), rpp = kWinThreads >> p.log_lanes, r_first = threadIdx.x >> p.log_lanes;
-    const int words = N == 2 ? (p.K + 1) / 2 : p.K;
-    const int last_word = l + p.lanes * (J - 1);
+    const int l = threadIdx.x & (L - 1), r0 = threadIdx.x / L;
+    const int words = N == 2 ? (p.K + 1) / 2 : p.K, last_word = l + L * (J - 1);
+    const uint32_t e0 = static_cast<uint32_t>(r0) * p.K, pass_words = static_cast<uint32_t>(kRows) * p.K / N;
+    Place a;
+    a.at = e0 / N + l;
+    a.head = N == 2 && (e0 & 1u) && l == 0;
+    a.last = last_word < words - 1 ? 2 : (last_word == words - 1 ? (N == 2 && !(e0 & 1u) ? 1 : 2) : 0);
+    // head of this lane's row in the first pass of a tile, and its steps from pass to pass and from tile to tile
+    uint32_t head = 0, head_pass = 0, head_tile = 0;
+    const uint32_t heads = static_cast<uint32_t>(p.heads);
+    if (DIFF && !p.lam_rows) {
+        head = static_cast<uint32_t>((static_cast<unsigned long long>(blockIdx.x) * p.tile + r0) % heads);
+        head_pass = kRows % heads;
+        head_tile = static_cast<uint32_t>(static_cast<unsigned long long>(gridDim.x) * p.tile % heads);
+    }
     __syncthreads();
     int s = 0;
     uint32_t parity = 0;
     for (long long t = blockIdx.x; t < p.tiles; t += gridDim.x) {
         const long long row0 = t * p.tile;
         unsigned char* tile = smem + s * stage;
-        const uint32_t bytes = tile_bytes(t), bulk = bytes & ~15u;
+        const bool is_last = t == last_tile;
+        const int nrows = is_last ? last_rows : p.tile;
+        const uint32_t elems = static_cast<uint32_t>(nrows) * p.K, bytes = elems * sizeof(T), bulk = bytes & ~15u;
         const long long off = t * static_cast<long long>(buf);
-        if (!mbar_wait(&full[s], parity, guard, kSiteWin)) break;
+        // A wait that runs out records itself; the block then goes on to its end without copies, so that its
+        // threads keep meeting at the barriers (every later wait gives up at once).
+        if (!mbar_wait(&full[s], parity, guard, kSiteWin) && threadIdx.x == 0 && lost < 0)
+            lost = static_cast<int>((t - blockIdx.x) / gridDim.x);
         // the tensor may end inside a chunk: its last elements one by one
         const uint32_t tail = (bytes - bulk) / static_cast<uint32_t>(sizeof(T));
         if (tail != 0) {
@@ -322,83 +345,78 @@ __global__ void __launch_bounds__(kWinThreads) win_kernel(const __grid_constant_
             __syncthreads();
         }
         const unsigned long long block0 = static_cast<unsigned long long>(row0) * p.K / 8;   // row0 is a multiple of 8
-        const uint32_t octets = (bytes / static_cast<uint32_t>(sizeof(T)) + 7) / 8;
         if (BWD && dropping) {
-            drop_tile<T>(tile + (NB - 1) * buf, octets, block0, rng, p.drop.steps);
+            drop_tile<T>(tile + (NB - 1) * buf, (elems + 7) / 8, block0, rng, p.drop.steps);
             __syncthreads();
         }
-        uint32_t head0 = 0;
-        if (DIFF && !p.lam_rows)
-            head0 = p.rows32 ? static_cast<uint32_t>(row0) - fdiv(static_cast<uint32_t>(row0), p.fd_heads) * p.heads
-                             : static_cast<uint32_t>(row0 % p.heads);
-        const int nrows = static_cast<int>(min(static_cast<long long>(p.tile), p.rows - row0));
-        for (int r = r_first; r - r_first < nrows; r += rpp) {   // rows past the end work on what the buffer holds, for nothing
-            const uint32_t e0 = static_cast<uint32_t>(r) * p.K;
-            Place a;
-            a.s = reinterpret_cast<uint32_t*>(tile) + e0 / N + l;
-            a.lanes = p.lanes;
-            a.head = N == 2 && (e0 & 1u) && l == 0;
-            a.last = last_word < words - 1 ? 2 : (last_word == words - 1 ? (N == 2 && !(e0 & 1u) ? 1 : 2) : 0);
+        uint32_t* s1 = reinterpret_cast<uint32_t*>(tile) + a.at;
+        uint32_t h = head;
+        // rows past the end work on what the buffer holds, for nothing
+        for (int r = r0; r - r0 < nrows; r += kRows, s1 += pass_words) {
+            uint32_t* s2 = s1 + buf / 4;
+            const uint32_t* sg = s1 + (NB - 1) * (buf / 4);
             float lam = 0.f;
-            if (DIFF && r < nrows) {
+            if (DIFF) {
                 if (p.lam_rows) {
-                    lam = __ldg(p.lam + row0 + r);
+                    if (r < nrows) lam = __ldg(p.lam + row0 + r);
                 } else {
-                    const uint32_t h = head0 + r;
-                    lam = __ldg(p.lam + (h - fdiv(h, p.fd_heads) * p.heads));
+                    lam = __ldg(p.lam + h);
+                    h += head_pass;
+                    if (h >= heads) h -= heads;
                 }
             }
             uint32_t w[J];
             float v[NV];
-            row_load<T, J>(w, a, 0, Words<T>::kNegInf);
+            row_load<T, L, J>(w, s1, a, Words<T>::kNegInf);
             if (!BWD) {
-                row_scale(v, inverse_or_zero(row_exp<T, J>(w, v, p.lanes)) * p.drop.gain);
+                row_scale(v, inverse_or_zero(row_exp<T, L, J>(w, v)) * p.drop.gain);
                 if (DIFF) {
                     float u[NV];
-                    row_load<T, J>(w, a, buf / 4, Words<T>::kNegInf);
-                    const float b = inverse_or_zero(row_exp<T, J>(w, u, p.lanes)) * p.drop.gain;
+                    row_load<T, L, J>(w, s2, a, Words<T>::kNegInf);
+                    const float b = inverse_or_zero(row_exp<T, L, J>(w, u)) * p.drop.gain;
                     row_axpy(v, u, -(b * lam));
                 }
-                row_store<T, J>(v, a, 0);
+                row_store<T, L, J>(v, s1, a);
             } else {
                 float g[NV];
                 {
                     uint32_t gw[J];
-                    row_load<T, J>(gw, a, (NB - 1) * (buf / 4), 0u);
+                    row_load<T, L, J>(gw, sg, a, 0u);
 #pragma unroll
                     for (int j = 0; j < J; ++j) Words<T>::get(gw[j], g + j * N);
                 }
 #pragma unroll
                 for (int m = 0; m < NO; ++m) {
-                    if (m == 1) row_load<T, J>(w, a, buf / 4, Words<T>::kNegInf);
-                    const float inv = inverse_or_zero(row_exp<T, J>(w, v, p.lanes));
+                    if (m == 1) row_load<T, L, J>(w, s2, a, Words<T>::kNegInf);
+                    const float inv = inverse_or_zero(row_exp<T, L, J>(w, v));
                     const float k = inv * p.drop.gain * (m == 1 ? -lam : 1.f);
-                    float q = row_dot(v, g, p.lanes) * inv;
-                    if (fabsf(q) < INFINITY) {
-                        row_grad(v, g, k, q);
-                    }
-                    // a place of weight zero (a masked one) takes no part, whatever dy holds there: where the sum is not
-                    // finite it is taken again without those places.  Whole warps decide together, for the shuffles.
-                    if (__any_sync(0xffffffffu, !(fabsf(q) < INFINITY))) {
-                        const bool again = !(fabsf(q) < INFINITY);
+                    float q = row_dot<L>(v, g) * inv;
+                    const bool fine = fabsf(q) < INFINITY;
+                    if (__any_sync(0xffffffffu, !fine)) {
+                        // a place of weight zero (a masked one) takes no part, whatever dy holds there: where the sum is
+                        // not finite it is taken again without those places
                         float sum = 0.f;
 #pragma unroll
                         for (int i = 0; i < NV; ++i) sum += v[i] == 0.f ? 0.f : v[i] * g[i];
-                        sum = lanes_sum(sum, p.lanes);
-                        if (again) {
-                            q = sum * inv;
+                        sum = lanes_sum<L>(sum);
+                        if (!fine) q = sum * inv;
 #pragma unroll
-                            for (int i = 0; i < NV; ++i) v[i] = v[i] == 0.f ? 0.f : v[i] * k * (g[i] - q);
-                        }
+                        for (int i = 0; i < NV; ++i) v[i] = v[i] == 0.f ? 0.f : v[i] * k * (g[i] - q);
+                    } else {
+                        row_grad(v, g, k, q);
                     }
-                    row_store<T, J>(v, a, m == 0 ? 0 : buf / 4);
+                    row_store<T, L, J>(v, m == 0 ? s1 : s2, a);
                     if (m == 1 && r < nrows && l == 0) p.dlam[row0 + r] = -p.drop.gain * q;
                 }
             }
         }
+        if (DIFF) {
+            head += head_tile;
+            if (head >= heads) head -= heads;
+        }
         if (!BWD && dropping) {
             __syncthreads();
-            drop_tile<T>(tile, octets, block0, rng, p.drop.steps);
+            drop_tile<T>(tile, (elems + 7) / 8, block0, rng, p.drop.steps);
         }
         fence_proxy_async_smem();
         __syncthreads();
@@ -408,7 +426,7 @@ __global__ void __launch_bounds__(kWinThreads) win_kernel(const __grid_constant_
             for (int i = 0; i < NO; ++i)
                 reinterpret_cast<T*>(out[i] + bulk)[threadIdx.x] = reinterpret_cast<const T*>(tile + i * buf + bulk)[threadIdx.x];
         }
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && lost < 0) {
             if (bulk != 0) {
 #pragma unroll
                 for (int i = 0; i < NO; ++i) bulk_store(out[i], tile + i * buf, bulk);
@@ -424,7 +442,11 @@ __global__ void __launch_bounds__(kWinThreads) win_kernel(const __grid_constant_
             parity ^= 1u;
         }
     }
-    if (threadIdx.x == 0) tma_store_wait_read();
+    if (threadIdx.x == 0) {
+        tma_store_wait_read();
+        if (lost >= 0)   // the copies in flight have to land before the shared memory is given back
+            for (int i = lost; i < issued; ++i) mbar_drain(&full[i % p.stages], (i / p.stages) & 1, p.wait_ns);
+    }
 }
 
 // Rows that no tile holds (longer than 32 lanes of kMaxWords words): a block per row, read again for
@@ -434,20 +456,20 @@ __device__ __forceinline__ void block_reduce(float (&v)[N], bool maximum, float 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        v[i] = maximum ? lanes_max(v[i], 32) : lanes_sum(v[i], 32);
+        v[i] = maximum ? lanes_max<32>(v[i]) : lanes_sum<32>(v[i]);
         if (lane == 0) slot[i][warp] = v[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float t = lane < kWinThreads / 32 ? slot[i][lane] : (maximum ? -INFINITY : 0.f);
-        v[i] = maximum ? lanes_max(t, 32) : lanes_sum(t, 32);
+        const float t = lane < kLongThreads / 32 ? slot[i][lane] : (maximum ? -INFINITY : 0.f);
+        v[i] = maximum ? lanes_max<32>(t) : lanes_sum<32>(t);
     }
     __syncthreads();
 }
 
 template <typename T, bool DIFF, bool BWD>
-__global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_constant__ WinParams p) {
+__global__ void __launch_bounds__(kLongThreads) win_long_kernel(const __grid_constant__ WinParams p) {
     constexpr int M = DIFF ? 2 : 1;
     __shared__ float slot[2][8];
     const long long row = blockIdx.x;
@@ -467,7 +489,7 @@ __global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_cons
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    for (int t = threadIdx.x; t < p.K; t += kWinThreads)
+    for (int t = threadIdx.x; t < p.K; t += kLongThreads)
 #pragma unroll
         for (int i = 0; i < M; ++i) m[i] = fmaxf(m[i], Elem<T>::get(x[i][t]));
     block_reduce<M>(m, true, slot);
@@ -480,7 +502,7 @@ __global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_cons
         const float v = Elem<T>::get(x[i][t]);
         return fast_exp2(fmaf(far[i] ? v - m[i] : v, kLog2e, -ml2[i]));
     };
-    for (int t = threadIdx.x; t < p.K; t += kWinThreads)
+    for (int t = threadIdx.x; t < p.K; t += kLongThreads)
 #pragma unroll
         for (int i = 0; i < M; ++i) l[i] += weight(i, t);
     block_reduce<M>(l, false, slot);
@@ -492,7 +514,7 @@ __global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_cons
     if (BWD) {
 #pragma unroll
         for (int i = 0; i < M; ++i) q[i] = 0.f;
-        for (long long o = o0 + threadIdx.x; o < o1; o += kWinThreads) {
+        for (long long o = o0 + threadIdx.x; o < o1; o += kLongThreads) {
             const uint4 keep = dropping ? keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps) : uint4{};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -511,7 +533,7 @@ __global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_cons
         for (int i = 0; i < M; ++i) q[i] *= l[i];
         if (DIFF && threadIdx.x == 0) p.dlam[row] = -p.drop.gain * q[M - 1];
     }
-    for (long long o = o0 + threadIdx.x; o < o1; o += kWinThreads) {
+    for (long long o = o0 + threadIdx.x; o < o1; o += kLongThreads) {
         const uint4 keep = dropping ? keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps) : uint4{};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -540,81 +562,78 @@ __global__ void __launch_bounds__(kWinThreads) win_long_kernel(const __grid_cons
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kMaxWords = 12;             // words per lane, at most
-constexpr uint32_t kWinSmem = 200 * 1024; // shared memory of a multiprocessor that the blocks' rings share
+constexpr uint32_t kWinSmem = 220 * 1024; // shared memory of a multiprocessor that the blocks' rings share
 
-// Lanes per row and words per lane: the least work, a lane's words and what a row costs each of its lanes besides.
-inline bool plan_row(int words, int& lanes, int& log_lanes, int& per_lane) {
-    int best = 0;
-    for (int g = 1, lg = 0; g <= 32; g *= 2, ++lg) {
-        const int j = (words + g - 1) / g;
-        if (j > kMaxWords) continue;
-        const int cost = g * (12 * j + 8 * lg + 30);
-        if (best == 0 || cost < best) {
-            best = cost;
-            lanes = g;
-            log_lanes = lg;
-            per_lane = j;
-        }
-    }
-    return best != 0;
+template <typename T, bool DIFF, bool BWD, int L, int J>
+na_status run_win(WinParams& p, cudaStream_t s) {
+    constexpr uint32_t NB = (DIFF ? 2 : 1) + (BWD ? 1 : 0);
+    // a tile is whole passes of the threads, about kTileBytes per tensor; fewer passes where the grid is small
+    constexpr int kRows = kWinThreads / L;
+    const int row = p.K * static_cast<int>(sizeof(T));
+    int passes = kTileBytes / (kRows * row);
+    passes = passes < 1 ? 1 : passes;
+    while (passes > 1 && p.rows / (static_cast<long long>(kRows) * passes) < 8 * kSms) --passes;
+    p.tile = kRows * passes;
+    if (p.tile % 8 != 0) p.tile = kRows * (passes += passes & 1);   // 32 lanes: four rows a pass
+    p.tiles = (p.rows + p.tile - 1) / p.tile;
+    const uint32_t stage = NB * static_cast<uint32_t>(p.tile) * row;
+    p.stages = 3;
+    const size_t smem = static_cast<size_t>(p.stages) * stage;
+    const auto kernel = win_kernel<T, DIFF, BWD, L, J>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return NA_ERR_CUDA;
+    int per_sm = static_cast<int>(kWinSmem / (smem + 1024));
+    constexpr int kMost = win_blocks<DIFF, BWD, J>();
+    per_sm = per_sm < 1 ? 1 : (per_sm > kMost ? kMost : per_sm);
+    const long long most = static_cast<long long>(per_sm) * kSms;
+    kernel<<<static_cast<unsigned>(p.tiles < most ? p.tiles : most), kWinThreads, smem, s>>>(p);
+    return launch_result();
 }
 
-template <typename T, bool DIFF, bool BWD, int J>
-na_status run_win(WinParams& p, cudaStream_t s) {
-    if constexpr (J > kMaxWords) {
-        return NA_ERR_UNSUPPORTED;
-    } else {
-        constexpr uint32_t NB = (DIFF ? 2 : 1) + (BWD ? 1 : 0);
-        // a tile is whole passes of the threads, about 8 KB per tensor; fewer passes where the grid is small
-        const int rpp = kWinThreads / p.lanes, row = p.K * static_cast<int>(sizeof(T));
-        int passes = 8192 / (rpp * row);
-        passes = passes < 1 ? 1 : passes;
-        while (passes > 1 && p.rows / (static_cast<long long>(rpp) * passes) < 4 * kSms) --passes;
-        p.tile = rpp * passes;
-        p.tiles = (p.rows + p.tile - 1) / p.tile;
-        const uint32_t stage = NB * static_cast<uint32_t>(p.tile) * row;
-        p.stages = 3;
-        const size_t smem = static_cast<size_t>(p.stages) * stage;
-        const auto kernel = win_kernel<T, DIFF, BWD, J>;
-        if (smem > 48 * 1024 &&
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-            return NA_ERR_CUDA;
-        int per_sm = static_cast<int>(kWinSmem / smem);
-        per_sm = per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm);
-        const long long most = static_cast<long long>(per_sm) * kSms;
-        kernel<<<static_cast<unsigned>(p.tiles < most ? p.tiles : most), kWinThreads, smem, s>>>(p);
-        return launch_result();
+// Words per lane: exactly as many as the row needs.  With two lanes or more they are at least seven (else half the
+// lanes would do).
+template <typename T, bool DIFF, bool BWD, int L>
+na_status run_words(int j, WinParams& p, cudaStream_t s) {
+    if constexpr (L == 1) {
+        switch (j) {
+            case 1: return run_win<T, DIFF, BWD, L, 1>(p, s);
+            case 2: return run_win<T, DIFF, BWD, L, 2>(p, s);
+            case 3: return run_win<T, DIFF, BWD, L, 3>(p, s);
+            case 4: return run_win<T, DIFF, BWD, L, 4>(p, s);
+            case 5: return run_win<T, DIFF, BWD, L, 5>(p, s);
+            case 6: return run_win<T, DIFF, BWD, L, 6>(p, s);
+        }
+    }
+    switch (j) {
+        case 7: return run_win<T, DIFF, BWD, L, 7>(p, s);
+        case 8: return run_win<T, DIFF, BWD, L, 8>(p, s);
+        case 9: return run_win<T, DIFF, BWD, L, 9>(p, s);
+        case 10: return run_win<T, DIFF, BWD, L, 10>(p, s);
+        case 11: return run_win<T, DIFF, BWD, L, 11>(p, s);
+        default: return run_win<T, DIFF, BWD, L, kMaxWords>(p, s);
     }
 }
 
 template <typename T, bool DIFF, bool BWD>
 na_status launch_win_rows(WinParams& p, cudaStream_t s) {
-    int words = 0;
-    if (!plan_row(sizeof(T) == 4 ? p.K : (p.K + 1) / 2, p.lanes, p.log_lanes, words)) {
+    const int words = sizeof(T) == 4 ? p.K : (p.K + 1) / 2;
+    int lanes = 1;   // the fewest: a row costs each of its lanes its reductions besides its words
+    while (lanes < 32 && words > kMaxWords * lanes) lanes *= 2;
+    const int j = (words + lanes - 1) / lanes;
+    if (j > kMaxWords) {
         if (p.rows > 0x7fffffffLL) return NA_ERR_UNSUPPORTED;
-        win_long_kernel<T, DIFF, BWD><<<static_cast<unsigned>(p.rows), kWinThreads, 0, s>>>(p);
+        win_long_kernel<T, DIFF, BWD><<<static_cast<unsigned>(p.rows), kLongThreads, 0, s>>>(p);
         return launch_result();
     }
-    switch (words) {
-        case 1: return run_win<T, DIFF, BWD, 1>(p, s);
-        case 2: return run_win<T, DIFF, BWD, 2>(p, s);
-        case 3: return run_win<T, DIFF, BWD, 3>(p, s);
-        case 4: return run_win<T, DIFF, BWD, 4>(p, s);
-        case 5: return run_win<T, DIFF, BWD, 5>(p, s);
-        case 6: return run_win<T, DIFF, BWD, 6>(p, s);
-        case 7: return run_win<T, DIFF, BWD, 7>(p, s);
-        case 8: return run_win<T, DIFF, BWD, 8>(p, s);
-        case 9: return run_win<T, DIFF, BWD, 9>(p, s);
-        case 10: return run_win<T, DIFF, BWD, 10>(p, s);
-        case 11: return run_win<T, DIFF, BWD, 11>(p, s);
-        default: return run_win<T, DIFF, BWD, kMaxWords>(p, s);
+    switch (lanes) {
+        case 1: return run_words<T, DIFF, BWD, 1>(j, p, s);
+        case 2: return run_words<T, DIFF, BWD, 2>(j, p, s);
+        case 4: return run_words<T, DIFF, BWD, 4>(j, p, s);
+        case 8: return run_words<T, DIFF, BWD, 8>(j, p, s);
+        case 16: return run_words<T, DIFF, BWD, 16>(j, p, s);
+        default: return run_words<T, DIFF, BWD, 32>(j, p, s);
     }
-}
-
-template <typename T>
-na_status launch_win_type(WinParams& p, bool diff, bool bwd, cudaStream_t s) {
-    if (diff) return bwd ? launch_win_rows<T, true, true>(p, s) : launch_win_rows<T, true, false>(p, s);
-    return bwd ? launch_win_rows<T, false, true>(p, s) : launch_win_rows<T, false, false>(p, s);
 }
 
 }  // namespace

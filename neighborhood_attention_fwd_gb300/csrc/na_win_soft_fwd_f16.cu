@@ -1,0 +1,6 @@
+// na_win_soft_fwd_f16.cu -- window softmax with dropout, forward, f16: kernel instances.
+#include "na_win_impl.cuh"
+
+namespace na {
+na_status launch_soft_fwd_f16(WinParams& p, cudaStream_t s) { return launch_win_rows<__half, false, false>(p, s); }
+}  // namespace na

@@ -8,21 +8,23 @@
 namespace na {
 namespace {
 
+constexpr int kThreads = 256;
+
 // Sums of a [n, heads] matrix over n, per_block rows of it to each block: out[block][heads].
-__global__ void __launch_bounds__(kWinThreads) head_sum_kernel(const float* in, long long n, int heads, long long per_block,
+__global__ void __launch_bounds__(kThreads) head_sum_kernel(const float* in, long long n, int heads, long long per_block,
                                                               float* out) {
-    __shared__ float part[kWinThreads];
+    __shared__ float part[kThreads];
     const long long r0 = blockIdx.x * per_block, r1 = min(r0 + per_block, n);
     float* to = out + static_cast<long long>(blockIdx.x) * heads;
-    if (heads > kWinThreads) {
-        for (int h = threadIdx.x; h < heads; h += kWinThreads) {
+    if (heads > kThreads) {
+        for (int h = threadIdx.x; h < heads; h += kThreads) {
             float s = 0.f;
             for (long long r = r0; r < r1; ++r) s += in[r * heads + h];
             to[h] = s;
         }
         return;
     }
-    const int lanes = kWinThreads / heads, use = lanes * heads;
+    const int lanes = kThreads / heads, use = lanes * heads;
     float s = 0.f;
     if (threadIdx.x < use) {
         const long long end = r1 * heads;
@@ -46,23 +48,23 @@ __global__ void __launch_bounds__(kWinThreads) head_sum_kernel(const float* in, 
 // Dropout of a tensor: y = gain x where the generator keeps the element, else 0 (y may be x).  A thread takes
 // kOct octets of a block's run, loads them all, then draws.
 template <typename T>
-__global__ void __launch_bounds__(kWinThreads) dropout_kernel(const T* x, T* y, long long n, Dropout d) {
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, long long n, Dropout d) {
     using E = Elem<T>;
     constexpr int C = sizeof(T) == 4 ? 2 : 1, V = E::EPC, kOct = 4 / C;
-    const unsigned long long o0 = static_cast<unsigned long long>(blockIdx.x) * (kWinThreads * kOct) + threadIdx.x;
+    const unsigned long long o0 = static_cast<unsigned long long>(blockIdx.x) * (kThreads * kOct) + threadIdx.x;
     RngState rng{};
     if (d.state) rng = rng_load(d.state);
     uint4 r[kOct][C];
 #pragma unroll
     for (int j = 0; j < kOct; ++j) {
-        const unsigned long long o = o0 + static_cast<unsigned>(j) * kWinThreads;
+        const unsigned long long o = o0 + static_cast<unsigned>(j) * kThreads;
         if (static_cast<long long>(o * 8 + 8) <= n)
 #pragma unroll
             for (int c = 0; c < C; ++c) r[j][c] = ld_stream(x + o * 8 + c * V);
     }
 #pragma unroll
     for (int j = 0; j < kOct; ++j) {
-        const unsigned long long o = o0 + static_cast<unsigned>(j) * kWinThreads;
+        const unsigned long long o = o0 + static_cast<unsigned>(j) * kThreads;
         if (static_cast<long long>(o * 8) >= n) continue;
         if (static_cast<long long>(o * 8 + 8) <= n) {
 #pragma unroll
@@ -112,16 +114,17 @@ na_status win_common(int B, int ndim, const int* spatial, int heads, const int* 
     p.rows = tokens * heads;
     p.K = static_cast<int>(K);
     p.heads = heads;
-    p.rows32 = p.rows < (1LL << 31) ? 1u : 0u;
-    p.fd_heads = make_fastdiv(static_cast<uint32_t>(heads));
     p.wait_ns = wait_limit_ns();
     return NA_OK;
 }
 
 na_status launch_win(WinParams& p, na_dtype dtype, bool diff, bool bwd, cudaStream_t s) {
-    if (dtype == NA_BF16) return launch_win_bf16(p, diff, bwd, s);
-    if (dtype == NA_FP16) return launch_win_f16(p, diff, bwd, s);
-    return launch_win_f32(p, diff, bwd, s);
+    using Launch = na_status (*)(WinParams&, cudaStream_t);
+    static constexpr Launch kForms[2][2][3] = {
+        {{launch_soft_fwd_bf16, launch_soft_fwd_f32, launch_soft_fwd_f16}, {launch_soft_bwd_bf16, launch_soft_bwd_f32, launch_soft_bwd_f16}},
+        {{launch_diff_fwd_bf16, launch_diff_fwd_f32, launch_diff_fwd_f16}, {launch_diff_bwd_bf16, launch_diff_bwd_f32, launch_diff_bwd_f16}},
+    };
+    return kForms[diff][bwd][dtype](p, s);   // NA_BF16, NA_FP32, NA_FP16
 }
 
 Span weights_span(const void* t, const WinParams& p, na_dtype dtype) { return Span{t, p.rows * p.K * elem_bytes(dtype)}; }
@@ -157,16 +160,16 @@ na_status na_dropout(const void* x, void* y, int64_t n, double p, const void* rn
     if (!ptr_aligned(x, 16) || !ptr_aligned(y, 16) || !ptr_aligned(rng, 8)) return NA_ERR_ALIGNMENT;
     const Span sx{x, n * elem_bytes(dtype)}, sy{y, sx.bytes}, sr{rng, 16};
     if (!output_clear(sy, {sx}, {sr})) return NA_ERR_INVALID_ARG;
-    const long long per = 8LL * kWinThreads * (dtype == NA_FP32 ? 2 : 4), blocks = (n + per - 1) / per;
+    const long long per = 8LL * kThreads * (dtype == NA_FP32 ? 2 : 4), blocks = (n + per - 1) / per;
     if (blocks > 0x7fffffffLL) return NA_ERR_UNSUPPORTED;
     const unsigned nb = static_cast<unsigned>(blocks);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == NA_BF16)
-        dropout_kernel<<<nb, kWinThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), n, d);
+        dropout_kernel<<<nb, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), n, d);
     else if (dtype == NA_FP16)
-        dropout_kernel<<<nb, kWinThreads, 0, s>>>(static_cast<const __half*>(x), static_cast<__half*>(y), n, d);
+        dropout_kernel<<<nb, kThreads, 0, s>>>(static_cast<const __half*>(x), static_cast<__half*>(y), n, d);
     else
-        dropout_kernel<<<nb, kWinThreads, 0, s>>>(static_cast<const float*>(x), static_cast<float*>(y), n, d);
+        dropout_kernel<<<nb, kThreads, 0, s>>>(static_cast<const float*>(x), static_cast<float*>(y), n, d);
     return launch_result();
 }
 
@@ -277,8 +280,8 @@ na_status na_diff_softmax_bwd(const void* x1, const void* x2, const float* lam, 
         const long long tokens = w.rows / heads, per = sum_tokens(tokens);
         const int blocks = static_cast<int>((tokens + per - 1) / per);
         float* partial = w.dlam + (w.rows + 63) / 64 * 64;
-        head_sum_kernel<<<blocks, kWinThreads, 0, s>>>(w.dlam, tokens, heads, per, blocks == 1 ? dlam : partial);
-        if (blocks > 1) head_sum_kernel<<<1, kWinThreads, 0, s>>>(partial, blocks, heads, blocks, dlam);
+        head_sum_kernel<<<blocks, kThreads, 0, s>>>(w.dlam, tokens, heads, per, blocks == 1 ? dlam : partial);
+        if (blocks > 1) head_sum_kernel<<<1, kThreads, 0, s>>>(partial, blocks, heads, blocks, dlam);
         st = launch_result();
     }
     if (owned && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
