@@ -15,6 +15,7 @@ dropout or as the difference of two maps (na_softmax_dropout, na_diff_softmax, n
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -419,31 +420,60 @@ def na_mask_window(attn, sizes, kernel, dilation=None, stream=None):
 # Around the attention: rotary positions, layer norm, dropout, differential weights
 # ---------------------------------------------------------------------------------------------
 
-def _on_device(*tensors):
-    """Every tensor on the current CUDA device (kernels are launched on its stream)."""
-    here = None
+# These operators are small beside the attention, so their calls are kept short: sizes become C arrays once per
+# size, and the checks and the stream take the shortest way through torch.
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(vals):
+    """A C int array of a tuple of sizes."""
+    return (ctypes.c_int * len(vals))(*vals)
+
+
+def _like(t, shape, dtype, name):
+    """A contiguous tensor of this shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        _check(t, shape, dtype, name)
+
+
+def _launch_stream(stream, *tensors):
+    """The raw stream of a call, every tensor being on the current CUDA device (kernels are launched there)."""
+    here = -1
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:
             raise ValueError("expected CUDA tensors")
-        if here is None:
+        if here < 0:
             here = torch.cuda.current_device()
-        if t.device.index != here:
+        if at != here:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    return _stream(stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(ws, stream, nbytes, device):
+def _workspace(ws, stream, need, device):
     """(tensor, pointer, bytes) of a call's workspace.  Without one from the caller, a call on the current stream
     takes it from torch's allocator, which keeps freed memory at hand; a call on another stream leaves it to the
     library, which allocates on that stream."""
     if ws is None and stream is None:
-        ws = torch.empty(nbytes(), dtype=torch.uint8, device=device)
+        n = need()
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        return ws, ws.data_ptr(), n
     return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+_CODES = {torch.bfloat16: NA_BF16, torch.float32: NA_FP32, torch.float16: NA_FP16}
+
+
+def _code(t):
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 class RopeFreqs:
@@ -497,29 +527,31 @@ class RopeFreqs:
 
 
 def _rope(call, what, q, k, q_out, k_out, freqs, origin, stream):
-    B, ndim, spatial, heads, D = _geometry(q)
+    shape = q.shape
+    ndim = len(shape) - 3
+    if ndim < 1 or ndim > 3:
+        raise ValueError("expected [B, L_1..L_n, heads, D] with n in 1..3")
     if len(freqs._rot) != ndim:
         raise ValueError("the frequencies need one entry per spatial axis")
-    _check(q, q.shape, q.dtype, "q")
-    _check(q_out, q.shape, q.dtype, "q_out")
+    _like(q, shape, q.dtype, "q")
+    _like(q_out, shape, q.dtype, "q_out")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     heads_k = 0
     if k is not None:
-        if k.dim() != q.dim():
+        if k.dim() != ndim + 3:
             raise ValueError("k must have the axes of q")
-        heads_k = int(k.shape[-2])
-        _check(k, tuple(q.shape[:-2]) + (heads_k, D), q.dtype, "k")
-        _check(k_out, k.shape, q.dtype, "k_out")
-    _on_device(q, k, q_out, k_out)
-    if isinstance(origin, int):
-        origin = (origin,) * ndim
+        heads_k = k.shape[-2]
+        _like(k, shape[:-2] + (heads_k, shape[-1]), q.dtype, "k")
+        _like(k_out, k.shape, q.dtype, "k_out")
+    stream = _launch_stream(stream, q, k, q_out, k_out)
     if origin is not None:
+        origin = (origin,) * ndim if isinstance(origin, int) else tuple(origin)
         if len(origin) != ndim:
             raise ValueError("origin needs one entry per spatial axis")
         origin = (ctypes.c_int64 * ndim)(*[int(x) for x in origin])
-    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, ndim, _ints(spatial), heads, heads_k, D, freqs._rot,
-              freqs._freq, origin, freqs.amplitude, freqs._code, _dtype_code(q), _stream(stream))
+    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), shape[0], ndim, _sizes(tuple(shape[1:-2])), shape[-2],
+              heads_k, shape[-1], freqs._rot, freqs._freq, origin, freqs.amplitude, freqs._code, _code(q), stream)
     _ok(st, what)
 
 
@@ -545,107 +577,124 @@ def na_layernorm(x, w, b, y, mean=None, rstd=None, eps: float = 1e-5, stream=Non
     """y = (x - mean) * rstd * w + b over the last axis of x [.., C] (per head: [B, L.., heads, D]; per token:
     [B, L.., heads * D]).  w, b: fp32 [C] or None; mean, rstd: fp32 x.shape[:-1] for the backward, or None."""
     rows, C = _rows(x)
-    _check(x, x.shape, x.dtype, "x")
-    _check(y, x.shape, x.dtype, "y")
+    _like(x, x.shape, x.dtype, "x")
+    _like(y, x.shape, x.dtype, "y")
     for name, t in (("w", w), ("b", b)):
         if t is not None:
-            _check(t, (C,), torch.float32, name)
+            _like(t, (C,), torch.float32, name)
     if (mean is None) != (rstd is None):
         raise ValueError("mean and rstd go together")
     if mean is not None:
-        _check(mean, x.shape[:-1], torch.float32, "mean")
-        _check(rstd, x.shape[:-1], torch.float32, "rstd")
-    _on_device(x, w, b, y, mean, rstd)
-    st = load().na_layernorm(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, float(eps),
-                             _dtype_code(x), _stream(stream))
+        _like(mean, x.shape[:-1], torch.float32, "mean")
+        _like(rstd, x.shape[:-1], torch.float32, "rstd")
+    stream = _launch_stream(stream, x, w, b, y, mean, rstd)
+    st = load().na_layernorm(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, eps, _code(x),
+                             stream)
     _ok(st, "na_layernorm")
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_need(rows, C, code):
+    return int(load().na_layernorm_bwd_workspace_size(rows, C, code))
+
+
 def na_layernorm_bwd_workspace_size(rows: int, C: int, dtype=torch.bfloat16) -> int:
-    code = _dtype_code(torch.empty(0, dtype=dtype))
-    return int(load().na_layernorm_bwd_workspace_size(int(rows), int(C), code))
+    return _norm_need(int(rows), int(C), _CODES[dtype])
 
 
 def na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw=None, db=None, workspace=None, stream=None):
     """dx (may be dy or x) and, when given, dw and db (fp32 [C]) of na_layernorm."""
     rows, C = _rows(x)
     for name, t in (("x", x), ("dy", dy), ("dx", dx)):
-        _check(t, x.shape, x.dtype, name)
+        _like(t, x.shape, x.dtype, name)
     for name, t in (("w", w), ("dw", dw), ("db", db)):
         if t is not None:
-            _check(t, (C,), torch.float32, name)
+            _like(t, (C,), torch.float32, name)
     if (dw is None) != (db is None):
         raise ValueError("dw and db go together")
-    _check(mean, x.shape[:-1], torch.float32, "mean")
-    _check(rstd, x.shape[:-1], torch.float32, "rstd")
-    _on_device(dy, x, w, mean, rstd, dx, dw, db, workspace)
-    code = _dtype_code(x)
-    need = lambda: load().na_layernorm_bwd_workspace_size(rows, C, code)
-    ws, ws_ptr, ws_bytes = (None, None, 0) if dw is None else _workspace(workspace, stream, need, x.device)
+    _like(mean, x.shape[:-1], torch.float32, "mean")
+    _like(rstd, x.shape[:-1], torch.float32, "rstd")
+    raw = _launch_stream(stream, dy, x, w, mean, rstd, dx, dw, db, workspace)
+    code = _code(x)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if dw is None else _workspace(
+        workspace, stream, lambda: _norm_need(rows, C, code), x.device)
     st = load().na_layernorm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-                                 _ptr(dw), _ptr(db), rows, C, code, ws_ptr, ws_bytes, _stream(stream))
+                                 _ptr(dw), _ptr(db), rows, C, code, ws_ptr, ws_bytes, raw)
     _ok(st, "na_layernorm_bwd")
 
 
 def _rng(rng):
     if rng is not None:
-        _check(rng, (2,), torch.int64, "rng")
+        _like(rng, (2,), torch.int64, "rng")
     return _ptr(rng)
+
+
+def _window(x, kernel):
+    """B, ndim, the grid and the kernel as C arrays, and the heads between them, of weights [B, L.., heads, K]."""
+    shape = x.shape
+    ndim = len(shape) - 3
+    if ndim < 1 or ndim > 3:
+        raise ValueError("expected attention weights [B, L_1..L_n, heads, K] with n in 1..3")
+    kernel = (kernel,) * ndim if isinstance(kernel, int) else tuple(kernel)
+    if len(kernel) != ndim:
+        raise ValueError("kernel needs one entry per spatial axis")
+    if shape[-1] != math.prod(kernel):
+        raise ValueError(f"last axis of the attention weights must be {math.prod(kernel)}")
+    return shape[0], ndim, _sizes(tuple(shape[1:-2])), shape[-2], _sizes(kernel)
 
 
 def na_dropout(x, y, p: float, rng, stream=None):
     """y = dropout(x) (y may be x): each element zero with probability p, else scaled.  rng: int64 CUDA tensor
     (seed, offset); the same state keeps the same elements, so the gradient is na_dropout(dy, dx, p, rng)."""
-    _check(x, x.shape, x.dtype, "x")
-    _check(y, x.shape, x.dtype, "y")
+    _like(x, x.shape, x.dtype, "x")
+    _like(y, x.shape, x.dtype, "y")
     state = _rng(rng)
-    _on_device(x, y, rng)
-    st = load().na_dropout(x.data_ptr(), y.data_ptr(), x.numel(), float(p), state, _dtype_code(x), _stream(stream))
+    stream = _launch_stream(stream, x, y, rng)
+    st = load().na_dropout(x.data_ptr(), y.data_ptr(), x.numel(), p, state, _code(x), stream)
     _ok(st, "na_dropout")
 
 
 def na_softmax_dropout(x, y, kernel, p: float, rng, stream=None):
     """y = dropout(softmax(x)) over each row's K window weights (y may be x; keep x for the gradient)."""
-    B, ndim, spatial, heads, kernel = _attn_geometry(x, kernel)
-    _check(x, x.shape, x.dtype, "x")
-    _check(y, x.shape, x.dtype, "y")
+    B, ndim, grid, heads, kern = _window(x, kernel)
+    _like(x, x.shape, x.dtype, "x")
+    _like(y, x.shape, x.dtype, "y")
     state = _rng(rng)
-    _on_device(x, y, rng)
-    st = load().na_softmax_dropout(x.data_ptr(), y.data_ptr(), B, ndim, _ints(spatial), heads, _ints(kernel), float(p),
-                                   state, _dtype_code(x), _stream(stream))
+    stream = _launch_stream(stream, x, y, rng)
+    st = load().na_softmax_dropout(x.data_ptr(), y.data_ptr(), B, ndim, grid, heads, kern, p, state, _code(x), stream)
     _ok(st, "na_softmax_dropout")
 
 
 def na_softmax_dropout_bwd(x, dy, dx, kernel, p: float, rng, stream=None):
     """dx of na_softmax_dropout given its logits x, dy and the forward's p and rng (dx may be x or dy)."""
-    B, ndim, spatial, heads, kernel = _attn_geometry(x, kernel)
+    B, ndim, grid, heads, kern = _window(x, kernel)
     for name, t in (("x", x), ("dy", dy), ("dx", dx)):
-        _check(t, x.shape, x.dtype, name)
+        _like(t, x.shape, x.dtype, name)
     state = _rng(rng)
-    _on_device(x, dy, dx, rng)
-    st = load().na_softmax_dropout_bwd(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), B, ndim, _ints(spatial), heads,
-                                       _ints(kernel), float(p), state, _dtype_code(x), _stream(stream))
+    stream = _launch_stream(stream, x, dy, dx, rng)
+    st = load().na_softmax_dropout_bwd(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), B, ndim, grid, heads, kern, p, state,
+                                       _code(x), stream)
     _ok(st, "na_softmax_dropout_bwd")
 
 
 def _lam_rows(lam, rows_shape, heads):
     """0 for a weight per head ([heads]), 1 for one per row ([B, L.., heads])."""
     per_row = lam.dim() != 1
-    _check(lam, rows_shape if per_row else (heads,), torch.float32, "lam")
+    _like(lam, rows_shape if per_row else (heads,), torch.float32, "lam")
     return int(per_row)
 
 
 def na_diff_softmax(x1, x2, lam, y, kernel, p: float = 0.0, rng=None, stream=None):
     """y = dropout(softmax(x1) - lam * softmax(x2)) over each row's K window weights.  lam: fp32 [heads] or
     [B, L.., heads].  y may be x1 or x2 (keep the logits for the gradient)."""
-    B, ndim, spatial, heads, kernel = _attn_geometry(x1, kernel)
+    B, ndim, grid, heads, kern = _window(x1, kernel)
     for name, t in (("x1", x1), ("x2", x2), ("y", y)):
-        _check(t, x1.shape, x1.dtype, name)
+        _like(t, x1.shape, x1.dtype, name)
     per_row = _lam_rows(lam, x1.shape[:-1], heads)
     state = _rng(rng)
-    _on_device(x1, x2, lam, y, rng)
-    st = load().na_diff_softmax(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, y.data_ptr(), B, ndim,
-                                _ints(spatial), heads, _ints(kernel), float(p), state, _dtype_code(x1), _stream(stream))
+    stream = _launch_stream(stream, x1, x2, lam, y, rng)
+    st = load().na_diff_softmax(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, y.data_ptr(), B, ndim, grid, heads, kern,
+                                p, state, _code(x1), stream)
     _ok(st, "na_diff_softmax")
 
 
@@ -656,17 +705,16 @@ def na_diff_softmax_bwd_workspace_size(B, spatial, heads, kernel) -> int:
 
 def na_diff_softmax_bwd(x1, x2, lam, dy, dx1, dx2, dlam, kernel, p: float = 0.0, rng=None, workspace=None, stream=None):
     """dx1, dx2, dlam (the shape of lam) of na_diff_softmax given its logits, dy and the forward's p and rng."""
-    B, ndim, spatial, heads, kernel = _attn_geometry(x1, kernel)
+    B, ndim, grid, heads, kern = _window(x1, kernel)
     for name, t in (("x1", x1), ("x2", x2), ("dy", dy), ("dx1", dx1), ("dx2", dx2)):
-        _check(t, x1.shape, x1.dtype, name)
+        _like(t, x1.shape, x1.dtype, name)
     per_row = _lam_rows(lam, x1.shape[:-1], heads)
-    _check(dlam, lam.shape, torch.float32, "dlam")
+    _like(dlam, lam.shape, torch.float32, "dlam")
     state = _rng(rng)
-    _on_device(x1, x2, lam, dy, dx1, dx2, dlam, rng, workspace)
-    L, k = _ints(spatial), _ints(kernel)
-    need = lambda: load().na_diff_softmax_bwd_workspace_size(B, ndim, L, heads, k)
-    ws, ws_ptr, ws_bytes = (None, None, 0) if per_row else _workspace(workspace, stream, need, x1.device)
+    raw = _launch_stream(stream, x1, x2, lam, dy, dx1, dx2, dlam, rng, workspace)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if per_row else _workspace(
+        workspace, stream, lambda: load().na_diff_softmax_bwd_workspace_size(B, ndim, grid, heads, kern), x1.device)
     st = load().na_diff_softmax_bwd(x1.data_ptr(), x2.data_ptr(), lam.data_ptr(), per_row, dy.data_ptr(), dx1.data_ptr(),
-                                    dx2.data_ptr(), dlam.data_ptr(), B, ndim, L, heads, k, float(p), state,
-                                    _dtype_code(x1), ws_ptr, ws_bytes, _stream(stream))
+                                    dx2.data_ptr(), dlam.data_ptr(), B, ndim, grid, heads, kern, p, state, _code(x1),
+                                    ws_ptr, ws_bytes, raw)
     _ok(st, "na_diff_softmax_bwd")

@@ -157,28 +157,27 @@ __device__ __forceinline__ bool keep_of(const uint4& m, int i) {
     return ((w >> (16 * (i & 1))) & 1u) != 0u;
 }
 
-// Zeros the dropped elements of an octet: eight 16-bit elements, or eight 32-bit ones in two chunks.
-__device__ __forceinline__ void drop_octet(uint4& d, const RngState& s, unsigned long long block, uint32_t steps) {
-    const uint4 w = rng_block(s, block);
+// Zeros the dropped elements of an octet, given its block's bits: eight 16-bit elements, or eight 32-bit ones in
+// two chunks.
+__device__ __forceinline__ void drop_words(uint4& d, const uint4& bits, uint32_t steps) {
     auto drop = [steps](uint32_t& v, uint32_t r) {
         if (!keep_high(r, steps)) v &= 0x0000ffffu;
         if (!keep_low(r, steps)) v &= 0xffff0000u;
     };
-    drop(d.x, w.x);
-    drop(d.y, w.y);
-    drop(d.z, w.z);
-    drop(d.w, w.w);
+    drop(d.x, bits.x);
+    drop(d.y, bits.y);
+    drop(d.z, bits.z);
+    drop(d.w, bits.w);
 }
-__device__ __forceinline__ void drop_octet(uint4& a, uint4& b, const RngState& s, unsigned long long block, uint32_t steps) {
-    const uint4 w = rng_block(s, block);
+__device__ __forceinline__ void drop_words(uint4& a, uint4& b, const uint4& bits, uint32_t steps) {
     auto drop = [steps](uint32_t& lo, uint32_t& hi, uint32_t r) {
         if (!keep_low(r, steps)) lo = 0u;
         if (!keep_high(r, steps)) hi = 0u;
     };
-    drop(a.x, a.y, w.x);
-    drop(a.z, a.w, w.y);
-    drop(b.x, b.y, w.z);
-    drop(b.z, b.w, w.w);
+    drop(a.x, a.y, bits.x);
+    drop(a.z, a.w, bits.y);
+    drop(b.x, b.y, bits.z);
+    drop(b.z, b.w, bits.w);
 }
 
 }  // namespace na

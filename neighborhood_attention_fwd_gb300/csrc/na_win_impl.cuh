@@ -30,7 +30,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxStages = 3;
-constexpr int kTileBytes = 12 * 1024;
+constexpr int kStageBytes = 12 * 1024;   // a tile of every input, about
 constexpr int kLongThreads = 256;   // block of a row that no tile holds
 
 // A row's words: 4 bytes, one or two weights.
@@ -242,22 +242,29 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
                  : "memory");
 }
 
-// Zeros the dropped places of a tile in shared memory: octet o of the tile is block block0 + o of the tensor.
+// Zeros the dropped places of a tile in shared memory: octet o of the tile is block block0 + o of the tensor.  Several
+// octets at a time: a block's seven rounds are one chain of dependent instructions.
 template <typename T>
 __device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, unsigned long long block0, const RngState& rng,
                                           uint32_t steps) {
-    for (uint32_t o = threadIdx.x; o < octets; o += kWinThreads) {
-        if constexpr (sizeof(T) == 4) {
-            uint4* at = reinterpret_cast<uint4*>(tile) + 2 * o;
-            uint4 a = at[0], b = at[1];
-            drop_octet(a, b, rng, block0 + o, steps);
-            at[0] = a;
-            at[1] = b;
-        } else {
-            uint4* at = reinterpret_cast<uint4*>(tile) + o;
-            uint4 a = at[0];
-            drop_octet(a, rng, block0 + o, steps);
-            at[0] = a;
+    constexpr int U = 1, C = sizeof(T) == 4 ? 2 : 1;
+    uint4* at = reinterpret_cast<uint4*>(tile);
+    for (uint32_t o = threadIdx.x; o < octets; o += U * kWinThreads) {
+        uint4 r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = rng_block(rng, block0 + o + u * kWinThreads);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = o + u * kWinThreads;
+            if (i < octets) {
+                uint4 d[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) d[c] = at[C * i + c];
+                if constexpr (C == 2) drop_words(d[0], d[1], r[u], steps);
+                else drop_words(d[0], r[u], steps);
+#pragma unroll
+                for (int c = 0; c < C; ++c) at[C * i + c] = d[c];
+            }
         }
     }
 }
@@ -567,10 +574,10 @@ constexpr uint32_t kWinSmem = 220 * 1024; // shared memory of a multiprocessor t
 template <typename T, bool DIFF, bool BWD, int L, int J>
 na_status run_win(WinParams& p, cudaStream_t s) {
     constexpr uint32_t NB = (DIFF ? 2 : 1) + (BWD ? 1 : 0);
-    // a tile is whole passes of the threads, about kTileBytes per tensor; fewer passes where the grid is small
+    // a tile is whole passes of the threads, about kStageBytes for all inputs; fewer passes where the grid is small
     constexpr int kRows = kWinThreads / L;
     const int row = p.K * static_cast<int>(sizeof(T));
-    int passes = kTileBytes / (kRows * row);
+    int passes = kStageBytes / static_cast<int>(NB * kRows * row);
     passes = passes < 1 ? 1 : passes;
     while (passes > 1 && p.rows / (static_cast<long long>(kRows) * passes) < 8 * kSms) --passes;
     p.tile = kRows * passes;

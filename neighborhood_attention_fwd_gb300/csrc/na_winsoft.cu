@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, lon
                 r[j][c] = E::pack(f);
             }
             if (d.state) {
-                if constexpr (C == 2) drop_octet(r[j][0], r[j][1], rng, o, d.steps);
-                else drop_octet(r[j][0], rng, o, d.steps);
+                if constexpr (C == 2) drop_words(r[j][0], r[j][1], rng_block(rng, o), d.steps);
+                else drop_words(r[j][0], rng_block(rng, o), d.steps);
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) st_stream(y + o * 8 + c * V, r[j][c]);
