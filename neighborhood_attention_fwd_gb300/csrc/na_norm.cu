@@ -10,8 +10,11 @@
 // a thread's columns stay the same and the weight gradients accumulate in its registers; a block writes one
 // partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).
 #include "na_block.cuh"
+#include "na_device.cuh"
 
 namespace na {
+using namespace dev;
+
 namespace {
 
 constexpr int kNormThreads = 256;     // blocks of warp teams
@@ -30,14 +33,26 @@ struct NormParams {
     long long rows;
     int C, team;           // threads per row
     float eps, inv_c;
+    long long tiles;       // ring: tiles of `tile` rows
+    int tile;
+    unsigned* err;         // ring: device status word
+    unsigned long long wait_ns;
 };
 
-// A chunk: V elements, 16 bytes, or one element where a row is not whole chunks.
+// A chunk: V elements, 16 bytes, or one element where a row is not whole chunks.  Loads are unconditional (places past
+// the end are clamped to the last one and left out afterwards): a guarded load would be waited for before the next one.
 template <typename T, int V>
-__device__ __forceinline__ void load_chunk(const void* base, long long at, float (&f)[V]) {
-    if constexpr (V == 1) f[0] = Elem<T>::get(static_cast<const T*>(base)[at]);
-    else Elem<T>::unpack(ld_stream(static_cast<const T*>(base) + at), f);
-}
+struct Chunk {
+    uint4 raw;
+    __device__ __forceinline__ void load(const void* base, long long at) { raw = ld_stream(static_cast<const T*>(base) + at); }
+    __device__ __forceinline__ void get(float (&f)[V]) const { Elem<T>::unpack(raw, f); }
+};
+template <typename T>
+struct Chunk<T, 1> {
+    T raw;
+    __device__ __forceinline__ void load(const void* base, long long at) { raw = static_cast<const T*>(base)[at]; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = Elem<T>::get(raw); }
+};
 
 template <typename T, int V>
 __device__ __forceinline__ void store_chunk(void* base, long long at, const float (&f)[V]) {
@@ -61,6 +76,51 @@ __device__ __forceinline__ void load_weights(const float* w, int c, float (&f)[V
             f[e + 2] = t.z;
             f[e + 3] = t.w;
         }
+    }
+}
+
+// Chunk-wise fp32 arithmetic, in pairs where a chunk has them.
+template <int V>
+__device__ __forceinline__ float chunk_sum(const float (&x)[V]) {
+    if constexpr (V == 1) {
+        return x[0];
+    } else {
+        uint64_t t = pack2(x[0], x[1]);
+#pragma unroll
+        for (int e = 2; e < V; e += 2) t = add2(t, pack2(x[e], x[e + 1]));
+        float a, b;
+        split2(t, a, b);
+        return a + b;
+    }
+}
+template <int V>   // x -= m; returns the sum of squares
+__device__ __forceinline__ float chunk_centre(float (&x)[V], float m) {
+    if constexpr (V == 1) {
+        x[0] -= m;
+        return x[0] * x[0];
+    } else {
+        const uint64_t mm = pack2(-m, -m);
+        uint64_t t = 0;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const uint64_t d = add2(pack2(x[e], x[e + 1]), mm);
+            t = fma2(d, d, t);
+            split2(d, x[e], x[e + 1]);
+        }
+        float a, b;
+        split2(t, a, b);
+        return a + b;
+    }
+}
+template <int V>   // y = x r w + b
+__device__ __forceinline__ void chunk_affine(const float (&x)[V], float r, const float (&w)[V], const float (&b)[V], float (&y)[V]) {
+    if constexpr (V == 1) {
+        y[0] = fmaf(x[0] * r, w[0], b[0]);
+    } else {
+        const uint64_t rr = pack2(r, r);
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+            split2(fma2(mul2(pack2(x[e], x[e + 1]), rr), pack2(w[e], w[e + 1]), pack2(b[e], b[e + 1])), y[e], y[e + 1]);
     }
 }
 
@@ -91,14 +151,16 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*slot)[
     }
 }
 
+// Rows that a team works on at once: their loads are in flight together and their sums share the steps.
+__host__ __device__ constexpr int norm_rows(int J, bool bwd) { return bwd ? (J == 1 ? 2 : 1) : (J == 1 ? 4 : (J == 2 ? 2 : 1)); }
+
 template <typename T, int V, int J, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_kernel(const NormParams p) {
-    __shared__ float slots[2][1][32];
+    constexpr int R = norm_rows(J, false);
+    __shared__ float slots[2][R][32];
     const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1));
     const int team_in_block = BLOCK ? 0 : threadIdx.x / p.team, teams = BLOCK ? 1 : kNormThreads / p.team;
-    const long long step = static_cast<long long>(gridDim.x) * teams;
-    // every thread of a warp takes part in the sums: rows past the end are computed on zeros and not stored
-    const long long first = static_cast<long long>(blockIdx.x) * teams;
+    const long long step = static_cast<long long>(gridDim.x) * teams * R;   // a block's rows of one turn follow one another
     constexpr bool KEEP = J * V <= 16;   // weights stay in registers over the rows
     float w[KEEP ? J : 1][V], b[KEEP ? J : 1][V];
     if (KEEP) {
@@ -111,110 +173,74 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_ke
             }
         }
     }
-    for (long long r0 = first; r0 < p.rows; r0 += step) {
-        const long long row = r0 + team_in_block;
-        const bool live = row < p.rows;
-        float x[J][V];
-        float s[1] = {0.f};
+    // every thread of a warp takes part in the sums: rows past the end repeat the last one and are not stored
+    for (long long r0 = static_cast<long long>(blockIdx.x) * teams * R; r0 < p.rows; r0 += step) {
+        Chunk<T, V> raw[R][J];
+        float x[R][J][V], s[R], q[R], rstd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long row = min(r0 + r * teams + team_in_block, p.rows - 1);
+#pragma unroll
+            for (int j = 0; j < J; ++j) raw[r][j].load(p.x, row * p.C + min((l + p.team * j) * V, p.C - V));
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool in = (l + p.team * j) * V < p.C;
+                raw[r][j].get(x[r][j]);
+                const float t = chunk_sum<V>(x[r][j]);
+                s[r] += in ? t : 0.f;
+            }
+        }
+        team_sum<R, BLOCK>(s, p.team, slots[0]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] *= p.inv_c;   // the mean
+            q[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool in = (l + p.team * j) * V < p.C;
+                const float t = chunk_centre<V>(x[r][j], s[r]);
+                q[r] += in ? t : 0.f;
+            }
+        }
+        team_sum<R, BLOCK>(q, p.team, slots[1]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long row = r0 + r * teams + team_in_block;
+            rstd[r] = rsqrtf(fmaf(q[r], p.inv_c, p.eps));
+            if (l == 0 && p.mean && row < p.rows) {
+                p.mean[row] = s[r];
+                p.rstd[row] = rstd[r];
+            }
+        }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int c = (l + p.team * j) * V;
-            const bool in = live && c < p.C;
-            if (in) load_chunk<T, V>(p.x, row * p.C + c, x[j]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (!in) x[j][e] = 0.f;
-                s[0] += x[j][e];
+            if (c >= p.C) continue;
+            if (!KEEP) {
+                load_weights<V>(p.w, c, w[0], 1.f);
+                load_weights<V>(p.b, c, b[0], 0.f);
             }
-        }
-        team_sum<1, BLOCK>(s, p.team, slots[0]);
-        const float mean = s[0] * p.inv_c;
-        float q[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const bool in = (l + p.team * j) * V < p.C;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[j][e] = in ? x[j][e] - mean : 0.f;
-                q[0] = fmaf(x[j][e], x[j][e], q[0]);
-            }
-        }
-        team_sum<1, BLOCK>(q, p.team, slots[1]);
-        const float rstd = rsqrtf(fmaf(q[0], p.inv_c, p.eps));
-        if (live && l == 0 && p.mean) {
-            p.mean[row] = mean;
-            p.rstd[row] = rstd;
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int c = (l + p.team * j) * V;
-            if (live && c < p.C) {
-                if (!KEEP) {
-                    load_weights<V>(p.w, c, w[0], 1.f);
-                    load_weights<V>(p.b, c, b[0], 0.f);
+            for (int r = 0; r < R; ++r) {
+                const long long row = r0 + r * teams + team_in_block;
+                if (row < p.rows) {
+                    float y[V];
+                    chunk_affine<V>(x[r][j], rstd[r], w[KEEP ? j : 0], b[KEEP ? j : 0], y);
+                    store_chunk<T, V>(p.out, row * p.C + c, y);
                 }
-                float y[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) y[e] = fmaf(x[j][e] * rstd, w[KEEP ? j : 0][e], b[KEEP ? j : 0][e]);
-                store_chunk<T, V>(p.out, row * p.C + c, y);
             }
         }
     }
 }
 
-template <typename T, int V, int J, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_kernel(const NormParams p) {
-    __shared__ float slots[2][2][32];
-    extern __shared__ float cols[];   // warp teams: [warp][2][C]
-    const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1));
-    const int team_in_block = BLOCK ? 0 : threadIdx.x / p.team, teams = BLOCK ? 1 : kNormThreads / p.team;
-    const long long step = static_cast<long long>(gridDim.x) * teams;
-    float w[J][V], dw[J][V], db[J][V];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int c = (l + p.team * j) * V;
-        if (c < p.C) load_weights<V>(p.w, c, w[j], 1.f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
-    }
-    int turn = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * teams; r0 < p.rows; r0 += step, turn ^= 1) {
-        const long long row = r0 + team_in_block;
-        const bool live = row < p.rows;
-        const float mean = live ? __ldg(p.mean + row) : 0.f, rstd = live ? __ldg(p.rstd + row) : 0.f;
-        float h[J][V], g[J][V];
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int c = (l + p.team * j) * V;
-            if (live && c < p.C) {
-                load_chunk<T, V>(p.x, row * p.C + c, h[j]);
-                load_chunk<T, V>(p.dy, row * p.C + c, g[j]);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    h[j][e] = (h[j][e] - mean) * rstd;
-                    dw[j][e] = fmaf(g[j][e], h[j][e], dw[j][e]);
-                    db[j][e] += g[j][e];
-                    g[j][e] *= w[j][e];
-                    s[0] += g[j][e];
-                    s[1] = fmaf(g[j][e], h[j][e], s[1]);
-                }
-            }
-        }
-        team_sum<2, BLOCK>(s, p.team, slots[turn]);
-        const float c1 = s[0] * p.inv_c, c2 = s[1] * p.inv_c;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int c = (l + p.team * j) * V;
-            if (live && c < p.C) {
-                float d[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) d[e] = (g[j][e] - c1 - h[j][e] * c2) * rstd;
-                store_chunk<T, V>(p.out, row * p.C + c, d);
-            }
-        }
-    }
-    if (!p.partial) return;
+// A block's partial row of the weight gradients.  Warp teams: the warp's teams by shuffles, then the warps through
+// shared memory (cols: [warp][2][C]).
+template <int V, int J, bool BLOCK>
+__device__ __forceinline__ void store_partial(const NormParams& p, float (&dw)[J][V], float (&db)[J][V], int l, float* cols) {
     float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.C;
     if (BLOCK) {
 #pragma unroll
@@ -229,7 +255,6 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
         }
         return;
     }
-    // the warp's teams by shuffles, then the block's warps
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1)
         if (m >= p.team) {
@@ -264,31 +289,245 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
     }
 }
 
-// dw, db = sums of the blocks' partial rows.  A block takes 32 columns, its 32 warps every 32nd row each.
-__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* partial, int blocks, int C, float* dw, float* db) {
-    __shared__ float part[32][33];
+template <typename T, int V, int J, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_kernel(const NormParams p) {
+    constexpr int R = norm_rows(J, true);
+    __shared__ float slots[2][2 * R][32];
+    extern __shared__ float cols[];   // warp teams: [warp][2][C]
+    const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1));
+    const int team_in_block = BLOCK ? 0 : threadIdx.x / p.team, teams = BLOCK ? 1 : kNormThreads / p.team;
+    const long long step = static_cast<long long>(gridDim.x) * teams * R;   // a block's rows of one turn follow one another
+    float w[J][V], dw[J][V], db[J][V];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (l + p.team * j) * V;
+        load_weights<V>(c < p.C ? p.w : nullptr, c, w[j], 1.f);   // threads past the row multiply zeros: by ones
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
+    }
+    int turn = 0;
+    for (long long r0 = static_cast<long long>(blockIdx.x) * teams * R; r0 < p.rows; r0 += step, turn ^= 1) {
+        Chunk<T, V> rx[R][J], rg[R][J];
+        float h[R][J][V], g[R][J][V], s[2 * R], mean[R], rstd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long row = min(r0 + r * teams + team_in_block, p.rows - 1);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const long long at = row * p.C + min((l + p.team * j) * V, p.C - V);
+                rx[r][j].load(p.x, at);
+                rg[r][j].load(p.dy, at);
+            }
+            mean[r] = p.mean[row];
+            rstd[r] = p.rstd[row];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool live = r0 + r * teams + team_in_block < p.rows;
+            s[2 * r] = s[2 * r + 1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool in = live && (l + p.team * j) * V < p.C;
+                rx[r][j].get(h[r][j]);
+                rg[r][j].get(g[r][j]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    h[r][j][e] = in ? (h[r][j][e] - mean[r]) * rstd[r] : 0.f;
+                    g[r][j][e] = in ? g[r][j][e] : 0.f;
+                    dw[j][e] = fmaf(g[r][j][e], h[r][j][e], dw[j][e]);
+                    db[j][e] += g[r][j][e];
+                    g[r][j][e] *= w[j][e];
+                    s[2 * r] += g[r][j][e];
+                    s[2 * r + 1] = fmaf(g[r][j][e], h[r][j][e], s[2 * r + 1]);
+                }
+            }
+        }
+        team_sum<2 * R, BLOCK>(s, p.team, slots[turn]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long row = r0 + r * teams + team_in_block;
+            const float c1 = s[2 * r] * p.inv_c, c2 = s[2 * r + 1] * p.inv_c;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int c = (l + p.team * j) * V;
+                if (row < p.rows && c < p.C) {
+                    float d[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) d[e] = (g[r][j][e] - c1 - h[r][j][e] * c2) * rstd[r];
+                    store_chunk<T, V>(p.out, row * p.C + c, d);
+                }
+            }
+        }
+    }
+    if (p.partial) store_partial<V, J, BLOCK>(p, dw, db, l, cols);
+}
+
+// The backward of warp teams on whole chunks.  A register or two of loads per thread do not keep the memory busy
+// beside the accumulators, so x and dy come through a ring of tiles in shared memory (cp.async.bulk; rows are whole
+// chunks, so a tile is one run of bytes): a tile's stage is filled again once every thread has read it.  The
+// tile's statistics are read a tile ahead.
+constexpr int kNormStages = 2, kNormTileBytes = 8 * 1024, kNormTileRows = kNormThreads;   // a thread reads a row's statistics
+// Blocks per multiprocessor that the registers leave room for.
+__host__ __device__ constexpr int norm_ring_blocks(int J, int V) { return J == 1 ? 4 : (V == 8 ? 2 : 3); }
+
+template <typename T, int J>
+__global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J, Elem<T>::EPC)) norm_bwd_ring_kernel(const NormParams p) {
+    constexpr int V = Elem<T>::EPC;
+    extern __shared__ __align__(128) unsigned char smem[];   // [stage][x, dy][tile]; then the columns of store_partial
+    __shared__ uint64_t full[kNormStages];
+    __shared__ float stats[2][2][kNormTileRows];
+    __shared__ int issued, lost;   // thread 0's: tiles loaded; the first one whose copy did not land in time (-1: none)
+    const int l = threadIdx.x & (p.team - 1), first = threadIdx.x / p.team, teams = kNormThreads / p.team;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.C) * sizeof(T), buf = row_bytes * p.tile;
+    const WaitGuard guard{p.err, p.wait_ns};
+    auto rows_of = [&](long long t) { return static_cast<int>(min(static_cast<long long>(p.tile), p.rows - t * p.tile)); };
+    auto load = [&](long long t, int s) {   // thread 0
+        ++issued;
+        const uint32_t bytes = row_bytes * rows_of(t);
+        const long long off = t * static_cast<long long>(buf);
+        mbar_arrive_expect_tx(&full[s], 2 * bytes);
+        bulk_load(smem + (2 * s) * buf, static_cast<const char*>(p.x) + off, bytes, &full[s]);
+        bulk_load(smem + (2 * s + 1) * buf, static_cast<const char*>(p.dy) + off, bytes, &full[s]);
+    };
+    auto read_stats = [&](long long t, int i) {
+        if (t < p.tiles && static_cast<int>(threadIdx.x) < rows_of(t)) {
+            stats[i][0][threadIdx.x] = p.mean[t * p.tile + threadIdx.x];
+            stats[i][1][threadIdx.x] = p.rstd[t * p.tile + threadIdx.x];
+        }
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kNormStages; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+        issued = 0;
+        lost = -1;
+        long long t = blockIdx.x;
+        for (int s = 0; s < kNormStages && t < p.tiles; ++s, t += gridDim.x) load(t, s);
+    }
+    // Pairs of columns.  With d = x - mean and g' = dy rstd w the gradient of x is g' - sum g' / C - d rstd^2 sum (g' d) / C.
+    constexpr int H = V / 2;
+    uint64_t w[J][H], dw[J][H], db[J][H];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (l + p.team * j) * V;
+        float f[V];
+        load_weights<V>(c < p.C ? p.w : nullptr, c, f, 1.f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+            w[j][e] = pack2(f[2 * e], f[2 * e + 1]);
+            dw[j][e] = db[j][e] = 0;
+        }
+    }
+    read_stats(blockIdx.x, 0);
+    __syncthreads();
+    int s = 0, turn = 0;
+    uint32_t parity = 0;
+    for (long long t = blockIdx.x; t < p.tiles; t += gridDim.x, turn ^= 1) {
+        // a wait that runs out records itself; the block then goes on to its end without copies
+        if (!mbar_wait(&full[s], parity, guard, kSiteNorm) && threadIdx.x == 0 && lost < 0)
+            lost = static_cast<int>((t - blockIdx.x) / gridDim.x);
+        const int n = rows_of(t);
+        read_stats(t + gridDim.x, turn ^ 1);
+        const unsigned char* at = smem + (2 * s) * buf + first * row_bytes + l * 16;
+        T* to = static_cast<T*>(p.out) + (t * p.tile + first) * p.C + l * V;
+        // whole warps stay together, for the sums
+        for (int r = first; r - first < n; r += teams, at += teams * row_bytes, to += static_cast<long long>(teams) * p.C) {
+            const bool live = r < n;
+            const float mean = live ? stats[turn][0][r] : 0.f, rstd = live ? stats[turn][1][r] : 0.f;
+            const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
+            uint64_t d[J][H], g[J][H], s0 = 0, s1 = 0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (live && (l + p.team * j) * V < p.C) {
+                    float fx[V], fy[V];
+                    Elem<T>::unpack(*reinterpret_cast<const uint4*>(at + p.team * j * 16), fx);
+                    Elem<T>::unpack(*reinterpret_cast<const uint4*>(at + p.team * j * 16 + buf), fy);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        const uint64_t y = pack2(fy[2 * e], fy[2 * e + 1]), yr = mul2(y, rr);
+                        d[j][e] = add2(pack2(fx[2 * e], fx[2 * e + 1]), mm);
+                        dw[j][e] = fma2(yr, d[j][e], dw[j][e]);
+                        db[j][e] = add2(db[j][e], y);
+                        g[j][e] = mul2(yr, w[j][e]);
+                        s0 = add2(s0, g[j][e]);
+                        s1 = fma2(g[j][e], d[j][e], s1);
+                    }
+                }
+            }
+            float sums[2], other[2];
+            split2(s0, sums[0], other[0]);
+            split2(s1, sums[1], other[1]);
+            sums[0] += other[0];
+            sums[1] += other[1];
+            team_sum<2, false>(sums, p.team, nullptr);
+            const float k1 = -sums[0] * p.inv_c, k2 = -(rstd * rstd) * (sums[1] * p.inv_c);
+            const uint64_t kk1 = pack2(k1, k1), kk2 = pack2(k2, k2);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (live && (l + p.team * j) * V < p.C) {
+                    float f[V];
+#pragma unroll
+                    for (int e = 0; e < H; ++e) split2(fma2(d[j][e], kk2, add2(g[j][e], kk1)), f[2 * e], f[2 * e + 1]);
+                    store_chunk<T, V>(to, p.team * j * V, f);
+                }
+            }
+        }
+        __syncthreads();   // the tile has been read, the next statistics are in place
+        if (threadIdx.x == 0 && lost < 0) {
+            const long long next = t + static_cast<long long>(gridDim.x) * kNormStages;
+            if (next < p.tiles) load(next, s);
+        }
+        if (++s == kNormStages) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+    if (threadIdx.x == 0 && lost >= 0)   // the copies in flight have to land before the shared memory is given back
+        for (int i = lost; i < issued; ++i) mbar_drain(&full[i % kNormStages], (i / kNormStages) & 1, p.wait_ns);
+    __syncthreads();
+    if (!p.partial) return;
+    float fw[J][V], fb[J][V];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+            split2(dw[j][e], fw[j][2 * e], fw[j][2 * e + 1]);
+            split2(db[j][e], fb[j][2 * e], fb[j][2 * e + 1]);
+        }
+    store_partial<V, J, false>(p, fw, fb, l, reinterpret_cast<float*>(smem));
+}
+
+// dw, db = sums of the blocks' partial rows.  A block takes eight columns (a sector of each row), four rows a warp, so
+// every thread has its few loads in flight at once.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* partial, int blocks, int C, float* dw, float* db) {
+    __shared__ float part[kSumThreads / 32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const int c = blockIdx.x * 8 + (lane & 7);
     float s = 0.f;
     if (c < 2 * C)
-#pragma unroll 4
-        for (int r = warp; r < blocks; r += 32) s += partial[static_cast<long long>(r) * 2 * C + c];
-    part[warp][lane] = s;
+#pragma unroll 8
+        for (int r = threadIdx.x >> 3; r < blocks; r += kSumThreads / 8) s += partial[static_cast<long long>(r) * 2 * C + c];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < 8) part[warp][lane] = s;
     __syncthreads();
-    float t = part[lane][warp];
+    if (warp < 8) {
+        float t = part[lane][warp];
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-    const int cc = blockIdx.x * 32 + warp;
-    if (lane == 0 && cc < 2 * C) {
-        if (cc < C) dw[cc] = t;
-        else db[cc - C] = t;
+        for (int m = 16; m >= 1; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        const int cc = blockIdx.x * 8 + warp;
+        if (lane == 0 && cc < 2 * C) {
+            if (cc < C) dw[cc] = t;
+            else db[cc - C] = t;
+        }
     }
 }
 
 // How a problem is laid out: chunk width, chunks per thread, threads per row, blocks.
 struct NormPlan {
-    bool vec, block;
-    int j, team, blocks;
+    bool vec, block, ring;
+    int j, team, blocks, tile;
+    long long tiles;
 };
 
 NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
@@ -306,9 +545,21 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
         n.j = 1;
         while (n.j * n.team < chunks) n.j *= 2;
         if (!n.vec) n.j = bwd ? 2 : (n.j > 1 ? 4 : 1);
-        const long long teams = kNormThreads / n.team, need = (rows + teams - 1) / teams;
-        const long long most = static_cast<long long>(sms) * (bwd ? 4 : 16);
+        const long long per = static_cast<long long>(kNormThreads / n.team) * norm_rows(n.j, bwd), need = (rows + per - 1) / per;
+        const long long most = static_cast<long long>(sms) * (bwd ? 3 : 16);
         n.blocks = static_cast<int>(need < most ? need : most);
+        if (bwd && n.vec) {   // tiles of whole passes of the teams; fewer where the grid is small
+            n.ring = true;
+            const int teams = kNormThreads / n.team, per_sm = norm_ring_blocks(n.j, V);
+            int passes = kNormTileBytes / (teams * C * es);
+            if (passes * teams > kNormTileRows) passes = kNormTileRows / teams;   // at least 1
+            passes = passes < 1 ? 1 : passes;
+            while (passes > 1 && rows / (static_cast<long long>(teams) * passes) < 4 * per_sm * sms) --passes;
+            n.tile = teams * passes;
+            n.tiles = (rows + n.tile - 1) / n.tile;
+            const long long grid = static_cast<long long>(per_sm) * sms;
+            n.blocks = static_cast<int>(n.tiles < grid ? n.tiles : grid);
+        }
     } else {
         // few rows: a thread for every chunk; else two chunks each
         n.j = n.vec ? (rows < 4LL * sms ? 1 : 2) : 4;
@@ -325,7 +576,15 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
 template <typename T, int V, int J, bool BLOCK, bool BWD>
 na_status run_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
     const int threads = BLOCK ? n.team : kNormThreads;
-    if constexpr (BWD) {
+    if constexpr (BWD && !BLOCK && V > 1) {
+        const size_t ring = 2ull * kNormStages * n.tile * p.C * sizeof(T), sums = static_cast<size_t>(kNormThreads / 32) * 2 * p.C * sizeof(float);
+        const size_t smem = ring > sums ? ring : sums;
+        const auto kernel = norm_bwd_ring_kernel<T, J>;
+        if (smem > 40 * 1024 &&   // 48 KB without asking, static shared memory included
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+            return NA_ERR_CUDA;
+        kernel<<<n.blocks, threads, smem, s>>>(p);
+    } else if constexpr (BWD) {
         const size_t smem = BLOCK || !p.partial ? 0 : static_cast<size_t>(kNormThreads / 32) * 2 * p.C * sizeof(float);
         norm_bwd_kernel<T, V, J, BLOCK><<<n.blocks, threads, smem, s>>>(p);
     } else {
@@ -437,6 +696,10 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
     p.inv_c = 1.f / static_cast<float>(C);
     const NormPlan n = plan_norm(rows, C, elem_bytes(dtype), true);
     p.team = n.team;
+    p.tile = n.tile;
+    p.tiles = n.tiles;
+    p.wait_ns = wait_limit_ns();
+    if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
     bool owned = false;
@@ -456,7 +719,7 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
     p.partial = static_cast<float*>(ws);
     st = dispatch_norm<true>(p, n, dtype, s);
     if (st == NA_OK && dw) {
-        norm_sum_kernel<<<(2 * C + 31) / 32, 1024, 0, s>>>(p.partial, n.blocks, C, dw, db);
+        norm_sum_kernel<<<(2 * C + 7) / 8, kSumThreads, 0, s>>>(p.partial, n.blocks, C, dw, db);
         st = launch_result();
     }
     if (owned && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;

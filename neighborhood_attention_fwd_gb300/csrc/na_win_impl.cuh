@@ -64,29 +64,6 @@ struct Words<float> {
     static __device__ __forceinline__ float top(uint32_t w) { return __uint_as_float(w); }
 };
 
-// Pairs of fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // The place of a lane in its row.  Lane l of L holds words l, l + L, .., J of them; the row has (K + 1) / 2 words (K is
 // odd) and fills all but the last of every lane's: only word 0 (`head`: its low half is the row before's) and the
 // last words (`last` 0: past the row, 1: the low half alone, 2: whole) need care.
@@ -229,17 +206,6 @@ __device__ __forceinline__ void row_grad(float (&v)[NV], const float (&g)[NV], f
     for (int i = 0; i + 1 < NV; i += 2)
         split2(mul2(mul2(pack2(v[i], v[i + 1]), aa), add2(pack2(g[i], g[i + 1]), qq)), v[i], v[i + 1]);
     if (NV % 2) v[NV - 1] = v[NV - 1] * a * (g[NV - 1] - q);
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-                 : "memory");
 }
 
 // Zeros the dropped places of a tile in shared memory: octet o of the tile is block block0 + o of the tensor.  Several
@@ -587,7 +553,7 @@ na_status run_win(WinParams& p, cudaStream_t s) {
     p.stages = 3;
     const size_t smem = static_cast<size_t>(p.stages) * stage;
     const auto kernel = win_kernel<T, DIFF, BWD, L, J>;
-    if (smem > 48 * 1024 &&
+    if (smem > 40 * 1024 &&   // 48 KB without asking, static shared memory included
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return NA_ERR_CUDA;
     int per_sm = static_cast<int>(kWinSmem / (smem + 1024));
