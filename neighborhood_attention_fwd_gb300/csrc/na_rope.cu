@@ -14,6 +14,7 @@
 // What bounds it.  Every element is read and written once: memory.  A block takes consecutive tokens, computes the
 // tokens' angles once into shared memory (all heads of q and k share them) while its first loads are in
 // flight, and then streams the tokens' rows in 16-byte chunks.
+#include <algorithm>
 #include <cmath>
 
 #include "na_block.cuh"
@@ -23,6 +24,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;   // D / 2 at D = 128
+constexpr int kMaxTokens = 64;  // tokens of a block
+constexpr int kRopeBytes = 32 * 1024;   // rows of a block, about
 
 struct RopeParams {
     const void* x[2];          // q, k (k null: heads_k = 0)
@@ -36,6 +39,7 @@ struct RopeParams {
     unsigned long long turns[kMaxPairs];   // turns per position, 64-bit fixed point
     int pair_end[3];           // pairs of axes 0 .. a
     int np;                    // pairs in all
+    int row;                   // entries of a token's row of angles
     int cph;                   // 16-byte chunks per head row
     int lu;                    // log2 of the units per head row
     int tt;                    // tokens per block
@@ -47,27 +51,54 @@ struct RopeParams {
     uint8_t partner[128], pair[128];
 };
 
-// cos and sin of every pair of the block's tokens: tab[t * np + pair].
-__device__ __forceinline__ void fill_angles(const RopeParams& p, float2* tab, long long tok0, int tt) {
+// The grid positions of the block's tokens, one token per thread (a block has at most kMaxTokens).
+__device__ __forceinline__ void fill_positions(const RopeParams& p, int (*pos)[kMaxTokens], long long tok0, int tt) {
+    if (static_cast<int>(threadIdx.x) >= tt) return;
+    const long long tok = tok0 + threadIdx.x;
+    if (p.tokens < (1LL << 32)) {
+        const uint32_t r = static_cast<uint32_t>(tok), q2 = fdiv(r, p.fd_L[2]), q1 = fdiv(q2, p.fd_L[1]), q0 = fdiv(q1, p.fd_L[0]);
+        pos[2][threadIdx.x] = static_cast<int>(r - q2 * p.L[2]);
+        pos[1][threadIdx.x] = static_cast<int>(q2 - q1 * p.L[1]);
+        pos[0][threadIdx.x] = static_cast<int>(q1 - q0 * p.L[0]);
+    } else {
+        const long long q2 = tok / p.L[2], q1 = q2 / p.L[1];
+        pos[2][threadIdx.x] = static_cast<int>(tok - q2 * p.L[2]);
+        pos[1][threadIdx.x] = static_cast<int>(q2 - q1 * p.L[1]);
+        pos[0][threadIdx.x] = static_cast<int>(q1 % p.L[0]);
+    }
+}
+
+// The frequencies in shared memory: lanes that read different entries of a kernel parameter do so one by one.
+__device__ __forceinline__ void fill_turns(const RopeParams& p, unsigned long long* turns) {
+    if (static_cast<int>(threadIdx.x) < p.np) turns[threadIdx.x] = p.turns[threadIdx.x];
+}
+
+__device__ __forceinline__ int axis_of(const RopeParams& p, int pair) {
+    return pair < p.pair_end[0] ? 0 : (pair < p.pair_end[1] ? 1 : 2);
+}
+
+// cos and sin, times the amplitude, of a pair at grid position x of its axis.
+__device__ __forceinline__ float2 angle_of(const RopeParams& p, int axis, unsigned long long turns, int x) {
+    const unsigned long long o = axis == 0 ? p.origin[0] : (axis == 1 ? p.origin[1] : p.origin[2]);
+    const unsigned long long phase = (o + static_cast<unsigned long long>(x)) * turns;
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31 half turns
+    return make_float2(c * p.amp, s * p.amp * p.sgn);
+}
+
+// Where a pair's angle lies in its token's row of the table: units of G pairs, two entries apart where a unit is longer
+// than 16 bytes, so that the lanes of a head row, a unit each, read different banks.
+template <int G>
+__host__ __device__ constexpr int angle_at(int pair) { return pair + (G >= 4 ? pair / G * 2 : 0); }
+
+// The angles of every pair of the block's tokens.
+template <int G>
+__device__ __forceinline__ void fill_angles(const RopeParams& p, float2* tab, const unsigned long long* turns,
+                                            const int (*pos)[kMaxTokens], int tt) {
     for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(tt * p.np); i += kRopeThreads) {
-        const uint32_t t = fdiv(i, p.fd_np), pr = i - t * static_cast<uint32_t>(p.np);
-        const long long tok = tok0 + t;
-        int pos;
-        const int a = static_cast<int>(pr) < p.pair_end[0] ? 0 : (static_cast<int>(pr) < p.pair_end[1] ? 1 : 2);
-        if (p.tokens < (1LL << 32)) {
-            uint32_t r = static_cast<uint32_t>(tok);
-            const uint32_t q2 = fdiv(r, p.fd_L[2]);
-            const uint32_t q1 = fdiv(q2, p.fd_L[1]);
-            const uint32_t q0 = fdiv(q1, p.fd_L[0]);
-            pos = static_cast<int>(a == 2 ? r - q2 * p.L[2] : (a == 1 ? q2 - q1 * p.L[1] : q1 - q0 * p.L[0]));
-        } else {
-            const long long q2 = tok / p.L[2], q1 = q2 / p.L[1];
-            pos = static_cast<int>(a == 2 ? tok - q2 * p.L[2] : (a == 1 ? q2 - q1 * p.L[1] : q1 % p.L[0]));
-        }
-        const unsigned long long phase = (p.origin[a] + static_cast<unsigned long long>(pos)) * p.turns[pr];
-        float s, c;
-        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31 half turns
-        tab[i] = make_float2(c * p.amp, s * p.amp * p.sgn);
+        const uint32_t t = fdiv(i, p.fd_np);
+        const int pair = static_cast<int>(i - t * static_cast<uint32_t>(p.np)), a = axis_of(p, pair);
+        tab[t * p.row + angle_at<G>(pair)] = angle_of(p, a, turns[pair], pos[a][t]);
     }
 }
 
@@ -78,6 +109,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     using E = Elem<T>;
     constexpr int V = E::EPC, NC = INTER ? 1 : 2, U = INTER ? 8 : 4, NP = INTER ? V / 2 : V;
     extern __shared__ __align__(16) float2 tab[];
+    __shared__ int pos[3][kMaxTokens];
+    __shared__ unsigned long long turns[kMaxPairs];
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tt;
     const int tt = static_cast<int>(min(static_cast<long long>(p.tt), p.tokens - tok0));
     const uint32_t nq = static_cast<uint32_t>(tt) * p.upt[0], n = nq + static_cast<uint32_t>(tt) * p.upt[1];
@@ -106,7 +139,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
     };
     load(threadIdx.x);
-    fill_angles(p, tab, tok0, tt);
+    fill_positions(p, pos, tok0, tt);
+    fill_turns(p, turns);
+    __syncthreads();
+    fill_angles<NP>(p, tab, turns, pos, tt);
     __syncthreads();
     for (uint32_t base = threadIdx.x;;) {
 #pragma unroll
@@ -117,7 +153,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 const uint32_t k = w ? i - nq : i;
                 uint4* y = ys[w] + static_cast<long long>(k >> p.lu) * p.cph;
                 if (p0 < p.np) {
-                    const float2* cs = tab + fdiv(k, p.fd_upt[w]) * p.np + p0;
+                    const float2* cs = tab + fdiv(k, p.fd_upt[w]) * p.row + angle_at<NP>(p0);
                     float f[NC][V];
                     E::unpack(r[j][0], f[0]);
                     if (!INTER) E::unpack(r[j][NC - 1], f[NC - 1]);
@@ -155,46 +191,83 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
 }
 
-// Half layout with a block whose halves are not whole chunks: a chunk's partners come through shared
-// memory, 256 chunks (whole head rows) at a time.
+// Half layout with a block whose halves are not whole chunks: a chunk's partners lie anywhere in its head's row, so the
+// rows pass through shared memory, kSplit chunks (whole head rows) per thread at a time, the next ones on
+// their way meanwhile.  The angles are kept per channel, the sine with the sign it takes there:
+// y = x cos + partner sin.
+constexpr int kSplit = 4;
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_split_kernel(const __grid_constant__ RopeParams p) {
     using E = Elem<T>;
     constexpr int V = E::EPC;
-    extern __shared__ __align__(16) float2 tab[];
-    __shared__ uint4 rows[kRopeThreads];
+    extern __shared__ __align__(16) float2 tab[];   // [token][element of the chunk][chunk]: lanes read one after another
+    __shared__ uint4 rows[kSplit * kRopeThreads];
+    __shared__ int pos[3][kMaxTokens];
+    __shared__ unsigned long long turns[kMaxPairs];
+    __shared__ int where[2][kMaxPairs];   // a pair's two channels, as places in a token's row of the table
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tt;
     const int tt = static_cast<int>(min(static_cast<long long>(p.tt), p.tokens - tok0));
-    fill_angles(p, tab, tok0, tt);
-    const int c = threadIdx.x & (p.cph - 1);
-    const T* head = reinterpret_cast<const T*>(rows + (threadIdx.x - c));
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-        const uint32_t n = static_cast<uint32_t>(tt) * p.upt[w];
-        const uint4* x = static_cast<const uint4*>(p.x[w]) + tok0 * p.upt[w];
-        uint4* y = static_cast<uint4*>(p.y[w]) + tok0 * p.upt[w];
-        for (uint32_t base = 0; base < n; base += kRopeThreads) {
-            const uint32_t i = base + threadIdx.x;
-            __syncthreads();   // the angles; the last turn's reads of rows
-            if (i < n) rows[threadIdx.x] = ld_stream(x + i);
-            __syncthreads();
-            if (i < n) {
-                const float2* cs = tab + fdiv(i, p.fd_upt[w]) * p.np;
-                alignas(16) T v[V];
-                *reinterpret_cast<uint4*>(v) = rows[threadIdx.x];
+    const int D = p.cph * V, c = threadIdx.x & (p.cph - 1);
+    const uint32_t nq = static_cast<uint32_t>(tt) * p.upt[0], n = nq + static_cast<uint32_t>(tt) * p.upt[1];
+    const uint4* xs[2] = {static_cast<const uint4*>(p.x[0]) + tok0 * p.upt[0], static_cast<const uint4*>(p.x[1]) + tok0 * p.upt[1]};
+    uint4* ys[2] = {static_cast<uint4*>(p.y[0]) + tok0 * p.upt[0], static_cast<uint4*>(p.y[1]) + tok0 * p.upt[1]};
+    uint4 r[kSplit];
+    auto load = [&](uint32_t base) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int ch = c * V + e;
-                    if (p.pair[ch] != 0xff) {   // the others keep their bits
-                        const float2 t = cs[p.pair[ch]];
-                        const int other = p.partner[ch];
-                        const float o = E::get(head[other]), x0 = E::get(v[e]);
-                        v[e] = E::put(other > ch ? x0 * t.x - o * t.y : o * t.y + x0 * t.x);
-                    }
-                }
-                st_stream(y + i, *reinterpret_cast<const uint4*>(v));
-            }
+        for (int j = 0; j < kSplit; ++j) {
+            const uint32_t i = base + j * kRopeThreads;
+            if (i < n) r[j] = i < nq ? ld_stream(xs[0] + i) : ld_stream(xs[1] + (i - nq));
         }
+    };
+    load(threadIdx.x);
+    fill_positions(p, pos, tok0, tt);
+    fill_turns(p, turns);
+    auto place = [&](int ch) { return ch % V * p.cph + ch / V; };
+    if (static_cast<int>(threadIdx.x) < D) {
+        const int ch = threadIdx.x, pair = p.pair[ch];
+        if (pair != 0xff) where[p.partner[ch] < ch][pair] = place(ch);
+    }
+    int partner[V];   // of the thread's channels, which are the same in every turn
+    bool turned[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        turned[e] = p.pair[c * V + e] != 0xff;
+        partner[e] = turned[e] ? p.partner[c * V + e] : c * V + e;
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(tt * p.np); i += kRopeThreads) {
+        const uint32_t t = fdiv(i, p.fd_np);
+        const int pair = static_cast<int>(i - t * static_cast<uint32_t>(p.np)), a = axis_of(p, pair);
+        const float2 cs = angle_of(p, a, turns[pair], pos[a][t]);
+        tab[t * p.row + where[0][pair]] = make_float2(cs.x, -cs.y);
+        tab[t * p.row + where[1][pair]] = cs;
+    }
+    for (uint32_t base = threadIdx.x;;) {
+#pragma unroll
+        for (int j = 0; j < kSplit; ++j) rows[j * kRopeThreads + threadIdx.x] = r[j];
+        __syncthreads();   // the rows, and in the first turn the angles
+#pragma unroll
+        for (int j = 0; j < kSplit; ++j) {
+            const uint32_t i = base + j * kRopeThreads;
+            if (i >= n) continue;
+            const int w = i >= nq;
+            const uint32_t k = w ? i - nq : i;
+            const float2* cs = tab + fdiv(k, p.fd_upt[w]) * p.row + c;
+            const T* head = reinterpret_cast<const T*>(rows + j * kRopeThreads + (threadIdx.x - c));
+            alignas(16) T v[V];
+            *reinterpret_cast<uint4*>(v) = r[j];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float2 t = cs[e * p.cph];
+                const T y = E::put(fmaf(E::get(head[partner[e]]), t.y, E::get(v[e]) * t.x));
+                if (turned[e]) v[e] = y;   // the others keep their bits
+            }
+            st_stream(ys[w] + k, *reinterpret_cast<const uint4*>(v));
+        }
+        base += kSplit * kRopeThreads;
+        if (base - threadIdx.x >= n) break;
+        load(base);
+        __syncthreads();   // the rows have been read
     }
 }
 
@@ -299,11 +372,14 @@ na_status rope(const void* q, const void* k, void* q_out, void* k_out, int B, in
     }
     while ((1 << p.lu) < upr) ++p.lu;
     const long long upt_q = static_cast<long long>(heads_q) * upr, upt_k = static_cast<long long>(heads_k) * upr;
-    // tokens per block: about 32 KB of rows, at most 64 tokens (32 KB of angles), fewer where the grid would
+    // tokens per block: about kRopeBytes of rows and at most 24 KB of angles; fewer where the grid would
     // not fill the multiprocessors twice
     const long long row = (static_cast<long long>(heads_q) + heads_k) * D * es;
-    long long tt = 32768 / row;
-    tt = tt < 1 ? 1 : (tt > 64 ? 64 : tt);
+    const int g = inter ? V / 2 : V;   // pairs of a unit
+    p.row = split ? D : p.np + (g >= 4 ? (p.np + g - 1) / g * 2 : 0);
+    const long long angles = p.row * static_cast<long long>(sizeof(float2));
+    long long tt = std::min<long long>({kRopeBytes / row, kMaxTokens, 24 * 1024 / angles});
+    tt = tt < 1 ? 1 : tt;
     const long long fill = p.tokens / (2 * kSms);
     if (tt > fill) tt = fill < 1 ? 1 : fill;
     const long long blocks = (p.tokens + tt - 1) / tt;
@@ -312,7 +388,7 @@ na_status rope(const void* q, const void* k, void* q_out, void* k_out, int B, in
     p.upt[1] = static_cast<uint32_t>(upt_k);
     for (int i = 0; i < 2; ++i) p.fd_upt[i] = make_fastdiv(p.upt[i]);
     p.tt = static_cast<int>(tt);
-    const size_t smem = static_cast<size_t>(tt) * p.np * sizeof(float2);
+    const size_t smem = static_cast<size_t>(tt * angles);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned nb = static_cast<unsigned>(blocks);
     if (dtype == NA_BF16) launch_rope_t<__nv_bfloat16>(p, inter, split, nb, smem, s);
