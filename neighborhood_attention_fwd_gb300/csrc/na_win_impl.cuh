@@ -31,7 +31,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxStages = 3;
 constexpr int kStageBytes = 12 * 1024;   // a tile of every input, about
-constexpr int kLongThreads = 256;   // block of a row that no tile holds
+constexpr int kLongThreads = 128;   // block of a row that no tile holds
 
 // A row's words: 4 bytes, one or two weights.
 template <typename T>
@@ -422,10 +422,10 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
     }
 }
 
-// Rows that no tile holds (longer than 32 lanes of kMaxWords words): a block per row, read again for
-// each pass (a row is a few tens of KB at most for any sensible window, and stays in L1 or L2).
+// Rows that no tile holds (over 767 weights): a block per row, in aligned octets of the tensor (the row's first and last may
+// be shared with its neighbours), read again for each pass: a row is a few KB and stays in L1.
 template <int N>
-__device__ __forceinline__ void block_reduce(float (&v)[N], bool maximum, float (*slot)[8]) {
+__device__ __forceinline__ void block_reduce(float (&v)[N], bool maximum, float (*slot)[kLongThreads / 32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -441,91 +441,150 @@ __device__ __forceinline__ void block_reduce(float (&v)[N], bool maximum, float 
     __syncthreads();
 }
 
+// An octet of the tensor as fp32, with `fill` at the places outside [first, end).
+template <typename T>
+__device__ __forceinline__ void octet_load(const T* base, long long o, long long first, long long end, long long total, float fill,
+                                           float (&f)[8]) {
+    constexpr int V = Elem<T>::EPC;
+    const long long e0 = o * 8;
+    if (e0 + 8 <= total) {
+#pragma unroll
+        for (int c = 0; c < 8 / V; ++c) {
+            float g[V];
+            Elem<T>::unpack(*reinterpret_cast<const uint4*>(base + e0 + c * V), g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[c * V + e] = g[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e0 + e < total ? Elem<T>::get(base[e0 + e]) : fill;
+    }
+    if (e0 < first || e0 + 8 > end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e0 + e < first || e0 + e >= end) f[e] = fill;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void octet_store(T* base, long long o, long long first, long long end, const float (&f)[8]) {
+    constexpr int V = Elem<T>::EPC;
+    const long long e0 = o * 8;
+    if (e0 >= first && e0 + 8 <= end) {
+#pragma unroll
+        for (int c = 0; c < 8 / V; ++c) {
+            float g[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = f[c * V + e];
+            *reinterpret_cast<uint4*>(base + e0 + c * V) = Elem<T>::pack(g);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e0 + e >= first && e0 + e < end) base[e0 + e] = Elem<T>::put(f[e]);
+    }
+}
+
 template <typename T, bool DIFF, bool BWD>
 __global__ void __launch_bounds__(kLongThreads) win_long_kernel(const __grid_constant__ WinParams p) {
     constexpr int M = DIFF ? 2 : 1;
-    __shared__ float slot[2][8];
-    const long long row = blockIdx.x;
-    const long long first = row * p.K;
-    const T* x[2] = {static_cast<const T*>(p.x1) + first, static_cast<const T*>(DIFF ? p.x2 : p.x1) + first};
-    const T* dy = static_cast<const T*>(p.dy) + (BWD ? first : 0);
-    T* out[2] = {static_cast<T*>(p.out1) + first, static_cast<T*>(DIFF && BWD ? p.out2 : p.out1) + first};
+    __shared__ float slot[M][kLongThreads / 32];
+    const long long row = blockIdx.x, first = row * p.K, end = first + p.K, total = p.rows * p.K;
+    const long long o0 = (first >> 3) + threadIdx.x, o1 = (end + 7) >> 3;
+    const T* x[M];
+    x[0] = static_cast<const T*>(p.x1);
+    if (DIFF) x[M - 1] = static_cast<const T*>(p.x2);
+    const T* dy = static_cast<const T*>(p.dy);
     float lam = 0.f;
     if (DIFF) lam = __ldg(p.lam + (p.lam_rows ? row : row % p.heads));
     RngState rng{};
     const bool dropping = p.drop.state != nullptr;
     if (dropping) rng = rng_load(p.drop.state);
-    float m[M], l[M], ml2[M];
+    float m[M], l[M], ml2[M], q[M], f[8];
     bool far[M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-    }
-    for (int t = threadIdx.x; t < p.K; t += kLongThreads)
+    for (int i = 0; i < M; ++i) m[i] = -INFINITY;
+    for (long long o = o0; o < o1; o += kLongThreads)
 #pragma unroll
-        for (int i = 0; i < M; ++i) m[i] = fmaxf(m[i], Elem<T>::get(x[i][t]));
+        for (int i = 0; i < M; ++i) {
+            octet_load(x[i], o, first, end, total, -INFINITY, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[i] = fmaxf(m[i], f[e]);
+        }
     block_reduce<M>(m, true, slot);
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         m[i] = row_top(m[i], far[i]);
         ml2[i] = far[i] ? 0.f : m[i] * kLog2e;
+        l[i] = q[i] = 0.f;
     }
-    auto weight = [&](int i, int t) {
-        const float v = Elem<T>::get(x[i][t]);
-        return fast_exp2(fmaf(far[i] ? v - m[i] : v, kLog2e, -ml2[i]));
+    auto weights = [&](int i, long long o, float (&w)[8]) {   // exp(x - max): 0 outside the row
+        octet_load(x[i], o, first, end, total, -INFINITY, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = fast_exp2(fmaf(far[i] ? w[e] - m[i] : w[e], kLog2e, -ml2[i]));
     };
-    for (int t = threadIdx.x; t < p.K; t += kLongThreads)
+    auto gradient = [&](long long o, float (&g)[8]) {   // dy, 0 where it was dropped
+        octet_load(dy, o, first, end, total, 0.f, g);
+        if (dropping) {
+            const uint4 keep = keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps);
 #pragma unroll
-        for (int i = 0; i < M; ++i) l[i] += weight(i, t);
-    block_reduce<M>(l, false, slot);
+            for (int e = 0; e < 8; ++e)
+                if (!keep_of(keep, e)) g[e] = 0.f;
+        }
+    };
+    for (long long o = o0; o < o1; o += kLongThreads) {
+        float g[8];
+        if (BWD) gradient(o, g);
 #pragma unroll
-    for (int i = 0; i < M; ++i) l[i] = inverse_or_zero(l[i]);
-    // octets of the tensor that hold this row's weights; an octet shared with a neighbour is taken in part
-    const long long o0 = first >> 3, o1 = (first + p.K + 7) >> 3;
-    float q[M];
-    if (BWD) {
-#pragma unroll
-        for (int i = 0; i < M; ++i) q[i] = 0.f;
-        for (long long o = o0 + threadIdx.x; o < o1; o += kLongThreads) {
-            const uint4 keep = dropping ? keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps) : uint4{};
+        for (int i = 0; i < M; ++i) {
+            weights(i, o, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const long long t = o * 8 + e - first;
-                if (t < 0 || t >= p.K || (dropping && !keep_of(keep, e))) continue;
-                const float g = Elem<T>::get(dy[t]);
-#pragma unroll
-                for (int i = 0; i < M; ++i) {
-                    const float w = weight(i, static_cast<int>(t));
-                    q[i] += w == 0.f ? 0.f : w * g;
-                }
+                l[i] += f[e];
+                if (BWD) q[i] += f[e] == 0.f ? 0.f : f[e] * g[e];   // a place of weight zero takes no part
             }
         }
-        block_reduce<M>(q, false, slot);
-#pragma unroll
-        for (int i = 0; i < M; ++i) q[i] *= l[i];
-        if (DIFF && threadIdx.x == 0) p.dlam[row] = -p.drop.gain * q[M - 1];
     }
-    for (long long o = o0 + threadIdx.x; o < o1; o += kLongThreads) {
-        const uint4 keep = dropping ? keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps) : uint4{};
+    block_reduce<M>(l, false, slot);
+    if (BWD) block_reduce<M>(q, false, slot);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const long long t = o * 8 + e - first;
-            if (t < 0 || t >= p.K) continue;
-            const bool kept = !dropping || keep_of(keep, e);
-            float w[M];
+    for (int i = 0; i < M; ++i) {
+        l[i] = inverse_or_zero(l[i]);
+        q[i] *= l[i];
+        l[i] *= p.drop.gain;
+    }
+    if (DIFF && BWD && threadIdx.x == 0) p.dlam[row] = -p.drop.gain * q[M - 1];
+    if (DIFF) l[M - 1] *= -lam;
+    for (long long o = o0; o < o1; o += kLongThreads) {
+        if (BWD) {
+            float g[8];
+            gradient(o, g);
+            float w[M][8];
 #pragma unroll
-            for (int i = 0; i < M; ++i) w[i] = weight(i, static_cast<int>(t));
-            if (BWD) {
-                const float g = kept ? Elem<T>::get(dy[t]) : 0.f;
+            for (int i = 0; i < M; ++i) weights(i, o, w[i]);   // before any store: an output may be an input's tensor
 #pragma unroll
-                for (int i = 0; i < M; ++i)
-                    out[i][t] = Elem<T>::put(w[i] == 0.f ? 0.f : w[i] * (l[i] * p.drop.gain * (i == 1 ? -lam : 1.f)) * (g - q[i]));
-            } else {
-                float y = w[0] * (l[0] * p.drop.gain);
-                if (DIFF) y -= w[M - 1] * (l[M - 1] * p.drop.gain * lam);
-                out[0][t] = Elem<T>::put(kept ? y : 0.f);
+            for (int i = 0; i < M; ++i) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[i][e] = w[i][e] == 0.f ? 0.f : w[i][e] * l[i] * (g[e] - q[i]);
+                octet_store(static_cast<T*>(i == 0 ? p.out1 : p.out2), o, first, end, w[i]);
             }
+        } else {
+            float y[8];
+            weights(0, o, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= l[0];
+            if (DIFF) {
+                weights(M - 1, o, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = fmaf(f[e], l[M - 1], y[e]);
+            }
+            if (dropping) {
+                const uint4 keep = keep_masks(rng, static_cast<unsigned long long>(o), p.drop.steps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!keep_of(keep, e)) y[e] = 0.f;
+            }
+            octet_store(static_cast<T*>(p.out1), o, first, end, y);
         }
     }
 }
@@ -535,6 +594,7 @@ __global__ void __launch_bounds__(kLongThreads) win_long_kernel(const __grid_con
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kMaxWords = 12;             // words per lane, at most
+constexpr int kMaxWide = 24;              // of a warp's lanes on 4-byte weights (one to a word)
 constexpr uint32_t kWinSmem = 220 * 1024; // shared memory of a multiprocessor that the blocks' rings share
 
 template <typename T, bool DIFF, bool BWD, int L, int J>
@@ -584,8 +644,25 @@ na_status run_words(int j, WinParams& p, cudaStream_t s) {
         case 9: return run_win<T, DIFF, BWD, L, 9>(p, s);
         case 10: return run_win<T, DIFF, BWD, L, 10>(p, s);
         case 11: return run_win<T, DIFF, BWD, L, 11>(p, s);
-        default: return run_win<T, DIFF, BWD, L, kMaxWords>(p, s);
+        case 12: return run_win<T, DIFF, BWD, L, 12>(p, s);
     }
+    if constexpr (L == 32 && sizeof(T) == 4) {
+        switch (j) {
+            case 13: return run_win<T, DIFF, BWD, L, 13>(p, s);
+            case 14: return run_win<T, DIFF, BWD, L, 14>(p, s);
+            case 15: return run_win<T, DIFF, BWD, L, 15>(p, s);
+            case 16: return run_win<T, DIFF, BWD, L, 16>(p, s);
+            case 17: return run_win<T, DIFF, BWD, L, 17>(p, s);
+            case 18: return run_win<T, DIFF, BWD, L, 18>(p, s);
+            case 19: return run_win<T, DIFF, BWD, L, 19>(p, s);
+            case 20: return run_win<T, DIFF, BWD, L, 20>(p, s);
+            case 21: return run_win<T, DIFF, BWD, L, 21>(p, s);
+            case 22: return run_win<T, DIFF, BWD, L, 22>(p, s);
+            case 23: return run_win<T, DIFF, BWD, L, 23>(p, s);
+            case 24: return run_win<T, DIFF, BWD, L, 24>(p, s);
+        }
+    }
+    return NA_ERR_UNSUPPORTED;
 }
 
 template <typename T, bool DIFF, bool BWD>
@@ -594,7 +671,7 @@ na_status launch_win_rows(WinParams& p, cudaStream_t s) {
     int lanes = 1;   // the fewest: a row costs each of its lanes its reductions besides its words
     while (lanes < 32 && words > kMaxWords * lanes) lanes *= 2;
     const int j = (words + lanes - 1) / lanes;
-    if (j > kMaxWords) {
+    if (j > (sizeof(T) == 4 ? kMaxWide : kMaxWords)) {
         if (p.rows > 0x7fffffffLL) return NA_ERR_UNSUPPORTED;
         win_long_kernel<T, DIFF, BWD><<<static_cast<unsigned>(p.rows), kLongThreads, 0, s>>>(p);
         return launch_result();
