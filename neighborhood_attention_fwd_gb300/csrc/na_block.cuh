@@ -140,18 +140,59 @@ __device__ __forceinline__ uint4 rng_block(const RngState& s, unsigned long long
     return make_uint4(c0, c1, c2, c3);
 }
 
+// The same bits for the blocks below 2^32, whose upper counter word is zero: then all of the first round's second product and
+// the second round's first one are the same for every block.  A plan holds them folded into the constants that the
+// rounds xor in (12 products and 13 xors a block instead of 14 and 14 with 12 additions for the keys).
+struct RngPlan {
+    uint32_t c[4];               // o1 ^ k1[0], low(o0 M1) ^ k0[1], high(P M0) ^ k1[1], low(P M0) ^ k1[2]; P = high(o0 M1) ^ k0[0]
+    uint32_t k0[5], k1[4];       // k0[2..6], k1[3..6]
+    uint32_t pad[3];
+};
+
+__device__ __forceinline__ RngPlan rng_plan(const RngState& s) {
+    RngPlan p;
+    const unsigned long long b = static_cast<unsigned long long>(s.o0) * 0xCD9E8D57u;
+    const unsigned long long a = static_cast<unsigned long long>(static_cast<uint32_t>(b >> 32) ^ s.k0) * 0xD2511F53u;
+    auto k0 = [&](uint32_t r) { return s.k0 + r * 0x9E3779B9u; };
+    auto k1 = [&](uint32_t r) { return s.k1 + r * 0xBB67AE85u; };
+    p.c[0] = s.o1 ^ k1(0);
+    p.c[1] = static_cast<uint32_t>(b) ^ k0(1);
+    p.c[2] = static_cast<uint32_t>(a >> 32) ^ k1(1);
+    p.c[3] = static_cast<uint32_t>(a) ^ k1(2);
+#pragma unroll
+    for (uint32_t r = 0; r < 5; ++r) p.k0[r] = k0(2 + r);
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r) p.k1[r] = k1(3 + r);
+    p.pad[0] = p.pad[1] = p.pad[2] = 0;
+    return p;
+}
+
+__device__ __forceinline__ uint4 rng_block(const RngPlan& p, uint32_t block) {
+    auto mul = [](uint32_t x, uint32_t m) { return static_cast<unsigned long long>(x) * m; };
+    unsigned long long a = mul(block, 0xD2511F53u);
+    unsigned long long b = mul(static_cast<uint32_t>(a >> 32) ^ p.c[0], 0xCD9E8D57u);
+    const uint32_t x2 = static_cast<uint32_t>(a) ^ p.c[2], x1 = static_cast<uint32_t>(b);
+    a = mul(static_cast<uint32_t>(b >> 32) ^ p.c[1], 0xD2511F53u);
+    b = mul(x2, 0xCD9E8D57u);
+    uint32_t c0 = static_cast<uint32_t>(b >> 32) ^ x1 ^ p.k0[0], c1 = static_cast<uint32_t>(b);
+    uint32_t c2 = static_cast<uint32_t>(a >> 32) ^ p.c[3], c3 = static_cast<uint32_t>(a);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        a = mul(c0, 0xD2511F53u);
+        b = mul(c2, 0xCD9E8D57u);
+        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ p.k0[1 + r];
+        c1 = static_cast<uint32_t>(b);
+        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ p.k1[r];
+        c3 = static_cast<uint32_t>(a);
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
 // Whole words below steps << 16 are those whose high field is below steps (steps < 65536).
 __device__ __forceinline__ bool keep_high(uint32_t w, uint32_t steps) { return w < (steps << 16); }
 __device__ __forceinline__ bool keep_low(uint32_t w, uint32_t steps) { return (w << 16) < (steps << 16); }
 
-// Keep masks of the eight elements of one block: word j holds 0xffff in the half of each kept element
-// 2 j (low half) and 2 j + 1 (high half).
-__device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long long block, uint32_t steps) {
-    const uint4 w = rng_block(s, block);
-    auto masks = [steps](uint32_t v) { return (keep_high(v, steps) ? 0xffff0000u : 0u) | (keep_low(v, steps) ? 0x0000ffffu : 0u); };
-    return make_uint4(masks(w.x), masks(w.y), masks(w.z), masks(w.w));
-}
-
+// Whether masks of eight 16-bit elements (all bits of a kept one) keep element i.
 __device__ __forceinline__ bool keep_of(const uint4& m, int i) {
     const uint32_t w = i < 2 ? m.x : (i < 4 ? m.y : (i < 6 ? m.z : m.w));
     return ((w >> (16 * (i & 1))) & 1u) != 0u;
@@ -178,6 +219,13 @@ __device__ __forceinline__ void drop_words(uint4& a, uint4& b, const uint4& bits
     drop(a.z, a.w, bits.y);
     drop(b.x, b.y, bits.z);
     drop(b.z, b.w, bits.w);
+}
+
+// Masks of an octet's eight elements, 16 bits each, all ones where the element is kept.
+__device__ __forceinline__ uint4 keep_masks(const RngState& s, unsigned long long block, uint32_t steps) {
+    uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+    drop_words(m, rng_block(s, block), steps);
+    return m;
 }
 
 }  // namespace na

@@ -208,30 +208,31 @@ __device__ __forceinline__ void row_grad(float (&v)[NV], const float (&g)[NV], f
     if (NV % 2) v[NV - 1] = v[NV - 1] * a * (g[NV - 1] - q);
 }
 
-// Zeros the dropped places of a tile in shared memory: octet o of the tile is block block0 + o of the tensor.  Several
-// octets at a time: a block's seven rounds are one chain of dependent instructions.
+// Zeros the dropped places of a tile in shared memory: octet o of the tile is block block0 + o of the tensor.
+template <typename T, typename Bits>
+__device__ __forceinline__ void drop_octets(unsigned char* tile, uint32_t octets, uint32_t steps, Bits bits) {
+    constexpr int C = sizeof(T) == 4 ? 2 : 1;
+    for (uint32_t o = threadIdx.x; o < octets; o += kWinThreads) {
+        uint4* at = reinterpret_cast<uint4*>(tile) + C * o;
+        uint4 d[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) d[c] = at[c];
+        if constexpr (C == 2) drop_words(d[0], d[1], bits(o), steps);
+        else drop_words(d[0], bits(o), steps);
+#pragma unroll
+        for (int c = 0; c < C; ++c) at[c] = d[c];
+    }
+}
 template <typename T>
-__device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, unsigned long long block0, const RngState& rng,
-                                          uint32_t steps) {
-    constexpr int U = 1, C = sizeof(T) == 4 ? 2 : 1;
-    uint4* at = reinterpret_cast<uint4*>(tile);
-    for (uint32_t o = threadIdx.x; o < octets; o += U * kWinThreads) {
-        uint4 r[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = rng_block(rng, block0 + o + u * kWinThreads);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t i = o + u * kWinThreads;
-            if (i < octets) {
-                uint4 d[C];
-#pragma unroll
-                for (int c = 0; c < C; ++c) d[c] = at[C * i + c];
-                if constexpr (C == 2) drop_words(d[0], d[1], r[u], steps);
-                else drop_words(d[0], r[u], steps);
-#pragma unroll
-                for (int c = 0; c < C; ++c) at[C * i + c] = d[c];
-            }
-        }
+__device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, unsigned long long block0, const RngPlan* plan,
+                                          const unsigned long long* state, uint32_t steps) {
+    if (block0 + octets <= (1ull << 32)) {
+        const RngPlan p = *plan;
+        const uint32_t first = static_cast<uint32_t>(block0);
+        drop_octets<T>(tile, octets, steps, [&](uint32_t o) { return rng_block(p, first + o); });
+    } else {
+        const RngState rng = rng_load(state);
+        drop_octets<T>(tile, octets, steps, [&](uint32_t o) { return rng_block(rng, block0 + o); });
     }
 }
 
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
     constexpr int kRows = kWinThreads / L;   // rows of a pass: even, so a lane's place in its row is the same in every pass
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxStages];
+    __shared__ __align__(16) RngPlan plan;
     __shared__ int issued, lost;   // thread 0's: tiles loaded; the first one whose copy did not land in time (-1: none)
     const uint32_t buf = static_cast<uint32_t>(p.tile) * p.K * sizeof(T);   // a multiple of 16
     const uint32_t stage = NB * buf;
@@ -271,9 +273,8 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
         long long t = blockIdx.x;
         for (int s = 0; s < p.stages - 1 && t < p.tiles; ++s, t += gridDim.x) load(t, s);
     }
-    RngState rng{};
     const bool dropping = p.drop.state != nullptr;
-    if (dropping) rng = rng_load(p.drop.state);
+    if (dropping && threadIdx.x == 32) plan = rng_plan(rng_load(p.drop.state));
     const int l = threadIdx.x & (L - 1), r0 = threadIdx.x / L;
     const int words = N == 2 ? (p.K + 1) / 2 : p.K, last_word = l + L * (J - 1);
     const uint32_t e0 = static_cast<uint32_t>(r0) * p.K, pass_words = static_cast<uint32_t>(kRows) * p.K / N;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
         }
         const unsigned long long block0 = static_cast<unsigned long long>(row0) * p.K / 8;   // row0 is a multiple of 8
         if (BWD && dropping) {
-            drop_tile<T>(tile + (NB - 1) * buf, (elems + 7) / 8, block0, rng, p.drop.steps);
+            drop_tile<T>(tile + (NB - 1) * buf, (elems + 7) / 8, block0, &plan, p.drop.state, p.drop.steps);
             __syncthreads();
         }
         uint32_t* s1 = reinterpret_cast<uint32_t*>(tile) + a.at;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
         }
         if (!BWD && dropping) {
             __syncthreads();
-            drop_tile<T>(tile, (elems + 7) / 8, block0, rng, p.drop.steps);
+            drop_tile<T>(tile, (elems + 7) / 8, block0, &plan, p.drop.state, p.drop.steps);
         }
         fence_proxy_async_smem();
         __syncthreads();

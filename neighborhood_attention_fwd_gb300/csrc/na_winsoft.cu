@@ -45,28 +45,28 @@ __global__ void __launch_bounds__(kThreads) head_sum_kernel(const float* in, lon
     }
 }
 
-// Dropout of a tensor: y = gain x where the generator keeps the element, else 0 (y may be x).  A thread takes
-// kOct octets of a block's run, loads them all, then draws.
+// Dropout of a tensor: y = gain x where the generator keeps the element, else 0 (y may be x).  A thread takes kOct octets of
+// a block's run: it loads them all, works out the generator's constants meanwhile, then draws.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, long long n, Dropout d) {
+constexpr int kOct = sizeof(T) == 4 ? 2 : 4;
+
+template <typename T, typename Bits>
+__device__ __forceinline__ void dropout_run(const T* x, T* y, long long n, const Dropout& d, long long o0, Bits bits) {
     using E = Elem<T>;
-    constexpr int C = sizeof(T) == 4 ? 2 : 1, V = E::EPC, kOct = 4 / C;
-    const unsigned long long o0 = static_cast<unsigned long long>(blockIdx.x) * (kThreads * kOct) + threadIdx.x;
-    RngState rng{};
-    if (d.state) rng = rng_load(d.state);
-    uint4 r[kOct][C];
+    constexpr int C = sizeof(T) == 4 ? 2 : 1, V = E::EPC;
+    uint4 r[kOct<T>][C];
 #pragma unroll
-    for (int j = 0; j < kOct; ++j) {
-        const unsigned long long o = o0 + static_cast<unsigned>(j) * kThreads;
-        if (static_cast<long long>(o * 8 + 8) <= n)
+    for (int j = 0; j < kOct<T>; ++j) {
+        const long long o = o0 + j * kThreads;
+        if (o * 8 + 8 <= n)
 #pragma unroll
             for (int c = 0; c < C; ++c) r[j][c] = ld_stream(x + o * 8 + c * V);
     }
+    const auto draw = bits();
 #pragma unroll
-    for (int j = 0; j < kOct; ++j) {
-        const unsigned long long o = o0 + static_cast<unsigned>(j) * kThreads;
-        if (static_cast<long long>(o * 8) >= n) continue;
-        if (static_cast<long long>(o * 8 + 8) <= n) {
+    for (int j = 0; j < kOct<T>; ++j) {
+        const long long o = o0 + j * kThreads;
+        if (o * 8 + 8 <= n) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float f[V];
@@ -76,18 +76,35 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, lon
                 r[j][c] = E::pack(f);
             }
             if (d.state) {
-                if constexpr (C == 2) drop_words(r[j][0], r[j][1], rng_block(rng, o), d.steps);
-                else drop_words(r[j][0], rng_block(rng, o), d.steps);
+                if constexpr (C == 2) drop_words(r[j][0], r[j][1], draw(o), d.steps);
+                else drop_words(r[j][0], draw(o), d.steps);
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) st_stream(y + o * 8 + c * V, r[j][c]);
-        } else {
-            const uint4 m = d.state ? keep_masks(rng, o, d.steps) : make_uint4(~0u, ~0u, ~0u, ~0u);
-            for (int e = 0; o * 8 + e < static_cast<unsigned long long>(n); ++e) {
+        } else if (o * 8 < n) {   // the tensor ends inside this octet
+            uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (d.state) drop_words(m, draw(o), d.steps);
+            for (int e = 0; o * 8 + e < n; ++e) {
                 const float v = E::get(x[o * 8 + e]) * d.gain;
                 y[o * 8 + e] = E::put(keep_of(m, e) ? v : 0.f);
             }
         }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, long long n, Dropout d) {
+    const long long first = static_cast<long long>(blockIdx.x) * (kThreads * kOct<T>);
+    const RngState rng = d.state ? rng_load(d.state) : RngState{};
+    if (first + kThreads * kOct<T> <= (1LL << 32)) {
+        dropout_run(x, y, n, d, first + threadIdx.x, [&] {
+            const RngPlan plan = rng_plan(rng);
+            return [plan](long long o) { return rng_block(plan, static_cast<uint32_t>(o)); };
+        });
+    } else {
+        dropout_run(x, y, n, d, first + threadIdx.x, [&] {
+            return [rng](long long o) { return rng_block(rng, static_cast<unsigned long long>(o)); };
+        });
     }
 }
 
@@ -160,7 +177,7 @@ na_status na_dropout(const void* x, void* y, int64_t n, double p, const void* rn
     if (!ptr_aligned(x, 16) || !ptr_aligned(y, 16) || !ptr_aligned(rng, 8)) return NA_ERR_ALIGNMENT;
     const Span sx{x, n * elem_bytes(dtype)}, sy{y, sx.bytes}, sr{rng, 16};
     if (!output_clear(sy, {sx}, {sr})) return NA_ERR_INVALID_ARG;
-    const long long per = 8LL * kThreads * (dtype == NA_FP32 ? 2 : 4), blocks = (n + per - 1) / per;
+    const long long per = 8LL * kThreads * (dtype == NA_FP32 ? kOct<float> : kOct<__half>), blocks = (n + per - 1) / per;
     if (blocks > 0x7fffffffLL) return NA_ERR_UNSUPPORTED;
     const unsigned nb = static_cast<unsigned>(blocks);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
