@@ -238,7 +238,7 @@ __device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, 
 
 // Blocks per multiprocessor that the registers leave room for: the backward holds a row's weights and gradients.
 template <bool DIFF, bool BWD, int J>
-constexpr int win_blocks() { return BWD || DIFF ? 6 : 8; }
+constexpr int win_blocks() { return BWD && DIFF ? 6 : (BWD || DIFF ? 7 : 8); }
 
 template <typename T, bool DIFF, bool BWD, int L, int J>
 __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_kernel(const __grid_constant__ WinParams p) {
