@@ -635,7 +635,7 @@ def _window(x, kernel):
     ndim = len(shape) - 3
     if ndim < 1 or ndim > 3:
         raise ValueError("expected attention weights [B, L_1..L_n, heads, K] with n in 1..3")
-    kernel = (kernel,) * ndim if isinstance(kernel, int) else tuple(kernel)
+    kernel = (kernel,) * ndim if isinstance(kernel, int) else tuple(map(int, kernel))
     if len(kernel) != ndim:
         raise ValueError("kernel needs one entry per spatial axis")
     if shape[-1] != math.prod(kernel):

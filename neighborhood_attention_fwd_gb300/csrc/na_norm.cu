@@ -9,6 +9,8 @@
 // the row: lanes of a warp (rows of up to 64 or 128 chunks), else a block.  The backward's teams walk many rows, so
 // a thread's columns stay the same and the weight gradients accumulate in its registers; a block writes one
 // partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).
+#include <type_traits>
+
 #include "na_block.cuh"
 #include "na_device.cuh"
 
@@ -151,12 +153,12 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*slot)[
     }
 }
 
-// Rows that a team works on at once: their loads are in flight together and their sums share the steps.
-__host__ __device__ constexpr int norm_rows(int J, bool bwd) { return bwd ? (J == 1 ? 2 : 1) : (J == 1 ? 4 : (J == 2 ? 2 : 1)); }
+// Rows that a team of the forward works on at once: their loads are in flight together and their sums share the steps.
+__host__ __device__ constexpr int norm_rows(int J) { return J == 1 ? 4 : (J == 2 ? 2 : 1); }
 
 template <typename T, int V, int J, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_kernel(const NormParams p) {
-    constexpr int R = norm_rows(J, false);
+    constexpr int R = norm_rows(J);
     __shared__ float slots[2][R][32];
     const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1));
     const int team_in_block = BLOCK ? 0 : threadIdx.x / p.team, teams = BLOCK ? 1 : kNormThreads / p.team;
@@ -298,89 +300,157 @@ __device__ __forceinline__ void store_partial(const NormParams& p, float (&dw)[J
     }
 }
 
+// Chunk-wise arithmetic of the backward, H words of one or two columns each: with d = x - mean and g' = dy rstd w the
+// gradient of x is g' - sum g' / C - d rstd^2 sum (g' d) / C.
+template <int V>
+struct Cols {
+    static constexpr int H = V == 1 ? 1 : V / 2;
+    using W = typename std::conditional<V == 1, float, uint64_t>::type;
+    static __device__ __forceinline__ W both(float a) {
+        if constexpr (V == 1) return a;
+        else return pack2(a, a);
+    }
+    static __device__ __forceinline__ W fma(W a, W b, W c) {
+        if constexpr (V == 1) return fmaf(a, b, c);
+        else return fma2(a, b, c);
+    }
+    static __device__ __forceinline__ W mul(W a, W b) {
+        if constexpr (V == 1) return a * b;
+        else return mul2(a, b);
+    }
+    static __device__ __forceinline__ W add(W a, W b) {
+        if constexpr (V == 1) return a + b;
+        else return add2(a, b);
+    }
+    static __device__ __forceinline__ float sum(W a) {
+        if constexpr (V == 1) {
+            return a;
+        } else {
+            float x, y;
+            split2(a, x, y);
+            return x + y;
+        }
+    }
+    static __device__ __forceinline__ void from(const float (&f)[V], W (&w)[H]) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+            if constexpr (V == 1) w[e] = f[e];
+            else w[e] = pack2(f[2 * e], f[2 * e + 1]);
+        }
+    }
+    static __device__ __forceinline__ void to(const W (&w)[H], float (&f)[V]) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+            if constexpr (V == 1) f[e] = w[e];
+            else split2(w[e], f[2 * e], f[2 * e + 1]);
+        }
+    }
+};
+
+// The backward of rows a block wide, and of rows that are not whole chunks.  The next row's loads are issued before this
+// one's sums where that pays for the registers: 2-byte rows of 1024 channels 66% -> 73% of the copy rate, of 4096 58% -> 69%,
+// fp32 rows of 8192 78% -> 89%; fp32 rows of 2048 lose (91% -> 82%).
 template <typename T, int V, int J, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_kernel(const NormParams p) {
-    constexpr int R = norm_rows(J, true);
-    __shared__ float slots[2][2 * R][32];
+    using A = Cols<V>;
+    using W = typename A::W;
+    constexpr int H = A::H;
+    __shared__ float slots[2][2][32];
     extern __shared__ float cols[];   // warp teams: [warp][2][C]
     const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1));
     const int team_in_block = BLOCK ? 0 : threadIdx.x / p.team, teams = BLOCK ? 1 : kNormThreads / p.team;
-    const long long step = static_cast<long long>(gridDim.x) * teams * R;   // a block's rows of one turn follow one another
-    float w[J][V], dw[J][V], db[J][V];
+    const long long step = static_cast<long long>(gridDim.x) * teams;
+    W w[J][H], dw[J][H], db[J][H];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int c = (l + p.team * j) * V;
-        load_weights<V>(c < p.C ? p.w : nullptr, c, w[j], 1.f);   // threads past the row multiply zeros: by ones
+        float f[V];
+        load_weights<V>(c < p.C ? p.w : nullptr, c, f, 1.f);   // threads past the row multiply zeros: by ones
+        A::from(f, w[j]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
+        for (int e = 0; e < H; ++e) dw[j][e] = db[j][e] = 0;
     }
+    constexpr bool AHEAD = V != 4 || J == 4;
+    Chunk<T, V> rx[J], rg[J];
+    float mean = 0.f, rstd = 0.f;
+    auto load = [&](long long r0) {
+        const long long row = min(r0 + team_in_block, p.rows - 1);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const long long at = row * p.C + min((l + p.team * j) * V, p.C - V);
+            rx[j].load(p.x, at);
+            rg[j].load(p.dy, at);
+        }
+        mean = p.mean[row];
+        rstd = p.rstd[row];
+    };
     int turn = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * teams * R; r0 < p.rows; r0 += step, turn ^= 1) {
-        Chunk<T, V> rx[R][J], rg[R][J];
-        float h[R][J][V], g[R][J][V], s[2 * R], mean[R], rstd[R];
+    if (AHEAD) load(static_cast<long long>(blockIdx.x) * teams);
+    for (long long r0 = static_cast<long long>(blockIdx.x) * teams; r0 < p.rows; r0 += step, turn ^= 1) {
+        if (!AHEAD) load(r0);
+        const long long row = r0 + team_in_block;
+        const bool live = row < p.rows;   // whole warps stay together, for the sums
+        W d[J][H], g[J][H], s0 = 0, s1 = 0;
+        const W mm = A::both(-mean), rr = A::both(rstd);
+        const float r2 = rstd * rstd;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const long long row = min(r0 + r * teams + team_in_block, p.rows - 1);
+        for (int j = 0; j < J; ++j) {
+            const bool in = live && (l + p.team * j) * V < p.C;
+            float fx[V], fy[V];
+            rx[j].get(fx);
+            rg[j].get(fy);
+            W y[H];
+            A::from(fx, d[j]);
+            A::from(fy, y);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const long long at = row * p.C + min((l + p.team * j) * V, p.C - V);
-                rx[r][j].load(p.x, at);
-                rg[r][j].load(p.dy, at);
-            }
-            mean[r] = p.mean[row];
-            rstd[r] = p.rstd[row];
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool live = r0 + r * teams + team_in_block < p.rows;
-            s[2 * r] = s[2 * r + 1] = 0.f;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const bool in = live && (l + p.team * j) * V < p.C;
-                rx[r][j].get(h[r][j]);
-                rg[r][j].get(g[r][j]);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    h[r][j][e] = in ? (h[r][j][e] - mean[r]) * rstd[r] : 0.f;
-                    g[r][j][e] = in ? g[r][j][e] : 0.f;
-                    dw[j][e] = fmaf(g[r][j][e], h[r][j][e], dw[j][e]);
-                    db[j][e] += g[r][j][e];
-                    g[r][j][e] *= w[j][e];
-                    s[2 * r] += g[r][j][e];
-                    s[2 * r + 1] = fmaf(g[r][j][e], h[r][j][e], s[2 * r + 1]);
-                }
+            for (int e = 0; e < H; ++e) {
+                if (!in) y[e] = 0;
+                const W yr = A::mul(y[e], rr);
+                d[j][e] = A::add(d[j][e], mm);
+                dw[j][e] = A::fma(yr, d[j][e], dw[j][e]);
+                db[j][e] = A::add(db[j][e], y[e]);
+                g[j][e] = A::mul(yr, w[j][e]);
+                s0 = A::add(s0, g[j][e]);
+                s1 = A::fma(g[j][e], d[j][e], s1);
             }
         }
-        team_sum<2 * R, BLOCK>(s, p.team, slots[turn]);
+        if (AHEAD && r0 + step < p.rows) load(r0 + step);
+        float s[2] = {A::sum(s0), A::sum(s1)};
+        team_sum<2, BLOCK>(s, p.team, slots[turn]);
+        const W k1 = A::both(-s[0] * p.inv_c), k2 = A::both(-r2 * (s[1] * p.inv_c));
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const long long row = r0 + r * teams + team_in_block;
-            const float c1 = s[2 * r] * p.inv_c, c2 = s[2 * r + 1] * p.inv_c;
+        for (int j = 0; j < J; ++j) {
+            const int c = (l + p.team * j) * V;
+            if (live && c < p.C) {
+                W o[H];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int c = (l + p.team * j) * V;
-                if (row < p.rows && c < p.C) {
-                    float d[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) d[e] = (g[r][j][e] - c1 - h[r][j][e] * c2) * rstd[r];
-                    store_chunk<T, V>(p.out, row * p.C + c, d);
-                }
+                for (int e = 0; e < H; ++e) o[e] = A::fma(d[j][e], k2, A::add(g[j][e], k1));
+                float f[V];
+                A::to(o, f);
+                store_chunk<T, V>(p.out, row * p.C + c, f);
             }
         }
     }
-    if (p.partial) store_partial<V, J, BLOCK>(p, dw, db, l, cols);
+    if (!p.partial) return;
+    float fw[J][V], fb[J][V];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        A::to(dw[j], fw[j]);
+        A::to(db[j], fb[j]);
+    }
+    store_partial<V, J, BLOCK>(p, fw, fb, l, cols);
 }
 
-// The backward of warp teams on whole chunks.  A register or two of loads per thread do not keep the memory busy
+// The backward of warp teams on whole chunks (one each, of 4-byte rows up to two).  A register or two of loads per thread do not keep the memory busy
 // beside the accumulators, so x and dy come through a ring of tiles in shared memory (cp.async.bulk; rows are whole
 // chunks, so a tile is one run of bytes): a tile's stage is filled again once every thread has read it.  The
 // tile's statistics are read a tile ahead.
 constexpr int kNormStages = 2, kNormTileBytes = 8 * 1024, kNormTileRows = kNormThreads;   // a thread reads a row's statistics
 // Blocks per multiprocessor that the registers leave room for.
-__host__ __device__ constexpr int norm_ring_blocks(int J, int V) { return J == 1 ? 4 : (V == 8 ? 2 : 3); }
+__host__ __device__ constexpr int norm_ring_blocks(int J) { return J == 1 ? 4 : 3; }
 
 template <typename T, int J>
-__global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J, Elem<T>::EPC)) norm_bwd_ring_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ring_kernel(const NormParams p) {
     constexpr int V = Elem<T>::EPC;
     extern __shared__ __align__(128) unsigned char smem[];   // [stage][x, dy][tile]; then the columns of store_partial
     __shared__ uint64_t full[kNormStages];
@@ -545,8 +615,9 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
     const int V = C % (16 / es) == 0 ? 16 / es : 1;
     n.vec = V > 1;
     const int chunks = (C + V - 1) / V;
-    // chunks per thread of a warp team: the backward keeps weights and two accumulators per column besides
-    const int warp_j = n.vec ? (bwd ? 2 : 4) : (bwd ? 2 : 4);
+    // Chunks per thread of a warp team, at most.  The backward keeps weights and two accumulators per column besides: 2-byte
+    // rows of 264 to 512 channels run faster as blocks of one warp with two chunks (512 channels: 64% -> 80% of the copy rate).
+    const int warp_j = !bwd ? 4 : (V == 8 ? 1 : 2);
     n.block = chunks > 32 * warp_j;
     if (!n.block) {
         n.team = 1;
@@ -554,12 +625,12 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
         n.j = 1;
         while (n.j * n.team < chunks) n.j *= 2;
         if (!n.vec) n.j = bwd ? 2 : (n.j > 1 ? 4 : 1);
-        const long long per = static_cast<long long>(kNormThreads / n.team) * norm_rows(n.j, bwd), need = (rows + per - 1) / per;
+        const long long per = static_cast<long long>(kNormThreads / n.team) * (bwd ? 1 : norm_rows(n.j)), need = (rows + per - 1) / per;
         const long long most = static_cast<long long>(sms) * (bwd ? 3 : 16);
         n.blocks = static_cast<int>(need < most ? need : most);
         if (bwd && n.vec) {   // tiles of whole passes of the teams; fewer where the grid is small
             n.ring = true;
-            const int teams = kNormThreads / n.team, per_sm = norm_ring_blocks(n.j, V);
+            const int teams = kNormThreads / n.team, per_sm = norm_ring_blocks(n.j);
             int passes = kNormTileBytes / (teams * C * es);
             if (passes * teams > kNormTileRows) passes = kNormTileRows / teams;   // at least 1
             passes = passes < 1 ? 1 : passes;
@@ -607,12 +678,13 @@ na_status launch_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
     constexpr int V = Elem<T>::EPC;
     if (n.vec && !n.block) {
         if (n.j == 1) return run_norm<T, V, 1, false, BWD>(p, n, s);
-        if (n.j == 2) return run_norm<T, V, 2, false, BWD>(p, n, s);
+        if constexpr (!BWD || V == 4)
+            if (n.j == 2) return run_norm<T, V, 2, false, BWD>(p, n, s);
         if constexpr (!BWD) return run_norm<T, V, 4, false, BWD>(p, n, s);
     } else if (n.vec) {
         if (n.j == 1) return run_norm<T, V, 1, true, BWD>(p, n, s);
         if (n.j == 2) return run_norm<T, V, 2, true, BWD>(p, n, s);
-        return run_norm<T, V, 4, true, BWD>(p, n, s);
+        if constexpr (V == 4) return run_norm<T, V, 4, true, BWD>(p, n, s);   // over 4096 channels of 4 bytes
     } else if (!n.block) {
         if constexpr (BWD) return run_norm<T, 1, 2, false, BWD>(p, n, s);
         else return n.j == 1 ? run_norm<T, 1, 1, false, BWD>(p, n, s) : run_norm<T, 1, 4, false, BWD>(p, n, s);

@@ -299,6 +299,8 @@ WIN = [
     ("fp32", 1, (7, 7, 8), 1, (7, 7, 7)), ("bf16", 1, (767,), 1, (767,)), ("bf16", 1, (765,), 1, (765,)),
     ("bf16", 1, (1031,), 2, (1001,)), ("fp32", 1, (400,), 3, (399,)), ("fp32", 1, (383,), 1, (383,)), ("fp32", 1, (385,), 1, (385,)),
     ("fp16", 1, (5001,), 1, (4999,)), ("bf16", 3, (50, 41), 300, (1, 3)),
+    ("fp32", 1, (9, 9, 9), 1, (9, 9, 9)), ("fp32", 1, (767,), 1, (767,)), ("fp32", 1, (770,), 1, (769,)),
+    ("fp16", 1, (9, 41), 3, (9, 9)), ("fp32", 1, (45,), 5, (11,)), ("bf16", 1, (1200,), 2, (33,)), ("fp16", 1, (700,), 3, (121,)),
 ]
 WIN_IDS = [str(c) for c in WIN]
 
@@ -462,6 +464,33 @@ def test_on_another_stream(cuda_lib):
     na.na_diff_softmax(tmp, x, lam, tmp, (9, 9), 0.1, rng, stream=s)  # a given stream, after the call before it
     s.synchronize()
     assert torch.equal(y, ref) and torch.equal(tmp, ref)
+
+
+def test_workspaces_on_another_stream(cuda_lib):
+    """The gradients that sum over rows, on a given stream (the library allocates there) and with the caller's
+    workspace, give what the current stream gives."""
+    na = cuda_lib
+    x1, x2, dy = (randn((2, 30, 41, 8, 45), "bf16", i).cuda() for i in range(3))
+    lam, w = torch.rand(8, device="cuda"), torch.rand(360, device="cuda")
+    rows = x1.view(-1, 360)
+    mean, rstd = torch.empty(rows.shape[0], device="cuda"), torch.empty(rows.shape[0], device="cuda")
+    y = torch.empty_like(rows)
+    na.na_layernorm(rows, w, None, y, mean, rstd)
+
+    def both(**kw):
+        o = [torch.empty_like(x1), torch.empty_like(x1), torch.empty_like(lam), torch.empty_like(rows), torch.empty_like(w),
+             torch.empty_like(w)]
+        torch.cuda.synchronize()
+        na.na_diff_softmax_bwd(x1, x2, lam, dy, o[0], o[1], o[2], (5, 9), 0.1, rng, **kw)
+        na.na_layernorm_bwd(dy.view(-1, 360), rows, w, mean, rstd, o[3], o[4], o[5], **kw)
+        torch.cuda.synchronize()
+        return o
+
+    rng = rng_state()
+    ref = both()
+    s = torch.cuda.Stream()
+    for o in (both(stream=s), both(stream=s.cuda_stream)):
+        assert all(torch.equal(a, b) for a, b in zip(o, ref))
 
 
 def test_captured_calls_read_the_generator_anew(cuda_lib):
