@@ -30,7 +30,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxStages = 3;
-constexpr int kStageBytes = 12 * 1024;   // a tile of every input, about
+constexpr int kStageBytes[2] = {12 * 1024, 21 * 1024};   // a tile of every input, about; with dropout
 constexpr int kLongThreads = 128;   // block of a row that no tile holds
 
 // A row's words: 4 bytes, one or two weights.
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
         issued = 0;
         lost = -1;
         long long t = blockIdx.x;
-        for (int s = 0; s < p.stages - 1 && t < p.tiles; ++s, t += gridDim.x) load(t, s);
+        for (int s = 0; s < 2 && t < p.tiles; ++s, t += gridDim.x) load(t, s);
     }
     const bool dropping = p.drop.state != nullptr;
     if (dropping && threadIdx.x == 32) plan = rng_plan(rng_load(p.drop.state));
@@ -319,8 +319,18 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
             __syncthreads();
         }
         const unsigned long long block0 = static_cast<unsigned long long>(row0) * p.K / 8;   // row0 is a multiple of 8
+        // With dropout there are two stages: the tile before this one leaves its buffer during the first of the tile's two
+        // phases, and the next one arrives during the second.
+        auto refill = [&] {
+            if (threadIdx.x == 0 && lost < 0 && t >= gridDim.x) {
+                tma_store_wait_read();
+                const long long next = t + gridDim.x;
+                if (next < p.tiles) load(next, s ^ 1);
+            }
+        };
         if (BWD && dropping) {
             drop_tile<T>(tile + (NB - 1) * buf, (elems + 7) / 8, block0, &plan, p.drop.state, p.drop.steps);
+            refill();
             __syncthreads();
         }
         uint32_t* s1 = reinterpret_cast<uint32_t*>(tile) + a.at;
@@ -389,6 +399,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
             if (head >= heads) head -= heads;
         }
         if (!BWD && dropping) {
+            refill();
             __syncthreads();
             drop_tile<T>(tile, (elems + 7) / 8, block0, &plan, p.drop.state, p.drop.steps);
         }
@@ -406,10 +417,12 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
                 for (int i = 0; i < NO; ++i) bulk_store(out[i], tile + i * buf, bulk);
             }
             tma_store_commit();
-            // the tile before this one has left its buffer: the tile stages - 1 on from here takes it
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            const long long next = t + static_cast<long long>(gridDim.x) * (p.stages - 1);
-            if (next < p.tiles) load(next, s == 0 ? p.stages - 1 : s - 1);
+            // without, three: the tile before this one has left its buffer, the second tile from here takes it
+            if (!dropping) {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                const long long next = t + 2LL * gridDim.x;
+                if (next < p.tiles) load(next, s == 0 ? 2 : s - 1);
+            }
         }
         if (++s == p.stages) {
             s = 0;
@@ -604,14 +617,15 @@ na_status run_win(WinParams& p, cudaStream_t s) {
     // a tile is whole passes of the threads, about kStageBytes for all inputs; fewer passes where the grid is small
     constexpr int kRows = kWinThreads / L;
     const int row = p.K * static_cast<int>(sizeof(T));
-    int passes = kStageBytes / static_cast<int>(NB * kRows * row);
+    const bool dropping = p.drop.state != nullptr;
+    int passes = kStageBytes[dropping] / static_cast<int>(NB * kRows * row);
     passes = passes < 1 ? 1 : passes;
     while (passes > 1 && p.rows / (static_cast<long long>(kRows) * passes) < 8 * kSms) --passes;
     p.tile = kRows * passes;
     if (p.tile % 8 != 0) p.tile = kRows * (passes += passes & 1);   // 32 lanes: four rows a pass
     p.tiles = (p.rows + p.tile - 1) / p.tile;
     const uint32_t stage = NB * static_cast<uint32_t>(p.tile) * row;
-    p.stages = 3;
+    p.stages = dropping ? 2 : 3;
     const size_t smem = static_cast<size_t>(p.stages) * stage;
     const auto kernel = win_kernel<T, DIFF, BWD, L, J>;
     if (smem > 40 * 1024 &&   // 48 KB without asking, static shared memory included
