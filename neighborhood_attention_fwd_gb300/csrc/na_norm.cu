@@ -780,22 +780,20 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
     p.tile = n.tile;
     p.tiles = n.tiles;
     p.wait_ns = wait_limit_ns();
-    if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void* ws = nullptr;
+    const size_t need = norm_workspace(n, C);
+    void* ws = dw ? workspace : nullptr;
     bool owned = false;
-    if (dw) {
-        const size_t need = norm_workspace(n, C);
-        if (workspace) {
-            if (workspace_bytes < need) return NA_ERR_WORKSPACE;
-            if (!ptr_aligned(workspace, 16)) return NA_ERR_ALIGNMENT;
-            const Span sws{workspace, static_cast<long long>(need)};
-            if (!output_clear(sws, {}, {sx, sdy, sdx, sw, sm, sr, sdw, sdb})) return NA_ERR_INVALID_ARG;
-            ws = workspace;
-        } else {
-            if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
-            owned = true;
-        }
+    if (ws) {
+        if (workspace_bytes < need) return NA_ERR_WORKSPACE;
+        if (!ptr_aligned(ws, 16)) return NA_ERR_ALIGNMENT;
+        const Span sws{ws, static_cast<long long>(need)};
+        if (!output_clear(sws, {}, {sx, sdy, sdx, sw, sm, sr, sdw, sdb})) return NA_ERR_INVALID_ARG;
+    }
+    if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
+    if (dw && !ws) {
+        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+        owned = true;
     }
     p.partial = static_cast<float*>(ws);
     st = dispatch_norm<true>(p, n, dtype, s);
