@@ -166,10 +166,11 @@ na_status na_device_status(void* stream, uint32_t* raw);
 
 /*
  * Test hook for the bounded device-side waits (the pages have no counterpart; it exists so that the
- * timeout path can be exercised without faulting a GPU).  For every later launch of the tensor-core
- * kernels (NA_BF16, NA_FP16) and of the other kernels with waits in this process it sets the time limit of one wait to limit_ns
- * (100 us .. 10 s; 0 restores the 2 s default) and, with withhold = 1, makes the tensor-core kernels' first CTA skip the
- * copy of its first halo chunk, so that the waits on that chunk run out.  Such a call leaves its
+ * timeout path can be exercised without faulting a GPU).  For every later launch in this process of the
+ * tensor-core kernels (NA_BF16, NA_FP16) and of those that na_layernorm_bwd, na_softmax_dropout and
+ * na_diff_softmax and their gradients fetch tiles with, it sets the time limit of one wait to limit_ns
+ * (100 us .. 10 s; 0 restores the 2 s default) and, with withhold = 1, makes the first CTA skip the
+ * copy of its first halo chunk or tile, so that the waits on it run out.  Such a call leaves its
  * outputs incomplete and na_device_status() then reports NA_ERR_TIMEOUT; the kernels stop issuing
  * work, let the copies already issued land, free their tensor memory and return.  Call it again with
  * (0, 0) to restore normal launches.  Process-wide; for tests only.

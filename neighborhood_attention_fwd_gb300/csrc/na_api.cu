@@ -19,6 +19,7 @@
 namespace na {
 na_status device_status_word(unsigned** out);
 unsigned long long wait_limit_ns();
+uint32_t wait_withhold();
 uint32_t tc_smem_bytes(int which, const TilePlan& pl, int D);
 int tc_tmem_cols(int which, int D);
 int tc_max_nc(int which, int D, int sbufs);
@@ -551,6 +552,7 @@ void unfused_tma_maps(na::UnfParams& p, int B, const void* src, const void* w, n
 namespace na {
 na_status device_status_word(unsigned** out) { return status_ptr(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
+uint32_t wait_withhold() { return g_withhold.load(); }
 }  // namespace na
 
 extern "C" {

@@ -14,9 +14,11 @@
 
 namespace na {
 
-// Device status word of the current device, and the time limit of one bounded wait (na_api.cu).
+// Device status word of the current device, the time limit of one bounded wait, and the test hook that withholds a copy
+// (na_api.cu).
 na_status device_status_word(unsigned** out);
 unsigned long long wait_limit_ns();
+uint32_t wait_withhold();
 
 // ---------------------------------------------------------------------------------------------
 // Host: argument checks

@@ -39,6 +39,7 @@ struct NormParams {
     int tile;
     unsigned* err;         // ring: device status word
     unsigned long long wait_ns;
+    uint32_t withhold;     // ring: test hook, block 0 leaves out its first copy
 };
 
 // A chunk: V elements, 16 bytes, or one element where a row is not whole chunks.  Loads are unconditional (places past
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ri
         const uint32_t bytes = row_bytes * rows_of(t);
         const long long off = t * static_cast<long long>(buf);
         mbar_arrive_expect_tx(&full[s], 2 * bytes);
+        if (p.withhold && blockIdx.x == 0 && issued == 1) return;   // test hook: the first copy never lands
         bulk_load(smem + (2 * s) * buf, static_cast<const char*>(p.x) + off, bytes, &full[s]);
         bulk_load(smem + (2 * s + 1) * buf, static_cast<const char*>(p.dy) + off, bytes, &full[s]);
     };
@@ -780,6 +782,7 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
     p.tile = n.tile;
     p.tiles = n.tiles;
     p.wait_ns = wait_limit_ns();
+    p.withhold = wait_withhold();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t need = norm_workspace(n, C);
     void* ws = dw ? workspace : nullptr;

@@ -103,7 +103,7 @@ __device__ __forceinline__ void fill_angles(const RopeParams& p, float2* tab, co
 }
 
 // Units of whole chunks: one chunk of pairs (2 i, 2 i + 1), or two chunks of pairs (i, i + rot/2).  A
-// thread keeps four units in flight; the first four are loaded before the angles are computed.
+// thread keeps four or eight units in flight; the first ones are loaded before the angles are computed.
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using E = Elem<T>;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tt;
     const int tt = static_cast<int>(min(static_cast<long long>(p.tt), p.tokens - tok0));
     const uint32_t nq = static_cast<uint32_t>(tt) * p.upt[0], n = nq + static_cast<uint32_t>(tt) * p.upt[1];
-    const uint32_t u = threadIdx.x & ((1u << p.lu) - 1u);   // 256 threads are whole head rows
+    const uint32_t u = threadIdx.x & ((1u << p.lu) - 1u);   // a block's threads are whole head rows
     const int ca = INTER ? static_cast<int>(u) : p.ua[u], cb = INTER ? 0 : p.ub[u];
     const int p0 = INTER ? static_cast<int>(u) * NP : (p.up[u] == 0xff ? p.np : p.up[u]);
     const uint4* xs[2];

@@ -23,6 +23,7 @@ struct WinParams {
     Dropout drop;
     unsigned* err;         // device status word
     unsigned long long wait_ns;
+    uint32_t withhold;     // test hook: block 0 leaves out its first copy
 };
 
 // Kernels of one type and form: `diff` the difference of two maps, `bwd` the gradients.

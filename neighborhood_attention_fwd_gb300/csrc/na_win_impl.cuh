@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_k
         const long long off = t * static_cast<long long>(buf);
         unsigned char* to = smem + s * stage;
         mbar_arrive_expect_tx(&full[s], NB * bulk);
-        if (bulk != 0) {
+        if (bulk != 0 && !(p.withhold && blockIdx.x == 0 && issued == 1)) {   // test hook: the first copy never lands
             bulk_load(to, static_cast<const char*>(p.x1) + off, bulk, &full[s]);
             if (DIFF) bulk_load(to + buf, static_cast<const char*>(p.x2) + off, bulk, &full[s]);
             if (BWD) bulk_load(to + (NB - 1) * buf, static_cast<const char*>(p.dy) + off, bulk, &full[s]);

@@ -133,6 +133,7 @@ na_status win_common(int B, int ndim, const int* spatial, int heads, const int* 
     p.K = static_cast<int>(K);
     p.heads = heads;
     p.wait_ns = wait_limit_ns();
+    p.withhold = wait_withhold();
     return NA_OK;
 }
 

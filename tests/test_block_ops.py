@@ -545,6 +545,52 @@ def test_captured_calls_read_the_generator_anew(cuda_lib):
     status_ok(na)
 
 
+@pytest.mark.parametrize("which", ["soft", "soft_bwd", "diff", "diff_bwd", "norm_bwd"])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_a_copy_that_never_lands_is_reported(which, p, cuda_lib):
+    """The test hook leaves out one tile's copy: the wait for it runs out after 2 ms, the kernel ends and reports it
+    (sites 9 and 10), and the next launch is clean."""
+    na = cuda_lib
+    shape, kernel = (1, 64, 64, 4, 25), (5, 5)
+    x1, x2, dy = (randn(shape, "bf16", i).cuda() for i in range(3))
+    lam, w = torch.rand(4, device="cuda"), torch.rand(100, device="cuda")
+    rows = randn((4096, 96), "bf16", 5).cuda()
+    g = randn((4096, 96), "bf16", 6).cuda()
+    mean, rstd = torch.zeros(4096, device="cuda"), torch.ones(4096, device="cuda")
+    rng = rng_state()
+
+    def call():
+        e = torch.empty_like
+        if which == "soft":
+            o = [e(x1)]
+            na.na_softmax_dropout(x1, o[0], kernel, p, rng)
+        elif which == "soft_bwd":
+            o = [e(x1)]
+            na.na_softmax_dropout_bwd(x1, dy, o[0], kernel, p, rng)
+        elif which == "diff":
+            o = [e(x1)]
+            na.na_diff_softmax(x1, x2, lam, o[0], kernel, p, rng)
+        elif which == "diff_bwd":
+            o = [e(x1), e(x1), e(lam)]
+            na.na_diff_softmax_bwd(x1, x2, lam, dy, *o, kernel, p, rng)
+        else:
+            o = [e(rows), e(w[:96]), e(w[:96])]
+            na.na_layernorm_bwd(g, rows, None, mean, rstd, *o)
+        return o
+
+    ref = call()
+    status_ok(na)
+    na.na_debug_wait_hook(2_000_000, True)
+    try:
+        call()
+        st, raw = na.na_device_status()
+    finally:
+        na.na_debug_wait_hook(0, False)
+    assert st == 5 and raw in (0x5009, 0x500A), (st, hex(raw))
+    assert all(torch.equal(a, b) for a, b in zip(call(), ref))
+    status_ok(na)
+
+
 def test_results_do_not_depend_on_the_run(cuda_lib):
     na = cuda_lib
     shape, kernel = (2, 50, 41, 8, 45), (5, 9)
