@@ -279,6 +279,74 @@ def test_dropout(dtype, n, p, cuda_lib):
         assert torch.equal(y.cpu(), x)
 
 
+def factor_at(first, n, p):
+    """dropout_factor's values of elements first .. first + n - 1 (first a multiple of 8)."""
+    i = np.arange(first // 8, (first + n + 7) // 8, dtype=np.uint64)
+    low, shift = np.uint64(0xFFFFFFFF), np.uint64(32)
+    full = lambda v: np.full(len(i), v, np.uint64)
+    words = ob.philox(np.stack([i & low, i >> shift, full(OFFSET & 0xFFFFFFFF), full(OFFSET >> 32)], 1),
+                      (SEED & 0xFFFFFFFF, SEED >> 32), 7)
+    fields = np.empty((len(i), 8), dtype=np.uint64)
+    fields[:, 0::2], fields[:, 1::2] = words & np.uint64(0xFFFF), words >> np.uint64(16)
+    steps = int(math.floor((1 - p) * 65536 + 0.5))
+    return np.where(fields.reshape(-1)[:n] < steps, 65536.0 / steps, 0.0)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("n", [(1 << 32) + 1003, (1 << 35) + 12347])
+def test_dropout_past_32_bits(n, cuda_lib):
+    """Element indices past 2^32, and generator blocks past 2^32, in place."""
+    na = cuda_lib
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("not enough free device memory")
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    na.na_dropout(x, x, 0.3, rng_state())
+    status_ok(na)
+    for at in (0, (1 << 32) - 64, (n - 4096) // 8 * 8):
+        got = x[at:at + 4096]
+        ref = factor_at(at, got.numel(), 0.3)
+        close("y", got, ref, 2 * E * ref, torch.bfloat16)
+        assert np.array_equal(f64(got) == 0, ref == 0)
+
+
+@pytest.mark.slow
+def test_rows_past_32_bits(cuda_lib):
+    """Weights and channels at offsets past 2^32 elements: the first rows, those around the border and the last ones."""
+    na = cuda_lib
+    K, heads = 81, 8
+    L = (1 << 32) // (K * heads) + 1001
+    rows = (0, (1 << 32) // (K * heads) - 1, L - 3)
+    x = torch.full((1, L, heads, K), 0.5, dtype=torch.bfloat16, device="cuda")
+    for r in rows:
+        x[0, r:r + 3].normal_()
+    before = [f64(x[0, r:r + 3]) for r in rows]
+    na.na_softmax_dropout(x, x, (K,), 0.3, rng_state())
+    status_ok(na)
+    for r, b in zip(rows, before):
+        first = r * heads * K // 8 * 8
+        f = factor_at(first, 3 * heads * K + 8, 0.3)[r * heads * K - first:][:3 * heads * K].reshape(3, heads, K)
+        s = ob.softmax(b)
+        ref = ob.softmax_dropout(b, f)
+        close("y", x[0, r:r + 3], ref, np.abs(ref) * map_error(b, s), torch.bfloat16)
+    C = 256
+    x = x.view(-1)[:(1 << 32) + 3 * C].view(-1, C)
+    n = x.shape[0]
+    x.normal_()
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd, db, dw = (torch.empty(m, device="cuda") for m in (n, n, C, C))
+    na.na_layernorm(x, None, None, y, mean, rstd)
+    na.na_layernorm_bwd(y, x, None, mean, rstd, dx, dw, db)
+    status_ok(na)
+    for r in (0, (1 << 32) // C - 1, n - 3):
+        X = f64(x[r:r + 3])
+        ry, _, rr = ob.layernorm(X, None, None, float(np.float32(1e-5)))
+        slack = 2 * DEPTH * E * (1 + np.abs(ry)) * (1 + rr[:, None])
+        close("y", y[r:r + 3], ry, slack, torch.bfloat16)
+        dy = f64(y[r:r + 3])
+        rdx = ob.layernorm_bwd(dy, X, None, f64(mean[r:r + 3]), f64(rstd[r:r + 3]))[0]
+        close("dx", dx[r:r + 3], rdx, 4 * DEPTH * E * (1 + rr[:, None]) * (1 + np.abs(dy)) * (1 + np.abs(ry)), torch.bfloat16)
+
+
 def test_dropout_drops_what_is_not_a_number(cuda_lib):
     na = cuda_lib
     x = torch.full((4096,), float("nan"), device="cuda")
