@@ -429,6 +429,12 @@ def _sizes(vals):
     return (ctypes.c_int * len(vals))(*vals)
 
 
+@functools.lru_cache(maxsize=1024)
+def _origins(vals):
+    """A C int64 array of a grid's first positions."""
+    return (ctypes.c_int64 * len(vals))(*vals)
+
+
 def _like(t, shape, dtype, name):
     """A contiguous tensor of this shape and type."""
     if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
@@ -445,7 +451,7 @@ def _launch_stream(stream, *tensors):
         if at < 0:
             raise ValueError("expected CUDA tensors")
         if here < 0:
-            here = torch.cuda.current_device()
+            here = torch._C._cuda_getDevice()
         if at != here:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
     if stream is None:
@@ -533,26 +539,28 @@ def _rope(call, what, q, k, q_out, k_out, freqs, origin, stream):
         raise ValueError("expected [B, L_1..L_n, heads, D] with n in 1..3")
     if len(freqs._rot) != ndim:
         raise ValueError("the frequencies need one entry per spatial axis")
-    _like(q, shape, q.dtype, "q")
-    _like(q_out, shape, q.dtype, "q_out")
+    dtype = q.dtype
+    _like(q, shape, dtype, "q")
+    _like(q_out, shape, dtype, "q_out")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     heads_k = 0
     if k is not None:
-        if k.dim() != ndim + 3:
-            raise ValueError("k must have the axes of q")
-        heads_k = k.shape[-2]
-        _like(k, shape[:-2] + (heads_k, shape[-1]), q.dtype, "k")
-        _like(k_out, k.shape, q.dtype, "k_out")
+        shape_k = k.shape
+        if shape_k != shape and (len(shape_k) != ndim + 3 or shape_k[:-2] != shape[:-2] or shape_k[-1] != shape[-1]):
+            raise ValueError("k must have the axes of q but for the heads")
+        heads_k = shape_k[-2]
+        _like(k, shape_k, dtype, "k")
+        _like(k_out, shape_k, dtype, "k_out")
     stream = _launch_stream(stream, q, k, q_out, k_out)
     if origin is not None:
-        origin = (origin,) * ndim if isinstance(origin, int) else tuple(origin)
+        origin = _origins((origin,) * ndim if isinstance(origin, int) else tuple(map(int, origin)))
         if len(origin) != ndim:
             raise ValueError("origin needs one entry per spatial axis")
-        origin = (ctypes.c_int64 * ndim)(*[int(x) for x in origin])
-    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), shape[0], ndim, _sizes(tuple(shape[1:-2])), shape[-2],
+    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), shape[0], ndim, _sizes(shape[1:-2]), shape[-2],
               heads_k, shape[-1], freqs._rot, freqs._freq, origin, freqs.amplitude, freqs._code, _code(q), stream)
-    _ok(st, what)
+    if st:
+        _ok(st, what)
 
 
 def na_rope(q, k, q_out, k_out, freqs: RopeFreqs, origin=None, stream=None):
@@ -567,26 +575,37 @@ def na_rope_bwd(dq_out, dk_out, dq, dk, freqs: RopeFreqs, origin=None, stream=No
 
 
 def _rows(x):
-    if x.dim() < 1 or x.numel() == 0:
+    shape = x.shape
+    n = x.numel()
+    if not shape or n == 0:
         raise ValueError("expected [.., C] with at least one element")
-    C = int(x.shape[-1])
-    return x.numel() // C, C
+    return shape, n // shape[-1], shape[-1]
+
+
+def _vectors(C, **named):
+    """fp32 [C] tensors, or None."""
+    for name, t in named.items():
+        if t is not None:
+            _like(t, (C,), torch.float32, name)
+
+
+def _statistics(shape, mean, rstd):
+    lead = shape[:-1]
+    _like(mean, lead, torch.float32, "mean")
+    _like(rstd, lead, torch.float32, "rstd")
 
 
 def na_layernorm(x, w, b, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
     """y = (x - mean) * rstd * w + b over the last axis of x [.., C] (per head: [B, L.., heads, D]; per token:
     [B, L.., heads * D]).  w, b: fp32 [C] or None; mean, rstd: fp32 x.shape[:-1] for the backward, or None."""
-    rows, C = _rows(x)
-    _like(x, x.shape, x.dtype, "x")
-    _like(y, x.shape, x.dtype, "y")
-    for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _like(t, (C,), torch.float32, name)
+    shape, rows, C = _rows(x)
+    _like(x, shape, x.dtype, "x")
+    _like(y, shape, x.dtype, "y")
+    _vectors(C, w=w, b=b)
     if (mean is None) != (rstd is None):
         raise ValueError("mean and rstd go together")
     if mean is not None:
-        _like(mean, x.shape[:-1], torch.float32, "mean")
-        _like(rstd, x.shape[:-1], torch.float32, "rstd")
+        _statistics(shape, mean, rstd)
     stream = _launch_stream(stream, x, w, b, y, mean, rstd)
     st = load().na_layernorm(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, eps, _code(x),
                              stream)
@@ -604,16 +623,15 @@ def na_layernorm_bwd_workspace_size(rows: int, C: int, dtype=torch.bfloat16) -> 
 
 def na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw=None, db=None, workspace=None, stream=None):
     """dx (may be dy or x) and, when given, dw and db (fp32 [C]) of na_layernorm."""
-    rows, C = _rows(x)
-    for name, t in (("x", x), ("dy", dy), ("dx", dx)):
-        _like(t, x.shape, x.dtype, name)
-    for name, t in (("w", w), ("dw", dw), ("db", db)):
-        if t is not None:
-            _like(t, (C,), torch.float32, name)
+    shape, rows, C = _rows(x)
+    dtype = x.dtype
+    _like(x, shape, dtype, "x")
+    _like(dy, shape, dtype, "dy")
+    _like(dx, shape, dtype, "dx")
+    _vectors(C, w=w, dw=dw, db=db)
     if (dw is None) != (db is None):
         raise ValueError("dw and db go together")
-    _like(mean, x.shape[:-1], torch.float32, "mean")
-    _like(rstd, x.shape[:-1], torch.float32, "rstd")
+    _statistics(shape, mean, rstd)
     raw = _launch_stream(stream, dy, x, w, mean, rstd, dx, dw, db, workspace)
     code = _code(x)
     ws, ws_ptr, ws_bytes = (None, None, 0) if dw is None else _workspace(
@@ -629,18 +647,22 @@ def _rng(rng):
     return _ptr(rng)
 
 
-def _window(x, kernel):
+@functools.lru_cache(maxsize=1024)
+def _window_of(shape, kernel):
     """B, ndim, the grid and the kernel as C arrays, and the heads between them, of weights [B, L.., heads, K]."""
-    shape = x.shape
     ndim = len(shape) - 3
     if ndim < 1 or ndim > 3:
         raise ValueError("expected attention weights [B, L_1..L_n, heads, K] with n in 1..3")
-    kernel = (kernel,) * ndim if isinstance(kernel, int) else tuple(map(int, kernel))
+    kernel = (kernel,) * ndim if isinstance(kernel, int) else kernel
     if len(kernel) != ndim:
         raise ValueError("kernel needs one entry per spatial axis")
     if shape[-1] != math.prod(kernel):
         raise ValueError(f"last axis of the attention weights must be {math.prod(kernel)}")
     return shape[0], ndim, _sizes(tuple(shape[1:-2])), shape[-2], _sizes(kernel)
+
+
+def _window(x, kernel):
+    return _window_of(x.shape, kernel if isinstance(kernel, int) else tuple(map(int, kernel)))
 
 
 def na_dropout(x, y, p: float, rng, stream=None):
