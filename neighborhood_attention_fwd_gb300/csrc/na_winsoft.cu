@@ -1,5 +1,6 @@
 // na_winsoft.cu -- dropout of a tensor, and the entry points of the window softmax with dropout and of the
 // differential window softmax (kernels in na_win_impl.cuh).
+#include <algorithm>
 #include <cmath>
 
 #include "na_block.cuh"
@@ -158,7 +159,11 @@ na_status all_aligned(std::initializer_list<const void*> ps) {
 
 // Workspace of the weights' gradient per head: a value per row, and a partial sum per block and head.
 constexpr int kSumBlocks = 2 * kSms;
-long long sum_tokens(long long tokens) { return (tokens + kSumBlocks - 1) / kSumBlocks; }
+// Tokens of a block: at least sixteen values for every thread, so that small grids take one block and one launch.
+long long sum_tokens(long long tokens, int heads) {
+    const long long share = (tokens + kSumBlocks - 1) / kSumBlocks, least = std::max(1, 16 * kThreads / heads);
+    return std::max(share, least);
+}
 
 size_t diff_workspace(const WinParams& p) {
     const size_t rows = (static_cast<size_t>(p.rows) * 4 + 255) / 256 * 256;
@@ -296,7 +301,7 @@ na_status na_diff_softmax_bwd(const void* x1, const void* x2, const float* lam, 
     st = launch_win(w, dtype, true, true, s);
     if (st == NA_OK && !lam_per_row) {
         // the rows' values [tokens, heads] summed over the tokens, in two steps of a fixed order
-        const long long tokens = w.rows / heads, per = sum_tokens(tokens);
+        const long long tokens = w.rows / heads, per = sum_tokens(tokens, heads);
         const int blocks = static_cast<int>((tokens + per - 1) / per);
         float* partial = w.dlam + (w.rows + 63) / 64 * 64;
         head_sum_kernel<<<blocks, kThreads, 0, s>>>(w.dlam, tokens, heads, per, blocks == 1 ? dlam : partial);
