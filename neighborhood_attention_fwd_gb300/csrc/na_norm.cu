@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_ke
         }
     }
     // Every thread of a warp takes part in the sums: rows past the end repeat the last one and are not stored.  The next
-    // turn's loads are issued before this turn's sums where that pays for the registers: 2-byte rows of 1024 channels 68%
-    // -> 75% of the copy rate, of 4096 61% -> 84%, fp32 rows of 8192 59% -> 89%; heads of 32 lose (84% -> 82%), and
+    // turn's loads are issued before this turn's sums where that pays for the registers: 2-byte rows of 2048 channels 67%
+    // -> 86% of the copy rate, of 4096 61% -> 84%, fp32 rows of 8192 59% -> 89%; heads of 32 lose (84% -> 82%), and
     // fp32 rows of 2048 (97% -> 89%).
-    constexpr bool AHEAD = V == 8 ? BLOCK || J > 1 : V == 4 && BLOCK && J == 4;
+    constexpr bool AHEAD = BLOCK && (V == 8 || (V == 4 && J == 4));
     Chunk<T, V> raw[R][J];
     auto load = [&](long long r0) {
 #pragma unroll
@@ -618,9 +618,9 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
     const int V = C % (16 / es) == 0 ? 16 / es : 1;
     n.vec = V > 1;
     const int chunks = (C + V - 1) / V;
-    // Chunks per thread of a warp team, at most.  The backward keeps weights and two accumulators per column besides: 2-byte
-    // rows of 264 to 512 channels run faster as blocks of one warp with two chunks (512 channels: 64% -> 80% of the copy rate).
-    const int warp_j = !bwd ? 4 : (V == 8 ? 1 : 2);
+    // Chunks per thread of a warp team, at most; longer rows are a block's.  2-byte rows run faster as small blocks with
+    // two chunks to a thread (forward, 1024 channels 75% -> 87% of the copy rate; backward, 512 channels 64% -> 80%).
+    const int warp_j = V == 8 ? 1 : (V == 4 || bwd ? 2 : 4);
     n.block = chunks > 32 * warp_j;
     if (!n.block) {
         n.team = 1;
@@ -686,11 +686,11 @@ na_status launch_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
     constexpr int V = Elem<T>::EPC;
     if (n.vec && !n.block) {
         if (n.j == 1) return run_norm<T, V, 1, false, BWD>(p, n, s);
-        if constexpr (!BWD || V == 4)
+        if constexpr (V == 4)
             if (n.j == 2) return run_norm<T, V, 2, false, BWD>(p, n, s);
-        if constexpr (!BWD) return run_norm<T, V, 4, false, BWD>(p, n, s);
     } else if (n.vec) {
-        if (n.j == 1) return run_norm<T, V, 1, true, BWD>(p, n, s);
+        if constexpr (BWD)
+            if (n.j == 1) return run_norm<T, V, 1, true, BWD>(p, n, s);
         if (n.j == 2) return run_norm<T, V, 2, true, BWD>(p, n, s);
         if constexpr (V == 4) return run_norm<T, V, 4, true, BWD>(p, n, s);   // over 4096 channels of 4 bytes
     } else if (!n.block) {

@@ -237,11 +237,11 @@ __device__ __forceinline__ void drop_tile(unsigned char* tile, uint32_t octets, 
 }
 
 // Blocks per multiprocessor that the registers leave room for: the backward holds a row's weights and gradients.
-template <bool DIFF, bool BWD, int J>
+template <bool DIFF, bool BWD>
 constexpr int win_blocks() { return BWD && DIFF ? 6 : (BWD || DIFF ? 7 : 8); }
 
 template <typename T, bool DIFF, bool BWD, int L, int J>
-__global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD, J>()) win_kernel(const __grid_constant__ WinParams p) {
+__global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD>()) win_kernel(const __grid_constant__ WinParams p) {
     constexpr int N = Words<T>::N, NV = J * N, NB = (DIFF ? 2 : 1) + (BWD ? 1 : 0), NO = DIFF && BWD ? 2 : 1;
     constexpr int kRows = kWinThreads / L;   // rows of a pass: even, so a lane's place in its row is the same in every pass
     extern __shared__ __align__(128) unsigned char smem[];
@@ -632,7 +632,7 @@ na_status run_win(WinParams& p, cudaStream_t s) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return NA_ERR_CUDA;
     int per_sm = static_cast<int>(kWinSmem / (smem + 1024));
-    constexpr int kMost = win_blocks<DIFF, BWD, J>();
+    constexpr int kMost = win_blocks<DIFF, BWD>();
     per_sm = per_sm < 1 ? 1 : (per_sm > kMost ? kMost : per_sm);
     const long long most = static_cast<long long>(per_sm) * kSms;
     kernel<<<static_cast<unsigned>(p.tiles < most ? p.tiles : most), kWinThreads, smem, s>>>(p);
