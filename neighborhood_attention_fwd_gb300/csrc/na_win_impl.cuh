@@ -14,6 +14,12 @@
 // halves), and the result overwrites the logits in shared memory.  Persistent blocks keep a ring of tiles, so that the
 // next tiles are on their way while one is worked on.  Dropout works on aligned octets of the tile, one
 // generator block each, before (backward) or after (forward) the rows.  fp32 arithmetic runs on pairs (f32x2).
+//
+// Measured (bf16; share of the copy rate): softmax with dropout over 9x9 windows at 1024x1024 x 8 heads 472 us, 5.8 TB/s (85%;
+// without dropout 454 us); its gradient over (3,5,5) at 4x256x256 x 8 heads, fp16, 168 us (83%); differential softmax with
+// dropout at 512x512 184 us (82%); its gradients without dropout over (5,7,7) at 2x8x128x128 849 us, 6.1 TB/s (89%).
+// A ring per warp instead of per block took 528 us and more where this took 505, hand-over by a counter instead of
+// barriers 550.
 #pragma once
 
 #include <cmath>
@@ -30,7 +36,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxStages = 3;
-constexpr int kStageBytes[2] = {12 * 1024, 21 * 1024};   // a tile of every input, about; with dropout
+// A tile of every input, about; with dropout.  Without: 8 to 24 KB run alike, 12 best.  With (two stages): softmax forward at
+// 1024x1024 464 us at 16 KB, 468 at 21, 512 at 32; its gradient at 4x256x256 199, 181, 210.
+constexpr int kStageBytes[2] = {12 * 1024, 21 * 1024};
 constexpr int kLongThreads = 128;   // block of a row that no tile holds
 
 // A row's words: 4 bytes, one or two weights.
