@@ -6,7 +6,7 @@
 //
 // What bounds it.  A row is read once and held in registers for its statistics and its result (the variance from the
 // centred values, so a large mean costs no digits): memory.  A row belongs to a team of threads, each with J chunks of
-// the row: lanes of a warp (rows of up to 64 or 128 chunks), else a block.  The backward's teams walk many rows, so
+// the row: lanes of a warp (rows of up to 32 chunks, of 4-byte elements 64), else a block.  The backward's teams walk many rows, so
 // a thread's columns stay the same and the weight gradients accumulate in its registers; a block writes one
 // partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).
 //
