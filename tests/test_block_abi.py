@@ -158,6 +158,23 @@ def test_binding_checks():
         na.RopeFreqs.scaled((16,), scaling="other")
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A tensor of a device other than the current one, or of two devices, raises before the library is called."""
+    class Fake:
+        def __init__(self, at):
+            self.at, self.device = at, f"cuda:{at}"
+
+        def get_device(self):
+            return self.at
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda at: 77 + at, raising=False)
+    assert na._launch_stream(None, Fake(0), None, Fake(0)) == 77
+    for tensors in ((Fake(1),), (Fake(0), Fake(1)), (Fake(0), Fake(-1))):
+        with pytest.raises(ValueError):
+            na._launch_stream(None, *tensors)
+
+
 def test_scaled_frequencies():
     plain = na.RopeFreqs.scaled((32, 8)).freqs
     assert plain[0][0] == 1.0 and len(plain[0]) == 16 and len(plain[1]) == 4

@@ -534,6 +534,88 @@ def test_on_another_stream(cuda_lib):
     assert torch.equal(y, ref) and torch.equal(tmp, ref)
 
 
+def test_everything_dropped(cuda_lib):
+    """p = 1: zeros everywhere, also where the logits or the gradient are not numbers."""
+    na = cuda_lib
+    x = randn((1, 40, 3, 25), "bf16", 1).cuda()
+    x[0, 3, 1, 2] = float("nan")
+    y, dx, d2 = (torch.full_like(x, 5.0) for _ in range(3))
+    lam, dl = torch.rand(3, device="cuda"), torch.full((3,), 5.0, device="cuda")
+    na.na_softmax_dropout(x, y, (25,), 1.0, rng_state())
+    assert torch.equal(y, torch.zeros_like(y))
+    na.na_diff_softmax(x, x, lam, y, (25,), 1.0, rng_state())
+    assert torch.equal(y, torch.zeros_like(y))
+    x[0, 3, 1, 2] = 1.0
+    dy = torch.full_like(x, float("inf"))
+    na.na_softmax_dropout_bwd(x, dy, dx, (25,), 1.0, rng_state())
+    na.na_diff_softmax_bwd(x, x, lam, dy, y, d2, dl, (25,), 1.0, rng_state())
+    for t in (dx, y, d2, dl):
+        assert torch.equal(t, torch.zeros_like(t))
+    status_ok(na)
+
+
+def test_calls_on_two_streams_at_once(cuda_lib):
+    na = cuda_lib
+    x = [randn((1, 96, 96, 8, 49), "bf16", i).cuda() for i in range(4)]
+    q = [randn((1, 96, 96, 8, 64), "bf16", 9 + i).cuda() for i in range(4)]
+    lam, rng, f = torch.rand(8, device="cuda"), rng_state(), na.RopeFreqs.scaled((20, 22))
+
+    def work(i, **kw):
+        o = [torch.empty_like(x[i]), torch.empty_like(x[i]), torch.empty_like(lam), torch.empty_like(q[i]), torch.empty_like(q[i])]
+        st = torch.empty(q[i].shape[:-1], device="cuda"), torch.empty(q[i].shape[:-1], device="cuda")
+        for _ in range(5):
+            na.na_diff_softmax_bwd(x[i], x[(i + 1) % 4], lam, x[(i + 2) % 4], o[0], o[1], o[2], (7, 7), 0.2, rng)
+            na.na_rope(q[i], None, o[3], None, f)
+            na.na_layernorm(o[3], None, None, o[4], *st)
+            na.na_layernorm_bwd(q[(i + 1) % 4], o[3], None, *st, o[4])
+        return o
+
+    ref = [work(i) for i in range(4)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            got.append(work(i))
+    torch.cuda.synchronize()
+    status_ok(na)
+    for r, g in zip(ref, got):
+        assert all(torch.equal(a, b) for a, b in zip(r, g))
+
+
+def test_the_binding_refuses_other_layouts(cuda_lib):
+    na = cuda_lib
+    x = torch.zeros(1, 8, 8, 2, 32, device="cuda")
+    f = na.RopeFreqs.scaled((16, 16))
+    bad = [
+        lambda: na.na_rope(x.transpose(1, 2), None, x, None, f),                          # strided
+        lambda: na.na_rope(x, x.double(), x, x, f),                                       # another type
+        lambda: na.na_rope(x, None, x, x, f),                                             # k_out without k
+        lambda: na.na_rope(x, None, x, None, na.RopeFreqs.scaled((16,))),                 # frequencies of one axis
+        lambda: na.na_rope(x, x[:, :4].contiguous(), x, x[:, :4].contiguous(), f),        # another grid
+        lambda: na.na_rope(x, None, x, None, f, origin=(1, 2, 3)),
+        lambda: na.na_layernorm(x, torch.zeros(31, device="cuda"), None, x),
+        lambda: na.na_layernorm(x, torch.zeros(32, device="cuda", dtype=torch.bfloat16), None, x),
+        lambda: na.na_layernorm(x, None, None, x, torch.zeros(1, 8, 8, 2, device="cuda")),
+        lambda: na.na_layernorm(x[..., :0], None, None, x[..., :0]),
+        lambda: na.na_dropout(x, x, 0.1, torch.zeros(2, device="cuda")),                  # the state's type
+        lambda: na.na_dropout(x, x, 0.1, torch.zeros(2, dtype=torch.int64)),              # on the host
+        lambda: na.na_softmax_dropout(x, x, (5, 5), 0.1, rng_state()),                    # not 32 weights
+        lambda: na.na_diff_softmax(x, x, torch.zeros(3, device="cuda"), x, (32,)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(f"call {i} was taken")
+    for call in (lambda: na.na_dropout(x, x, 0.1, None), lambda: na.na_dropout(x, x, 1.5, rng_state()),
+                 lambda: na.na_rope(x, None, x, None, na.RopeFreqs.scaled((32, 32))),
+                 lambda: na.na_rope(x[..., 1:17].contiguous().view(-1)[1:-15].view(-1, 1, 1, 16)[:8].view(1, 8, 1, 16), None,
+                                    torch.zeros(1, 8, 1, 16, device="cuda"), None, na.RopeFreqs.scaled((16,)))):
+        with pytest.raises(na.NAError):
+            call()
+    status_ok(na)
+
+
 def test_workspaces_on_another_stream(cuda_lib):
     """The gradients that sum over rows, on a given stream (the library allocates there) and with the caller's
     workspace, give what the current stream gives."""
