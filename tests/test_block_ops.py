@@ -73,6 +73,10 @@ ROPE = [
     ("bf16", 1, (3, 4), 2, 2, 32, (0, 32), "half", (5, 5)),                 # an axis without channels
     ("bf16", 1, (70, 33), 16, 16, 128, (64, 64), "half", None),             # several passes per block
     ("fp32", 1, (40, 33), 16, 7, 128, (64, 62), "interleaved", None),
+    ("bf16", 1, (9, 31), 3, 2, 32, (8, 12), "half", None),                  # even halves, some channels copied
+    ("fp16", 2, (5, 7, 9), 2, 5, 64, (20, 20, 24), "half", (1, 2, 3)),
+    ("bf16", 1, (300,), 40, 1, 128, (44,), "half", None),                   # several turns of a block
+    ("fp16", 1, (300,), 40, 3, 128, (46,), "half", None),
 ]
 
 
