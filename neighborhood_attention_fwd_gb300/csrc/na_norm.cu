@@ -159,7 +159,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*slot)[
 }
 
 // Rows that a team of the forward works on at once: their loads are in flight together and their sums share the steps.
-__host__ __device__ constexpr int norm_rows(int J) { return J == 1 ? 4 : (J == 2 ? 2 : 1); }
+__host__ __device__ constexpr int norm_rows(int J) { return J == 1 ? 4 : (J <= 4 ? 2 : 1); }
 
 template <typename T, int V, int J, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_kernel(const NormParams p) {
@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_fwd_ke
     }
     // Every thread of a warp takes part in the sums: rows past the end repeat the last one and are not stored.  The next
     // turn's loads are issued before this turn's sums where that pays for the registers: 2-byte rows of 2048 channels 67%
-    // -> 86% of the copy rate, of 4096 61% -> 84%, fp32 rows of 8192 59% -> 89%; heads of 32 lose (84% -> 82%), and
-    // fp32 rows of 2048 (97% -> 89%).
-    constexpr bool AHEAD = BLOCK && (V == 8 || (V == 4 && J == 4));
+    // -> 86% of the copy rate, of 4096 61% -> 84%, fp32 rows of 8192 59% -> 89% (two rows at once: 94%), of 1001, element by
+    // element, 52% -> 67% (73%); heads of 32 lose (84% -> 82%), and fp32 rows of 2048 (97% -> 89%).
+    constexpr bool AHEAD = BLOCK && (V == 8 || J == 4);
     Chunk<T, V> raw[R][J];
     auto load = [&](long long r0) {
 #pragma unroll
