@@ -315,7 +315,8 @@ na_status na_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk
 na_status na_layernorm(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd, int64_t rows,
                        int C, float eps, na_dtype dtype, void* stream);
 
-/* Bytes of device workspace na_layernorm_bwd needs for dw and db (0 on invalid arguments). */
+/* Bytes of device workspace na_layernorm_bwd needs for dw and db (0 for few wide rows, which need none, and on invalid
+ * arguments). */
 size_t na_layernorm_bwd_workspace_size(int64_t rows, int C, na_dtype dtype);
 
 /*

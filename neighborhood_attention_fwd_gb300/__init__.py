@@ -469,6 +469,8 @@ def _workspace(ws, stream, need, device):
     library, which allocates on that stream."""
     if ws is None and stream is None:
         n = need()
+        if n == 0:
+            return None, None, 0
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         return ws, ws.data_ptr(), n
     return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())

@@ -8,10 +8,11 @@
 // centred values, so a large mean costs no digits): memory.  A row belongs to a team of threads, each with J chunks of
 // the row: lanes of a warp (rows of up to 32 chunks, of 4-byte elements 64), else a block.  The backward's teams walk many rows, so
 // a thread's columns stay the same and the weight gradients accumulate in its registers; a block writes one
-// partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).
+// partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).  Few wide rows need
+// neither: blocks of columns beside the rows' blocks read x and dy again.
 //
 // Measured (bf16; share of the copy rate): 2M rows of 32 channels forward 51 us, 5.6 TB/s (82%); 1M rows of 256 backward
-// 275 us, 5.9 TB/s (87%).
+// 275 us, 5.9 TB/s (87%); fp32, 333 rows of 2048 backward 9.3 us a call, 3.9 us on the GPU.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,6 +37,9 @@ struct NormParams {
     float* mean;           // forward: written (null: not wanted); backward: read
     float* rstd;
     float* partial;        // backward: [blocks][2][C], null: no weight gradients
+    float* dw;             // few rows: written by the blocks of columns
+    float* db;
+    int cols, first;       // few rows: blocks of columns, and the first block of the launch (rows follow columns)
     long long rows;
     int C, team;           // threads per row
     float eps, inv_c;
@@ -446,6 +450,120 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
     store_partial<V, J, BLOCK>(p, fw, fb, l, cols);
 }
 
+// The backward of few wide rows in one launch without a workspace: dw and db need only the saved statistics, so blocks of
+// columns take them from x and dy (a second read, out of L2) beside the blocks that each take a row for dx.  A block of
+// columns has eight words of them (a sector of a row); its groups of eight lanes each take every 64th row, and the groups'
+// sums are added in a fixed order.  Where dx overwrites x or dy the columns are a launch of their own before the rows.
+constexpr int kFewThreads = 512, kFewWords = 8;
+template <typename T, int J>
+__global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormParams p) {
+    constexpr int V = Elem<T>::EPC, PER = 4 / static_cast<int>(sizeof(T)), GROUPS = kFewThreads / kFewWords;
+    __shared__ float slots[2][32];
+    __shared__ float sums[kFewThreads / 32][2][kFewWords * PER];
+    const int block = blockIdx.x + p.first;
+    if (block < p.cols) {
+        const int word = threadIdx.x % kFewWords, c = (block * kFewWords + word) * PER;
+        float dw[PER] = {}, db[PER] = {};
+        if (c < p.C) {
+            const char* x = static_cast<const char*>(p.x) + static_cast<long long>(c) * sizeof(T);
+            const char* dy = static_cast<const char*>(p.dy) + static_cast<long long>(c) * sizeof(T);
+            const long long pitch = static_cast<long long>(p.C) * sizeof(T);
+            const int rows = static_cast<int>(p.rows);
+#pragma unroll 4
+            for (int r = threadIdx.x / kFewWords; r < rows; r += GROUPS) {
+                float fx[PER], fy[PER];
+                const uint32_t wx = *reinterpret_cast<const uint32_t*>(x + r * pitch), wy = *reinterpret_cast<const uint32_t*>(dy + r * pitch);
+                if constexpr (PER == 1) {
+                    fx[0] = __uint_as_float(wx);
+                    fy[0] = __uint_as_float(wy);
+                } else {
+                    Elem<T>::two(wx, fx[0], fx[1]);
+                    Elem<T>::two(wy, fy[0], fy[1]);
+                }
+                const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    dw[e] = fmaf(fy[e] * rstd, fx[e] - mean, dw[e]);
+                    db[e] += fy[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 16; m >= kFewWords; m >>= 1)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
+                db[e] += __shfl_xor_sync(0xffffffffu, db[e], m);
+            }
+        if ((threadIdx.x & 31) < kFewWords) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                sums[threadIdx.x >> 5][0][word * PER + e] = dw[e];
+                sums[threadIdx.x >> 5][1][word * PER + e] = db[e];
+            }
+        }
+        __syncthreads();
+        const int which = threadIdx.x / (kFewWords * PER), k = threadIdx.x % (kFewWords * PER);
+        if (which < 2 && block * kFewWords * PER + k < p.C) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kFewThreads / 32; ++i) s += sums[i][which][k];
+            (which ? p.db : p.dw)[block * kFewWords * PER + k] = s;
+        }
+        return;
+    }
+    const long long row = block - p.cols;
+    Chunk<T, V> rx[J], rg[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const long long at = row * p.C + min((static_cast<int>(threadIdx.x) + kFewThreads * j) * V, p.C - V);
+        rx[j].load(p.x, at);
+        rg[j].load(p.dy, at);
+    }
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    using A = Cols<V>;
+    using W = typename A::W;
+    constexpr int H = A::H;
+    W d[J][H], g[J][H], s0 = 0, s1 = 0;
+    const W mm = A::both(-mean), rr = A::both(rstd);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (threadIdx.x + kFewThreads * j) * V;
+        if (c < p.C) {
+            float fx[V], fy[V], fw[V];
+            load_weights<V>(p.w, c, fw, 1.f);
+            rx[j].get(fx);
+            rg[j].get(fy);
+            W y[H], w[H];
+            A::from(fx, d[j]);
+            A::from(fy, y);
+            A::from(fw, w);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                d[j][e] = A::add(d[j][e], mm);
+                g[j][e] = A::mul(A::mul(y[e], rr), w[e]);
+                s0 = A::add(s0, g[j][e]);
+                s1 = A::fma(g[j][e], d[j][e], s1);
+            }
+        }
+    }
+    float s[2] = {A::sum(s0), A::sum(s1)};
+    team_sum<2, true>(s, kFewThreads, slots);
+    const W k1 = A::both(-s[0] * p.inv_c), k2 = A::both(-(rstd * rstd) * (s[1] * p.inv_c));
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (threadIdx.x + kFewThreads * j) * V;
+        if (c < p.C) {
+            W o[H];
+#pragma unroll
+            for (int e = 0; e < H; ++e) o[e] = A::fma(d[j][e], k2, A::add(g[j][e], k1));
+            float f[V];
+            A::to(o, f);
+            store_chunk<T, V>(p.out, row * p.C + c, f);
+        }
+    }
+}
+
 // The backward of warp teams on whole chunks (one each, of 4-byte rows up to two).  A register or two of loads per thread do not keep the memory busy
 // beside the accumulators, so x and dy come through a ring of tiles in shared memory (cp.async.bulk; rows are whole
 // chunks, so a tile is one run of bytes): a tile's stage is filled again once every thread has read it.  The
@@ -608,9 +726,15 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* part
     }
 }
 
+// Wide rows up to here take the one launch (in a graph, before -> after: 333 rows of 2048, fp32 8.5 -> 3.8 us, bf16 9.0 -> 3.7;
+// 1500 rows of 2048, fp32 15.9 -> 10.3; 1000 rows of 8192, fp32 37.7 -> 33.9; beyond, 1500 rows of 8192, fp32 47.1 -> 50.7, 4000 of
+// 520, bf16 11.2 -> 13.5).
+constexpr int kFewRows = 1536;
+constexpr long long kFewBytes = 32ll << 20;
+
 // How a problem is laid out: chunk width, chunks per thread, threads per row, blocks.
 struct NormPlan {
-    bool vec, block, ring;
+    bool vec, block, ring, few;
     int j, team, blocks, tile;
     long long tiles;
 };
@@ -646,9 +770,12 @@ NormPlan plan_norm(long long rows, int C, int es, bool bwd) {
             const long long grid = static_cast<long long>(per_sm) * sms;
             n.blocks = static_cast<int>(n.tiles < grid ? n.tiles : grid);
         }
+    } else if (bwd && n.vec && rows <= kFewRows && rows * C * es <= kFewBytes) {
+        n.few = true;
+        n.j = (chunks + kFewThreads - 1) / kFewThreads;   // 1, 2, 4 (or 3)
+        n.blocks = (chunks * 4 + kFewWords - 1) / kFewWords;
     } else {
-        // two chunks to a thread; in the backward of few rows, one (fp32, 333 rows of 2048: 9.5 us instead of 10.7)
-        n.j = n.vec ? (bwd && rows < 4LL * sms ? 1 : 2) : 4;
+        n.j = n.vec ? 2 : 4;   // chunks to a thread
         while (n.j * kNormBlock < chunks) n.j *= n.vec ? 2 : 4;
         const int t = (chunks + n.j - 1) / n.j;
         n.team = (t + 31) / 32 * 32;
@@ -692,8 +819,6 @@ na_status launch_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
         if constexpr (V == 4)
             if (n.j == 2) return run_norm<T, V, 2, false, BWD>(p, n, s);
     } else if (n.vec) {
-        if constexpr (BWD)
-            if (n.j == 1) return run_norm<T, V, 1, true, BWD>(p, n, s);
         if (n.j == 2) return run_norm<T, V, 2, true, BWD>(p, n, s);
         if constexpr (V == 4) return run_norm<T, V, 4, true, BWD>(p, n, s);   // over 4096 channels of 4 bytes
     } else if (!n.block) {
@@ -701,6 +826,24 @@ na_status launch_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
         else return n.j == 1 ? run_norm<T, 1, 1, false, BWD>(p, n, s) : run_norm<T, 1, 4, false, BWD>(p, n, s);
     }
     return n.j == 4 ? run_norm<T, 1, 4, true, BWD>(p, n, s) : run_norm<T, 1, 16, true, BWD>(p, n, s);
+}
+
+// n.blocks: of columns
+template <typename T>
+na_status launch_few(NormParams p, const NormPlan& n, cudaStream_t s) {
+    auto run = [&](int first, int blocks) {
+        p.first = first;
+        if (n.j == 1) norm_bwd_few_kernel<T, 1><<<blocks, kFewThreads, 0, s>>>(p);
+        else if (n.j == 2) norm_bwd_few_kernel<T, 2><<<blocks, kFewThreads, 0, s>>>(p);
+        else if constexpr (sizeof(T) == 4) norm_bwd_few_kernel<T, 4><<<blocks, kFewThreads, 0, s>>>(p);
+        return launch_result();
+    };
+    const int rows = static_cast<int>(p.rows);
+    p.cols = p.dw ? n.blocks : 0;
+    const bool over = p.out == p.x || p.out == p.dy;
+    if (!over || !p.cols) return run(0, p.cols + rows);
+    const na_status st = run(0, p.cols);
+    return st == NA_OK ? run(p.cols, rows) : st;
 }
 
 template <bool BWD>
@@ -717,6 +860,7 @@ na_status norm_sizes(long long rows, int C, na_dtype dtype) {
 }
 
 size_t norm_workspace(const NormPlan& n, int C) {
+    if (n.few) return 0;
     return (static_cast<size_t>(n.blocks) * 2 * C * sizeof(float) + 255) / 256 * 256;
 }
 
@@ -803,6 +947,12 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
         if (!output_clear(sws, {}, {sx, sdy, sdx, sw, sm, sr, sdw, sdb})) return NA_ERR_INVALID_ARG;
     }
     if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
+    if (n.few) {
+        p.dw = dw;
+        p.db = db;
+        if (dtype == NA_BF16) return launch_few<__nv_bfloat16>(p, n, s);
+        return dtype == NA_FP16 ? launch_few<__half>(p, n, s) : launch_few<float>(p, n, s);
+    }
     if (dw && !ws) {
         if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
         owned = true;

@@ -179,6 +179,8 @@ NORM = [
     ("bf16", 17, 1024), ("fp16", 17, 1032), ("fp32", 333, 2048), ("bf16", 1300, 2048), ("bf16", 5, 8192), ("fp32", 5, 8192),
     ("bf16", 19, 7), ("fp16", 130, 33), ("fp32", 57, 63), ("bf16", 57, 65), ("fp32", 13, 129), ("bf16", 9, 1001), ("fp32", 9, 4099),
     ("fp16", 3, 8191), ("bf16", 40000, 24),
+    # wide rows around the fewest that take the gradients' general kernels
+    ("bf16", 1536, 264), ("bf16", 1537, 264), ("fp32", 1536, 296), ("fp32", 1100, 4096), ("fp32", 1, 8192), ("fp16", 65, 4104), ("fp32", 63, 4100),
 ]
 
 
@@ -231,6 +233,40 @@ def test_layernorm_and_its_gradients(case, affine, cuda_lib):
     y2 = xd.clone()
     na.na_layernorm(y2, wd, bd, y2)
     assert torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layernorm_gradients_of_few_wide_rows_over_their_inputs(dtype, cuda_lib):
+    """Few wide rows need no workspace; dx over x or dy gives what a separate dx gives, also without dw and db, and in a
+    captured graph."""
+    na = cuda_lib
+    for rows, C in ((1, 520), (130, 2048), (500, 6000)):
+        x, dy = randn((rows, C), dtype, 1).cuda(), randn((rows, C), dtype, 2).cuda()
+        w = torch.rand(C, device="cuda")
+        y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        na.na_layernorm(x, w, None, y, mean, rstd)
+        assert na.na_layernorm_bwd_workspace_size(rows, C, TYPES[dtype]) == 0
+
+        def grads(over=None, sums=True):
+            a, b = x.clone(), dy.clone()
+            dx = {None: torch.empty_like(x), "x": a, "dy": b}[over]
+            dw, db = (torch.full((C,), 9.0, device="cuda") for _ in range(2))
+            na.na_layernorm_bwd(b, a, w, mean, rstd, dx, *((dw, db) if sums else ()))
+            return (dx, dw, db) if sums else (dx,)
+
+        ref = grads()
+        for over in ("x", "dy"):
+            assert all(torch.equal(g, r) for g, r in zip(grads(over), ref))
+            assert torch.equal(grads(over, False)[0], ref[0])
+        assert torch.equal(grads(None, False)[0], ref[0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = grads("x")
+        for t in out:
+            t.zero_()
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    status_ok(na)
 
 
 def test_layernorm_keeps_its_digits_far_from_zero(cuda_lib):
