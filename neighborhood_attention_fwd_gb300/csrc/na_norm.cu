@@ -12,7 +12,7 @@
 // neither: blocks of columns beside the rows' blocks read x and dy again.
 //
 // Measured (bf16; share of the copy rate): 2M rows of 32 channels forward 51 us, 5.6 TB/s (82%); 1M rows of 256 backward
-// 275 us, 5.9 TB/s (87%); fp32, 333 rows of 2048 backward 9.3 us a call, 3.9 us on the GPU.
+// 275 us, 5.9 TB/s (87%); fp32, 333 rows of 2048 backward 9 to 12 us a call, 3.9 us on the GPU.
 #include <algorithm>
 #include <type_traits>
 
