@@ -123,12 +123,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// The reference point of a row's exponentials: its maximum, or 0 for a row of -inf alone.  A maximum near the
-// type's limits (a mask of the lowest finite value) would overflow once multiplied by log2 e: `far` says that the
-// row has to be shifted before, not after, that product.
+// The reference point of a row's exponentials: its maximum, or 0 for a row of -inf alone.  exp(x - m) is taken as
+// 2^(x c - round(m c)), c = log2 e, so every exponent of the row is off by the rounding of m c, up to |m| 2^-23.5: a common
+// factor, which cancels against the sum while the exponentials stay in range (a sixteenth in the exponent at 2^20, hundreds
+// from 10^10 on, and a mask of the lowest finite value overflows).  `far` says that the row has to be shifted before, not
+// after, that product: its largest exponent is then 0.
 __device__ __forceinline__ float row_top(float m, bool& far) {
     if (m == -INFINITY) m = 0.f;
-    far = !(fabsf(m) < 1e37f);
+    far = !(fabsf(m) < 1048576.f);
     return m;
 }
 
@@ -170,7 +172,7 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[J], float (&v)[J * 
     return lanes_sum<L>(a);
 }
 
-// 1 / l of a row's sum: at least 1 (its largest term), 0 for an empty row, or NaN.
+// 1 / l of a row's sum, whose largest term is 1 to within 2^(1/16): 0 for an empty row, or NaN.
 __device__ __forceinline__ float inverse_or_zero(float l) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));

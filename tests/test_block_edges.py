@@ -1,0 +1,83 @@
+"""Edges of the operators around the attention that a call's documentation allows: logits far from zero, statistics
+near the ends of fp32, rows that share a warp with rows of other kinds, host threads at once, sizes past 32 bits.
+Tolerances are those of test_block_ops.py, derived there.
+"""
+import math
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import neighborhood_attention_fwd_gb300 as nab
+import oracle.block as ob
+import test_block_ops as tb
+from neighborhood_attention_fwd_gb300 import build as nabuild
+
+TYPES, E, DEPTH, close, f64, randn = tb.TYPES, tb.E, tb.DEPTH, tb.close, tb.f64, tb.randn
+
+
+def bits(t):
+    """A tensor's bit patterns: 0 and -0 differ, as do NaNs."""
+    return t.view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+# ---------------------------------------------------------------------------------------------
+# Window softmax
+# ---------------------------------------------------------------------------------------------
+
+FAR = [1e10, 1e12, 1e20, 1e30, 1e36, 1e37, 2e9, 1.5e8, 3e6, 2.0 ** 20, 2.0 ** 20 - 1, 65504.0]
+
+
+def far_logits(shape, dtype, seed):
+    """Rows around +-FAR and the type's extremes: of one value, of one value but for a few places (some of them masked),
+    and spread by a few units (which a type of few digits rounds away far from zero)."""
+    x = randn(shape, "fp32", seed, 2.0).double()
+    rows = x.view(-1, shape[-1])
+    top = torch.finfo(TYPES[dtype]).max
+    bases = [s * b for b in FAR for s in (1, -1)] + [top, -top]
+    for i in range(rows.shape[0]):
+        base, kind = bases[(i + seed) % len(bases)], (i // len(bases)) % 3
+        if kind == 2 and abs(base) < top:
+            rows[i] += base
+            continue
+        rows[i] = base
+        if kind == 1 and shape[-1] > 4:
+            rows[i, 1] = base - abs(base) / 64
+            rows[i, 3] = -top
+            rows[i, 4] = -math.inf
+    return x.to(TYPES[dtype])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [5, 81, 399, 765, 1001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logits_far_from_zero(dtype, K, cuda_lib):
+    """A row's weights depend on the differences of its logits, wherever they lie."""
+    na = cuda_lib
+    shape, kernel, heads = (1, max(K, 80), 3, K), (K,), 3
+    x1, x2, dy = far_logits(shape, dtype, 0), far_logits(shape, dtype, 7), randn(shape, dtype, 3)
+    lam = randn((heads,), "fp32", 4)
+    d1, d2, dd, dl, rng = x1.cuda(), x2.cuda(), dy.cuda(), lam.cuda(), tb.rng_state()
+    y, dx, z, g1, g2 = (torch.full_like(d1, 5.0) for _ in range(5))
+    gl = torch.full_like(dl, 5.0)
+    na.na_softmax_dropout(d1, y, kernel, 0.2, rng)
+    na.na_softmax_dropout_bwd(d1, dd, dx, kernel, 0.2, rng)
+    na.na_diff_softmax(d1, d2, dl, z, kernel)
+    na.na_diff_softmax_bwd(d1, d2, dl, dd, g1, g2, gl, kernel)
+    tb.status_ok(na)
+    X1, X2, D, L = f64(x1), f64(x2), f64(dy), f64(lam)
+    s1, s2 = ob.softmax(X1), ob.softmax(X2)
+    e1, e2 = tb.map_error(X1, s1), tb.map_error(X2, s2)
+    f, one = ob.dropout_factor(x1.numel(), 0.2, tb.SEED, tb.OFFSET).reshape(shape), np.ones(shape)
+    ref = ob.softmax_dropout(X1, f)
+    close("y", y, ref, np.abs(ref) * e1 + 2.0 ** -120, TYPES[dtype])
+    close("dx", dx, ob.softmax_dropout_bwd(X1, D, f), tb.grad_slack(s1, e1, D, f)[0], TYPES[dtype])
+    lr = np.abs(L)[:, None]
+    close("diff", z, ob.diff_softmax(X1, X2, L, one), s1 * e1 + lr * s2 * (e2 + 4 * E) + 2.0 ** -120, TYPES[dtype])
+    r1, r2, rl = ob.diff_softmax_bwd(X1, X2, L, D, one)
+    (k1, _), (k2, row) = tb.grad_slack(s1, e1, D, one), tb.grad_slack(s2, e2, D, one)
+    close("dx1", g1, r1, k1, TYPES[dtype])
+    close("dx2", g2, r2, lr * (k2 + 4 * E * np.abs(r2)), TYPES[dtype])
+    each = np.abs((s2 * D).sum(-1)).reshape(-1, heads).sum(0)
+    close("dlam", gl, rl, row.reshape(-1, heads).sum(0) + (shape[1] / 8 + 300) * E * each)
