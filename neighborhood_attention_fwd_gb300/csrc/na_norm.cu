@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
         const long long row = r0 + team_in_block;
         const bool live = row < p.rows;   // whole warps stay together, for the sums
         W d[J][H], g[J][H], s0 = 0, s1 = 0;
-        const W mm = A::both(-mean), rr = A::both(rstd);
+        // a team past the end adds zeros made of zeros: what it read of the last row need not be finite, and may be dx already
+        const W mm = A::both(-mean), rr = A::both(BLOCK || live ? rstd : 0.f);
         const float r2 = rstd * rstd;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
                 if (!in) y[e] = 0;
                 const W yr = A::mul(y[e], rr);
                 d[j][e] = A::add(d[j][e], mm);
+                if (!BLOCK && !live) d[j][e] = 0;
                 dw[j][e] = A::fma(yr, d[j][e], dw[j][e]);
                 db[j][e] = A::add(db[j][e], y[e]);
                 g[j][e] = A::mul(yr, w[j][e]);

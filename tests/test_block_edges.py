@@ -81,3 +81,35 @@ def test_logits_far_from_zero(dtype, K, cuda_lib):
     close("dx2", g2, r2, lr * (k2 + 4 * E * np.abs(r2)), TYPES[dtype])
     each = np.abs((s2 * D).sum(-1)).reshape(-1, heads).sum(0)
     close("dlam", gl, rl, row.reshape(-1, heads).sum(0) + (shape[1] / 8 + 300) * E * each)
+
+
+# ---------------------------------------------------------------------------------------------
+# Layer norm
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows,C", [("bf16", 9, 33), ("fp32", 9, 63), ("fp16", 257, 7), ("fp32", 33, 3)])
+def test_gradients_of_odd_rows_whose_last_is_not_finite(dtype, rows, C, cuda_lib):
+    """An infinite value in the last row reaches its own column of dw and no other sum, and the weights' gradients
+    do not depend on whether dx overwrites its inputs."""
+    na = cuda_lib
+    x, dy, w = randn((rows, C), dtype, 1), randn((rows, C), dtype, 2), 1 + 0.3 * randn((C,), "fp32", 3)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    x[-1, 0], dy[-1, 0] = float("inf"), 1.0
+    xd, dyd, wd = x.cuda(), dy.cuda(), w.cuda()
+    dx, dw, db = torch.empty_like(xd), torch.empty_like(wd), torch.empty_like(wd)
+    na.na_layernorm_bwd(dyd, xd, wd, mean, rstd, dx, dw, db)
+    assert torch.isposinf(dw[0])
+    ref = (f64(dy) * np.where(np.isinf(f64(x)), 0, f64(x))).sum(0)
+    close("dw", dw[1:], ref[1:], DEPTH * E * np.abs(f64(dy)[:, 1:] * f64(x)[:, 1:]).sum(0))
+    close("db", db, f64(dy).sum(0), DEPTH * E * np.abs(f64(dy)).sum(0))
+    # a row of dx that is not finite, written over the row of x that teams past the end read
+    xd[-1, 0] = 0.5
+    dyd[-1, -1] = float("inf")
+    na.na_layernorm_bwd(dyd, xd, wd, mean, rstd, dx, dw, db)
+    assert not torch.isfinite(dx[-1]).any() and torch.isfinite(dw[:-1]).all() and torch.isfinite(dx[:-1]).all()
+    for _ in range(20):
+        over, dw2, db2 = xd.clone(), torch.empty_like(dw), torch.empty_like(db)
+        na.na_layernorm_bwd(dyd, over, wd, mean, rstd, over, dw2, db2)
+        assert torch.equal(dw2, dw) and torch.equal(db2, db) and torch.equal(over[:-1], dx[:-1])
+    tb.status_ok(na)
