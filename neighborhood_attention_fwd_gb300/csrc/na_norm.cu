@@ -309,8 +309,9 @@ __device__ __forceinline__ void store_partial(const NormParams& p, float (&dw)[J
     }
 }
 
-// Chunk-wise arithmetic of the backward, H words of one or two columns each: with d = x - mean and g' = dy rstd w the
-// gradient of x is g' - sum g' / C - d rstd^2 sum (g' d) / C.
+// Chunk-wise arithmetic of the backward, H words of one or two columns each: with h = (x - mean) rstd and g = dy w the
+// gradient of x is rstd g - rstd sum g / C - h rstd sum (g h) / C.  No square of rstd, which could leave fp32's range where
+// every term is within it.
 template <int V>
 struct Cols {
     static constexpr int H = V == 1 ? 1 : V / 2;
@@ -399,10 +400,10 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
         if (!AHEAD) load(r0);
         const long long row = r0 + team_in_block;
         const bool live = row < p.rows;   // whole warps stay together, for the sums
-        W d[J][H], g[J][H], s0 = 0, s1 = 0;
+        W h[J][H], g[J][H], s0 = 0, s1 = 0;
         // a team past the end adds zeros made of zeros: what it read of the last row need not be finite, and may be dx already
-        const W mm = A::both(-mean), rr = A::both(BLOCK || live ? rstd : 0.f);
-        const float r2 = rstd * rstd;
+        const float rs = rstd;   // the next row's loads overwrite it
+        const W mm = A::both(-mean), rr = A::both(rs);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const bool in = live && (l + p.team * j) * V < p.C;
@@ -410,32 +411,31 @@ __global__ void __launch_bounds__(BLOCK ? kNormBlock : kNormThreads) norm_bwd_ke
             rx[j].get(fx);
             rg[j].get(fy);
             W y[H];
-            A::from(fx, d[j]);
+            A::from(fx, h[j]);
             A::from(fy, y);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
                 if (!in) y[e] = 0;
-                const W yr = A::mul(y[e], rr);
-                d[j][e] = A::add(d[j][e], mm);
-                if (!BLOCK && !live) d[j][e] = 0;
-                dw[j][e] = A::fma(yr, d[j][e], dw[j][e]);
+                h[j][e] = A::mul(A::add(h[j][e], mm), rr);
+                if (!BLOCK && !live) h[j][e] = 0;
+                dw[j][e] = A::fma(y[e], h[j][e], dw[j][e]);
                 db[j][e] = A::add(db[j][e], y[e]);
-                g[j][e] = A::mul(yr, w[j][e]);
+                g[j][e] = A::mul(y[e], w[j][e]);
                 s0 = A::add(s0, g[j][e]);
-                s1 = A::fma(g[j][e], d[j][e], s1);
+                s1 = A::fma(g[j][e], h[j][e], s1);
             }
         }
         if (AHEAD && r0 + step < p.rows) load(r0 + step);
         float s[2] = {A::sum(s0), A::sum(s1)};
         team_sum<2, BLOCK>(s, p.team, slots[turn]);
-        const W k1 = A::both(-s[0] * p.inv_c), k2 = A::both(-r2 * (s[1] * p.inv_c));
+        const W k1 = A::both(-rs * (s[0] * p.inv_c)), k2 = A::both(-rs * (s[1] * p.inv_c));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int c = (l + p.team * j) * V;
             if (live && c < p.C) {
                 W o[H];
 #pragma unroll
-                for (int e = 0; e < H; ++e) o[e] = A::fma(d[j][e], k2, A::add(g[j][e], k1));
+                for (int e = 0; e < H; ++e) o[e] = A::fma(h[j][e], k2, A::fma(g[j][e], rr, k1));
                 float f[V];
                 A::to(o, f);
                 store_chunk<T, V>(p.out, row * p.C + c, f);
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormPar
                 const float mean = p.mean[r], rstd = p.rstd[r];
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
-                    dw[e] = fmaf(fy[e] * rstd, fx[e] - mean, dw[e]);
+                    dw[e] = fmaf(fy[e], (fx[e] - mean) * rstd, dw[e]);
                     db[e] += fy[e];
                 }
             }
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormPar
     using A = Cols<V>;
     using W = typename A::W;
     constexpr int H = A::H;
-    W d[J][H], g[J][H], s0 = 0, s1 = 0;
+    W h[J][H], g[J][H], s0 = 0, s1 = 0;
     const W mm = A::both(-mean), rr = A::both(rstd);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -537,28 +537,28 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormPar
             rx[j].get(fx);
             rg[j].get(fy);
             W y[H], w[H];
-            A::from(fx, d[j]);
+            A::from(fx, h[j]);
             A::from(fy, y);
             A::from(fw, w);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
-                d[j][e] = A::add(d[j][e], mm);
-                g[j][e] = A::mul(A::mul(y[e], rr), w[e]);
+                h[j][e] = A::mul(A::add(h[j][e], mm), rr);
+                g[j][e] = A::mul(y[e], w[e]);
                 s0 = A::add(s0, g[j][e]);
-                s1 = A::fma(g[j][e], d[j][e], s1);
+                s1 = A::fma(g[j][e], h[j][e], s1);
             }
         }
     }
     float s[2] = {A::sum(s0), A::sum(s1)};
     team_sum<2, true>(s, kFewThreads, slots);
-    const W k1 = A::both(-s[0] * p.inv_c), k2 = A::both(-(rstd * rstd) * (s[1] * p.inv_c));
+    const W k1 = A::both(-rstd * (s[0] * p.inv_c)), k2 = A::both(-rstd * (s[1] * p.inv_c));
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int c = (threadIdx.x + kFewThreads * j) * V;
         if (c < p.C) {
             W o[H];
 #pragma unroll
-            for (int e = 0; e < H; ++e) o[e] = A::fma(d[j][e], k2, A::add(g[j][e], k1));
+            for (int e = 0; e < H; ++e) o[e] = A::fma(h[j][e], k2, A::fma(g[j][e], rr, k1));
             float f[V];
             A::to(o, f);
             store_chunk<T, V>(p.out, row * p.C + c, f);
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ri
         long long t = blockIdx.x;
         for (int s = 0; s < kNormStages && t < p.tiles; ++s, t += gridDim.x) load(t, s);
     }
-    // Pairs of columns.  With d = x - mean and g' = dy rstd w the gradient of x is g' - sum g' / C - d rstd^2 sum (g' d) / C.
+    // pairs of columns
     constexpr int H = V / 2;
     uint64_t w[J][H], dw[J][H], db[J][H];
 #pragma unroll
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ri
             const bool live = r < n;
             const float mean = live ? stats[turn][0][r] : 0.f, rstd = live ? stats[turn][1][r] : 0.f;
             const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
-            uint64_t d[J][H], g[J][H], s0 = 0, s1 = 0;
+            uint64_t h[J][H], g[J][H], s0 = 0, s1 = 0;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (live && (l + p.team * j) * V < p.C) {
@@ -648,13 +648,13 @@ __global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ri
                     Elem<T>::unpack(*reinterpret_cast<const uint4*>(at + p.team * j * 16 + buf), fy);
 #pragma unroll
                     for (int e = 0; e < H; ++e) {
-                        const uint64_t y = pack2(fy[2 * e], fy[2 * e + 1]), yr = mul2(y, rr);
-                        d[j][e] = add2(pack2(fx[2 * e], fx[2 * e + 1]), mm);
-                        dw[j][e] = fma2(yr, d[j][e], dw[j][e]);
+                        const uint64_t y = pack2(fy[2 * e], fy[2 * e + 1]);
+                        h[j][e] = mul2(add2(pack2(fx[2 * e], fx[2 * e + 1]), mm), rr);
+                        dw[j][e] = fma2(y, h[j][e], dw[j][e]);
                         db[j][e] = add2(db[j][e], y);
-                        g[j][e] = mul2(yr, w[j][e]);
+                        g[j][e] = mul2(y, w[j][e]);
                         s0 = add2(s0, g[j][e]);
-                        s1 = fma2(g[j][e], d[j][e], s1);
+                        s1 = fma2(g[j][e], h[j][e], s1);
                     }
                 }
             }
@@ -664,14 +664,14 @@ __global__ void __launch_bounds__(kNormThreads, norm_ring_blocks(J)) norm_bwd_ri
             sums[0] += other[0];
             sums[1] += other[1];
             team_sum<2, false>(sums, p.team, nullptr);
-            const float k1 = -sums[0] * p.inv_c, k2 = -(rstd * rstd) * (sums[1] * p.inv_c);
+            const float k1 = -rstd * (sums[0] * p.inv_c), k2 = -rstd * (sums[1] * p.inv_c);
             const uint64_t kk1 = pack2(k1, k1), kk2 = pack2(k2, k2);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (live && (l + p.team * j) * V < p.C) {
                     float f[V];
 #pragma unroll
-                    for (int e = 0; e < H; ++e) split2(fma2(d[j][e], kk2, add2(g[j][e], kk1)), f[2 * e], f[2 * e + 1]);
+                    for (int e = 0; e < H; ++e) split2(fma2(h[j][e], kk2, fma2(g[j][e], rr, kk1)), f[2 * e], f[2 * e + 1]);
                     store_chunk<T, V>(to, p.team * j * V, f);
                 }
             }

@@ -113,3 +113,42 @@ def test_gradients_of_odd_rows_whose_last_is_not_finite(dtype, rows, C, cuda_lib
         na.na_layernorm_bwd(dyd, over, wd, mean, rstd, over, dw2, db2)
         assert torch.equal(dw2, dw) and torch.equal(db2, db) and torch.equal(over[:-1], dx[:-1])
     tb.status_ok(na)
+
+
+def norm_slack(g, h, r):
+    """Error bound of dx, as in test_block_ops.py."""
+    mean = lambda a: a.mean(-1, keepdims=True)
+    c1, c2 = np.abs(mean(g)), np.abs(mean(g * h))
+    return r * E * (8 * (np.abs(g) + c1 + np.abs(h) * c2) + (DEPTH + 8) * (mean(np.abs(g)) + np.abs(h) * mean(np.abs(g * h))))
+
+
+def norm_grads_close(na, dtype, x, dy, w, mean, rstd):
+    """dx, dw, db of one call against the reference at the given statistics.  A column's sum here: a thread's run of at
+    most a dozen rows, then shuffles, warps and blocks, within DEPTH steps."""
+    C = x.shape[-1]
+    dx, dw, db = torch.full_like(x, 5.0), torch.full((C,), 9.0, device="cuda"), torch.full((C,), 9.0, device="cuda")
+    na.na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db)
+    tb.status_ok(na)
+    X, D, W, m, r = f64(x), f64(dy), f64(w), f64(mean), f64(rstd)
+    rdx, rdw, rdb = ob.layernorm_bwd(D, X, W, m, r)
+    h = (X - m[:, None]) * r[:, None]
+    close("dx", dx, rdx, norm_slack(D * W, h, r[:, None]), TYPES[dtype])
+    close("dw", dw, rdw, DEPTH * E * np.abs(D * h).sum(0))
+    close("db", db, rdb, DEPTH * E * np.abs(D).sum(0))
+    return dx, dw, db
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [1e-22, 1e22])
+@pytest.mark.parametrize("dtype,rows,C", [
+    ("bf16", 700, 32), ("fp32", 700, 200), ("bf16", 1600, 520), ("fp32", 1600, 520), ("bf16", 9, 2048), ("fp32", 9, 8192),
+    ("bf16", 57, 65), ("fp32", 19, 7), ("fp32", 9, 1001)])
+def test_gradients_of_very_small_and_large_spreads(dtype, rows, C, spread, cuda_lib):
+    """rstd far from 1, its square past the range of fp32 (eps = 0, or statistics from elsewhere): the gradient's own terms
+    are all within it."""
+    x = (randn((rows, C), "fp32", 1).double() * spread).to(TYPES[dtype]).cuda()
+    dy, w = randn((rows, C), dtype, 2).cuda(), (1 + 0.3 * randn((C,), "fp32", 3)).cuda()
+    X = x.double()
+    mean = X.mean(-1)
+    rstd = (X - mean[:, None]).square().mean(-1).rsqrt().clamp(max=4 / spread)   # rows of few channels too
+    norm_grads_close(cuda_lib, dtype, x, dy, w, mean.float(), rstd.float())
