@@ -394,10 +394,13 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD>()) win_kern
                         for (int i = 0; i < NV; ++i) sum += v[i] == 0.f ? 0.f : v[i] * g[i];
                         sum = lanes_sum<L>(sum);
                         if (!fine) q = sum * inv;
+                    }
+                    // by the row's own sum: the rows that share the warp, or lie past the end, have no say in its bits
+                    if (fine) {
+                        row_grad(v, g, k, q);
+                    } else {
 #pragma unroll
                         for (int i = 0; i < NV; ++i) v[i] = v[i] == 0.f ? 0.f : v[i] * k * (g[i] - q);
-                    } else {
-                        row_grad(v, g, k, q);
                     }
                     row_store<T, L, J>(v, m == 0 ? s1 : s2, a);
                     if (m == 1 && r < nrows && l == 0) p.dlam[row0 + r] = -p.drop.gain * q;

@@ -83,6 +83,42 @@ def test_logits_far_from_zero(dtype, K, cuda_lib):
     close("dlam", gl, rl, row.reshape(-1, heads).sum(0) + (shape[1] / 8 + 300) * E * each)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [1, 5, 81, 399, 1001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_a_row_does_not_depend_on_its_neighbours(dtype, K, cuda_lib):
+    """Bit for bit, the sign of zeros at masked places included: rows beside one whose gradient is infinite, and rows
+    after a launch that leaves NaN in shared memory."""
+    na = cuda_lib
+    L = max(K, 37)   # 3 L rows: no whole number of a kernel's passes
+    shape, kernel = (1, L, 3, K), (K,)
+    x1, x2, dy = tb.logits(shape, dtype, 1, True).cuda(), tb.logits(shape, dtype, 2, True).cuda(), randn(shape, dtype, 3).cuda()
+    lam = torch.rand(3, device="cuda")
+    x1[0, 20, 1], x2[0, 20, 1] = 0.5, 0.25   # a row without masked places
+    ill = dy.clone()
+    ill[0, 20, 1] = float("inf")
+    others = torch.ones(shape[:-1], dtype=torch.bool, device="cuda")
+    others[0, 20, 1] = False
+
+    def grads(dy):
+        a, b, c, l = torch.empty_like(x1), torch.empty_like(x1), torch.empty_like(x1), torch.empty(shape[:-1], device="cuda")
+        na.na_softmax_dropout_bwd(x1, dy, a, kernel, 0.0, None)
+        na.na_diff_softmax_bwd(x1, x2, lam[None, None].expand(shape[:-1]).contiguous(), dy, b, c, l, kernel)
+        return a, b, c, l
+
+    def litter(value):   # every multiprocessor's shared memory
+        t = torch.full((1, max(K, 400000 // K), 3, K), value, dtype=x1.dtype, device="cuda")
+        na.na_softmax_dropout_bwd(t, t, torch.empty_like(t), kernel, 0.0, None)
+
+    litter(0.0)
+    ref = grads(dy)
+    for got in (grads(ill), (litter(float("nan")), grads(dy))[1]):
+        for name, g, r in zip(("dx", "dx1", "dx2", "dlam"), got, ref):
+            assert torch.equal(bits(g)[others], bits(r)[others]), name
+    assert torch.isnan(grads(ill)[0][0, 20, 1]).all()
+    tb.status_ok(na)
+
+
 # ---------------------------------------------------------------------------------------------
 # Layer norm
 # ---------------------------------------------------------------------------------------------
