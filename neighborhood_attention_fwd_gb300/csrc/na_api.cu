@@ -10,7 +10,9 @@
 #include <atomic>
 #include <map>
 #include <mutex>
+#include <set>
 #include <tuple>
+#include <utility>
 
 #include "../../include/na.h"
 #include "na_device.cuh"
@@ -550,6 +552,26 @@ void unfused_tma_maps(na::UnfParams& p, int B, const void* src, const void* w, n
 }  // namespace
 
 namespace na {
+bool allow_shared(const void* kernel) {
+    static std::mutex mu;
+    static std::set<std::pair<const void*, int>> done;
+    int dev = 0, most = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({kernel, dev})) return true;
+    cudaFuncAttributes a{};
+    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess ||
+        cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(a.sharedSizeBytes)) !=
+            cudaSuccess)
+        return false;
+    try {
+        done.insert({kernel, dev});
+    } catch (...) {   // no memory for the note: the next call sets the same limit again
+    }
+    return true;
+}
+
 na_status device_status_word(unsigned** out) { return status_ptr(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 uint32_t wait_withhold() { return g_withhold.load(); }

@@ -143,6 +143,11 @@ struct UnfParams {
     unsigned long long wait_ns; // time limit of one wait
 };
 
+// Lets launches of a kernel on the current device take all of a block's shared memory; false on an error.  The limit belongs
+// to the kernel, not to the launch: set to each launch's own size, one host thread's launch fails on the limit that another
+// thread has just lowered.  It is set once per kernel and device, and never lowered.
+bool allow_shared(const void* kernel);
+
 // Tokens per block of the bias-gradient reduction's first stage, and the size of its partial sums.
 int rpb_grad_tokens_per_block(int K);
 size_t rpb_grad_workspace_bytes(long long tokens, int heads, int K, int table);

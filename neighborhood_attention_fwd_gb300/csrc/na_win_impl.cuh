@@ -641,9 +641,8 @@ na_status run_win(WinParams& p, cudaStream_t s) {
     p.stages = dropping ? 2 : 3;
     const size_t smem = static_cast<size_t>(p.stages) * stage;
     const auto kernel = win_kernel<T, DIFF, BWD, L, J>;
-    if (smem > 40 * 1024 &&   // 48 KB without asking, static shared memory included
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return NA_ERR_CUDA;
+    // 48 KB without asking, static shared memory included
+    if (smem > 40 * 1024 && !allow_shared(reinterpret_cast<const void*>(kernel))) return NA_ERR_CUDA;
     int per_sm = static_cast<int>(kWinSmem / (smem + 1024));
     constexpr int kMost = win_blocks<DIFF, BWD>();
     per_sm = per_sm < 1 ? 1 : (per_sm > kMost ? kMost : per_sm);

@@ -119,6 +119,42 @@ def test_a_row_does_not_depend_on_its_neighbours(dtype, K, cuda_lib):
     tb.status_ok(na)
 
 
+@pytest.mark.gpu
+def test_host_threads_with_rows_of_one_kernel(cuda_lib):
+    """Rows of 363 and 383 weights are the same kernel's with different amounts of shared memory, both over what a launch
+    has without asking; calls of several host threads do not take it from one another.  The library is called as it
+    is, so that the threads meet there and not before."""
+    na = cuda_lib
+    call, stream = na.load().na_diff_softmax_bwd, torch.cuda.current_stream().cuda_stream
+    start, failed, work = threading.Barrier(6), [], []
+    for i in range(6):
+        K = (363, 383)[i % 2]
+        shape = (1, 400, 1, K)
+        x1, x2, dy = (randn(shape, "bf16", i // 2 * 3 + j).cuda() for j in range(3))
+        lam = torch.rand(shape[:-1], device="cuda")
+        want, got = ([torch.empty_like(x1), torch.empty_like(x1), torch.empty_like(lam)] for _ in range(2))
+        na.na_diff_softmax_bwd(x1, x2, lam, dy, *want, (K,))
+        p = lambda t: t.data_ptr()
+        args = (p(x1), p(x2), p(lam), 1, p(dy), *map(p, got), 1, 1, na._ints((400,)), 1, na._ints((K,)), 0.0, None, na.NA_BF16,
+                None, 0, stream)
+        work.append((args, want, got, (x1, x2, dy, lam)))
+    torch.cuda.synchronize()
+
+    def run(args):
+        start.wait(60)
+        failed.extend(st for st in (call(*args) for _ in range(4000)) if st)
+
+    threads = [threading.Thread(target=run, args=(w[0],)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    tb.status_ok(na)
+    assert not failed, f"{len(failed)} calls refused, status {set(failed)}"
+    for _, want, got, _ in work:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 # ---------------------------------------------------------------------------------------------
 # Layer norm
 # ---------------------------------------------------------------------------------------------
