@@ -79,7 +79,15 @@ std::atomic<uint32_t> g_withhold{0};
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+// The tensor map encoder, ready for use on this host thread: encoding takes a current context, which a thread that has made no
+// runtime call of its own lacks (naming a device does not give it one, looking a symbol up does).
 na_status get_encoder() {
+    static thread_local bool bound = false;
+    if (!bound) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return NA_ERR_CUDA;
+        bound = true;
+    }
     std::lock_guard<std::mutex> lk(g_mu);
     if (g_encode) return NA_OK;
     void* fn = nullptr;

@@ -1,0 +1,65 @@
+"""Calls from host threads of the program's own, as a loader or a server makes them."""
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def attention(na, q, k, v, kernel):
+    """The fused forward and gradients, and the unfused chain: [o, lse, dq, dk, dv, weights, sums, and their gradients]."""
+    e = torch.empty_like
+    o, lse, d = e(q), torch.empty(q.shape[:-1], device="cuda"), [e(q) for _ in range(3)]
+    na.na_fwd(q, k, v, o, lse, kernel)
+    na.na_bwd(q, k, v, o, v, lse, *d, kernel)
+    K = kernel[0] * kernel[1]
+    w, dw, av, dv, dq, dk = torch.empty(q.shape[:-1] + (K,), dtype=q.dtype, device="cuda"), None, e(q), e(q), e(q), e(q)
+    na.na_qk(q, k, w, kernel)
+    na.na_softmax(w, w, kernel)
+    na.na_av(w, v, av, kernel)
+    dw = e(w)
+    na.na_av_bwd(q, w, v, dw, dv, kernel)
+    na.na_qk_bwd(dw, q, k, dq, dk, kernel)
+    return [o, lse, *d, w, av, dw, dv, dq, dk]
+
+
+def test_the_first_calls_of_a_thread(cuda_lib):
+    """A thread that has made no CUDA call yet gets what the main thread gets, bit for bit."""
+    na = cuda_lib
+    q, k, v = (bf16((1, 20, 24, 2, 32), i) for i in range(3))
+    e = torch.empty_like
+    ref = attention(na, q, k, v, (5, 5))
+    o, lse = e(q), torch.empty(q.shape[:-1], device="cuda")
+    w, av, dq, dk = e(ref[5]), e(q), e(q), e(q)
+    torch.cuda.synchronize()
+    calls = {   # each the first of a thread of its own; outputs made before
+        "na_fwd": lambda: na.na_fwd(q, k, v, o, lse, (5, 5)),
+        "na_qk": lambda: na.na_qk(q, k, w, (5, 5)),
+        "na_av": lambda: na.na_av(ref[5], v, av, (5, 5)),
+        "na_qk_bwd": lambda: na.na_qk_bwd(ref[7], q, k, dq, dk, (5, 5)),
+    }
+    failed = {}
+
+    def run(name, call):
+        try:
+            call()
+        except Exception as ex:   # noqa: BLE001  (handed to the test's own thread)
+            failed[name] = ex
+
+    for item in calls.items():
+        t = threading.Thread(target=run, args=item)
+        t.start()
+        t.join()
+    assert not failed, failed
+    torch.cuda.synchronize()
+    logits = e(w)
+    na.na_qk(q, k, logits, (5, 5))
+    for name, got, want in (("o", o, ref[0]), ("lse", lse, ref[1]), ("logits", w, logits), ("sums", av, ref[6]), ("dq", dq, ref[9]),
+                            ("dk", dk, ref[10])):
+        assert torch.equal(got, want), name
