@@ -1650,9 +1650,9 @@ template <int D, int WHICH, bool F16, int SB>
 int launch_tc_sb(const TcParams& p0, cudaStream_t stream) {
     const int smem = p0.plan.smem_bytes;
     auto kernel = tc_kernel<D, WHICH, F16, SB>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (!allow_shared(reinterpret_cast<const void*>(kernel))) return static_cast<int>(cudaErrorInvalidValue);
     if (p0.plan.ctas <= 0) return 0;
+    cudaError_t e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return static_cast<int>(e);
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)

@@ -1545,8 +1545,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                     const long long units = batch * p.L[0] * p.L[1] * p.strips2 * p.heads;
                     const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
                     auto run = [&](auto kernel) {
-                        if (smem > 48 * 1024)
-                            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                        if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(kernel));
                         kernel<<<g2, b2, smem, s>>>(p);
                     };
                     if (p.rpb) run(dot_tma_kernel<T, D, true>);
@@ -1560,8 +1559,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                 const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
                 const size_t smem = static_cast<size_t>(kMmaThreads / 32) * 16 * p.K * sizeof(T);
                 auto run = [&](auto kernel, size_t bytes) {
-                    if (bytes > 48 * 1024)
-                        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+                    if (bytes > 48 * 1024) allow_shared(reinterpret_cast<const void*>(kernel));
                     kernel<<<g2, b2, bytes, s>>>(p);
                 };
                 if (smem <= 200 * 1024) {   // stage the rows; past that, write each weight directly
@@ -1587,9 +1585,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                     const long long batch = p.rows / (static_cast<long long>(p.L[0]) * p.L[1] * p.L[2] * p.heads);
                     const long long units = batch * p.L[0] * p.L[1] * p.strips2 * p.heads;
                     const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
-                    if (smem > 48 * 1024)
-                        cudaFuncSetAttribute(wsum_tma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                    if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(wsum_tma_kernel<T, D>));
                     wsum_tma_kernel<T, D><<<g2, b2, smem, s>>>(p);
                     done = true;
                 }
@@ -1600,9 +1596,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                     const long long batch = p.rows / (static_cast<long long>(p.L[0]) * p.L[1] * p.L[2] * p.heads);
                     const long long units = batch * p.L[0] * p.L[1] * p.strips2 * p.heads;
                     const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
-                    if (smem > 48 * 1024)
-                        cudaFuncSetAttribute(wsum_mma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                    if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(wsum_mma_kernel<T, D>));
                     wsum_mma_kernel<T, D><<<g2, b2, smem, s>>>(p);
                     done = true;
                 }
@@ -1619,9 +1613,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                     const long long batch = p.rows / (static_cast<long long>(p.L[0]) * p.L[1] * p.L[2] * p.heads);
                     const long long units = batch * p.L[0] * p.L[1] * p.strips2 * p.heads;
                     const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
-                    if (smem > 48 * 1024)
-                        cudaFuncSetAttribute(scatter_tma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                    if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(scatter_tma_kernel<T, D>));
                     scatter_tma_kernel<T, D><<<g2, b2, smem, s>>>(p);
                     done = true;
                 }
@@ -1632,9 +1624,7 @@ int launch_op_td(Op op, const UnfParams& p, cudaStream_t s) {
                     const long long batch = p.rows / (static_cast<long long>(p.L[0]) * p.L[1] * p.L[2] * p.heads);
                     const long long units = batch * p.L[0] * p.L[1] * p.strips2 * p.heads;
                     const dim3 g2(static_cast<unsigned>((units * 32 + kMmaThreads - 1) / kMmaThreads)), b2(kMmaThreads);
-                    if (smem > 48 * 1024)
-                        cudaFuncSetAttribute(scatter_mma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                    if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(scatter_mma_kernel<T, D>));
                     scatter_mma_kernel<T, D><<<g2, b2, smem, s>>>(p);
                     done = true;
                 }
@@ -1674,7 +1664,7 @@ int launch_softmax_t(bool bwd, const UnfParams& p, cudaStream_t s) {
             const dim3 grid(launch_blocks(warps * 32)), block(kThreads);
             const int smem = (kThreads / 32) * kSoftRows8 * p.K * 2 * (bwd ? 2 : 1);
             auto run = [&](auto kernel) {
-                if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(kernel));
                 kernel<<<grid, block, smem, s>>>(p);
             };
             if (bwd) run(softmax8_kernel<T, true>);
@@ -1718,8 +1708,7 @@ int launch_unfused_rpb_grad(const UnfParams& p, int elem, long long tokens, floa
     if (smem > 227 * 1024) return static_cast<int>(cudaErrorInvalidValue);   // heads x table too large
     const dim3 grid(static_cast<unsigned>(chunks));
     auto run = [&](auto kernel) {
-        if (smem > 48 * 1024)   // many heads or very large windows: more than the default
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (smem > 48 * 1024) allow_shared(reinterpret_cast<const void*>(kernel));   // many heads or very large windows: more than the default
         kernel<<<grid, kThreads, smem, s>>>(p, tokens, tpb, partial);
     };
     if (elem == 0)
