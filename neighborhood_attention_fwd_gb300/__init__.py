@@ -116,8 +116,18 @@ def na_strerror(status: int) -> str:
     return load().na_strerror(int(status)).decode()
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fits(what, *sizes):
+    """Refuses sizes that a C int would cut."""
+    if max(sizes, default=0) > _INT_MAX:
+        raise NAError(2, f"{what}: a size past 2^31 - 1")
+
+
 def _ints(vals):
     vals = [int(x) for x in vals]
+    _fits("sizes", *vals)
     return (ctypes.c_int * len(vals))(*vals)
 
 
@@ -134,6 +144,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _geometry(q: torch.Tensor):
     if q.dim() < 4 or q.dim() > 6:
         raise ValueError("expected [B, L_1..L_n, heads, D] with n in 1..3")
+    _fits("sizes", *q.shape)
     B = q.shape[0]
     spatial = tuple(int(s) for s in q.shape[1:-2])
     return B, len(spatial), spatial, int(q.shape[-2]), int(q.shape[-1])
@@ -290,6 +301,7 @@ def _attn_geometry(attn: torch.Tensor, kernel):
         raise ValueError("kernel needs one entry per spatial axis")
     if int(attn.shape[-1]) != _window_size(kernel):
         raise ValueError(f"last axis of the attention weights must be {_window_size(kernel)}")
+    _fits("sizes", *attn.shape)
     return int(attn.shape[0]), ndim, tuple(int(s) for s in attn.shape[1:-2]), int(attn.shape[-2]), kernel
 
 
@@ -426,12 +438,22 @@ def na_mask_window(attn, sizes, kernel, dilation=None, stream=None):
 @functools.lru_cache(maxsize=1024)
 def _sizes(vals):
     """A C int array of a tuple of sizes."""
+    _fits("sizes", *vals)
     return (ctypes.c_int * len(vals))(*vals)
+
+
+@functools.lru_cache(maxsize=1024)
+def _grid(shape):
+    """The spatial axes of [B, L.., heads, D] as a C int array."""
+    _fits("sizes", *shape)
+    return _sizes(shape[1:-2])
 
 
 @functools.lru_cache(maxsize=1024)
 def _origins(vals):
     """A C int64 array of a grid's first positions."""
+    if not all(-2 ** 63 <= v < 2 ** 63 for v in vals):
+        raise ValueError("origin must fit 64 bits")
     return (ctypes.c_int64 * len(vals))(*vals)
 
 
@@ -552,6 +574,8 @@ def _rope(call, what, q, k, q_out, k_out, freqs, origin, stream):
         if shape_k != shape and (len(shape_k) != ndim + 3 or shape_k[:-2] != shape[:-2] or shape_k[-1] != shape[-1]):
             raise ValueError("k must have the axes of q but for the heads")
         heads_k = shape_k[-2]
+        if heads_k > _INT_MAX:
+            _fits(what, heads_k)
         _like(k, shape_k, dtype, "k")
         _like(k_out, shape_k, dtype, "k_out")
     stream = _launch_stream(stream, q, k, q_out, k_out)
@@ -559,7 +583,7 @@ def _rope(call, what, q, k, q_out, k_out, freqs, origin, stream):
         origin = _origins((origin,) * ndim if isinstance(origin, int) else tuple(map(int, origin)))
         if len(origin) != ndim:
             raise ValueError("origin needs one entry per spatial axis")
-    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), shape[0], ndim, _sizes(shape[1:-2]), shape[-2],
+    st = call(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), shape[0], ndim, _grid(shape), shape[-2],
               heads_k, shape[-1], freqs._rot, freqs._freq, origin, freqs.amplitude, freqs._code, _code(q), stream)
     if st:
         _ok(st, what)
@@ -581,6 +605,8 @@ def _rows(x):
     n = x.numel()
     if not shape or n == 0:
         raise ValueError("expected [.., C] with at least one element")
+    if shape[-1] > _INT_MAX:
+        _fits("channels", shape[-1])
     return shape, n // shape[-1], shape[-1]
 
 
@@ -620,7 +646,7 @@ def _norm_need(rows, C, code):
 
 
 def na_layernorm_bwd_workspace_size(rows: int, C: int, dtype=torch.bfloat16) -> int:
-    return _norm_need(int(rows), int(C), _CODES[dtype])
+    return _norm_need(int(rows), int(C), _CODES[dtype]) if int(C) <= _INT_MAX else 0
 
 
 def na_layernorm_bwd(dy, x, w, mean, rstd, dx, dw=None, db=None, workspace=None, stream=None):
@@ -660,6 +686,7 @@ def _window_of(shape, kernel):
         raise ValueError("kernel needs one entry per spatial axis")
     if shape[-1] != math.prod(kernel):
         raise ValueError(f"last axis of the attention weights must be {math.prod(kernel)}")
+    _fits("sizes", *shape)
     return shape[0], ndim, _sizes(tuple(shape[1:-2])), shape[-2], _sizes(kernel)
 
 
@@ -724,6 +751,8 @@ def na_diff_softmax(x1, x2, lam, y, kernel, p: float = 0.0, rng=None, stream=Non
 
 def na_diff_softmax_bwd_workspace_size(B, spatial, heads, kernel) -> int:
     kernel = (kernel,) * len(spatial) if isinstance(kernel, int) else tuple(kernel)
+    if max(int(B), int(heads), *map(int, spatial), *map(int, kernel)) > _INT_MAX:
+        return 0
     return int(load().na_diff_softmax_bwd_workspace_size(int(B), len(spatial), _ints(spatial), int(heads), _ints(kernel)))
 
 

@@ -224,3 +224,54 @@ def test_gradients_of_very_small_and_large_spreads(dtype, rows, C, spread, cuda_
     mean = X.mean(-1)
     rstd = (X - mean[:, None]).square().mean(-1).rsqrt().clamp(max=4 / spread)   # rows of few channels too
     norm_grads_close(cuda_lib, dtype, x, dy, w, mean.float(), rstd.float())
+
+
+# ---------------------------------------------------------------------------------------------
+# The binding
+# ---------------------------------------------------------------------------------------------
+
+BIG = 2 ** 32 + 7   # 7 to a C int
+UNSUPPORTED = 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    nabuild.build()
+    return nab.load()
+
+
+def test_sizes_past_32_bits_are_refused(lib, monkeypatch):
+    """Every size that the library takes as a C int; the tensors have no memory, so no call could be launched."""
+    monkeypatch.setattr(nab, "_launch_stream", lambda stream, *tensors: None)
+    m = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")
+    f32 = torch.float32
+    f = nab.RopeFreqs.scaled((16,))
+    rope = lambda q, k: (q, k, q, k, f)
+    bad = [
+        (nab.na_rope, rope(m(1, BIG, 1, 16), None)), (nab.na_rope, rope(m(BIG, 1, 1, 16), None)),
+        (nab.na_rope, rope(m(1, 1, BIG, 16), None)), (nab.na_rope_bwd, rope(m(1, 1, 1, 16), m(1, 1, BIG, 16))),
+        (nab.na_rope, rope(m(1, 1, 1, BIG), None)),
+        (nab.na_layernorm, (m(2, BIG), None, None, m(2, BIG))),
+        (nab.na_layernorm_bwd, (m(2, BIG), m(2, BIG), None, m(2, dtype=f32), m(2, dtype=f32), m(2, BIG))),
+    ]
+    for shape, kernel in (((1, BIG, 1, 3), 3), ((BIG, 4, 1, 3), (3,)), ((1, 4, BIG, 3), (3,))):
+        x, lam = m(*shape), m(*shape[:-1], dtype=f32)
+        bad += [(nab.na_softmax_dropout, (x, x, kernel, 0.0, None)), (nab.na_softmax_dropout_bwd, (x, x, x, kernel, 0.0, None)),
+                (nab.na_diff_softmax, (x, x, lam, x, kernel)), (nab.na_diff_softmax_bwd, (x, x, lam, x, x, x, lam, kernel))]
+    for call, args in bad:
+        with pytest.raises(nab.NAError) as e:
+            call(*args)
+        assert e.value.status == UNSUPPORTED, (call.__name__, [tuple(a.shape) for a in args if torch.is_tensor(a)])
+    assert nab.na_layernorm_bwd_workspace_size(8, BIG) == 0
+    assert nab.na_layernorm_bwd_workspace_size(BIG, 8) > 0          # rows are counted in 64 bits
+    assert nab.na_diff_softmax_bwd_workspace_size(1, (BIG,), 1, (3,)) == 0
+    assert nab.na_diff_softmax_bwd_workspace_size(BIG, (8,), 1, (3,)) == 0
+    assert nab.na_diff_softmax_bwd_workspace_size(1, (8,), BIG, (3,)) == 0
+
+
+def test_origins_past_64_bits_are_refused(lib, monkeypatch):
+    monkeypatch.setattr(nab, "_launch_stream", lambda stream, *tensors: None)
+    q = torch.empty((1, 4, 4, 1, 16), device="meta")
+    for origin in (1 << 63, (0, -(1 << 63) - 1)):
+        with pytest.raises(ValueError):
+            nab.na_rope(q, None, q, None, nab.RopeFreqs.scaled((8, 8)), origin=origin)
