@@ -207,6 +207,8 @@ def na_bwd(q, k, v, o, dO, lse, dQ, dK, dV, kernel, dilation=None, scale=None, w
     _check(lse, q.shape[:-1], torch.float32, "lse")
     kernel, dilation = _kd(ndim, kernel, dilation)
     scale = D ** -0.5 if scale is None else float(scale)
+    if workspace is not None:
+        _check(workspace, workspace.shape, workspace.dtype, "workspace")
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = load().na_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(),
                        dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), B, ndim, _ints(spatial), heads, D,
@@ -337,6 +339,8 @@ def na_rpb_grad(dattn, drpb, kernel, dilation=None, workspace=None, stream=None)
     kernel, dilation = _kd(ndim, kernel, dilation)
     _check(dattn, dattn.shape, dattn.dtype, "dattn")
     _check(drpb, _rpb_shape(heads, kernel), torch.float32, "drpb")
+    if workspace is not None:
+        _check(workspace, workspace.shape, workspace.dtype, "workspace")
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = load().na_rpb_grad(dattn.data_ptr(), drpb.data_ptr(), B, ndim, _ints(spatial), heads, _ints(kernel),
                             _ints(dilation), _dtype_code(dattn), ws_ptr, ws_bytes, _stream(stream))
@@ -495,7 +499,11 @@ def _workspace(ws, stream, need, device):
             return None, None, 0
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         return ws, ws.data_ptr(), n
-    return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())
+    if ws is None:
+        return None, None, 0
+    if not ws.is_contiguous():   # a broadcast view has fewer bytes than its elements
+        raise ValueError("workspace must be contiguous")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 _CODES = {torch.bfloat16: NA_BF16, torch.float32: NA_FP32, torch.float16: NA_FP16}

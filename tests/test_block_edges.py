@@ -275,3 +275,31 @@ def test_origins_past_64_bits_are_refused(lib, monkeypatch):
     for origin in (1 << 63, (0, -(1 << 63) - 1)):
         with pytest.raises(ValueError):
             nab.na_rope(q, None, q, None, nab.RopeFreqs.scaled((8, 8)), origin=origin)
+
+
+def test_a_workspace_without_memory_of_its_own_is_refused():
+    """A workspace's bytes are counted from its elements, so a broadcast view would promise more than there is."""
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(4, 4).t()):
+        with pytest.raises(ValueError):
+            nab._workspace(ws, None, lambda: 1 << 20, "cpu")
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    assert nab._workspace(ws, None, lambda: 1 << 20, "cpu") == (ws, ws.data_ptr(), 1 << 20)
+
+
+@pytest.mark.gpu
+def test_workspaces_elsewhere_are_refused(cuda_lib):
+    """On the host, or a broadcast view of a few bytes: every call that takes a workspace raises before it launches."""
+    na = cuda_lib
+    e = torch.empty_like
+    q = randn((1, 8, 8, 2, 32), "bf16", 1).cuda()
+    lse = torch.zeros(q.shape[:-1], device="cuda")
+    x, lam = randn((1, 8, 8, 2, 9), "bf16", 2).cuda(), torch.rand(2, device="cuda")
+    rows, w, st = randn((64, 64), "bf16", 3).cuda(), torch.rand(64, device="cuda"), torch.ones(64, device="cuda")
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)):
+        for call in (lambda: na.na_bwd(q, q, q, q, q, lse, e(q), e(q), e(q), (3, 3), workspace=ws),
+                     lambda: na.na_rpb_grad(x, torch.empty(2, 5, 5, device="cuda"), (3, 3), workspace=ws),
+                     lambda: na.na_layernorm_bwd(rows, rows, w, st, st, e(rows), e(w), e(w), workspace=ws),
+                     lambda: na.na_diff_softmax_bwd(x, x, lam, x, e(x), e(x), e(lam), (3, 3), workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
+    tb.status_ok(na)
