@@ -798,12 +798,8 @@ na_status run_norm(const NormParams& p, const NormPlan& n, cudaStream_t s) {
     const int threads = BLOCK ? n.team : kNormThreads;
     if constexpr (BWD && !BLOCK && V > 1) {
         const size_t ring = 2ull * kNormStages * n.tile * p.C * sizeof(T), sums = static_cast<size_t>(kNormThreads / 32) * 2 * p.C * sizeof(float);
-        const size_t smem = ring > sums ? ring : sums;
-        const auto kernel = norm_bwd_ring_kernel<T, J>;
-        if (smem > 40 * 1024 &&   // 48 KB without asking, static shared memory included
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-            return NA_ERR_CUDA;
-        kernel<<<n.blocks, threads, smem, s>>>(p);
+        // at most 32 KB, which a launch has without asking: one pass of the teams is up to 8 KB of x, a tile of several no more
+        norm_bwd_ring_kernel<T, J><<<n.blocks, threads, ring > sums ? ring : sums, s>>>(p);
     } else if constexpr (BWD) {
         const size_t smem = BLOCK || !p.partial ? 0 : static_cast<size_t>(kNormThreads / 32) * 2 * p.C * sizeof(float);
         norm_bwd_kernel<T, V, J, BLOCK><<<n.blocks, threads, smem, s>>>(p);

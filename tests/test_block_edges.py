@@ -155,6 +155,24 @@ def test_host_threads_with_rows_of_one_kernel(cuda_lib):
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", tb.WIN, ids=tb.WIN_IDS)
+def test_zeros_are_where_the_reference_has_them(case, cuda_lib):
+    """Dropped and masked places are zero, and places whose weight is well within the type's range are not."""
+    na = cuda_lib
+    dtype, B, grid, heads, kernel = case
+    shape = (B, *grid, heads, math.prod(kernel))
+    x = tb.logits(shape, dtype, 21, True)
+    y = torch.full_like(x, 5.0).cuda()
+    na.na_softmax_dropout(x.cuda(), y, kernel, 0.2, tb.rng_state())
+    tb.status_ok(na)
+    ref = ob.softmax_dropout(f64(x), ob.dropout_factor(x.numel(), 0.2, tb.SEED, tb.OFFSET).reshape(shape))
+    zero = f64(y) == 0
+    assert zero[ref == 0].all()
+    # exponentials under 2^-126 count as zero; a weight times the gain is at most 1.25 of its exponential
+    assert not zero[ref > max(2.0 ** -120, torch.finfo(TYPES[dtype]).smallest_normal)].any()
+
+
 # ---------------------------------------------------------------------------------------------
 # Layer norm
 # ---------------------------------------------------------------------------------------------
@@ -224,6 +242,51 @@ def test_gradients_of_very_small_and_large_spreads(dtype, rows, C, spread, cuda_
     mean = X.mean(-1)
     rstd = (X - mean[:, None]).square().mean(-1).rsqrt().clamp(max=4 / spread)   # rows of few channels too
     norm_grads_close(cuda_lib, dtype, x, dy, w, mean.float(), rstd.float())
+
+
+NORM_TURNS = [
+    # dtype, rows, C, whether the gradients take the one launch of few wide rows
+    # gradients of block-wide rows on both sides of that launch's limits, of every type and number of chunks to a thread
+    ("fp32", 1536, 520, True), ("fp32", 1537, 520, False), ("fp32", 1537, 2048, False), ("fp32", 1537, 8192, False),
+    ("fp16", 1536, 2048, True), ("fp16", 1537, 2048, False), ("bf16", 1537, 2048, False), ("bf16", 1537, 8192, False),
+    ("fp32", 1024, 8192, True), ("fp32", 1025, 8192, False),
+    # several turns of a block's loop: wide rows, odd rows, and rings of five tiles a block and more
+    ("fp32", 2600, 2048, False), ("fp32", 1300, 8192, False), ("bf16", 6000, 2048, False), ("bf16", 3000, 1001, False),
+    ("fp32", 3000, 1001, False), ("fp16", 1300, 4099, False), ("bf16", 20000, 33, False), ("bf16", 100000, 64, False),
+    ("fp16", 100000, 40, False), ("fp32", 20000, 200, False), ("fp32", 60000, 72, False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows,C,few", NORM_TURNS, ids=[str(c) for c in NORM_TURNS])
+def test_layernorm_of_many_turns(dtype, rows, C, few, cuda_lib):
+    na = cuda_lib
+    assert (na.na_layernorm_bwd_workspace_size(rows, C, TYPES[dtype]) == 0) == few
+    x = (randn((rows, C), "fp32", 1) * 1.5 + randn((rows, 1), "fp32", 2)).to(TYPES[dtype]).cuda()
+    w, b = (1 + 0.3 * randn((C,), "fp32", 3)).cuda(), randn((C,), "fp32", 4).cuda()
+    dy = randn((rows, C), dtype, 5).cuda()
+    y, mean, rstd = torch.full_like(x, 5.0), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    na.na_layernorm(x, w, b, y, mean, rstd)
+    tb.status_ok(na)
+    X, W, Bv = f64(x), f64(w), f64(b)
+    ry, rm, rr = ob.layernorm(X, W, Bv, float(np.float32(1e-5)))
+    em = DEPTH * E * np.abs(X).mean(-1)
+    er = (DEPTH + 8) * E + (em * rr) ** 2
+    close("mean", mean, rm, em)
+    close("rstd", rstd, rr, rr * er)
+    h = np.abs(X - rm[:, None]) * rr[:, None]
+    W = np.abs(W)
+    close("y", y, ry, W * (rr * em)[:, None] + h * W * (er[:, None] + 8 * E) + 2 * E * np.abs(Bv), TYPES[dtype])
+    dx, dw, db = norm_grads_close(na, dtype, x, dy, w, mean, rstd)
+    z = x.clone()
+    na.na_layernorm(z, w, b, z)
+    assert torch.equal(z, y)
+    for over in (0, 1):   # dx over x, over dy
+        t = [x.clone(), dy.clone()]
+        dw2, db2 = torch.empty_like(dw), torch.empty_like(db)
+        na.na_layernorm_bwd(t[1], t[0], w, mean, rstd, t[over], dw2, db2)
+        assert torch.equal(t[over], dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+    tb.status_ok(na)
 
 
 # ---------------------------------------------------------------------------------------------
