@@ -372,6 +372,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// A softmax's exponentials exp(x - m) are taken as 2^(x c - round(m c)), c = log2 e: every exponent of the row is off by the
+// rounding of m c, up to |m| 2^-23.5.  That is a common factor, which cancels against the sum while the exponentials stay in
+// range: a sixteenth in the exponent at 2^20, hundreds from 10^10 on, and a mask of the lowest finite value overflows.  Rows
+// whose maximum m is beyond this limit are shifted before, not after, that product; their largest exponent is then 0.
+constexpr float kFarLogit = 1048576.f;
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

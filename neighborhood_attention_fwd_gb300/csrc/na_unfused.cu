@@ -443,6 +443,30 @@ __device__ __forceinline__ float half_maxf(float v) {
     return v;
 }
 
+// The powers of two of a row's exponentials exp(v - m).  Far from zero (kFarLogit) values of fp32 are shifted by m first, one more
+// operation for each; values of two bytes are thousands apart there, so that all but the largest have weight 0 in any
+// base, and in base 2 the product with m is exact.  A row of -inf alone gives NaN.
+template <typename T>
+struct RowPowers {
+    float c, b, off;
+    __device__ __forceinline__ explicit RowPowers(float m) {
+        const bool near = fabsf(m) < kFarLogit;
+        if constexpr (sizeof(T) == 2) {
+            const float mc = m * kLog2eF;
+            c = near ? kLog2eF : 1.f;
+            b = near ? -mc : -m;
+        } else {
+            c = kLog2eF;
+            off = near ? 0.f : m;
+            b = -(m - off) * kLog2eF;
+        }
+    }
+    __device__ __forceinline__ float operator()(float v) const {
+        if constexpr (sizeof(T) == 4) v -= off;
+        return fast_exp2(fmaf(v, c, b));
+    }
+};
+
 // y = softmax(x) over each row of K weights (x and y may be the same tensor: every read of a row
 // happens before its first write).  Rows of at most kRegK weights: two per warp, lanes 16 h .. 16 h + 15
 // on row 2 w + h (the warp's pair of rows, row2 = 2 w); longer rows: one per warp.
@@ -465,10 +489,10 @@ __device__ __forceinline__ void softmax_pair(const UnfParams& p, long long row2,
     }
     m = half_maxf(m);
     float l = 0.f;
-    const float ml2 = m * kLog2eF;
+    const RowPowers<T> power(m);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        v[i] = live && l16 + 16 * i < p.K ? fast_exp2(fmaf(v[i], kLog2eF, -ml2)) : 0.f;
+        v[i] = live && l16 + 16 * i < p.K ? power(v[i]) : 0.f;
         l += v[i];
     }
     const float inv = 1.f / half_sum(l);
@@ -487,11 +511,11 @@ __device__ __forceinline__ void softmax_row(const UnfParams& p, long long row, i
     for (int t = lane; t < p.K; t += 32) m = fmaxf(m, E::get(x[t]));
     m = warp_maxf(m);
     float l = 0.f;
-    const float ml2 = m * kLog2eF;
-    for (int t = lane; t < p.K; t += 32) l += fast_exp2(fmaf(E::get(x[t]), kLog2eF, -ml2));
+    const RowPowers<T> power(m);
+    for (int t = lane; t < p.K; t += 32) l += power(E::get(x[t]));
     const float inv = 1.f / warp_sum(l);
     __syncwarp();
-    for (int t = lane; t < p.K; t += 32) y[t] = E::put(fast_exp2(fmaf(E::get(x[t]), kLog2eF, -ml2)) * inv);
+    for (int t = lane; t < p.K; t += 32) y[t] = E::put(power(E::get(x[t])) * inv);
     __syncwarp();
 }
 
@@ -602,13 +626,13 @@ __global__ void __launch_bounds__(kThreads) softmax8_kernel(const UnfParams p) {
         for (int t = q; t < K; t += 4) m = fmaxf(m, E::get(xr[t]));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float ml2 = m * kLog2eF;
+        const RowPowers<T> power(m);
         float l = 0.f;
-        for (int t = q; t < K; t += 4) l += fast_exp2(fmaf(E::get(xr[t]), kLog2eF, -ml2));
+        for (int t = q; t < K; t += 4) l += power(E::get(xr[t]));
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         const float inv = 1.f / l;
-        for (int t = q; t < K; t += 4) xr[t] = E::put(fast_exp2(fmaf(E::get(xr[t]), kLog2eF, -ml2)) * inv);
+        for (int t = q; t < K; t += 4) xr[t] = E::put(power(E::get(xr[t])) * inv);
     } else {
         T* dr = sd + r * K;
         float sum = 0.f;

@@ -123,14 +123,11 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// The reference point of a row's exponentials: its maximum, or 0 for a row of -inf alone.  exp(x - m) is taken as
-// 2^(x c - round(m c)), c = log2 e, so every exponent of the row is off by the rounding of m c, up to |m| 2^-23.5: a common
-// factor, which cancels against the sum while the exponentials stay in range (a sixteenth in the exponent at 2^20, hundreds
-// from 10^10 on, and a mask of the lowest finite value overflows).  `far` says that the row has to be shifted before, not
-// after, that product: its largest exponent is then 0.
+// The reference point of a row's exponentials: its maximum, or 0 for a row of -inf alone.  `far`: the row has to be shifted
+// before the product with log2 e.
 __device__ __forceinline__ float row_top(float m, bool& far) {
     if (m == -INFINITY) m = 0.f;
-    far = !(fabsf(m) < 1048576.f);
+    far = !(fabsf(m) < kFarLogit);
     return m;
 }
 

@@ -84,6 +84,20 @@ def test_logits_far_from_zero(dtype, K, cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [5, 81, 201, 399, 1001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logits_far_from_zero_without_dropout(dtype, K, cuda_lib):
+    """The plain window softmax of the same rows."""
+    na = cuda_lib
+    x = far_logits((1, max(K, 80), 3, K), dtype, 0)
+    y = torch.full_like(x, 5.0).cuda()
+    na.na_softmax(x.cuda(), y, (K,))
+    tb.status_ok(na)
+    s = ob.softmax(f64(x))
+    close("y", y, s, s * tb.map_error(f64(x), s) + 2.0 ** -120, TYPES[dtype])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [1, 5, 81, 399, 1001])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_a_row_does_not_depend_on_its_neighbours(dtype, K, cuda_lib):
