@@ -310,7 +310,9 @@ na_status na_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk
  * y = (x - mean) * rstd * w + b.  The norm per head of a [B, L.., heads, D] tensor has C = D, per token
  * C = heads * D.  w, b: fp32 [C] whatever the tensors' type, each may be null (ones, zeros).  mean, rstd: fp32
  * [rows], 4-byte aligned, written for the backward, or both null.  y may be x.  1 <= C <= 8192 (else
- * NA_ERR_UNSUPPORTED); rows whose length is not a multiple of 16 bytes are read element by element.
+ * NA_ERR_UNSUPPORTED); rows whose length is not a multiple of 16 bytes are read element by element.  The squares of
+ * x - mean are fp32 numbers: without an eps to cover it, a spread under 1e-19 loses digits of rstd, and one over 1e19
+ * gives rstd = 0.
  */
 na_status na_layernorm(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd, int64_t rows,
                        int C, float eps, na_dtype dtype, void* stream);

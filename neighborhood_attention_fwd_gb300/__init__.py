@@ -262,8 +262,9 @@ def na_device_status(stream=None):
 
 
 def na_debug_wait_hook(limit_ns: int = 0, withhold: bool = False) -> None:
-    """Test hook: the wait limit of later tensor-core launches (0: the 2 s default) and, with
-    withhold, the first CTA's first halo chunk left unfilled so that a wait runs out."""
+    """Test hook: the wait limit of later launches that fetch tiles (the tensor-core kernels, the window softmax with
+    dropout and differences, the layer norm's gradients; 0: the 2 s default) and, with withhold, the first CTA's
+    first halo chunk or tile left unfilled so that a wait runs out."""
     _ok(load().na_debug_wait_hook(int(limit_ns), 1 if withhold else 0), "na_debug_wait_hook")
 
 

@@ -11,8 +11,8 @@
 // partial row, and a second kernel adds the partial rows in a fixed order (no atomics: deterministic).  Few wide rows need
 // neither: blocks of columns beside the rows' blocks read x and dy again.
 //
-// Measured (bf16; share of the copy rate): 2M rows of 32 channels forward 51 us, 5.6 TB/s (82%); 1M rows of 256 backward
-// 275 us, 5.9 TB/s (87%); fp32, 333 rows of 2048 backward 9 to 12 us a call, 3.9 us on the GPU.
+// Measured (bf16; share of the copy rate): 2M rows of 32 channels forward 52 us, 5.5 TB/s (81%); 1M rows of 256 backward
+// 286 us, 5.7 TB/s (83%); fp32, 333 rows of 2048 backward 9 to 12 us a call, 3.9 us on the GPU.
 #include <algorithm>
 #include <type_traits>
 

@@ -1,6 +1,6 @@
 // na_win_impl.cuh -- the window softmax in the forms that a transformer's training needs: with dropout on its
 // weights, and as the difference of two softmax maps with learned weights, forward and backward.  Included by
-// na_win_bf16.cu, na_win_f16.cu and na_win_f32.cu (one type's instances each).
+// na_win_soft_*.cu and na_win_diff_*.cu (the instances of one form, direction and type each).
 //
 //   s_m = softmax(x_m) over a row's K weights (a row of -inf alone has no weights: s_m = 0)
 //   forward:  y = drop(s_1), or drop(s_1 - lam s_2);  drop(v) = gain v where the generator keeps the place, else 0
@@ -16,8 +16,8 @@
 // generator block each, before (backward) or after (forward) the rows.  fp32 arithmetic runs on pairs (f32x2).
 //
 // Measured (bf16; share of the copy rate): softmax with dropout over 9x9 windows at 1024x1024 x 8 heads 472 us, 5.8 TB/s (85%;
-// without dropout 454 us); its gradient over (3,5,5) at 4x256x256 x 8 heads, fp16, 168 us (83%); differential softmax with
-// dropout at 512x512 184 us (82%); its gradients without dropout over (5,7,7) at 2x8x128x128 849 us, 6.1 TB/s (89%).
+// without dropout 454 us); its gradient over (3,5,5) at 4x256x256 x 8 heads, fp16, 167 us (83%); differential softmax with
+// dropout at 512x512 184 us (82%); its gradients without dropout over (5,7,7) at 2x8x128x128 847 us, 6.1 TB/s (89%).
 // A ring per warp instead of per block took 528 us and more where this took 505, hand-over by a counter instead of
 // barriers 550.
 #pragma once
@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kWinThreads, win_blocks<DIFF, BWD>()) win_kern
 }
 
 // Rows that no tile holds (over 767 weights): a block per row, in aligned octets of the tensor (the row's first and last may
-// be shared with its neighbours), read again for each pass: a row is a few KB and stays in L1.
+// be shared with its neighbours), read again for each pass: a row is a few KB and stays in L1.  Bound by the latency of a
+// block's passes: 11x11x11 at 16x32x32 x 8 heads runs at 24 to 34% of the copy rate in bf16, 53 to 68% in fp32.
 template <int N>
 __device__ __forceinline__ void block_reduce(float (&v)[N], bool maximum, float (*slot)[kLongThreads / 32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
