@@ -376,6 +376,88 @@ na_status na_diff_softmax_bwd(const void* x1, const void* x2, const float* lam, 
                               const int* kernel, double p, const void* rng, na_dtype dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * After the attention.  The rest of a block: its output added to the stream between norms, and the gated feed-forward
+ * product.  The conventions are those of the operators above.
+ */
+
+typedef enum {
+    NA_NORM_NONE = 0,
+    NA_NORM_LAYER = 1,   /* (v - mean) * rstd, rstd = (sum (v - mean)^2 / C + eps)^-1/2 */
+    NA_NORM_RMS = 2      /* v * rstd, rstd = (sum v^2 / C + eps)^-1/2 */
+} na_norm_kind;
+
+/*
+ * The residual add of a block with the norms on both sides of it, on `rows` rows of C channels:
+ *   s = residual * x + scale * gate * (post(y) * post_w + post_b),   h = norm(s) * w + b.
+ * x: the stream, y: the block's output, s: the stream after it, h: what the next block reads.  post and norm are kinds
+ * of norm; without one, y is taken as it is, and h is null.  h is made from the fp32 values that s rounds.
+ * Vectors are fp32 whatever the tensors' type, each may be null (weights and gates of one, shifts of zero; null where its
+ * norm is none): post_w, post_b [C]; gate [gate_groups, C]; w, b [w_groups, C].  The rows are cut into that many runs of
+ * equal length (a batch entry each, say), run i taking vector i; groups of 1 serve all rows.  w_groups and gate_groups
+ * divide rows and are equal where both exceed 1 (else NA_ERR_INVALID_ARG), at most 32768 (else NA_ERR_UNSUPPORTED).
+ * mean, rstd (of s), post_mean, post_rstd (of y): fp32 [rows], 4-byte aligned, written for the backward, or null; a mean
+ * goes with layer norm only.  s may be null where nothing needs it (h then must not be).  s and h may each be x or y, but
+ * not the same one.  1 <= C <= 8192 (else NA_ERR_UNSUPPORTED).  The range of the squares is na_layernorm's.
+ */
+na_status na_addnorm(const void* x, const void* y, void* s, void* h, const float* w, const float* b, const float* gate,
+                     const float* post_w, const float* post_b, float* mean, float* rstd, float* post_mean, float* post_rstd,
+                     int64_t rows, int C, int64_t w_groups, int64_t gate_groups, na_norm_kind norm, na_norm_kind post,
+                     float scale, float residual, float eps, na_dtype dtype, void* stream);
+
+/* Bytes of device workspace na_addnorm_bwd needs for every gradient of a vector (0 on invalid arguments). */
+size_t na_addnorm_bwd_workspace_size(int64_t rows, int C, int64_t w_groups, int64_t gate_groups, na_dtype dtype);
+
+/*
+ * Gradients of na_addnorm from dh, ds (the gradient that reaches s from elsewhere; null: none), s, y and the saved
+ * statistics.  With e = (s - mean) * rstd, g = dh * w and D = ds + rstd * (g - sum g / C - e * sum (g e) / C):
+ *   dx = residual * D;  f = (y - post_mean) * post_rstd, q = D * scale * gate * post_w,
+ *   dy = post_rstd * (q - sum q / C - f * sum (q f) / C);
+ *   dw = sum dh e, db = sum dh, dgate = scale * sum D (f post_w + post_b), dpost_w = scale * sum D gate f,
+ *   dpost_b = scale * sum D gate
+ * (no sums of g and q alone for NA_NORM_RMS; D = ds without a norm, where dh and s are null; f = y and dy = q without a
+ * post norm).  dx and dy are written; the gradients of vectors are fp32, laid out as their vectors and overwritten,
+ * each may be null, and dgate must be where gate is.  dx may be dh, ds or s, dy may be dh, ds, s or y, but dx not dy.
+ * Workspace as for na_rpb_grad: null, or na_addnorm_bwd_workspace_size bytes; unused without gradients of vectors.
+ */
+na_status na_addnorm_bwd(const void* dh, const void* ds, const void* s, const void* y, const float* w, const float* gate,
+                         const float* post_w, const float* post_b, const float* mean, const float* rstd,
+                         const float* post_mean, const float* post_rstd, void* dx, void* dy, float* dw, float* db,
+                         float* dgate, float* dpost_w, float* dpost_b, int64_t rows, int C, int64_t w_groups,
+                         int64_t gate_groups, na_norm_kind norm, na_norm_kind post, float scale, float residual,
+                         na_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum {
+    NA_ACT_SILU = 0,       /* v / (1 + exp(-v)) */
+    NA_ACT_GELU = 1,       /* v Phi(v), Phi the normal distribution */
+    NA_ACT_GELU_TANH = 2,  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    NA_ACT_RELU = 3,       /* max(v, 0); slope 0 at 0 */
+    NA_ACT_SIGMOID = 4     /* 1 / (1 + exp(-v)) */
+} na_glu_act;
+
+/*
+ * The gated feed-forward product: h = act(x Wg^T + bg) * (x Wu^T + bu) for `rows` tokens, both products, the activation
+ * and the gating in one kernel.  x: [rows, D], wg, wu: [F, D] (halves of one [2 F, D] array will do), bg, bu: [F] or null
+ * (zeros), h: [rows, F], all of the tensors' type.  Sums in fp32, h rounded once.  2-byte tensors with D a multiple of 8
+ * run on tensor cores, others on FMA units.  rows < 2^31, D and F up to 2^20 (else NA_ERR_UNSUPPORTED).
+ */
+na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* h, int64_t rows, int D,
+                 int F, na_glu_act act, na_dtype dtype, void* stream);
+
+/* Bytes of device workspace na_glu_bwd needs (0 on invalid arguments): dg, du (below) and sums over runs of tokens. */
+size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype);
+
+/*
+ * Gradients of na_glu from dh and its inputs; nothing of the forward is kept, g = x Wg^T + bg and u = x Wu^T + bu are made
+ * again.  With dg = dh * u * act'(g) and du = dh * act(g), each rounded to the tensors' type:
+ *   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg = sum over tokens of dg,  dbu = sum over tokens of du,
+ * laid out and typed as their tensors, overwritten.  dx may be null, dwg and dwu both null, dbg and dbu each (and must
+ * be where the bias is).  Workspace: null (allocated on the stream), or na_glu_bwd_workspace_size bytes.
+ */
+na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* dx,
+                     void* dwg, void* dwu, void* dbg, void* dbu, int64_t rows, int D, int F, na_glu_act act, na_dtype dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ Tensors are contiguous [B, L_1, .., L_n, heads, D] (n = 1..3); lse/delta are fp3
 The unfused operations (na_qk, na_softmax, na_av and their gradients) keep the attention weights
 as [B, L.., heads, K], K = the product of the kernel sizes, window offsets first axis outermost.
 Around the attention: rotary positions (na_rope), layer norm (na_layernorm), and the window softmax with
-dropout or as the difference of two maps (na_softmax_dropout, na_diff_softmax, na_dropout).
+dropout or as the difference of two maps (na_softmax_dropout, na_diff_softmax, na_dropout).  After it: the
+residual add between norms (na_addnorm) and the gated feed-forward product (na_glu).
 """
 from __future__ import annotations
 
@@ -31,6 +32,7 @@ __all__ = [
     "RopeFreqs", "na_rope", "na_rope_bwd", "na_layernorm", "na_layernorm_bwd", "na_layernorm_bwd_workspace_size",
     "na_dropout", "na_softmax_dropout", "na_softmax_dropout_bwd", "na_diff_softmax", "na_diff_softmax_bwd",
     "na_diff_softmax_bwd_workspace_size",
+    "na_addnorm", "na_addnorm_bwd", "na_addnorm_bwd_workspace_size", "na_glu", "na_glu_bwd", "na_glu_bwd_workspace_size",
 ]
 
 NA_BF16, NA_FP32, NA_FP16 = 0, 1, 2
@@ -101,6 +103,16 @@ def load(path: str | None = None):
     lib.na_diff_softmax_bwd.argtypes = [P, P, P, I, P, P, P, P] + geo_nd + drop + [P, Z, P]
     lib.na_diff_softmax_bwd_workspace_size.argtypes = [I, I, IP, I, IP]
     lib.na_diff_softmax_bwd_workspace_size.restype = Z
+    lib.na_addnorm.argtypes = [P] * 13 + [L, I, L, L, I, I, F, F, F, I, P]
+    lib.na_addnorm_bwd.argtypes = [P] * 19 + [L, I, L, L, I, I, F, F, I, P, Z, P]
+    lib.na_addnorm_bwd_workspace_size.argtypes = [L, I, L, L, I]
+    lib.na_addnorm_bwd_workspace_size.restype = Z
+    lib.na_glu.argtypes = [P] * 6 + [L, I, I, I, I, P]
+    lib.na_glu_bwd.argtypes = [P] * 11 + [L, I, I, I, I, P, Z, P]
+    lib.na_glu_bwd_workspace_size.argtypes = [L, I, I, I]
+    lib.na_glu_bwd_workspace_size.restype = Z
+    for f in ("na_addnorm", "na_addnorm_bwd", "na_glu", "na_glu_bwd"):
+        getattr(lib, f).restype = I
     for f in ("na_rope", "na_rope_bwd", "na_layernorm", "na_layernorm_bwd", "na_dropout", "na_softmax_dropout",
               "na_softmax_dropout_bwd", "na_diff_softmax", "na_diff_softmax_bwd"):
         getattr(lib, f).restype = I
@@ -780,3 +792,188 @@ def na_diff_softmax_bwd(x1, x2, lam, dy, dx1, dx2, dlam, kernel, p: float = 0.0,
                                     dx2.data_ptr(), dlam.data_ptr(), B, ndim, grid, heads, kern, p, state, _code(x1),
                                     ws_ptr, ws_bytes, raw)
     _ok(st, "na_diff_softmax_bwd")
+
+
+# ---------------------------------------------------------------------------------------------
+# After the attention: the residual add between norms, the gated feed-forward product
+# ---------------------------------------------------------------------------------------------
+
+_NORMS = {"none": 0, "layer": 1, "rms": 2}
+
+
+def _norms(norm, post):
+    if norm not in _NORMS or post not in _NORMS:
+        raise ValueError("norm and post must be 'none', 'layer' or 'rms'")
+    return _NORMS[norm], _NORMS[post]
+
+
+def _groups(shape, C, **named):
+    """Number of vectors of fp32 tensors [C], or [.., C] with leading axes of the rows (a vector for each); all alike."""
+    lead = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        own = t.shape[:-1]
+        _like(t, shape[:len(own)] + (C,), torch.float32, name)
+        if len(own) >= len(shape):
+            raise ValueError(f"{name} has more axes than the rows")
+        if lead is None:
+            lead = own
+        elif lead != own:
+            raise ValueError(f"{name} must have the shape of {next(iter(named))}")
+    return 1 if not lead else math.prod(lead)
+
+
+def _moments(shape, kind, name, mean, rstd, needed):
+    """The statistics of a norm: both for layer norm, rstd alone for root mean square."""
+    if kind == 0 and (mean is not None or rstd is not None):
+        raise ValueError(f"no {name}norm, no statistics of it")
+    if kind == 2 and mean is not None:
+        raise ValueError(f"a root mean square norm has no {name}mean")
+    if (kind and needed and rstd is None) or (kind == 1 and (mean is None) != (rstd is None)):
+        raise ValueError(f"{name}mean and {name}rstd go together" if kind == 1 else f"{name}rstd is needed")
+    for what, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _like(t, shape[:-1], torch.float32, name + what)
+
+
+def na_addnorm(x, y, s, h, w=None, b=None, gate=None, post_w=None, post_b=None, norm: str = "layer", post: str = "none",
+               scale: float = 1.0, residual: float = 1.0, eps: float = 1e-5, mean=None, rstd=None, post_mean=None,
+               post_rstd=None, stream=None):
+    """The residual add of a block with the norms on both sides of it, over the last axis of x [.., C]:
+      s = residual * x + scale * gate * (post(y) * post_w + post_b),   h = norm(s) * w + b.
+    norm, post: "none", "layer" or "rms" (norm="none": h is None).  Vectors are fp32 or None: post_w, post_b [C]; gate, w
+    and b (w and b alike) [C], or with leading axes of x, a vector for each ([B, C]: one per batch entry).  s may be None
+    (nothing but h is wanted); s and h may each be x or y.  mean, rstd, post_mean, post_rstd: fp32 x.shape[:-1] for
+    the backward, or None; root mean square norms have no mean."""
+    shape, rows, C = _rows(x)
+    for name, t in (("x", x), ("y", y), ("s", s), ("h", h)):
+        if t is not None:
+            _like(t, shape, x.dtype, name)
+    kind, post_kind = _norms(norm, post)
+    if (h is None) != (kind == 0):
+        raise ValueError("h goes with a norm")
+    if s is None and h is None:
+        raise ValueError("s is needed without a norm")
+    if (kind == 0 and not (w is None and b is None)) or (post_kind == 0 and not (post_w is None and post_b is None)):
+        raise ValueError("weights of a norm that is none")
+    _vectors(C, post_w=post_w, post_b=post_b)
+    w_groups, gate_groups = _groups(shape, C, w=w, b=b), _groups(shape, C, gate=gate)
+    _moments(shape, kind, "", mean, rstd, False)
+    _moments(shape, post_kind, "post_", post_mean, post_rstd, False)
+    raw = _launch_stream(stream, x, y, s, h, w, b, gate, post_w, post_b, mean, rstd, post_mean, post_rstd)
+    st = load().na_addnorm(x.data_ptr(), y.data_ptr(), _ptr(s), _ptr(h), _ptr(w), _ptr(b), _ptr(gate), _ptr(post_w), _ptr(post_b),
+                           _ptr(mean), _ptr(rstd), _ptr(post_mean), _ptr(post_rstd), rows, C, w_groups, gate_groups, kind,
+                           post_kind, scale, residual, eps, _code(x), raw)
+    _ok(st, "na_addnorm")
+
+
+@functools.lru_cache(maxsize=1024)
+def _add_need(rows, C, w_groups, gate_groups, code):
+    return int(load().na_addnorm_bwd_workspace_size(rows, C, w_groups, gate_groups, code))
+
+
+def na_addnorm_bwd_workspace_size(rows: int, C: int, w_groups: int = 1, gate_groups: int = 1, dtype=torch.bfloat16) -> int:
+    return _add_need(int(rows), int(C), int(w_groups), int(gate_groups), _CODES[dtype]) if int(C) <= _INT_MAX else 0
+
+
+def na_addnorm_bwd(dh, ds, s, y, dx, dy, w=None, gate=None, post_w=None, post_b=None, norm: str = "layer", post: str = "none",
+                   scale: float = 1.0, residual: float = 1.0, mean=None, rstd=None, post_mean=None, post_rstd=None, dw=None,
+                   db=None, dgate=None, dpost_w=None, dpost_b=None, workspace=None, stream=None):
+    """dx, dy and, where given, the gradients of the vectors (laid out as these) of na_addnorm, from dh, the gradient ds that
+    reaches s from elsewhere (or None), s, y and the forward's statistics.  Without a norm dh and s are None.  dx may be
+    dh, ds or s, dy may be dh, ds, s or y, but not dx."""
+    shape, rows, C = _rows(y)
+    dtype = y.dtype
+    for name, t in (("dh", dh), ("ds", ds), ("s", s), ("y", y), ("dx", dx), ("dy", dy)):
+        if t is not None:
+            _like(t, shape, dtype, name)
+    kind, post_kind = _norms(norm, post)
+    if (dh is None) != (kind == 0) or (s is None) != (kind == 0):
+        raise ValueError("dh and s go with a norm")
+    if ds is None and kind == 0:
+        raise ValueError("ds is needed without a norm")
+    if (kind == 0 and not (w is None and dw is None and db is None)) or (
+            post_kind == 0 and not (post_w is None and post_b is None and dpost_w is None and dpost_b is None)):
+        raise ValueError("weights of a norm that is none")
+    if gate is None and dgate is not None:
+        raise ValueError("dgate goes with gate")
+    _vectors(C, post_w=post_w, post_b=post_b, dpost_w=dpost_w, dpost_b=dpost_b)
+    w_groups, gate_groups = _groups(shape, C, w=w, dw=dw, db=db), _groups(shape, C, gate=gate, dgate=dgate)
+    _moments(shape, kind, "", mean, rstd, True)
+    _moments(shape, post_kind, "post_", post_mean, post_rstd, True)
+    raw = _launch_stream(stream, dh, ds, s, y, dx, dy, w, gate, post_w, post_b, mean, rstd, post_mean, post_rstd, dw, db, dgate,
+                         dpost_w, dpost_b, workspace)
+    code = _code(y)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if dw is db is dgate is dpost_w is dpost_b is None else _workspace(
+        workspace, stream, lambda: _add_need(rows, C, w_groups, gate_groups, code), y.device)
+    st = load().na_addnorm_bwd(_ptr(dh), _ptr(ds), _ptr(s), y.data_ptr(), _ptr(w), _ptr(gate), _ptr(post_w), _ptr(post_b), _ptr(mean),
+                               _ptr(rstd), _ptr(post_mean), _ptr(post_rstd), dx.data_ptr(), dy.data_ptr(), _ptr(dw), _ptr(db),
+                               _ptr(dgate), _ptr(dpost_w), _ptr(dpost_b), rows, C, w_groups, gate_groups, kind, post_kind, scale,
+                               residual, code, ws_ptr, ws_bytes, raw)
+    _ok(st, "na_addnorm_bwd")
+
+
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
+
+
+def _glu(x, wg, wu, h, name, bg, bu, act):
+    """Checks of what both directions take; rows, D, F and the activation's code."""
+    shape, rows, D = _rows(x)
+    if wg.dim() != 2:
+        raise ValueError("wg must be [F, D]")
+    F = wg.shape[0]
+    if F < 1 or F > _INT_MAX:
+        raise ValueError("wg must have rows, at most 2^31 - 1")
+    dtype = x.dtype
+    _like(x, shape, dtype, "x")
+    _like(wg, (F, D), dtype, "wg")
+    _like(wu, (F, D), dtype, "wu")
+    _like(h, shape[:-1] + (F,), dtype, name)
+    for what, t in (("bg", bg), ("bu", bu)):
+        if t is not None:
+            _like(t, (F,), dtype, what)
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be 'silu', 'gelu', 'gelu_tanh', 'relu' or 'sigmoid'")
+    return rows, D, F, code
+
+
+def na_glu(x, wg, wu, h, bg=None, bu=None, act: str = "silu", stream=None):
+    """h = act(x wg^T + bg) * (x wu^T + bu) for x [.., D], wg and wu [F, D], bg and bu [F] or None, h [.., F], all of one type.
+    act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid"."""
+    rows, D, F, code = _glu(x, wg, wu, h, "h", bg, bu, act)
+    raw = _launch_stream(stream, x, wg, wu, h, bg, bu)
+    st = load().na_glu(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), _ptr(bg), _ptr(bu), h.data_ptr(), rows, D, F, code, _code(x), raw)
+    _ok(st, "na_glu")
+
+
+@functools.lru_cache(maxsize=1024)
+def _glu_need(rows, D, F, code):
+    return int(load().na_glu_bwd_workspace_size(rows, D, F, code))
+
+
+def na_glu_bwd_workspace_size(rows: int, D: int, F: int, dtype=torch.bfloat16) -> int:
+    return _glu_need(int(rows), int(D), int(F), _CODES[dtype]) if max(int(D), int(F)) <= _INT_MAX else 0
+
+
+def na_glu_bwd(dh, x, wg, wu, dx=None, dwg=None, dwu=None, bg=None, bu=None, dbg=None, dbu=None, act: str = "silu",
+               workspace=None, stream=None):
+    """Gradients of na_glu from dh and its inputs, each laid out as its tensor and left out where None (dwg and dwu go
+    together).  Nothing of the forward is kept: the products are made again."""
+    rows, D, F, code = _glu(x, wg, wu, dh, "dh", bg, bu, act)
+    if (dwg is None) != (dwu is None):
+        raise ValueError("dwg and dwu go together")
+    if (bg is None and dbg is not None) or (bu is None and dbu is not None):
+        raise ValueError("dbg goes with bg, dbu with bu")
+    if dx is dwg is dbg is dbu is None:
+        raise ValueError("no gradient is wanted")
+    for name, t, like in (("dx", dx, x), ("dwg", dwg, wg), ("dwu", dwu, wu), ("dbg", dbg, bg), ("dbu", dbu, bu)):
+        if t is not None:
+            _like(t, like.shape, x.dtype, name)
+    raw = _launch_stream(stream, dh, x, wg, wu, bg, bu, dx, dwg, dwu, dbg, dbu, workspace)
+    dtype = _code(x)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, stream, lambda: _glu_need(rows, D, F, dtype), x.device)
+    st = load().na_glu_bwd(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), _ptr(bg), _ptr(bu), _ptr(dx), _ptr(dwg), _ptr(dwu),
+                           _ptr(dbg), _ptr(dbu), rows, D, F, code, dtype, ws_ptr, ws_bytes, raw)
+    _ok(st, "na_glu_bwd")

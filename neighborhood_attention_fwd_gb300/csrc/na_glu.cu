@@ -1,0 +1,410 @@
+// na_glu.cu -- the gated feed-forward product h = act(x Wg^T + bg) * (x Wu^T + bu) and its gradients: host side, the
+// CUDA-core kernels (fp32 tensors, and 2-byte ones whose rows are not whole 16-byte chunks) and the sums that follow the
+// products.  The tensor-core kernels are in na_glu_tc.cu.
+//
+//   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u
+//   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg, dbu = column sums of dg, du
+//
+// Nothing is kept from the forward: the backward makes g and u again (4 T D F of its 12 T D F operations), so training holds
+// no array of T F elements between the passes.  dg and du go through the workspace in the tensors' type: the rounding is
+// the one that h itself has, and a sum over them averages it out.
+//
+// What bounds it: products.  fp32 runs on FMA units, in pairs (fma.rn.f32x2), no TF32: tiles of 128 x 128, 8 x 8 per
+// thread, operands widened and laid out [k][row] in shared memory, two stages of 16 steps of k.
+#include <algorithm>
+
+#include "na_block.cuh"
+#include "na_device.cuh"
+#include "na_glu.h"
+
+namespace na {
+using namespace dev;
+using namespace glu;
+
+namespace {
+
+constexpr int kTile = 128, kDepth = 16, kGluThreads = 256;
+constexpr int kPitch = kTile + 4;   // of an operand's row in shared memory
+
+// One operand of a product: rows (of the result's rows or columns) by k.  Element (r, k) is at base[r * ld + k], or with
+// ALONG_ROWS at base[k * ld + r].
+template <typename T>
+struct Operand {
+    const T* base;
+    long long ld;
+    long long rows, depth;   // zeros past them
+    bool wide;               // rows of memory start at 16 bytes
+};
+
+// A thread's eight elements of a 128 x 16 piece: from row r, steps k .. k + 7, or with ALONG_ROWS from step k, rows r .. r + 7.
+template <typename T, bool ALONG_ROWS>
+__device__ __forceinline__ void fetch(const Operand<T>& o, long long r, long long k, float (&f)[8]) {
+    constexpr int EPC = Elem<T>::EPC;
+    const bool in = r < o.rows && k < o.depth;
+    const long long left = ALONG_ROWS ? o.rows - r : o.depth - k;   // elements there along memory
+    const T* at = o.base + (ALONG_ROWS ? k * o.ld + r : r * o.ld + k);
+    if (in && o.wide && left >= 8) {
+#pragma unroll
+        for (int c = 0; c < 8 / EPC; ++c) {
+            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(at) + c);
+            float g[EPC];
+            Elem<T>::unpack(raw, g);
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) f[c * EPC + e] = g[e];
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = in && e < left ? Elem<T>::get(at[e]) : 0.f;
+}
+
+template <bool ALONG_ROWS>
+__device__ __forceinline__ void place(float (*sm)[kPitch], int t, const float (&f)[8]) {
+    if (ALONG_ROWS) {
+        float* to = &sm[t >> 4][(t & 15) * 8];
+        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sm[(t >> 7) * 8 + e][t & 127] = f[e];
+    }
+}
+
+// Products on CUDA cores.  A block makes 128 x 128 elements (kForward, kSlopes: 128 rows x 64 columns of g and the same of u);
+// rows along blockIdx.x, columns along blockIdx.y, kWeights: dWg, dWu and the runs of tokens along blockIdx.z.
+template <typename T, int WHICH>
+__global__ void __launch_bounds__(kGluThreads, 2) glu_fma_kernel(const GluParams p) {
+    constexpr bool PAIR = WHICH == kForward || WHICH == kSlopes;
+    constexpr bool A_ROWS = WHICH == kWeights, B_ROWS = !PAIR;
+    __shared__ __align__(16) float sa[2][kDepth][kPitch], sb[2][kDepth][kPitch];
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    const long long m0 = static_cast<long long>(blockIdx.x) * kTile, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? kTile / 2 : kTile);
+    const int half = WHICH == kWeights ? blockIdx.z & 1 : 0, split = WHICH == kWeights ? blockIdx.z >> 1 : 0;
+    const T *x = static_cast<const T*>(p.x), *wg = static_cast<const T*>(p.wg), *wu = static_cast<const T*>(p.wu);
+    const T *dg = static_cast<const T*>(p.dg), *du = static_cast<const T*>(p.du);
+    const bool wide = p.D % Elem<T>::EPC == 0;
+    // pieces of 16 steps of k; kTokens has two runs of them, dg Wg and du Wu
+    const long long k0 = split * p.run;
+    const long long depth = PAIR ? p.D : (WHICH == kTokens ? p.F : min(p.run, p.T - k0));
+    const long long pieces = (depth + kDepth - 1) / kDepth, total = WHICH == kTokens ? 2 * pieces : pieces;
+    // where this thread fetches within a piece
+    const int ra = A_ROWS ? (t & 15) * 8 : t & 127, ka = A_ROWS ? t >> 4 : (t >> 7) * 8;
+    const int rb = B_ROWS ? (t & 15) * 8 : t & 127, kb = B_ROWS ? t >> 4 : (t >> 7) * 8;
+    float fa[8], fb[8];
+    auto load = [&](long long i) {
+        const bool second = WHICH == kTokens && i >= pieces;
+        const long long k = (second ? i - pieces : i) * kDepth;
+        Operand<T> a, b;
+        if (PAIR) {
+            a = {x, p.D, p.T, p.D, wide};
+            b = {rb < kTile / 2 ? wg : wu, p.D, p.F, p.D, wide};
+            fetch<T, false>(a, m0 + ra, k + ka, fa);
+            fetch<T, false>(b, n0 + (rb & (kTile / 2 - 1)), k + kb, fb);
+        } else if (WHICH == kTokens) {
+            a = {second ? du : dg, p.pitch, p.T, p.F, true};
+            b = {second ? wu : wg, p.D, p.D, p.F, wide};
+            fetch<T, false>(a, m0 + ra, k + ka, fa);
+            fetch<T, true>(b, n0 + rb, k + kb, fb);
+        } else {
+            a = {half ? du : dg, p.pitch, p.F, k0 + depth, true};
+            b = {x, p.D, p.D, k0 + depth, wide};
+            fetch<T, true>(a, m0 + ra, k0 + k + ka, fa);
+            fetch<T, true>(b, n0 + rb, k0 + k + kb, fb);
+        }
+    };
+    uint64_t acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+    load(0);
+    for (long long i = 0; i < total; ++i) {
+        const int st = static_cast<int>(i & 1);
+        place<A_ROWS>(sa[st], t, fa);
+        place<B_ROWS>(sb[st], t, fb);
+        __syncthreads();   // also: the stage filled next was last read before this barrier
+        if (i + 1 < total) load(i + 1);
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) {
+            const float4 a0 = *reinterpret_cast<const float4*>(&sa[st][k][ty * 4]), a1 = *reinterpret_cast<const float4*>(&sa[st][k][64 + ty * 4]);
+            const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][tx * 4]), b1 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][64 + tx * 4]);
+            const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const uint64_t b[4] = {b0.x, b0.y, b1.x, b1.y};
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const uint64_t aa = pack2(a[r], a[r]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[r][c] = fma2(aa, b[c], acc[r][c]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const long long row = m0 + (r < 4 ? ty * 4 + r : 64 + ty * 4 + r - 4);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) split2(acc[r][c], v[2 * c], v[2 * c + 1]);
+        if constexpr (PAIR) {
+            if (row >= p.T) continue;
+            with_act(p.act, [&](auto tag) {
+                constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const long long f = n0 + tx * 4 + c;
+                    if (f >= p.F) break;
+                    const float g = v[c] + (p.bg ? Elem<T>::get(static_cast<const T*>(p.bg)[f]) : 0.f);
+                    const float u = v[4 + c] + (p.bu ? Elem<T>::get(static_cast<const T*>(p.bu)[f]) : 0.f);
+                    float a, slope;
+                    activate<ACT, false>(g, a, slope);
+                    if constexpr (WHICH == kForward) {
+                        static_cast<T*>(p.h)[row * p.F + f] = Elem<T>::put(a * u);
+                    } else {
+                        const float dh = Elem<T>::get(static_cast<const T*>(p.dh)[row * p.F + f]);
+                        static_cast<T*>(p.dg)[row * p.pitch + f] = Elem<T>::put(dh * u * slope);
+                        static_cast<T*>(p.du)[row * p.pitch + f] = Elem<T>::put(dh * a);
+                    }
+                }
+            });
+        } else {
+            if (row >= (WHICH == kTokens ? p.T : p.F)) continue;
+            const long long size = static_cast<long long>(p.F) * p.D;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const long long col = n0 + (c < 4 ? tx * 4 + c : 64 + tx * 4 + c - 4);
+                if (col >= p.D) continue;
+                const long long at = row * p.D + col;
+                if (WHICH == kTokens) static_cast<T*>(p.dx)[at] = Elem<T>::put(v[c]);
+                else if (p.splits > 1) p.partial[(2LL * split + half) * size + at] = v[c];
+                else static_cast<T*>(half ? p.dwu : p.dwg)[at] = Elem<T>::put(v[c]);
+            }
+        }
+    }
+}
+
+// out0[i], out1[i] = sums over the runs of partial[run][2][n], in order; either may be null.
+template <typename T>
+__global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int runs, long long n, T* out0, T* out1) {
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * n; i += gridDim.x * 256LL) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < runs; ++r) s += partial[r * 2 * n + i];
+        T* out = i < n ? out0 : out1;
+        if (out) out[i < n ? i : i - n] = Elem<T>::put(s);
+    }
+}
+
+// Column sums of dg and du over runs of tokens: partial[run][2][F].  A warp takes 32 columns, a block's warps every eighth row.
+template <typename T>
+__global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* du, long long T_, int F, long long pitch, long long run, float* partial) {
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    const T* from = blockIdx.z ? du : dg;
+    const long long first = blockIdx.y * run, end = min(first + run, T_);
+    float s = 0.f;
+    if (c < F)
+#pragma unroll 8
+        for (long long r = first + warp; r < end; r += 8) s += Elem<T>::get(from[r * pitch + c]);
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < F) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sums[i][lane];
+        partial[(blockIdx.y * 2LL + blockIdx.z) * F + c] = s;
+    }
+}
+
+constexpr int kGluMaxWidth = 1 << 20;              // of D and F
+constexpr long long kGluMaxRows = (1LL << 31) - 1;
+
+// How a problem is laid out: the workspace's arrays, and how the weights' gradients are cut.
+struct GluPlan {
+    long long pitch;                 // of a row of dg and du
+    size_t array;                    // bytes of one of them
+    int splits, runs;                // runs of tokens of dWg and dWu, of dbg and dbu
+    long long run, column_run;
+    size_t partial, columns;         // bytes
+};
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
+    GluPlan n{};
+    const int es = elem_bytes(dtype), chunk = 16 / es;
+    n.pitch = (static_cast<long long>(F) + chunk - 1) / chunk * chunk;
+    n.array = up256(static_cast<size_t>(T) * n.pitch * es);
+    // runs of tokens: enough blocks to fill the GPU twice, at least 256 tokens each, at most 8192 in one sum
+    const long long tiles = 2LL * ((F + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
+    long long splits = std::max((T + 8191) / 8192, std::min((T + 255) / 256, (4 * kSms + tiles - 1) / tiles));
+    splits = std::min(splits, 1024LL);
+    n.run = ((T + splits - 1) / splits + 63) / 64 * 64;
+    n.splits = static_cast<int>((T + n.run - 1) / n.run);
+    n.partial = n.splits > 1 ? up256(static_cast<size_t>(n.splits) * 2 * F * D * sizeof(float)) : 0;
+    const long long columns = 2LL * ((F + 31) / 32);
+    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (8 * kSms + columns - 1) / columns)), 1024LL);
+    n.column_run = (T + runs - 1) / runs;
+    n.runs = static_cast<int>((T + n.column_run - 1) / n.column_run);
+    n.columns = up256(static_cast<size_t>(n.runs) * 2 * F * sizeof(float));
+    return n;
+}
+
+na_status glu_sizes(long long rows, int D, int F, na_dtype dtype) {
+    if (rows < 1 || D < 1 || F < 1 || !known_dtype(dtype)) return NA_ERR_INVALID_ARG;
+    if (D > kGluMaxWidth || F > kGluMaxWidth || rows > kGluMaxRows || rows > (1LL << 40) / D || rows > (1LL << 40) / F) return NA_ERR_UNSUPPORTED;
+    return NA_OK;
+}
+
+bool known_act(na_glu_act a) { return a >= NA_ACT_SILU && a <= NA_ACT_SIGMOID; }
+
+template <typename T>
+na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
+    auto blocks = [](long long n, int tile) { return static_cast<unsigned>((n + tile - 1) / tile); };
+    const unsigned rows = blocks(p.T, kTile);
+    switch (which) {
+        case kForward: glu_fma_kernel<T, kForward><<<dim3(rows, blocks(p.F, kTile / 2)), kGluThreads, 0, s>>>(p); break;
+        case kSlopes: glu_fma_kernel<T, kSlopes><<<dim3(rows, blocks(p.F, kTile / 2)), kGluThreads, 0, s>>>(p); break;
+        case kTokens: glu_fma_kernel<T, kTokens><<<dim3(rows, blocks(p.D, kTile)), kGluThreads, 0, s>>>(p); break;
+        case kWeights: glu_fma_kernel<T, kWeights><<<dim3(blocks(p.F, kTile), blocks(p.D, kTile), 2 * p.splits), kGluThreads, 0, s>>>(p); break;
+    }
+    return launch_result();
+}
+
+na_status launch_product(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
+    if (dtype == NA_BF16) return launch_fma<__nv_bfloat16>(p, which, s);
+    if (dtype == NA_FP16) return launch_fma<__half>(p, which, s);
+    return launch_fma<float>(p, which, s);
+}
+
+template <typename T>
+na_status launch_sum(const float* partial, int runs, long long n, void* out0, void* out1, cudaStream_t s) {
+    const long long blocks = std::min((2 * n + 255) / 256, 8LL * kSms);
+    glu_sum_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(partial, runs, n, static_cast<T*>(out0), static_cast<T*>(out1));
+    return launch_result();
+}
+
+na_status sum_runs(const float* partial, int runs, long long n, void* out0, void* out1, na_dtype dtype, cudaStream_t s) {
+    if (dtype == NA_BF16) return launch_sum<__nv_bfloat16>(partial, runs, n, out0, out1, s);
+    if (dtype == NA_FP16) return launch_sum<__half>(partial, runs, n, out0, out1, s);
+    return launch_sum<float>(partial, runs, n, out0, out1, s);
+}
+
+template <typename T>
+na_status launch_columns(const GluParams& p, const GluPlan& n, float* partial, cudaStream_t s) {
+    glu_column_kernel<T><<<dim3((p.F + 31) / 32, n.runs, 2), 256, 0, s>>>(static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T, p.F,
+                                                                         p.pitch, n.column_run, partial);
+    return launch_result();
+}
+
+na_status column_sums(const GluParams& p, const GluPlan& n, float* partial, void* dbg, void* dbu, na_dtype dtype, cudaStream_t s) {
+    na_status st;
+    if (dtype == NA_BF16) st = launch_columns<__nv_bfloat16>(p, n, partial, s);
+    else if (dtype == NA_FP16) st = launch_columns<__half>(p, n, partial, s);
+    else st = launch_columns<float>(p, n, partial, s);
+    return st == NA_OK ? sum_runs(partial, n.runs, p.F, dbg, dbu, dtype, s) : st;
+}
+
+}  // namespace
+}  // namespace na
+
+extern "C" {
+
+na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* h, int64_t rows, int D,
+                 int F, na_glu_act act, na_dtype dtype, void* stream) {
+    using namespace na;
+    na_status st = glu_sizes(rows, D, F, dtype);
+    if (st != NA_OK) return st;
+    if (!x || !wg || !wu || !h || !known_act(act)) return NA_ERR_INVALID_ARG;
+    for (const void* q : {x, wg, wu, bg, bu, static_cast<const void*>(h)})
+        if (!ptr_aligned(q, 16)) return NA_ERR_ALIGNMENT;
+    const long long es = elem_bytes(dtype), wide = es * F * D;
+    if (!output_clear({h, rows * F * es}, {}, {{x, rows * D * es}, {wg, wide}, {wu, wide}, {bg, F * es}, {bu, F * es}})) return NA_ERR_INVALID_ARG;
+    GluParams p{};
+    p.x = x;
+    p.wg = wg;
+    p.wu = wu;
+    p.bg = bg;
+    p.bu = bu;
+    p.h = h;
+    p.T = rows;
+    p.D = D;
+    p.F = F;
+    p.act = act;
+    return launch_product(p, kForward, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype) {
+    using namespace na;
+    if (glu_sizes(rows, D, F, dtype) != NA_OK) return 0;
+    const GluPlan n = plan_glu(rows, D, F, dtype);
+    return 2 * n.array + std::max(n.partial, n.columns);
+}
+
+na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* dx,
+                     void* dwg, void* dwu, void* dbg, void* dbu, int64_t rows, int D, int F, na_glu_act act, na_dtype dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace na;
+    na_status st = glu_sizes(rows, D, F, dtype);
+    if (st != NA_OK) return st;
+    if (!dh || !x || !wg || !wu || (dwg == nullptr) != (dwu == nullptr) || (dbg && !bg) || (dbu && !bu) || (!dx && !dwg && !dbg && !dbu) ||
+        !known_act(act))
+        return NA_ERR_INVALID_ARG;
+    for (const void* q : {dh, x, wg, wu, bg, bu, static_cast<const void*>(dx), static_cast<const void*>(dwg), static_cast<const void*>(dwu),
+                          static_cast<const void*>(dbg), static_cast<const void*>(dbu)})
+        if (!ptr_aligned(q, 16)) return NA_ERR_ALIGNMENT;
+    const long long es = elem_bytes(dtype), wide = es * F * D;
+    const Span in[] = {{dh, rows * F * es}, {x, rows * D * es}, {wg, wide}, {wu, wide}, {bg, F * es}, {bu, F * es}};
+    const Span out[] = {{dx, rows * D * es}, {dwg, wide}, {dwu, wide}, {dbg, F * es}, {dbu, F * es}};
+    for (int i = 0; i < 5; ++i) {
+        for (const Span& q : in)
+            if (spans_overlap(out[i], q)) return NA_ERR_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (spans_overlap(out[i], out[k])) return NA_ERR_INVALID_ARG;
+    }
+    const GluPlan n = plan_glu(rows, D, F, dtype);
+    const size_t need = 2 * n.array + std::max(n.partial, n.columns);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* ws = workspace;
+    if (ws) {
+        if (workspace_bytes < need) return NA_ERR_WORKSPACE;
+        if (!ptr_aligned(ws, 16)) return NA_ERR_ALIGNMENT;
+        const Span sws{ws, static_cast<long long>(need)};
+        for (const Span& q : in)
+            if (spans_overlap(sws, q)) return NA_ERR_INVALID_ARG;
+        for (const Span& q : out)
+            if (spans_overlap(sws, q)) return NA_ERR_INVALID_ARG;
+    } else if (cudaMallocAsync(&ws, need, s) != cudaSuccess) {
+        return NA_ERR_WORKSPACE;
+    }
+    GluParams p{};
+    p.dh = dh;
+    p.x = x;
+    p.wg = wg;
+    p.wu = wu;
+    p.bg = bg;
+    p.bu = bu;
+    p.dx = dx;
+    p.dwg = dwg;
+    p.dwu = dwu;
+    p.dg = ws;
+    p.du = static_cast<char*>(ws) + n.array;
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n.array);
+    p.T = rows;
+    p.pitch = n.pitch;
+    p.D = D;
+    p.F = F;
+    p.act = act;
+    p.splits = n.splits;
+    p.run = n.run;
+    st = launch_product(p, kSlopes, dtype, s);
+    if (st == NA_OK && dx) st = launch_product(p, kTokens, dtype, s);
+    if (st == NA_OK && dwg) {
+        st = launch_product(p, kWeights, dtype, s);
+        if (st == NA_OK && n.splits > 1) st = sum_runs(p.partial, n.splits, static_cast<long long>(F) * D, dwg, dwu, dtype, s);
+    }
+    if (st == NA_OK && (dbg || dbu)) st = column_sums(p, n, p.partial, dbg, dbu, dtype, s);
+    if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
+    return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,100 @@
+// na_glu.h -- the gated feed-forward product's parameters, shared by its host code and CUDA-core kernels (na_glu.cu) and its
+// tensor-core kernels (na_glu_tc.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/na.h"
+
+namespace na {
+namespace glu {
+
+// The products.  kForward: h from x and both weights.  kSlopes: the same product again, and dg, du from it and dh.
+// kTokens: dx = dg Wg + du Wu.  kWeights: dWg = dg^T x, dWu = du^T x.
+enum Product { kForward = 0, kSlopes = 1, kTokens = 2, kWeights = 3 };
+
+struct GluParams {
+    const void* x;        // [T, D]
+    const void* wg;       // [F, D]
+    const void* wu;
+    const void* bg;       // [F], null: zeros
+    const void* bu;
+    const void* dh;       // [T, F]
+    void* h;              // [T, F]
+    void* dg;             // [T, pitch], workspace
+    void* du;
+    void* dx;             // [T, D]
+    void* dwg;            // [F, D]
+    void* dwu;
+    float* partial;       // kWeights with several splits: [split][2][F][D]
+    long long T, pitch;   // pitch: F rounded up to whole 16-byte chunks
+    int D, F;
+    int act;              // na_glu_act
+    int splits;           // kWeights: runs of tokens summed apart
+    long long run;        // tokens of a run (a multiple of 64)
+    unsigned* err;        // device status word, limit of one wait, test hook (tensor-core kernels)
+    unsigned long long wait_ns;
+    uint32_t withhold;
+};
+
+// act(v) and its derivative.  FAST: exponentials and quotients of the hardware's approximations, off by less than 2^-17 of
+// their value in the range that 2-byte results have; else the full ones of fp32.
+template <int ACT>   // an activation as a type
+struct ActTag {
+    static constexpr int value = ACT;
+};
+
+template <bool FAST>
+__device__ __forceinline__ float exp_of(float v) {
+    if constexpr (FAST) return __expf(v);
+    else return expf(v);
+}
+template <bool FAST>
+__device__ __forceinline__ float inverse(float v) {
+    if constexpr (FAST) return __fdividef(1.f, v);
+    else return 1.f / v;
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ void activate(float v, float& a, float& slope) {
+    if constexpr (ACT == NA_ACT_RELU) {
+        a = v < 0.f ? 0.f : v;   // a NaN stays one
+        slope = v > 0.f ? 1.f : 0.f;
+    } else if constexpr (ACT == NA_ACT_GELU) {
+        // v Phi(v), and Phi(v) + v phi(v); the complementary error function keeps Phi's digits far below zero
+        const float cdf = 0.5f * erfcf(v * -0.70710678118654752f);
+        a = v * cdf;
+        slope = fmaf(v * 0.39894228040143268f, exp_of<FAST>(-0.5f * v * v), cdf);
+    } else if constexpr (ACT == NA_ACT_GELU_TANH) {
+        // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t)), t = sqrt(2 / pi) (v + 0.044715 v^3); beyond |v| = 100 it is 0 or 1
+        const float v2 = fminf(v * v, 10000.f), t2 = v * fmaf(v2, 2.f * 0.79788456080286536f * 0.044715f, 2.f * 0.79788456080286536f);
+        const float y = inverse<FAST>(1.f + exp_of<FAST>(-t2));
+        const float rise = fmaf(v2, 6.f * 0.79788456080286536f * 0.044715f, 2.f * 0.79788456080286536f);
+        a = v * y;
+        slope = fmaf(a * (1.f - y), rise, y);
+    } else {
+        const float e = exp_of<FAST>(-v), y = inverse<FAST>(1.f + e);
+        if constexpr (ACT == NA_ACT_SIGMOID) {
+            a = y;
+            slope = y * (v > 0.f ? e * y : 1.f - y);   // 1 - y without cancellation on either side
+        } else {
+            a = v * y;
+            slope = fmaf(a, 1.f - y, y);
+        }
+    }
+}
+
+// Calls f<ACT>() for a run-time activation.
+template <typename Call>
+__device__ __forceinline__ void with_act(int act, Call&& call) {
+    switch (act) {
+        case NA_ACT_RELU: call(ActTag<NA_ACT_RELU>{}); break;
+        case NA_ACT_GELU: call(ActTag<NA_ACT_GELU>{}); break;
+        case NA_ACT_GELU_TANH: call(ActTag<NA_ACT_GELU_TANH>{}); break;
+        case NA_ACT_SIGMOID: call(ActTag<NA_ACT_SIGMOID>{}); break;
+        default: call(ActTag<NA_ACT_SILU>{}); break;
+    }
+}
+
+}  // namespace glu
+}  // namespace na

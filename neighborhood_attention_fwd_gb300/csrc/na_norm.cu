@@ -14,13 +14,11 @@
 // Measured (bf16; share of the copy rate): 2M rows of 32 channels forward 52 us, 5.5 TB/s (81%); 1M rows of 256 backward
 // 286 us, 5.7 TB/s (83%); fp32, 333 rows of 2048 backward 9 to 12 us a call, 3.9 us on the GPU.
 #include <algorithm>
-#include <type_traits>
 
-#include "na_block.cuh"
-#include "na_device.cuh"
+#include "na_rows.cuh"
 
 namespace na {
-using namespace dev;
+using namespace rows;
 
 namespace {
 
@@ -49,46 +47,6 @@ struct NormParams {
     unsigned long long wait_ns;
     uint32_t withhold;     // ring: test hook, block 0 leaves out its first copy
 };
-
-// A chunk: V elements, 16 bytes, or one element where a row is not whole chunks.  Loads are unconditional (places past
-// the end are clamped to the last one and left out afterwards): a guarded load would be waited for before the next one.
-template <typename T, int V>
-struct Chunk {
-    uint4 raw;
-    __device__ __forceinline__ void load(const void* base, long long at) { raw = ld_stream(static_cast<const T*>(base) + at); }
-    __device__ __forceinline__ void get(float (&f)[V]) const { Elem<T>::unpack(raw, f); }
-};
-template <typename T>
-struct Chunk<T, 1> {
-    T raw;
-    __device__ __forceinline__ void load(const void* base, long long at) { raw = static_cast<const T*>(base)[at]; }
-    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = Elem<T>::get(raw); }
-};
-
-template <typename T, int V>
-__device__ __forceinline__ void store_chunk(void* base, long long at, const float (&f)[V]) {
-    if constexpr (V == 1) static_cast<T*>(base)[at] = Elem<T>::put(f[0]);
-    else st_stream(static_cast<T*>(base) + at, Elem<T>::pack(f));
-}
-
-template <int V>
-__device__ __forceinline__ void load_weights(const float* w, int c, float (&f)[V], float none) {
-    if (!w) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) f[e] = none;
-    } else if constexpr (V == 1) {
-        f[0] = __ldg(w + c);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; e += 4) {
-            const float4 t = __ldg(reinterpret_cast<const float4*>(w + c + e));
-            f[e] = t.x;
-            f[e + 1] = t.y;
-            f[e + 2] = t.z;
-            f[e + 3] = t.w;
-        }
-    }
-}
 
 // Chunk-wise fp32 arithmetic, in pairs where a chunk has them.
 template <int V>
@@ -132,33 +90,6 @@ __device__ __forceinline__ void chunk_affine(const float (&x)[V], float r, const
 #pragma unroll
         for (int e = 0; e < V; e += 2)
             split2(fma2(mul2(pack2(x[e], x[e + 1]), rr), pack2(w[e], w[e + 1]), pack2(b[e], b[e + 1])), y[e], y[e + 1]);
-    }
-}
-
-// Sums N values over the row's team: lanes of a warp, or the whole block through shared memory (slot: one of
-// two buffers taken in turn, so that one barrier per sum is enough).
-template <int N, bool BLOCK>
-__device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*slot)[32]) {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        if (BLOCK || m < team) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
-        }
-    if (BLOCK) {
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) slot[i][threadIdx.x >> 5] = v[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = lane < warps ? slot[i][lane] : 0.f;
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-            v[i] = s;
-        }
     }
 }
 
@@ -309,53 +240,8 @@ __device__ __forceinline__ void store_partial(const NormParams& p, float (&dw)[J
     }
 }
 
-// Chunk-wise arithmetic of the backward, H words of one or two columns each: with h = (x - mean) rstd and g = dy w the
-// gradient of x is rstd g - rstd sum g / C - h rstd sum (g h) / C.  No square of rstd, which could leave fp32's range where
-// every term is within it.
-template <int V>
-struct Cols {
-    static constexpr int H = V == 1 ? 1 : V / 2;
-    using W = typename std::conditional<V == 1, float, uint64_t>::type;
-    static __device__ __forceinline__ W both(float a) {
-        if constexpr (V == 1) return a;
-        else return pack2(a, a);
-    }
-    static __device__ __forceinline__ W fma(W a, W b, W c) {
-        if constexpr (V == 1) return fmaf(a, b, c);
-        else return fma2(a, b, c);
-    }
-    static __device__ __forceinline__ W mul(W a, W b) {
-        if constexpr (V == 1) return a * b;
-        else return mul2(a, b);
-    }
-    static __device__ __forceinline__ W add(W a, W b) {
-        if constexpr (V == 1) return a + b;
-        else return add2(a, b);
-    }
-    static __device__ __forceinline__ float sum(W a) {
-        if constexpr (V == 1) {
-            return a;
-        } else {
-            float x, y;
-            split2(a, x, y);
-            return x + y;
-        }
-    }
-    static __device__ __forceinline__ void from(const float (&f)[V], W (&w)[H]) {
-#pragma unroll
-        for (int e = 0; e < H; ++e) {
-            if constexpr (V == 1) w[e] = f[e];
-            else w[e] = pack2(f[2 * e], f[2 * e + 1]);
-        }
-    }
-    static __device__ __forceinline__ void to(const W (&w)[H], float (&f)[V]) {
-#pragma unroll
-        for (int e = 0; e < H; ++e) {
-            if constexpr (V == 1) f[e] = w[e];
-            else split2(w[e], f[2 * e], f[2 * e + 1]);
-        }
-    }
-};
+// The gradient of x with h = (x - mean) rstd and g = dy w is rstd g - rstd sum g / C - h rstd sum (g h) / C.  No square of
+// rstd, which could leave fp32's range where every term is within it.
 
 // The backward of rows a block wide, and of rows that are not whole chunks.  The next row's loads are issued before this
 // one's sums where that pays for the registers: 2-byte rows of 1024 channels 66% -> 73% of the copy rate, of 4096 58% -> 69%,
