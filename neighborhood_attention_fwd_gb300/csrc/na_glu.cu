@@ -181,15 +181,27 @@ __global__ void __launch_bounds__(kGluThreads, 2) glu_fma_kernel(const GluParams
     }
 }
 
-// out0[i], out1[i] = sums over the runs of partial[run][2][n], in order; either may be null.
-template <typename T>
-__global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int runs, long long n, T* out0, T* out1) {
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * n; i += gridDim.x * 256LL) {
-        float s = 0.f;
-#pragma unroll 8
-        for (int r = 0; r < runs; ++r) s += partial[r * 2 * n + i];
-        T* out = i < n ? out0 : out1;
-        if (out) out[i < n ? i : i - n] = Elem<T>::put(s);
+// out[i] = sums over the runs of partial[run][n], in order: the first `cut` elements to out0, the others to out1; either may
+// be null.  V elements at a time (n and cut are multiples of V).
+template <typename T, int V>
+__global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int runs, long long n, long long cut, T* out0, T* out1) {
+    for (long long i = (blockIdx.x * 256LL + threadIdx.x) * V; i < n; i += gridDim.x * 256LL * V) {
+        T* out = i < cut ? (out0 ? out0 + i : nullptr) : (out1 ? out1 + (i - cut) : nullptr);
+        if (!out) continue;
+        float s[V] = {};
+#pragma unroll 4
+        for (int r = 0; r < runs; ++r) {
+            if constexpr (V == 4) {
+                const float4 t = *reinterpret_cast<const float4*>(partial + r * n + i);
+                s[0] += t.x, s[1] += t.y, s[2] += t.z, s[3] += t.w;
+            } else {
+                s[0] += partial[r * n + i];
+            }
+        }
+        if constexpr (V == 4 && sizeof(T) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pair(s[0], s[1]), Elem<T>::pair(s[2], s[3]));
+        else
+#pragma unroll
+            for (int e = 0; e < V; ++e) out[e] = Elem<T>::put(s[e]);
     }
 }
 
@@ -218,34 +230,111 @@ __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* d
 constexpr int kGluMaxWidth = 1 << 20;              // of D and F
 constexpr long long kGluMaxRows = (1LL << 31) - 1;
 
+// How a product is cut on tensor cores.
+struct TilePlan {
+    bool pairs;              // tiles of 256 x 256 on pairs of blocks, else of 128 x 128
+    int few;                 // 16, 64, 128: the kernel of few tokens
+    unsigned rows, cols, steps, run, splits;
+};
+
+unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
+
+// Nanoseconds of a step of 64 along the summed axis of a tile, and of what a tile takes besides.
+constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000;
+// Steps summed in one accumulator at most (16384 products: the tensor cores cut their sums, a bias that grows with the steps).
+constexpr unsigned kMostSteps = 256;
+
+TilePlan plan_tiles(Product which, long long T, int D, int F) {
+    const bool pair = which == kForward || which == kSlopes;
+    TilePlan best{};
+    if (pair && T <= 128) {
+        // As many blocks to a tile's sum as make the fewest steps one after another, with two blocks to a multiprocessor and
+        // about eight steps' time for a block to start and end.
+        best.few = T <= 16 ? 16 : (T <= 64 ? 64 : 128);
+        best.rows = up(F, 64);
+        best.cols = 1;
+        best.steps = up(D, 64);
+        long long least = 0;
+        for (unsigned s = 1; s <= 8 && s <= best.steps; s *= 2) {
+            const unsigned run = up(best.steps, s);
+            if (up(best.steps, run) != s) continue;   // every block has steps
+            const long long time = static_cast<long long>(up(static_cast<long long>(best.rows) * s, 2 * kSms)) * (run + 8);
+            if (s == 1 || time < least) {
+                least = time;
+                best.run = run;
+                best.splits = s;
+            }
+        }
+        return best;
+    }
+    double least = 0;
+    for (int pairs = 0; pairs < 2; ++pairs) {
+        const int m = pairs ? 256 : 128, n = pair ? m / 2 : m, slots = pairs ? kSms / 2 : kSms;
+        TilePlan t{};
+        t.pairs = pairs != 0;
+        t.rows = which == kWeights ? 2 * up(F, m) : up(T, m);
+        t.cols = up(pair ? F : D, n);
+        t.steps = which == kWeights ? up(T, 64) : (which == kTokens ? 2 * up(F, 64) : up(D, 64));
+        const long long tiles = static_cast<long long>(t.rows) * t.cols;
+        const double size = which == kWeights ? 2.0 * F * D : static_cast<double>(T) * D;
+        const unsigned fewest = pair ? 1 : up(t.steps, kMostSteps), most = pair ? 1 : std::max(fewest, std::min(64u, t.steps / 4));
+        for (unsigned s = fewest; s <= most; ++s) {
+            const unsigned run = up(t.steps, s), splits = up(t.steps, run);
+            const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
+            // sums of several splits: written and read again by another kernel
+            const double time = waves * (run * (pairs ? kPairStep : kOneStep) + kTileTime) + (splits > 1 ? 3000 + 8.0 * size * splits / 5000 : 0);
+            if (best.splits == 0 || time < least) {
+                least = time;
+                best = t;
+                best.run = run;
+                best.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 // How a problem is laid out: the workspace's arrays, and how the weights' gradients are cut.
 struct GluPlan {
+    bool tensor;                     // tensor cores
     long long pitch;                 // of a row of dg and du
     size_t array;                    // bytes of one of them
-    int splits, runs;                // runs of tokens of dWg and dWu, of dbg and dbu
+    int splits, runs;                // CUDA cores: runs of tokens of dWg and dWu; of dbg and dbu
     long long run, column_run;
-    size_t partial, columns;         // bytes
+    TilePlan tokens, weights;        // tensor cores
+    size_t partial;                  // bytes
 };
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+bool on_tensor_cores(int D, na_dtype dtype) { return dtype != NA_FP32 && D % 8 == 0; }
+
 GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
     GluPlan n{};
     const int es = elem_bytes(dtype), chunk = 16 / es;
+    n.tensor = on_tensor_cores(D, dtype);
     n.pitch = (static_cast<long long>(F) + chunk - 1) / chunk * chunk;
     n.array = up256(static_cast<size_t>(T) * n.pitch * es);
-    // runs of tokens: enough blocks to fill the GPU twice, at least 256 tokens each, at most 8192 in one sum
-    const long long tiles = 2LL * ((F + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
-    long long splits = std::max((T + 8191) / 8192, std::min((T + 255) / 256, (4 * kSms + tiles - 1) / tiles));
-    splits = std::min(splits, 1024LL);
-    n.run = ((T + splits - 1) / splits + 63) / 64 * 64;
-    n.splits = static_cast<int>((T + n.run - 1) / n.run);
-    n.partial = n.splits > 1 ? up256(static_cast<size_t>(n.splits) * 2 * F * D * sizeof(float)) : 0;
+    size_t floats = 0;
+    if (n.tensor) {
+        n.tokens = plan_tiles(kTokens, T, D, F);
+        n.weights = plan_tiles(kWeights, T, D, F);
+        if (n.tokens.splits > 1) floats = static_cast<size_t>(n.tokens.splits) * T * D;
+        if (n.weights.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights.splits) * 2 * F * D);
+    } else {
+        // runs of tokens: enough blocks to fill the GPU twice, at least 256 tokens each, at most 8192 in one sum
+        const long long tiles = 2LL * ((F + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
+        long long splits = std::max((T + 8191) / 8192, std::min((T + 255) / 256, (4 * kSms + tiles - 1) / tiles));
+        splits = std::min(splits, 1024LL);
+        n.run = ((T + splits - 1) / splits + 63) / 64 * 64;
+        n.splits = static_cast<int>((T + n.run - 1) / n.run);
+        if (n.splits > 1) floats = static_cast<size_t>(n.splits) * 2 * F * D;
+    }
     const long long columns = 2LL * ((F + 31) / 32);
     const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (8 * kSms + columns - 1) / columns)), 1024LL);
     n.column_run = (T + runs - 1) / runs;
     n.runs = static_cast<int>((T + n.column_run - 1) / n.column_run);
-    n.columns = up256(static_cast<size_t>(n.runs) * 2 * F * sizeof(float));
+    n.partial = up256(std::max(floats, static_cast<size_t>(n.runs) * 2 * F) * sizeof(float));
     return n;
 }
 
@@ -270,23 +359,100 @@ na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
     return launch_result();
 }
 
-na_status launch_product(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
+// A product on tensor cores: its tensor maps, boxes of 64 elements by as many rows as one copy brings (na_glu_tc.cuh).
+na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na_dtype dtype, cudaStream_t s) {
+    GluTcParams q{};
+    const bool pair = which == kForward || which == kSlopes;
+    const uint64_t D = p.D, F = p.F, T = p.T, pitch = 2 * static_cast<uint64_t>(p.pitch);
+    na_status st = device_status_word(&q.err);
+    auto map = [&](CUtensorMap& m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box) {
+        const uint64_t sizes[2] = {inner, rows};
+        if (st == NA_OK) st = encode_box(&m, base, dtype, 2, sizes, &row_bytes, 64, box);
+    };
+    const uint32_t a_rows = which == kWeights ? 64 : (n.few ? n.few : 128), b_rows = pair && n.pairs ? 128 : 64;
+    if (pair) {
+        map(q.a[0], p.x, D, T, 2 * D, a_rows);
+    } else {
+        map(q.a[0], p.dg, F, T, pitch, a_rows);
+        map(q.a[1], p.du, F, T, pitch, a_rows);
+    }
+    if (which == kWeights) {
+        map(q.b[0], p.x, D, T, 2 * D, b_rows);
+    } else {
+        map(q.b[0], p.wg, D, F, 2 * D, b_rows);
+        map(q.b[1], p.wu, D, F, 2 * D, b_rows);
+    }
+    q.wide = p.F % 8 == 0;
+    q.split = !pair && n.splits > 1;
+    if (which == kForward) {
+        if (q.wide && !n.few) map(q.out[0], p.h, F, T, 2 * F, 32);
+    } else if (which == kSlopes) {
+        if (!n.few) {
+            if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32);
+            map(q.out[0], p.dg, F, T, pitch, 32);
+            map(q.out[1], p.du, F, T, pitch, 32);
+        }
+    } else if (q.split) {
+        const uint64_t rows = which == kWeights ? F : T, sizes[3] = {D, rows, static_cast<uint64_t>(n.splits) * (which == kWeights ? 2 : 1)};
+        const uint64_t pitches[2] = {4 * D, 4 * D * rows};
+        if (st == NA_OK) st = encode_box(&q.out[0], p.partial, NA_FP32, 3, sizes, pitches, 32, 32);
+    } else if (which == kTokens) {
+        map(q.out[0], p.dx, D, T, 2 * D, 32);
+    } else {
+        map(q.out[0], p.dwg, D, F, 2 * D, 32);
+        map(q.out[1], p.dwu, D, F, 2 * D, 32);
+    }
+    if (st != NA_OK) return st;
+    q.bg = p.bg;
+    q.bu = p.bu;
+    q.dh = p.dh;
+    q.h = p.h;
+    q.dg = p.dg;
+    q.du = p.du;
+    q.pitch = p.pitch;
+    q.T = static_cast<int>(p.T);
+    q.D = p.D;
+    q.F = p.F;
+    q.act = p.act;
+    q.rows = n.rows;
+    q.cols = n.cols;
+    q.steps = n.steps;
+    q.run = n.run;
+    q.splits = n.splits;
+    q.wait_ns = wait_limit_ns();
+    q.withhold = wait_withhold();
+    const bool f16 = dtype == NA_FP16;
+    switch (which) {
+        case kForward:
+            if (n.few) return f16 ? launch_few<kForward, __half>(q, n.few, s) : launch_few<kForward, __nv_bfloat16>(q, n.few, s);
+            return f16 ? launch_tiles<kForward, __half>(q, n.pairs, s) : launch_tiles<kForward, __nv_bfloat16>(q, n.pairs, s);
+        case kSlopes:
+            if (n.few) return f16 ? launch_few<kSlopes, __half>(q, n.few, s) : launch_few<kSlopes, __nv_bfloat16>(q, n.few, s);
+            return f16 ? launch_tiles<kSlopes, __half>(q, n.pairs, s) : launch_tiles<kSlopes, __nv_bfloat16>(q, n.pairs, s);
+        case kTokens: return f16 ? launch_tiles<kTokens, __half>(q, n.pairs, s) : launch_tiles<kTokens, __nv_bfloat16>(q, n.pairs, s);
+        default: return f16 ? launch_tiles<kWeights, __half>(q, n.pairs, s) : launch_tiles<kWeights, __nv_bfloat16>(q, n.pairs, s);
+    }
+}
+
+na_status launch_fma(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
     if (dtype == NA_BF16) return launch_fma<__nv_bfloat16>(p, which, s);
     if (dtype == NA_FP16) return launch_fma<__half>(p, which, s);
     return launch_fma<float>(p, which, s);
 }
 
 template <typename T>
-na_status launch_sum(const float* partial, int runs, long long n, void* out0, void* out1, cudaStream_t s) {
-    const long long blocks = std::min((2 * n + 255) / 256, 8LL * kSms);
-    glu_sum_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(partial, runs, n, static_cast<T*>(out0), static_cast<T*>(out1));
+na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s) {
+    const bool wide = n % 4 == 0 && cut % 4 == 0;
+    const unsigned blocks = static_cast<unsigned>(std::min((n / (wide ? 4 : 1) + 255) / 256, 8LL * kSms));
+    if (wide) glu_sum_kernel<T, 4><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
+    else glu_sum_kernel<T, 1><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
     return launch_result();
 }
 
-na_status sum_runs(const float* partial, int runs, long long n, void* out0, void* out1, na_dtype dtype, cudaStream_t s) {
-    if (dtype == NA_BF16) return launch_sum<__nv_bfloat16>(partial, runs, n, out0, out1, s);
-    if (dtype == NA_FP16) return launch_sum<__half>(partial, runs, n, out0, out1, s);
-    return launch_sum<float>(partial, runs, n, out0, out1, s);
+na_status sum_runs(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, na_dtype dtype, cudaStream_t s) {
+    if (dtype == NA_BF16) return launch_sum<__nv_bfloat16>(partial, runs, n, cut, out0, out1, s);
+    if (dtype == NA_FP16) return launch_sum<__half>(partial, runs, n, cut, out0, out1, s);
+    return launch_sum<float>(partial, runs, n, cut, out0, out1, s);
 }
 
 template <typename T>
@@ -301,7 +467,7 @@ na_status column_sums(const GluParams& p, const GluPlan& n, float* partial, void
     if (dtype == NA_BF16) st = launch_columns<__nv_bfloat16>(p, n, partial, s);
     else if (dtype == NA_FP16) st = launch_columns<__half>(p, n, partial, s);
     else st = launch_columns<float>(p, n, partial, s);
-    return st == NA_OK ? sum_runs(partial, n.runs, p.F, dbg, dbu, dtype, s) : st;
+    return st == NA_OK ? sum_runs(partial, n.runs, 2LL * p.F, p.F, dbg, dbu, dtype, s) : st;
 }
 
 }  // namespace
@@ -330,14 +496,15 @@ na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, 
     p.D = D;
     p.F = F;
     p.act = act;
-    return launch_product(p, kForward, dtype, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return on_tensor_cores(D, dtype) ? launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s) : launch_fma(p, kForward, dtype, s);
 }
 
 size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype) {
     using namespace na;
     if (glu_sizes(rows, D, F, dtype) != NA_OK) return 0;
     const GluPlan n = plan_glu(rows, D, F, dtype);
-    return 2 * n.array + std::max(n.partial, n.columns);
+    return 2 * n.array + n.partial;
 }
 
 na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* dx,
@@ -362,7 +529,7 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
             if (spans_overlap(out[i], out[k])) return NA_ERR_INVALID_ARG;
     }
     const GluPlan n = plan_glu(rows, D, F, dtype);
-    const size_t need = 2 * n.array + std::max(n.partial, n.columns);
+    const size_t need = 2 * n.array + n.partial;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = workspace;
     if (ws) {
@@ -396,11 +563,17 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.act = act;
     p.splits = n.splits;
     p.run = n.run;
-    st = launch_product(p, kSlopes, dtype, s);
-    if (st == NA_OK && dx) st = launch_product(p, kTokens, dtype, s);
+    const long long size = static_cast<long long>(F) * D;
+    st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, D, F), dtype, s) : launch_fma(p, kSlopes, dtype, s);
+    if (st == NA_OK && dx) {
+        st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : launch_fma(p, kTokens, dtype, s);
+        if (st == NA_OK && n.tensor && n.tokens.splits > 1)
+            st = sum_runs(p.partial, n.tokens.splits, rows * D, rows * D, dx, nullptr, dtype, s);
+    }
     if (st == NA_OK && dwg) {
-        st = launch_product(p, kWeights, dtype, s);
-        if (st == NA_OK && n.splits > 1) st = sum_runs(p.partial, n.splits, static_cast<long long>(F) * D, dwg, dwu, dtype, s);
+        st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : launch_fma(p, kWeights, dtype, s);
+        const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.splits;
+        if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, dwg, dwu, dtype, s);
     }
     if (st == NA_OK && (dbg || dbu)) st = column_sums(p, n, p.partial, dbg, dbu, dtype, s);
     if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;

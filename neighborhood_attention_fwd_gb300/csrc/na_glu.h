@@ -2,6 +2,7 @@
 // tensor-core kernels (na_glu_tc.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/na.h"
@@ -26,13 +27,34 @@ struct GluParams {
     void* dx;             // [T, D]
     void* dwg;            // [F, D]
     void* dwu;
-    float* partial;       // kWeights with several splits: [split][2][F][D]
+    float* partial;       // sums of several splits: [split][2][F][D] of kWeights, [split][T][D] of kTokens
     long long T, pitch;   // pitch: F rounded up to whole 16-byte chunks
     int D, F;
     int act;              // na_glu_act
     int splits;           // kWeights: runs of tokens summed apart
     long long run;        // tokens of a run (a multiple of 64)
-    unsigned* err;        // device status word, limit of one wait, test hook (tensor-core kernels)
+};
+
+// Parameters of the tensor-core kernels.
+struct alignas(64) GluTcParams {
+    CUtensorMap a[2];     // rows' operand: x; dg, du
+    CUtensorMap b[2];     // columns' operand: Wg, Wu; x
+    CUtensorMap in;       // slopes: dh
+    CUtensorMap out[2];   // h; dg, du; dx; dWg, dWu; or the fp32 partial sums
+    const void* bg;
+    const void* bu;
+    const void* dh;
+    void* h;
+    long long pitch;      // few tokens: of dg and du
+    void* dg;
+    void* du;
+    int T, D, F, act;
+    uint32_t wide;        // rows of h and dh are whole 16-byte chunks: they go by TMA
+    uint32_t split;       // results are partial sums
+    unsigned rows, cols;  // tiles (weights: rows of dWg and dWu together)
+    unsigned splits;
+    unsigned steps, run;  // steps of 64 along the summed axis, and of one split
+    unsigned* err;
     unsigned long long wait_ns;
     uint32_t withhold;
 };
@@ -95,6 +117,13 @@ __device__ __forceinline__ void with_act(int act, Call&& call) {
         default: call(ActTag<NA_ACT_SILU>{}); break;
     }
 }
+
+// Launchers of the tensor-core kernels (na_glu_tc.cuh).  pairs: tiles of 256 x 256 on pairs of blocks, else of 128 x 128;
+// tokens: 16, 64 or 128, the most that a product of few tokens holds.
+template <int WHICH, typename T>
+na_status launch_tiles(const GluTcParams& p, bool pairs, cudaStream_t s);
+template <int WHICH, typename T>
+na_status launch_few(const GluTcParams& p, int tokens, cudaStream_t s);
 
 }  // namespace glu
 }  // namespace na

@@ -258,6 +258,9 @@ GLU = [
     ("bf16", 700, 200, 1000, "silu", False), ("fp16", 513, 64, 600, "gelu_tanh", True), ("bf16", 2049, 256, 512, "silu", True),
     ("bf16", 20000, 32, 24, "silu", True), ("fp16", 64, 1024, 256, "silu", False), ("bf16", 16, 2048, 304, "gelu", False),
     ("bf16", 7, 1000, 2736, "silu", True), ("fp16", 257, 8, 8, "silu", True), ("bf16", 385, 392, 24, "sigmoid", False),
+    # enough tiles for pairs of blocks, forward and for every gradient
+    ("bf16", 5200, 136, 1000, "silu", True), ("fp16", 5001, 72, 2001, "relu", True), ("fp16", 2900, 1032, 1304, "silu", False),
+    ("bf16", 40000, 264, 88, "sigmoid", False),
     # rows that are not whole 16-byte chunks
     ("bf16", 1, 1, 1, "silu", True), ("bf16", 37, 99, 50, "silu", True), ("fp16", 200, 130, 131, "gelu", False),
 ]
