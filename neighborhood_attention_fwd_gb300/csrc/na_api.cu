@@ -580,19 +580,16 @@ bool allow_shared(const void* kernel) {
     return true;
 }
 
-na_status encode_box(CUtensorMap* m, const void* base, na_dtype dtype, int axes, const uint64_t* sizes, const uint64_t* pitches,
-                     uint32_t inner, uint32_t rows) {
+na_status encode_box(CUtensorMap* m, const void* base, na_dtype dtype, const uint64_t (&sizes)[2], uint64_t pitch, uint32_t wide,
+                     uint32_t rows) {
     const na_status st = get_encoder();
     if (st != NA_OK) return st;
-    cuuint64_t dims[3], strides[2];
-    for (int i = 0; i < axes; ++i) dims[i] = sizes[i];
-    for (int i = 0; i + 1 < axes; ++i) strides[i] = pitches[i];
-    const cuuint32_t box[3] = {inner, rows, 1}, step[3] = {1, 1, 1};
-    const CUtensorMapDataType type = dtype == NA_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     : dtype == NA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return g_encode(m, type, static_cast<cuuint32_t>(axes), const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    const cuuint64_t dims[2] = {sizes[0], sizes[1]}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {wide, rows}, step[2] = {1, 1};
+    return g_encode(m, dtype == NA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? NA_OK
                : NA_ERR_CUDA;
 }

@@ -20,10 +20,9 @@ na_status device_status_word(unsigned** out);
 unsigned long long wait_limit_ns();
 uint32_t wait_withhold();
 
-// Tensor map of a tensor of 2 or 3 axes, innermost first, whose pitches (bytes, of every axis but the innermost) are multiples of
-// 16; boxes of `inner` elements (128 bytes of them, swizzled as such) by `rows` (na_api.cu).
-na_status encode_box(CUtensorMap* m, const void* base, na_dtype dtype, int axes, const uint64_t* sizes, const uint64_t* pitches,
-                     uint32_t inner, uint32_t rows);
+// Tensor map of a matrix of bf16 or fp16 (sizes: elements of a row, rows; the pitch in bytes a multiple of 16) in boxes of `wide`
+// elements (64 or 32: 128 or 64 bytes, swizzled as such) by `rows` (na_api.cu).
+na_status encode_box(CUtensorMap* m, const void* base, na_dtype dtype, const uint64_t (&sizes)[2], uint64_t pitch, uint32_t wide, uint32_t rows);
 
 // ---------------------------------------------------------------------------------------------
 // Host: argument checks

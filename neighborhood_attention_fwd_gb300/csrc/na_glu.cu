@@ -235,12 +235,15 @@ struct TilePlan {
     bool pairs;              // tiles of 256 x 256 on pairs of blocks, else of 128 x 128
     int few;                 // 16, 64, 128: the kernel of few tokens
     unsigned rows, cols, steps, run, splits;
+    unsigned last_nf, span, groups;   // forward, slopes
 };
 
 unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
 
-// Nanoseconds of a step of 64 along the summed axis of a tile, and of what a tile takes besides.
+// Nanoseconds of a step of 64 along the summed axis of a tile, for pairs of blocks and for one, and of what a tile takes besides.
 constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000;
+// The same where the rows' operand stays for several columns of tiles.
+constexpr long long kPairStay = 230, kOneStay = 160;
 // Steps summed in one accumulator at most (16384 products: the tensor cores cut their sums, a bias that grows with the steps).
 constexpr unsigned kMostSteps = 256;
 
@@ -269,15 +272,40 @@ TilePlan plan_tiles(Product which, long long T, int D, int F) {
     }
     double least = 0;
     for (int pairs = 0; pairs < 2; ++pairs) {
-        const int m = pairs ? 256 : 128, n = pair ? m / 2 : m, slots = pairs ? kSms / 2 : kSms;
+        const int m = pairs ? 256 : 128, slots = pairs ? kSms / 2 : kSms;
         TilePlan t{};
         t.pairs = pairs != 0;
+        t.splits = 1;
+        if (pair) {
+            // a row's last tile is only as wide as it has to be: a product of pairs takes 32 columns (16 of g) at a time, of one
+            // block 16
+            t.rows = up(T, m);
+            t.cols = up(F, m / 2);
+            t.last_nf = up(F - (t.cols - 1) * (m / 2), pairs ? 16 : 8) * (pairs ? 16 : 8);
+            t.steps = t.run = up(D, 64);
+            const unsigned stay = which == kForward ? kPairRows<kForward> : kPairRows<kSlopes>;
+            for (unsigned span = 1; span <= t.cols; ++span) {
+                if (span > 1 && (t.steps > stay || span > 64)) break;
+                const unsigned groups = up(t.cols, span);
+                if (span > 1 && up(t.cols, span - 1) == groups) continue;   // no fewer items than with the shorter run
+                const double waves = static_cast<double>((static_cast<long long>(t.rows) * groups + slots - 1) / slots);
+                const long long step = span > 1 ? (pairs ? kPairStay : kOneStay) : (pairs ? kPairStep : kOneStep);
+                const double time = waves * std::min<double>(span, static_cast<double>(F) / (m / 2)) * t.steps * step + kTileTime;
+                if (best.groups == 0 || time < least) {
+                    least = time;
+                    best = t;
+                    best.span = span;
+                    best.groups = groups;
+                }
+            }
+            continue;
+        }
         t.rows = which == kWeights ? 2 * up(F, m) : up(T, m);
-        t.cols = up(pair ? F : D, n);
-        t.steps = which == kWeights ? up(T, 64) : (which == kTokens ? 2 * up(F, 64) : up(D, 64));
+        t.cols = up(D, m);
+        t.steps = which == kWeights ? up(T, 64) : 2 * up(F, 64);
         const long long tiles = static_cast<long long>(t.rows) * t.cols;
         const double size = which == kWeights ? 2.0 * F * D : static_cast<double>(T) * D;
-        const unsigned fewest = pair ? 1 : up(t.steps, kMostSteps), most = pair ? 1 : std::max(fewest, std::min(64u, t.steps / 4));
+        const unsigned fewest = up(t.steps, kMostSteps), most = std::max(fewest, std::min(64u, t.steps / 4));
         for (unsigned s = fewest; s <= most; ++s) {
             const unsigned run = up(t.steps, s), splits = up(t.steps, run);
             const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
@@ -365,9 +393,9 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     const bool pair = which == kForward || which == kSlopes;
     const uint64_t D = p.D, F = p.F, T = p.T, pitch = 2 * static_cast<uint64_t>(p.pitch);
     na_status st = device_status_word(&q.err);
-    auto map = [&](CUtensorMap& m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box) {
+    auto map = [&](CUtensorMap& m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box, uint32_t wide = 64) {
         const uint64_t sizes[2] = {inner, rows};
-        if (st == NA_OK) st = encode_box(&m, base, dtype, 2, sizes, &row_bytes, 64, box);
+        if (st == NA_OK) st = encode_box(&m, base, dtype, sizes, row_bytes, wide, box);
     };
     const uint32_t a_rows = which == kWeights ? 64 : (n.few ? n.few : 128), b_rows = pair && n.pairs ? 128 : 64;
     if (pair) {
@@ -381,27 +409,22 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     } else {
         map(q.b[0], p.wg, D, F, 2 * D, b_rows);
         map(q.b[1], p.wu, D, F, 2 * D, b_rows);
+        if (pair && !n.few) {
+            map(q.b[2], p.wg, D, F, 2 * D, n.last_nf);
+            map(q.b[3], p.wu, D, F, 2 * D, n.last_nf);
+        }
     }
     q.wide = p.F % 8 == 0;
-    q.split = !pair && n.splits > 1;
-    if (which == kForward) {
-        if (q.wide && !n.few) map(q.out[0], p.h, F, T, 2 * F, 32);
-    } else if (which == kSlopes) {
-        if (!n.few) {
-            if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32);
-            map(q.out[0], p.dg, F, T, pitch, 32);
-            map(q.out[1], p.du, F, T, pitch, 32);
+    if (pair && !n.few) {   // results and dh: boxes of 32 by 32
+        if (which == kSlopes) {
+            if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32, 32);
+            map(q.out[0], p.dg, F, T, pitch, 32, 32);
+            map(q.out[1], p.du, F, T, pitch, 32, 32);
+        } else if (q.wide) {
+            map(q.out[0], p.h, F, T, 2 * F, 32, 32);
         }
-    } else if (q.split) {
-        const uint64_t rows = which == kWeights ? F : T, sizes[3] = {D, rows, static_cast<uint64_t>(n.splits) * (which == kWeights ? 2 : 1)};
-        const uint64_t pitches[2] = {4 * D, 4 * D * rows};
-        if (st == NA_OK) st = encode_box(&q.out[0], p.partial, NA_FP32, 3, sizes, pitches, 32, 32);
-    } else if (which == kTokens) {
-        map(q.out[0], p.dx, D, T, 2 * D, 32);
-    } else {
-        map(q.out[0], p.dwg, D, F, 2 * D, 32);
-        map(q.out[1], p.dwu, D, F, 2 * D, 32);
     }
+    q.split = !pair && n.splits > 1;
     if (st != NA_OK) return st;
     q.bg = p.bg;
     q.bu = p.bu;
@@ -409,6 +432,10 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     q.h = p.h;
     q.dg = p.dg;
     q.du = p.du;
+    q.dx = p.dx;
+    q.dwg = p.dwg;
+    q.dwu = p.dwu;
+    q.partial = p.partial;
     q.pitch = p.pitch;
     q.T = static_cast<int>(p.T);
     q.D = p.D;
@@ -419,6 +446,9 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     q.steps = n.steps;
     q.run = n.run;
     q.splits = n.splits;
+    q.last_nf = n.last_nf;
+    q.span = n.span;
+    q.groups = n.groups;
     q.wait_ns = wait_limit_ns();
     q.withhold = wait_withhold();
     const bool f16 = dtype == NA_FP16;

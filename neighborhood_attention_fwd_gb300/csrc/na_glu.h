@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/na.h"
+#include "na_device.cuh"
 
 namespace na {
 namespace glu {
@@ -36,22 +37,28 @@ struct GluParams {
 };
 
 // Parameters of the tensor-core kernels.
-struct alignas(64) GluTcParams {
+struct GluTcParams {
     CUtensorMap a[2];     // rows' operand: x; dg, du
-    CUtensorMap b[2];     // columns' operand: Wg, Wu; x
+    CUtensorMap b[4];     // columns' operand: Wg, Wu (and again in boxes for a row's last tile); x
     CUtensorMap in;       // slopes: dh
-    CUtensorMap out[2];   // h; dg, du; dx; dWg, dWu; or the fp32 partial sums
+    CUtensorMap out[2];   // forward: h; slopes: dg, du
     const void* bg;
     const void* bu;
     const void* dh;
     void* h;
-    long long pitch;      // few tokens: of dg and du
     void* dg;
     void* du;
+    void* dx;
+    void* dwg;
+    void* dwu;
+    float* partial;
+    long long pitch;      // of dg and du
     int T, D, F, act;
-    uint32_t wide;        // rows of h and dh are whole 16-byte chunks: they go by TMA
-    uint32_t split;       // results are partial sums
+    uint32_t wide;        // rows of h and dh are whole 16-byte chunks
+    uint32_t split;       // results are sums of splits, to partial
     unsigned rows, cols;  // tiles (weights: rows of dWg and dWu together)
+    unsigned last_nf;     // forward, slopes: columns of g (and of u) of a row's last tile
+    unsigned span, groups;   // forward, slopes: columns of tiles that a block takes in a row, and such runs of a row
     unsigned splits;
     unsigned steps, run;  // steps of 64 along the summed axis, and of one split
     unsigned* err;
@@ -59,8 +66,8 @@ struct alignas(64) GluTcParams {
     uint32_t withhold;
 };
 
-// act(v) and its derivative.  FAST: exponentials and quotients of the hardware's approximations, off by less than 2^-17 of
-// their value in the range that 2-byte results have; else the full ones of fp32.
+// act(v) and its derivative.  FAST: exponentials and reciprocals of the hardware's approximations (results below 2^-126 are
+// zeros), off by less than 2^-17 of their value in the range that 2-byte results have; else the full ones of fp32.
 template <int ACT>   // an activation as a type
 struct ActTag {
     static constexpr int value = ACT;
@@ -68,13 +75,18 @@ struct ActTag {
 
 template <bool FAST>
 __device__ __forceinline__ float exp_of(float v) {
-    if constexpr (FAST) return __expf(v);
+    if constexpr (FAST) return dev::fast_exp2(v * 1.4426950408889634f);
     else return expf(v);
 }
 template <bool FAST>
 __device__ __forceinline__ float inverse(float v) {
-    if constexpr (FAST) return __fdividef(1.f, v);
-    else return 1.f / v;
+    if constexpr (FAST) {
+        float y;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+        return y;
+    } else {
+        return 1.f / v;
+    }
 }
 
 template <int ACT, bool FAST>
@@ -117,6 +129,10 @@ __device__ __forceinline__ void with_act(int act, Call&& call) {
         default: call(ActTag<NA_ACT_SILU>{}); break;
     }
 }
+
+// Steps of the rows' operand that a block of the forward or of the slopes holds.
+template <int WHICH>
+constexpr int kPairRows = WHICH == kForward ? 6 : 5;
 
 // Launchers of the tensor-core kernels (na_glu_tc.cuh).  pairs: tiles of 256 x 256 on pairs of blocks, else of 128 x 128;
 // tokens: 16, 64 or 128, the most that a product of few tokens holds.

@@ -1,19 +1,19 @@
 // na_glu_tc.cuh -- tensor-core kernels of the gated feed-forward product (bf16 or fp16 operands, fp32 accumulators).
 //
-// A product's result is cut into tiles, 256 x 256 for a pair of blocks (tcgen05.mma with cta_group::2: each block holds 128
+// A product's result is cut into tiles, up to 256 x 256 for a pair of blocks (tcgen05.mma with cta_group::2: each block holds 128
 // rows and half of the columns' operand) or 128 x 128 for one block.  Blocks stay and take tiles in turn.  Per tile, steps of
-// 64 along the summed axis come by TMA through a ring of stages (128-byte swizzle), one thread issues the products, and eight
-// (or four) warps take the finished accumulators from TMEM while the next tile's products fill the other half of it.
+// 64 along the summed axis come by TMA through rings in shared memory (128-byte swizzle), one thread issues the products, and
+// eight to sixteen warps take the finished accumulators from TMEM while the next tile's products fill the other half of it.
 //   forward, slopes   rows: tokens; columns: as many of g as of u, so that both factors of an element meet in one thread
 //   tokens            dx: rows: tokens; columns: channels; summed over the columns of dg, then of du
 //   weights           dWg, dWu: rows: columns of dg or du; columns: channels; summed over tokens, operands turned by the
 //                     descriptors (both run along the other axis in memory)
-// Results leave through shared memory by TMA (32 rows of 128 bytes a warp), which also cuts them at the ragged edges.
 // Few tokens have a kernel of their own (glu_few_kernel), which streams the weights as the rows of the product.
 //
 // Every wait is bounded (na_device.cuh).
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "na_block.cuh"
@@ -43,8 +43,10 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t local, uint32_t rank) 
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
+// Relaxed: what it tells of, loads from TMEM, is ordered by the tcgen05 fences.  A release to the cluster waits for the warp's
+// stores to global memory first (most of the warps' time: 2D tokens 756 us against 651).
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
@@ -52,24 +54,27 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// A wait on a barrier that the other block of a pair arrives on: acquire at cluster scope.
-__device__ __forceinline__ bool mbar_spin_cluster(uint64_t* bar, uint32_t parity, const WaitGuard& err, unsigned site) {
-    const unsigned long long t0 = globaltimer();
+// The warps that issue copies and products run as whole warps, one elected lane issuing: operands then stay in uniform registers
+// (one lane alone spent 70 cycles on a product, and its 285 a step bounded the kernel).  A spinning wait of a whole warp; its
+// clock is first read after 64 tests: these warps wait at every step, mostly shorter than that read takes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitGuard& err, unsigned site) {
+    unsigned long long t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((i & 63u) == 0u && (ld_volatile(err.word) != 0u || globaltimer() - t0 > err.limit_ns)) {
-            record_error(err.word, site);
-            return false;
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+        if ((i & 63u) == 0u) {
+            const unsigned long long now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(0xffffffffu, ld_volatile(err.word) != 0u || now - t0 > err.limit_ns)) {
+                record_error(err.word, site);
+                return false;
+            }
         }
     }
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <int CG>
@@ -128,14 +133,10 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
             : "memory");
     }
 }
+
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
                  "r"(src), "r"(x), "r"(y)
-                 : "memory");
-}
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 
@@ -164,6 +165,14 @@ __device__ __forceinline__ float widen(const void* base, long long at) {
     Elem<T>::two(static_cast<const uint16_t*>(base)[at], lo, hi);
     return lo;
 }
+__device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t ld_shared_b32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Word w of row r of a buffer with rows of 64 bytes in 64-byte swizzle.
+__device__ __forceinline__ uint32_t word_at(uint32_t base, int r, int w) { return base + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) + (w & 3) * 4; }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -182,45 +191,383 @@ __device__ __forceinline__ void settle() {
 
 constexpr uint32_t kBand = 16;   // rows of tiles that are finished together: their operand and all columns' stay in L2
 
-template <int WHICH, int CG, int NT>
-struct TileShape {
-    static constexpr bool PAIR = WHICH == kForward || WHICH == kSlopes;
-    static constexpr int NF = NT / 2;                            // PAIR: columns of g (and of u) of a tile
+// Item i of rows x cols, by bands of rows, down the columns of a band.
+struct Place {
+    unsigned row, col;
+};
+__device__ __forceinline__ Place place_of(unsigned i, unsigned rows, unsigned cols) {
+    const unsigned band = i / (kBand * cols), base = band * kBand, height = min(kBand, rows - base);
+    i -= base * cols;
+    return {base + i % height, i / height};
+}
+
+// ---------------------------------------------------------------------------------------------
+// Forward and slopes.  A tile: 128 CG rows of tokens, 64 CG columns of g and the same of u, fewer of them in the last of a row.  The rows' and the columns' operand have
+// rings of their own: where all of a row of tiles' operand (its steps of 64) fits its ring, it is brought once for the `span`
+// columns of tiles that a block takes in a row, which halves what comes out of L2, the bound of short sums (2D tokens: 13 TB/s).
+// The epilogue has sixteen (eight) warps, each for 32 rows by 32 columns.
+// ---------------------------------------------------------------------------------------------
+
+template <int WHICH, int CG>
+struct PairShape {
+    static constexpr int NF = 64 * CG;                           // most columns of g of a tile
     static constexpr int M = 128 * CG;                           // rows of a tile
-    static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = NT / CG * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int WARPS = PAIR ? NF / 16 : 8;             // of the epilogue
-    static constexpr int OUT = PAIR ? 64 : NT / 2;               // columns of a warp
-    static constexpr int BUFFERS = WHICH == kForward ? 1 : 2;    // of 4 KB, a warp's
-    static constexpr int STAGES = CG == 1 ? 5 : (WHICH == kSlopes ? 4 : 5);
+    static constexpr uint32_t SLOT = 128 * 128;                  // either ring's
+    static constexpr int ROWS = kPairRows<WHICH>, COLS = WHICH == kForward ? 5 : 4;   // slots
+    static constexpr int PARTS = NF / 32, WARPS = 4 * PARTS;     // of the epilogue
+    static constexpr uint32_t WARP_STAGING = WHICH == kForward ? 2048 : 4096;   // 32 rows of 64 bytes: results; dh
     static constexpr int THREADS = 128 + 32 * WARPS;
-    static constexpr uint32_t STAGING = STAGES * STAGE, BIAS = STAGING + WARPS * BUFFERS * 4096;
-    static constexpr uint32_t BYTES = BIAS + (PAIR ? WARPS * 128 * 4 : 0) + 1024;   // 1024: to align the start
+    static constexpr uint32_t TMEM = 256;                        // columns of one of the two accumulators
+    static constexpr uint32_t STAGING = (ROWS + COLS) * SLOT, BIAS = STAGING + WARPS * WARP_STAGING;
+    static constexpr uint32_t BYTES = BIAS + WARPS * 64 * 4 + 1024;   // 1024: to align the start
+    static_assert(BYTES <= 227 * 1024 - 512, "more than a block's shared memory");
+};
+
+// The tiles of a block, in order.
+template <int CG>
+struct PairWalk {
+    const GluTcParams& p;
+    unsigned item, items, row, col, end;   // tile (row, col); the item ends before column `end`
+    __device__ __forceinline__ explicit PairWalk(const GluTcParams& q) : p(q), item(blockIdx.x / CG), items(q.rows * q.groups) { open(); }
+    __device__ __forceinline__ void open() {
+        if (item >= items) return;
+        const Place at = place_of(item, p.rows, p.groups);
+        row = at.row;
+        col = at.col * p.span;
+        end = min(p.cols, col + p.span);
+    }
+    __device__ __forceinline__ bool more() const { return item < items; }
+    __device__ __forceinline__ void next() {
+        if (++col < end) return;
+        item += gridDim.x / CG;
+        open();
+    }
+};
+
+template <int WHICH, int CG, typename T>
+__global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_kernel(const __grid_constant__ GluTcParams p) {
+    using S = PairShape<WHICH, CG>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ uint64_t rows_full[S::ROWS], rows_empty[S::ROWS], cols_full[S::COLS], cols_empty[S::COLS], acc_full[2], acc_empty[2], dh_full[S::WARPS];
+    __shared__ uint32_t tmem_base;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const WaitGuard guard{p.err, p.wait_ns};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::ROWS; ++s) {
+            mbar_init(&rows_full[s], 1);
+            mbar_init(&rows_empty[s], 1);
+        }
+        for (int s = 0; s < S::COLS; ++s) {
+            mbar_init(&cols_full[s], 1);
+            mbar_init(&cols_empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], CG * S::WARPS);
+        }
+        for (int i = 0; i < S::WARPS; ++i) mbar_init(&dh_full[i], 1);
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_take<CG>(&tmem_base, 2 * S::TMEM);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        // copies
+        const uint32_t rows_at = CG == 2 ? peer_address(smem_u32(rows_full), 0) : smem_u32(rows_full);   // the leading block's barriers
+        const uint32_t cols_at = CG == 2 ? peer_address(smem_u32(cols_full), 0) : smem_u32(cols_full);
+        uint32_t sa = 0, pa = 1, sb = 0, pb = 1;
+        const bool leader = elect_one();
+        bool ok = true, withhold = p.withhold && blockIdx.x == 0, fresh = true;
+        for (PairWalk<CG> w(p); ok && w.more();) {
+            for (unsigned k = 0; k < p.steps; ++k) {
+                if (fresh) {
+                    if (!(ok = warp_wait(&rows_empty[sa], pa, guard, kSiteEmpty))) break;
+                    if (leader) {
+                        if (rank == 0) mbar_arrive_expect_tx(&rows_full[sa], CG * S::SLOT);
+                        // test hook: the first copy never lands
+                        if (!withhold) load_box<CG>(smem + sa * S::SLOT, &p.a[0], rows_at + sa * 8, k * 64, w.row * S::M + rank * 128);
+                    }
+                    withhold = false;
+                    if (++sa == S::ROWS) {
+                        sa = 0;
+                        pa ^= 1u;
+                    }
+                }
+                if (!(ok = warp_wait(&cols_empty[sb], pb, guard, kSiteEmpty))) break;
+                const unsigned at = w.col + 1 == p.cols ? 2 : 0, nf = at ? p.last_nf : S::NF;
+                const uint32_t to = smem + (S::ROWS + sb) * S::SLOT, bar = cols_at + sb * 8;
+                if (leader) {
+                    if (rank == 0) mbar_arrive_expect_tx(&cols_full[sb], 2 * nf * 128);   // of both blocks
+                    if constexpr (CG == 2) {
+                        load_box<CG>(to, &p.b[at + rank], bar, k * 64, w.col * S::NF);
+                    } else {
+                        load_box<CG>(to, &p.b[at], bar, k * 64, w.col * S::NF);
+                        load_box<CG>(to + nf * 128, &p.b[at + 1], bar, k * 64, w.col * S::NF);
+                    }
+                }
+                if (++sb == S::COLS) {
+                    sb = 0;
+                    pb ^= 1u;
+                }
+            }
+            const unsigned item = w.item;
+            w.next();
+            fresh = w.item != item;
+        }
+        if (!ok) settle();
+    } else if (warp == 1 && rank == 0) {
+        // products.  Rows of 128 bytes, eight to an atom of the swizzle; 16 elements along the summed axis are 32 bytes of a row
+        constexpr uint32_t TYPES = std::is_same<T, __half>::value ? ~((7u << 7) | (7u << 10)) : ~0u;
+        const uint64_t desc = sdesc(0u, 16u, 1024u, 2u);
+        uint32_t sa0 = 0, pa0 = 0, sb = 0, pb = 0, n = 0;   // sa0, pa0: of the item's first step
+        const bool leader = elect_one();
+        bool ok = true, fresh = true;
+        for (PairWalk<CG> w(p); ok && w.more(); ++n) {
+            const uint32_t buf = n & 1u, acc = tmem + buf * S::TMEM;
+            if (!(ok = warp_wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP))) break;
+            tc_fence_after();
+            const bool last = w.col + 1 == w.end;
+            const uint32_t idesc = idesc_bf16(S::M, 2 * (w.col + 1 == p.cols ? p.last_nf : S::NF), false, false) & TYPES;
+            uint32_t sa = sa0, pa = pa0;
+            for (unsigned k = 0; k < p.steps; ++k) {
+                if (fresh && !(ok = warp_wait(&rows_full[sa], pa, guard, kSiteKV))) break;
+                if (!(ok = warp_wait(&cols_full[sb], pb, guard, kSiteKV))) break;
+                tc_fence_after();
+                const uint32_t at = smem + sa * S::SLOT, bt = smem + (S::ROWS + sb) * S::SLOT;
+                if (leader) {
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) mma<CG>(acc, desc + ((at + j * 32) >> 4), desc + ((bt + j * 32) >> 4), idesc, k > 0 || j > 0);
+                    commit<CG>(&cols_empty[sb]);
+                    if (last) commit<CG>(&rows_empty[sa]);
+                }
+                if (++sa == S::ROWS) {
+                    sa = 0;
+                    pa ^= 1u;
+                }
+                if (++sb == S::COLS) {
+                    sb = 0;
+                    pb ^= 1u;
+                }
+            }
+            if (ok && leader) commit<CG>(&acc_full[buf]);
+            const unsigned item = w.item;
+            w.next();
+            fresh = w.item != item;
+            if (fresh) {
+                sa0 = sa;
+                pa0 = pa;
+            }
+        }
+        if (!ok) settle();
+    } else if (warp >= 4) {
+        // results: warp e takes rows 32 (e & 3) .. of the block and 32 columns
+        const int e = warp - 4, quarter = e & 3, part = e >> 2;
+        const uint32_t staging = smem + S::STAGING + e * S::WARP_STAGING, dh_at = staging + 2048;
+        float* bias = reinterpret_cast<float*>(raw_smem + (smem - smem_u32(raw_smem)) + S::BIAS) + e * 64;
+        const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(acc_empty), 0) : 0u;
+        auto release = [&](uint32_t buf) {   // this warp has read its accumulators
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) arrive_remote(acc_at + buf * 8);
+                else mbar_arrive(&acc_empty[buf]);
+            }
+        };
+        auto row_of = [&](const PairWalk<CG>& w) { return static_cast<int>(w.row * S::M + rank * 128 + quarter * 32); };
+        auto col_of = [&](const PairWalk<CG>& w) { return static_cast<int>(w.col * S::NF + part * 32); };
+        auto fetch = [&](const PairWalk<CG>& w) {   // a tile's dh, ahead of it
+            if (lane == 0 && w.more()) {
+                mbar_arrive_expect_tx(&dh_full[e], 2048);
+                load_box<1>(dh_at, &p.in, smem_u32(&dh_full[e]), col_of(w), row_of(w));
+            }
+        };
+        // element by element, where rows are not whole chunks
+        auto by_elements = [&](int m0, int f0) {
+            __syncwarp();
+            uint16_t* out = static_cast<uint16_t*>(p.h);
+            for (int r = lane >> 4; r < 32 && m0 + r < p.T; r += 2) {
+                const int f = f0 + 2 * (lane & 15);
+                const uint32_t w = ld_shared_b32(word_at(staging, r, lane & 15));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (f + j < p.F) out[static_cast<long long>(m0 + r) * p.F + f + j] = static_cast<uint16_t>(w >> (16 * j));
+            }
+            __syncwarp();
+        };
+        auto by_tma = [&](const CUtensorMap* map, int m0, int f0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                store_box(map, staging, f0, m0);
+                tma_store_commit();
+            }
+        };
+        const uint32_t row = staging + lane * 64, dh_row = dh_at + lane * 64, sw = (lane >> 1) & 3;   // rows of 64 bytes in 64-byte swizzle
+        const bool biased = p.bg || p.bu;
+        // a loop for each activation: only one is run
+        auto results = [&](auto tag) {
+            constexpr int ACT = decltype(tag)::value;
+            PairWalk<CG> w(p);
+            if constexpr (WHICH == kSlopes)
+                if (p.wide) fetch(w);
+            for (uint32_t n = 0; w.more(); ++n) {
+                const uint32_t buf = n & 1u;
+                const int m0 = row_of(w), f0 = col_of(w);
+                const uint32_t nf = w.col + 1 == p.cols ? p.last_nf : S::NF;
+                const uint32_t taddr = tmem + buf * S::TMEM + (static_cast<uint32_t>(quarter * 32) << 16) + part * 32;
+                const bool there = f0 < p.F && m0 < p.T;   // else nothing but to give the accumulators back
+                w.next();
+                uint32_t dh[16];
+                if constexpr (WHICH == kSlopes) {
+                    if (!p.wide) {
+                        __syncwarp();
+                        if (there) {
+                            const uint16_t* from = static_cast<const uint16_t*>(p.dh);
+                            for (int r = lane >> 4; r < 32; r += 2) {
+                                const int f = f0 + 2 * (lane & 15);
+                                uint32_t v = 0;
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (m0 + r < p.T && f + j < p.F)
+                                        v |= static_cast<uint32_t>(from[static_cast<long long>(m0 + r) * p.F + f + j]) << (16 * j);
+                                st_shared_b32(word_at(dh_at, r, lane & 15), v);
+                            }
+                        }
+                        __syncwarp();
+                    } else if (!__all_sync(0xffffffffu, mbar_wait(&dh_full[e], n & 1u, guard, kSiteQ))) {
+                        settle();
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 v = ld_shared_v4(dh_row + (j ^ sw) * 16);
+                        dh[4 * j] = v.x, dh[4 * j + 1] = v.y, dh[4 * j + 2] = v.z, dh[4 * j + 3] = v.w;
+                    }
+                    __syncwarp();
+                    if (p.wide) fetch(w);
+                }
+                if (biased) {
+                    __syncwarp();
+                    if (f0 + lane < p.F) {
+                        bias[lane] = p.bg ? widen<T>(p.bg, f0 + lane) : 0.f;
+                        bias[32 + lane] = p.bu ? widen<T>(p.bu, f0 + lane) : 0.f;
+                    }
+                }
+                if (lane == 0) tma_store_wait_read();   // the results before have left the staging
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal))) {
+                    settle();
+                    break;
+                }
+                tc_fence_after();
+                if (!there) {
+                    release(buf);
+                    continue;
+                }
+                uint32_t du[16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t rg[16], ru[16];
+                    tmem_ld16(taddr + c * 16, rg);
+                    tmem_ld16(taddr + nf + c * 16, ru);
+                    tmem_ld_wait_all();
+                    reg_fence16(rg);
+                    reg_fence16(ru);
+                    if (c == 1) release(buf);
+                    float g[16], u[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        g[k] = __uint_as_float(rg[k]);
+                        u[k] = __uint_as_float(ru[k]);
+                    }
+                    if (biased) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            g[k] += bias[c * 16 + k];
+                            u[k] += bias[32 + c * 16 + k];
+                        }
+                    }
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float a0, a1, s0, s1;
+                        activate<ACT, true>(g[2 * k], a0, s0);
+                        activate<ACT, true>(g[2 * k + 1], a1, s1);
+                        if constexpr (WHICH == kForward) {
+                            v[k] = Elem<T>::pair(a0 * u[2 * k], a1 * u[2 * k + 1]);
+                        } else {
+                            float d0, d1;
+                            Elem<T>::two(dh[8 * c + k], d0, d1);
+                            v[k] = Elem<T>::pair(d0 * u[2 * k] * s0, d1 * u[2 * k + 1] * s1);
+                            du[8 * c + k] = Elem<T>::pair(d0 * a0, d1 * a1);
+                        }
+                    }
+                    st_shared_v4(row + ((2 * c) ^ sw) * 16, v[0], v[1], v[2], v[3]);
+                    st_shared_v4(row + ((2 * c + 1) ^ sw) * 16, v[4], v[5], v[6], v[7]);
+                }
+                if constexpr (WHICH == kForward) {
+                    if (p.wide) by_tma(&p.out[0], m0, f0);
+                    else by_elements(m0, f0);
+                } else {
+                    // dg, then du through the same staging
+                    by_tma(&p.out[0], m0, f0);
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) st_shared_v4(row + (j ^ sw) * 16, du[4 * j], du[4 * j + 1], du[4 * j + 2], du[4 * j + 3]);
+                    by_tma(&p.out[1], m0, f0);
+                }
+            }
+        };
+        with_act(p.act, results);
+        if (lane == 0) tma_store_wait_all();
+        tc_fence_before();
+    }
+    __syncwarp();
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_give<CG>(tmem, 2 * S::TMEM);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Tokens and weights: plain products, 256 x 256 on pairs of blocks or 128 x 128, the summed axis cut into splits where there
+// are few tiles (their fp32 sums are added by another kernel).
+// ---------------------------------------------------------------------------------------------
+
+template <int CG>
+struct TileShape {
+    static constexpr int N = 128 * CG, M = 128 * CG;
+    static constexpr uint32_t A_BYTES = 128 * 128, STAGE = 2 * A_BYTES;
+    static constexpr int WARPS = 8, OUT = N / 2;                 // of the epilogue; columns of a warp
+    static constexpr int STAGES = 5, THREADS = 128 + 32 * WARPS;
+    static constexpr uint32_t STAGING = STAGES * STAGE;          // 4 KB a warp: 32 rows of 128 bytes
+    static constexpr uint32_t BYTES = STAGING + WARPS * 4096 + 1024;
+    static_assert(BYTES <= 227 * 1024 - 512, "more than a block's shared memory");
 };
 
 struct Tile {
     unsigned row, col, first, last, split;   // steps [first, last)
 };
-template <int WHICH>
 __device__ __forceinline__ Tile tile_of(const GluTcParams& p, unsigned i) {
-    const unsigned per = p.rows * p.cols;
-    Tile t;
-    t.split = i / per;
-    i -= t.split * per;
-    const unsigned band = i / (kBand * p.cols), base = band * kBand, height = min(kBand, p.rows - base);
-    i -= base * p.cols;
-    t.col = i / height;
-    t.row = base + i - t.col * height;
-    t.first = t.split * p.run;
-    t.last = min(p.steps, t.first + p.run);
-    return t;
+    const unsigned per = p.rows * p.cols, split = i / per;
+    const Place at = place_of(i - split * per, p.rows, p.cols);
+    const unsigned first = split * p.run;
+    return {at.row, at.col, first, min(p.steps, first + p.run), split};
 }
 
-template <int WHICH, int CG, int NT, typename T>
-__global__ void __launch_bounds__(TileShape<WHICH, CG, NT>::THREADS, 1) glu_tile_kernel(const __grid_constant__ GluTcParams p) {
-    using S = TileShape<WHICH, CG, NT>;
-    constexpr bool PAIR = S::PAIR, WEIGHTS = WHICH == kWeights;
+template <int WHICH, int CG, typename T>
+__global__ void __launch_bounds__(TileShape<CG>::THREADS, 1) glu_tile_kernel(const __grid_constant__ GluTcParams p) {
+    using S = TileShape<CG>;
+    constexpr bool WEIGHTS = WHICH == kWeights;
     extern __shared__ uint8_t raw_smem[];
-    __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], dh_full[S::WARPS];
+    __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_base;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -236,54 +583,49 @@ __global__ void __launch_bounds__(TileShape<WHICH, CG, NT>::THREADS, 1) glu_tile
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], CG * S::WARPS);
         }
-        for (int i = 0; i < S::WARPS; ++i) mbar_init(&dh_full[i], 1);
         fence_barrier_init();
     }
-    if (warp == 2) tmem_take<CG>(&tmem_base, 2 * NT);
+    if (warp == 2) tmem_take<CG>(&tmem_base, 2 * S::N);
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // copies
         const uint32_t full_at = CG == 2 ? peer_address(smem_u32(full), 0) : smem_u32(full);   // the leading block's barriers
         int s = 0;
         uint32_t parity = 1;
+        const bool leader = elect_one();
         bool ok = true, withhold = p.withhold && blockIdx.x == 0;
         for (unsigned i = mine; ok && i < tiles; i += all) {
-            const Tile t = tile_of<WHICH>(p, i);
+            const Tile t = tile_of(p, i);
             for (unsigned k = t.first; k < t.last; ++k) {
-                ok = CG == 2 ? mbar_spin_cluster(&empty[s], parity, guard, kSiteEmpty) : mbar_spin(&empty[s], parity, guard, kSiteEmpty);
+                ok = warp_wait(&empty[s], parity, guard, kSiteEmpty);
                 if (!ok) break;
                 const uint32_t to = smem + s * S::STAGE;
                 const uint32_t bar = full_at + s * 8;
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * S::STAGE);
-                if (withhold) {   // test hook: the first copy never lands
-                    withhold = false;
-                } else if constexpr (PAIR) {
-                    load_box<CG>(to, &p.a[0], bar, k * 64, t.row * S::M + rank * 128);
-                    if constexpr (CG == 2) {
-                        load_box<CG>(to + S::A_BYTES, &p.b[rank], bar, k * 64, t.col * S::NF);
+                if (leader) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * S::STAGE);
+                    if (withhold) {
+                        // test hook: the first copy never lands
+                    } else if constexpr (WHICH == kTokens) {
+                        const unsigned half = k >= p.steps / 2, at = (k - half * (p.steps / 2)) * 64;
+                        load_box<CG>(to, &p.a[half], bar, at, t.row * S::M + rank * 128);
+    #pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[half], bar, t.col * S::N + rank * 128 + j * 64, at);
                     } else {
-                        load_box<CG>(to + S::A_BYTES, &p.b[0], bar, k * 64, t.col * S::NF);
-                        load_box<CG>(to + S::A_BYTES + S::B_BYTES / 2, &p.b[1], bar, k * 64, t.col * S::NF);
+                        const unsigned half = t.row >= p.rows / 2, row = (t.row - half * (p.rows / 2)) * S::M + rank * 128;
+    #pragma unroll
+                        for (int j = 0; j < 2; ++j) load_box<CG>(to + j * 8192, &p.a[half], bar, row + j * 64, k * 64);
+    #pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[0], bar, t.col * S::N + rank * 128 + j * 64, k * 64);
                     }
-                } else if constexpr (WHICH == kTokens) {
-                    const unsigned half = k >= p.steps / 2, at = (k - half * (p.steps / 2)) * 64;
-                    load_box<CG>(to, &p.a[half], bar, at, t.row * S::M + rank * 128);
-#pragma unroll
-                    for (int j = 0; j < NT / CG / 64; ++j)
-                        load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[half], bar, t.col * NT + rank * (NT / 2) + j * 64, at);
-                } else {
-                    const unsigned half = t.row >= p.rows / 2, row = (t.row - half * (p.rows / 2)) * S::M + rank * 128;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) load_box<CG>(to + j * 8192, &p.a[half], bar, row + j * 64, k * 64);
-#pragma unroll
-                    for (int j = 0; j < NT / CG / 64; ++j)
-                        load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[0], bar, t.col * NT + rank * (NT / 2) + j * 64, k * 64);
                 }
+                withhold = false;
                 if (++s == S::STAGES) {
                     s = 0;
                     parity ^= 1u;
@@ -291,46 +633,46 @@ __global__ void __launch_bounds__(TileShape<WHICH, CG, NT>::THREADS, 1) glu_tile
             }
         }
         if (!ok) settle();
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // products
-        const uint32_t bf = idesc_bf16(S::M, NT, WEIGHTS, !PAIR), idesc = std::is_same<T, __half>::value ? bf & ~((7u << 7) | (7u << 10)) : bf;
+        const uint32_t bf = idesc_bf16(S::M, S::N, WEIGHTS, true), idesc = std::is_same<T, __half>::value ? bf & ~((7u << 7) | (7u << 10)) : bf;
         // rows of 128 bytes: eight make an atom of the swizzle.  Along the summed axis 16 elements are 32 bytes of a row, or where
         // the operand runs along the other axis 16 rows; there the next 64 of that axis are 8 KB on
-        const uint64_t da = sdesc(0u, WEIGHTS ? 8192u : 16u, 1024u, 2u), db = sdesc(0u, PAIR ? 16u : 8192u, 1024u, 2u);
-        constexpr uint32_t KA = WEIGHTS ? 2048 : 32, KB = PAIR ? 32 : 2048;
+        const uint64_t da = sdesc(0u, WEIGHTS ? 8192u : 16u, 1024u, 2u), db = sdesc(0u, 8192u, 1024u, 2u);
+        constexpr uint32_t KA = WEIGHTS ? 2048 : 32, KB = 2048;
         int s = 0;
         uint32_t parity = 0, n = 0;
+        const bool leader = elect_one();
         bool ok = true;
         for (unsigned i = mine; ok && i < tiles; i += all, ++n) {
-            const Tile t = tile_of<WHICH>(p, i);
-            const uint32_t buf = n & 1u, acc = tmem + buf * NT;
-            ok = CG == 2 ? mbar_spin_cluster(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP)
-                         : mbar_spin(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP);
+            const Tile t = tile_of(p, i);
+            const uint32_t buf = n & 1u, acc = tmem + buf * S::N;
+            ok = warp_wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP);
             if (!ok) break;
             tc_fence_after();
             for (unsigned k = t.first; k < t.last; ++k) {
-                ok = CG == 2 ? mbar_spin_cluster(&full[s], parity, guard, kSiteKV) : mbar_spin(&full[s], parity, guard, kSiteKV);
+                ok = warp_wait(&full[s], parity, guard, kSiteKV);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = smem + s * S::STAGE;
+                if (leader) {
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    mma<CG>(acc, da + ((at + j * KA) >> 4), db + ((at + S::A_BYTES + j * KB) >> 4), idesc, k > t.first || j > 0);
-                commit<CG>(&empty[s]);
+                    for (uint32_t j = 0; j < 4; ++j)
+                        mma<CG>(acc, da + ((at + j * KA) >> 4), db + ((at + S::A_BYTES + j * KB) >> 4), idesc, k > t.first || j > 0);
+                    commit<CG>(&empty[s]);
+                }
                 if (++s == S::STAGES) {
                     s = 0;
                     parity ^= 1u;
                 }
             }
-            if (ok) commit<CG>(&acc_full[buf]);
+            if (ok && leader) commit<CG>(&acc_full[buf]);
         }
         if (!ok) settle();
     } else if (warp >= 4) {
         // results: warp e takes rows 32 (e & 3) .. of the block and the (e / 4)-th run of columns
         const int e = warp - 4, quarter = e & 3, part = e >> 2;
-        const uint32_t staging = smem + S::STAGING + e * S::BUFFERS * 4096;
-        float* bias = reinterpret_cast<float*>(raw_smem + (smem - smem_u32(raw_smem)) + S::BIAS) + e * 128;
-        const uint32_t row = staging + lane * 128, sw = lane & 7;
+        const uint32_t staging = smem + S::STAGING + e * 4096;
         uint32_t n = 0;
         const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(acc_empty), 0) : 0u;
         auto release = [&](uint32_t buf) {   // this warp has read its accumulators
@@ -341,188 +683,66 @@ __global__ void __launch_bounds__(TileShape<WHICH, CG, NT>::THREADS, 1) glu_tile
                 else mbar_arrive(&acc_empty[buf]);
             }
         };
-        for (unsigned i = mine; i < tiles; i += all, ++n) {
-            const Tile t = tile_of<WHICH>(p, i);
-            const uint32_t buf = n & 1u;
-            const int m0 = static_cast<int>((WEIGHTS && t.row >= p.rows / 2 ? t.row - p.rows / 2 : t.row) * S::M + rank * 128 + quarter * 32);
-            const uint32_t taddr = tmem + buf * NT + (static_cast<uint32_t>(quarter * 32) << 16);
-            if constexpr (PAIR) {
-                const int f0 = static_cast<int>(t.col * S::NF + part * 64);
-                // what the tile needs besides its products
-                if (lane == 0) tma_store_wait_read();
-                __syncwarp();
-                if constexpr (WHICH == kSlopes) {
-                    if (p.wide) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&dh_full[e], 4096);
-                            load_box<1>(staging, &p.in, smem_u32(&dh_full[e]), f0, m0);
-                        }
-                    } else {
-                        const uint16_t* from = static_cast<const uint16_t*>(p.dh);
-                        for (int r = 0; r < 32; ++r) {
-                            uint32_t w = 0;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (m0 + r < p.T && f0 + 2 * lane + j < p.F)
-                                    w |= static_cast<uint32_t>(from[static_cast<long long>(m0 + r) * p.F + f0 + 2 * lane + j]) << (16 * j);
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4), "r"(w) : "memory");
-                        }
-                    }
-                }
-                if (p.bg || p.bu) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int f = f0 + lane + 32 * j;
-                        bias[lane + 32 * j] = p.bg && f < p.F ? widen<T>(p.bg, f) : 0.f;
-                        bias[64 + lane + 32 * j] = p.bu && f < p.F ? widen<T>(p.bu, f) : 0.f;
-                    }
-                }
-                __syncwarp();
-                bool ok = mbar_wait(&acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal);
-                if constexpr (WHICH == kSlopes)
-                    if (p.wide) ok = ok && mbar_wait(&dh_full[e], n & 1u, guard, kSiteQ);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    settle();
-                    break;
-                }
-                tc_fence_after();
-                uint32_t g[2][16], u[2][16];
-                tmem_ld16(taddr + part * 64, g[0]);
-                tmem_ld16(taddr + S::NF + part * 64, u[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait_all();
-                    reg_fence16(g[c & 1]);
-                    reg_fence16(u[c & 1]);
-                    if (c < 3) {
-                        tmem_ld16(taddr + part * 64 + (c + 1) * 16, g[(c + 1) & 1]);
-                        tmem_ld16(taddr + S::NF + part * 64 + (c + 1) * 16, u[(c + 1) & 1]);
-                    } else {
-                        release(buf);
-                    }
-                    float fg[16], fu[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        fg[k] = __uint_as_float(g[c & 1][k]);
-                        fu[k] = __uint_as_float(u[c & 1][k]);
-                    }
-                    if (p.bg || p.bu) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            fg[k] += bias[c * 16 + k];
-                            fu[k] += bias[64 + c * 16 + k];
-                        }
-                    }
-                    const uint32_t at0 = row + ((2 * c) ^ sw) * 16, at1 = row + ((2 * c + 1) ^ sw) * 16;
-                    uint32_t w[8], v[8];
-                    if constexpr (WHICH == kSlopes) {
-                        const uint4 a = ld_shared_v4(at0), b = ld_shared_v4(at1);
-                        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-                    }
-                    with_act(p.act, [&](auto tag) {
-                        constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float a0, a1, s0, s1;
-                            activate<ACT, true>(fg[2 * k], a0, s0);
-                            activate<ACT, true>(fg[2 * k + 1], a1, s1);
-                            if constexpr (WHICH == kForward) {
-                                w[k] = Elem<T>::pair(a0 * fu[2 * k], a1 * fu[2 * k + 1]);
+                    const uint32_t row = staging + lane * 128, sw = lane & 7;   // rows of 128 bytes in 128-byte swizzle
+                    for (unsigned i = mine; i < tiles; i += all, ++n) {
+                        const Tile t = tile_of(p, i);
+                        const uint32_t buf = n & 1u;
+                        const int m0 = static_cast<int>((WEIGHTS && t.row >= p.rows / 2 ? t.row - p.rows / 2 : t.row) * S::M + rank * 128 + quarter * 32);
+                        const uint32_t taddr = tmem + buf * S::N + (static_cast<uint32_t>(quarter * 32) << 16);
+                                        const int c0 = static_cast<int>(t.col * S::N + part * S::OUT);
+                                        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal))) {
+                                            settle();
+                                            break;
+                                        }
+                                        tc_fence_after();
+                                        const unsigned half = WEIGHTS && t.row >= p.rows / 2;
+                        const int last_row = WEIGHTS ? p.F : p.T;
+                        float* sums = p.partial + static_cast<long long>(WEIGHTS ? t.split * 2 + half : t.split) * last_row * p.D;
+                        T* result = static_cast<T*>(WHICH == kTokens ? p.dx : half ? p.dwu : p.dwg);
+                        uint32_t v[2][16];
+                        tmem_ld16(taddr + part * S::OUT, v[0]);
+                        constexpr int PIECES = S::OUT / 16;
+        #pragma unroll
+                        for (int c = 0; c < PIECES; ++c) {
+                            const int per = p.split ? 2 : 4, at = c % per;   // the staging holds 64 columns of 2 bytes or 32 of 4
+                            tmem_ld_wait_all();
+                            reg_fence16(v[c & 1]);
+                            if (c + 1 < PIECES) tmem_ld16(taddr + part * S::OUT + (c + 1) * 16, v[(c + 1) & 1]);
+                            else release(buf);
+                            if (p.split) {
+        #pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    st_shared_v4(row + ((4 * at + j) ^ sw) * 16, v[c & 1][4 * j], v[c & 1][4 * j + 1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]);
                             } else {
-                                float d0, d1;
-                                Elem<T>::two(w[k], d0, d1);
-                                w[k] = Elem<T>::pair(d0 * fu[2 * k] * s0, d1 * fu[2 * k + 1] * s1);
-                                v[k] = Elem<T>::pair(d0 * a0, d1 * a1);
+                                uint32_t w[8];
+        #pragma unroll
+                                for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pair(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
+                                st_shared_v4(row + ((2 * at) ^ sw) * 16, w[0], w[1], w[2], w[3]);
+                                st_shared_v4(row + ((2 * at + 1) ^ sw) * 16, w[4], w[5], w[6], w[7]);
+                            }
+                            if (at == per - 1) {   // out by rows: eight lanes a row
+                                __syncwarp();
+                                const int r = lane >> 3, col = c0 + (c / per) * per * 16 + (lane & 7) * (p.split ? 4 : 8);
+        #pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint4 w = ld_shared_v4(staging + (r + 4 * j) * 128 + (((lane & 7) ^ ((r + 4 * j) & 7)) << 4));
+                                    const long long to = static_cast<long long>(m0 + r + 4 * j) * p.D + col;
+                                    if (m0 + r + 4 * j < last_row && col < p.D) {
+                                        if (p.split) st_stream(sums + to, w);
+                                        else st_stream(result + to, w);
+                                    }
+                                }
+                                __syncwarp();
                             }
                         }
-                    });
-                    st_shared_v4(at0, w[0], w[1], w[2], w[3]);
-                    st_shared_v4(at1, w[4], w[5], w[6], w[7]);
-                    if constexpr (WHICH == kSlopes) {
-                        st_shared_v4(at0 + 4096, v[0], v[1], v[2], v[3]);
-                        st_shared_v4(at1 + 4096, v[4], v[5], v[6], v[7]);
                     }
-                }
-                if (WHICH == kSlopes || p.wide) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (f0 < p.F && m0 < p.T) {
-                            store_box(&p.out[0], staging, f0, m0);
-                            if constexpr (WHICH == kSlopes) store_box(&p.out[1], staging + 4096, f0, m0);
-                        }
-                        tma_store_commit();
-                    }
-                } else {
-                    __syncwarp();
-                    uint16_t* to = static_cast<uint16_t*>(p.h);
-                    for (int r = 0; r < 32 && m0 + r < p.T; ++r) {
-                        uint32_t w;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) : "memory");
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (f0 + 2 * lane + j < p.F) to[static_cast<long long>(m0 + r) * p.F + f0 + 2 * lane + j] = static_cast<uint16_t>(w >> (16 * j));
-                    }
-                }
-            } else {
-                const int c0 = static_cast<int>(t.col * NT + part * S::OUT);
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal))) {
-                    settle();
-                    break;
-                }
-                tc_fence_after();
-                const unsigned half = WEIGHTS && t.row >= p.rows / 2;
-                uint32_t v[2][16];
-                tmem_ld16(taddr + part * S::OUT, v[0]);
-                constexpr int PIECES = S::OUT / 16;
-#pragma unroll
-                for (int c = 0; c < PIECES; ++c) {
-                    // a buffer holds 64 columns of 2 bytes or 32 of 4
-                    const int per = p.split ? 2 : 4, at = c % per;
-                    const uint32_t box = (c / per) & 1;
-                    if (at == 0) {   // the store before the last has read this buffer
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        __syncwarp();
-                    }
-                    tmem_ld_wait_all();
-                    reg_fence16(v[c & 1]);
-                    if (c + 1 < PIECES) tmem_ld16(taddr + part * S::OUT + (c + 1) * 16, v[(c + 1) & 1]);
-                    else release(buf);
-                    const uint32_t to = row + box * 4096;
-                    if (p.split) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            st_shared_v4(to + ((4 * at + j) ^ sw) * 16, v[c & 1][4 * j], v[c & 1][4 * j + 1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]);
-                    } else {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pair(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
-                        st_shared_v4(to + ((2 * at) ^ sw) * 16, w[0], w[1], w[2], w[3]);
-                        st_shared_v4(to + ((2 * at + 1) ^ sw) * 16, w[4], w[5], w[6], w[7]);
-                    }
-                    if (at == per - 1) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            const int x = c0 + (c / per) * per * 16;
-                            if (x < p.D && m0 < (WEIGHTS ? p.F : p.T)) {
-                                if (p.split) store_box(&p.out[0], staging + box * 4096, x, m0, WEIGHTS ? t.split * 2 + half : t.split);
-                                else store_box(&p.out[half], staging + box * 4096, x, m0);
-                            }
-                            tma_store_commit();   // an empty group too: the waits count groups
-                        }
-                    }
-                }
-            }
-        }
-        if (lane == 0) tma_store_wait_all();
         tc_fence_before();
     }
     __syncwarp();
     if constexpr (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_give<CG>(tmem, 2 * NT);
+    if (warp == 2) tmem_give<CG>(tmem, 2 * S::N);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -568,36 +788,41 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     bool ok = true;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        const bool leader = elect_one();
         bool withhold = p.withhold && blockIdx.x == 0;
         for (unsigned k = first; k < last; ++k) {
             const unsigned n = k - first, s = n % S::STAGES;
-            if (!(ok = mbar_spin(&empty[s], (n / S::STAGES & 1u) ^ 1u, guard, kSiteEmpty))) break;
+            if (!(ok = warp_wait(&empty[s], (n / S::STAGES & 1u) ^ 1u, guard, kSiteEmpty))) break;
             const uint32_t to = smem + s * S::STAGE, bar = smem_u32(&full[s]);
-            mbar_arrive_expect_tx(&full[s], S::STAGE);
-            if (withhold) {   // test hook: the first copy never lands
-                withhold = false;
-                continue;
+            if (leader) {
+                mbar_arrive_expect_tx(&full[s], S::STAGE);
+                if (!withhold) {   // test hook: the first copy never lands
+                    load_box<1>(to, &p.b[0], bar, k * 64, f0);
+                    load_box<1>(to + 8192, &p.b[1], bar, k * 64, f0);
+                    load_box<1>(to + S::A_BYTES, &p.a[0], bar, k * 64, 0);
+                }
             }
-            load_box<1>(to, &p.b[0], bar, k * 64, f0);
-            load_box<1>(to + 8192, &p.b[1], bar, k * 64, f0);
-            load_box<1>(to + S::A_BYTES, &p.a[0], bar, k * 64, 0);
+            withhold = false;
         }
         if (!ok) settle();
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         const uint32_t bf = idesc_bf16(128, NTOK, false, false), idesc = std::is_same<T, __half>::value ? bf & ~((7u << 7) | (7u << 10)) : bf;
         const uint64_t d = sdesc(0u, 16u, 1024u, 2u);
+        const bool leader = elect_one();
         for (unsigned k = first; k < last; ++k) {
             const unsigned n = k - first, s = n % S::STAGES;
-            if (!(ok = mbar_spin(&full[s], n / S::STAGES & 1u, guard, kSiteKV))) break;
+            if (!(ok = warp_wait(&full[s], n / S::STAGES & 1u, guard, kSiteKV))) break;
             tc_fence_after();
             const uint32_t at = smem + s * S::STAGE;
+            if (leader) {
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) umma_bf16(tmem, d + ((at + j * 32) >> 4), d + ((at + S::A_BYTES + j * 32) >> 4), idesc, n > 0 || j > 0);
-            umma_commit(&empty[s]);
+                for (uint32_t j = 0; j < 4; ++j) umma_bf16(tmem, d + ((at + j * 32) >> 4), d + ((at + S::A_BYTES + j * 32) >> 4), idesc, n > 0 || j > 0);
+                umma_commit(&empty[s]);
+            }
         }
-        if (ok) umma_commit(&done);
-        else settle();
+        if (!ok) settle();
+        else if (leader) umma_commit(&done);
     } else if (warp >= 2) {
         ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, guard, kSiteFinal));
         if (!ok) settle();
@@ -709,16 +934,19 @@ na_status launch_glu(Kernel* kernel, const GluTcParams& p, unsigned blocks, int 
     return cudaLaunchKernelEx(&c, kernel, p) == cudaSuccess ? NA_OK : NA_ERR_CUDA;
 }
 
-// pairs: tiles of 256 x 256 on pairs of blocks, else of 128 x 128.
+template <int WHICH, int CG, typename T>
+na_status launch_tiles(const GluTcParams& p, unsigned tiles, cudaStream_t s) {
+    const unsigned blocks = CG * std::min<unsigned>(tiles, kSms / CG);
+    if constexpr (WHICH == kForward || WHICH == kSlopes)
+        return launch_glu(glu_pair_kernel<WHICH, CG, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
+    else
+        return launch_glu(glu_tile_kernel<WHICH, CG, T>, p, blocks, CG, TileShape<CG>::THREADS, TileShape<CG>::BYTES, s);
+}
+
 template <int WHICH, typename T>
 na_status launch_tiles(const GluTcParams& p, bool pairs, cudaStream_t s) {
-    const unsigned tiles = p.rows * p.cols * p.splits;
-    if (pairs) {
-        using S = TileShape<WHICH, 2, 256>;
-        return launch_glu(glu_tile_kernel<WHICH, 2, 256, T>, p, 2 * (tiles < kSms / 2 ? tiles : kSms / 2), 2, S::THREADS, S::BYTES, s);
-    }
-    using S = TileShape<WHICH, 1, 128>;
-    return launch_glu(glu_tile_kernel<WHICH, 1, 128, T>, p, tiles < kSms ? tiles : kSms, 1, S::THREADS, S::BYTES, s);
+    const unsigned tiles = WHICH == kForward || WHICH == kSlopes ? p.rows * p.groups : p.rows * p.cols * p.splits;
+    return pairs ? launch_tiles<WHICH, 2, T>(p, tiles, s) : launch_tiles<WHICH, 1, T>(p, tiles, s);
 }
 
 template <int WHICH, typename T>
