@@ -24,7 +24,7 @@ namespace {
 constexpr int kAddThreads = 256;   // blocks of warp teams
 constexpr int kAddBlock = 512;     // most threads of a row's block (128 registers each)
 constexpr int kAddMaxC = 8192;
-constexpr int kAddTileBytes = 4 * 1024;   // of a tile of the ring, an array
+constexpr int kAddTileBytes = 8 * 1024;   // of a tile of the ring, an array
 constexpr int kAddTileRows = 32;         // most rows of a tile: a lane holds a row's statistics
 constexpr long long kAddMaxGroups = 32768;   // a group is a row of blocks of the second kernel
 
@@ -57,7 +57,6 @@ struct AddParams {
     long long rows, group_rows;
     int groups, per_group;    // parts of a group
     int tile;                 // rows of a turn of a unit
-    int stages;               // ring: tiles, at most kAddStages
     unsigned* err;            // ring: device status word
     unsigned long long wait_ns;
     uint32_t withhold;        // ring: test hook, block 0 leaves out its first copy
@@ -83,8 +82,11 @@ __device__ __forceinline__ void gate_weights(const AddParams& p, const float* ga
 struct Walk {
     const AddParams& p;
     int unit, units, part, group;
-    long long row, end;   // the tile's first row, the end of the group
-    __device__ __forceinline__ Walk(const AddParams& q, int u, int n) : p(q), unit(u), units(n), part(blockIdx.x) { open(); }
+    long long step, row, end;   // rows to the next tile; the tile's first row, the end of the group
+    __device__ __forceinline__ Walk(const AddParams& q, int u, int n)
+        : p(q), unit(u), units(n), part(blockIdx.x), step(static_cast<long long>(q.tile) * q.per_group * n) {
+        open();
+    }
     __device__ __forceinline__ bool parts() const { return part < p.groups * p.per_group; }
     __device__ __forceinline__ void open() {
         if (!parts()) return;
@@ -94,7 +96,7 @@ struct Walk {
     }
     __device__ __forceinline__ bool here() const { return row < end; }   // the part has this tile
     __device__ __forceinline__ int rows() const { return static_cast<int>(min(static_cast<long long>(p.tile), end - row)); }
-    __device__ __forceinline__ void next() { row += static_cast<long long>(p.tile) * p.per_group * units; }
+    __device__ __forceinline__ void next() { row += step; }
     __device__ __forceinline__ void next_part() {
         part += gridDim.x;
         open();
@@ -109,7 +111,7 @@ struct Walk {
 // A unit's rows of several arrays through a ring of tiles in shared memory (cp.async.bulk; rows are whole chunks, so a tile is one
 // run of bytes of each array): registers alone do not keep enough loads under way beside the sums.  The unit's first thread
 // fills a stage again once the unit has read it.
-constexpr int kAddStages = 3;
+constexpr int kAddStages = 2;
 template <int N, bool BLOCK>
 struct Ring {
     uint64_t* full;                // shared: a barrier a stage
@@ -147,9 +149,9 @@ struct Ring {
         issued = 0;
         lost = -1;
         if (first) {
-            for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
+            for (int i = 0; i < kAddStages; ++i) mbar_init(&full[i], 1);
             fence_barrier_init();
-            for (int i = 0; i < p.stages; ++i) load(p, ahead, i);
+            for (int i = 0; i < kAddStages; ++i) load(p, ahead, i);
         }
         sync();
     }
@@ -163,19 +165,46 @@ struct Ring {
     __device__ __forceinline__ void done(const AddParams& p, Walk& ahead) {   // the unit has read the tile
         sync();
         if (first && lost < 0) load(p, ahead, s);
-        if (++s == p.stages) {
+        if (++s == kAddStages) {
             s = 0;
             parity ^= 1u;
         }
     }
     __device__ __forceinline__ void finish(const AddParams& p) {   // the copies in flight have to land before the memory is given back
         if (first && lost >= 0)
-            for (int i = lost; i < issued; ++i) mbar_drain(&full[i % p.stages], (i / p.stages) & 1, p.wait_ns);
+            for (int i = lost; i < issued; ++i) mbar_drain(&full[i % kAddStages], (i / kAddStages) & 1, p.wait_ns);
     }
 };
 
-// Blocks of warp teams per multiprocessor that the registers leave room for, with E channels to a thread.
-__host__ __device__ constexpr int add_fwd_blocks(int E) { return E <= 8 ? 3 : 2; }
+// Sums over a row's team; of a block's, every thread adds the warps' sums itself (slots: [value][warp], zeros of warps that are
+// not there), which is shorter than a second round of shuffles.
+template <int N, bool BLOCK>
+__device__ __forceinline__ void row_sum(float (&v)[N], int team, float (*slot)[16]) {
+    if constexpr (!BLOCK) {
+        team_sum<N, false>(v, team, nullptr);
+    } else {
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) slot[i][threadIdx.x >> 5] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.f;
+            for (int w = 0; w < static_cast<int>(blockDim.x >> 5); w += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(&slot[i][w]);
+                v[i] += (t.x + t.y) + (t.z + t.w);
+            }
+        }
+    }
+}
+
+// Blocks of the forward's warp teams per multiprocessor that the registers leave room for, with E channels to a thread.
+__host__ __device__ constexpr int add_fwd_blocks(int E, bool lean) { return E <= 8 && lean ? 3 : 2; }
 
 // A chunk of a row, of the ring or of memory; zeros where it is not there.
 template <typename T, int V, bool RING>
@@ -185,14 +214,15 @@ __device__ __forceinline__ void take(Chunk<T, V>& c, bool there, const unsigned 
     if (!there) c = Chunk<T, V>{};
 }
 
-template <typename T, int V, int J, bool BLOCK, bool RING>
-__global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RING ? 1 : add_fwd_blocks(J * V)) add_fwd_kernel(const AddParams p) {
+// LEAN: neither norm has a mean, and there are no shifts.
+template <typename T, int V, int J, bool BLOCK, bool RING, bool LEAN>
+__global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RING ? 1 : add_fwd_blocks(J * V, LEAN)) add_fwd_kernel(const AddParams p) {
     using A = Cols<V>;
     using W = typename A::W;
     constexpr int H = A::H;
     constexpr bool KEEP = J * V <= 8;   // vectors stay in registers over a part's rows
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float slots[2][4][1][32];   // taken in turn by the rows: a row's sums may be one
+    __shared__ __align__(16) float slots[2][4][1][16];   // taken in turn by the rows: a row's sums may be one
     constexpr int UNITS = BLOCK ? 1 : kAddThreads / 32;
     __shared__ uint64_t full[UNITS][kAddStages];
     const int l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1)), unit = BLOCK ? 0 : threadIdx.x >> 5;
@@ -201,8 +231,12 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
     auto inside = [&](int j) { return (l + p.team * j) * V < p.C; };
     Walk w(p, unit, UNITS), ahead(w);
     const uint32_t row_bytes = p.C * static_cast<uint32_t>(sizeof(T));
-    Ring<2, BLOCK> ring{full[unit], smem + static_cast<size_t>(unit) * p.stages * 2 * p.tile * row_bytes, {p.y, p.x}, row_bytes,
+    Ring<2, BLOCK> ring{full[unit], smem + static_cast<size_t>(unit) * kAddStages * 2 * p.tile * row_bytes, {p.y, p.x}, row_bytes,
                         BLOCK ? threadIdx.x == 0 : (threadIdx.x & 31) == 0};
+    if constexpr (BLOCK) {
+        for (int i = threadIdx.x; i < static_cast<int>(sizeof slots / sizeof(float)); i += blockDim.x) (&slots[0][0][0][0])[i] = 0.f;
+        __syncthreads();
+    }
     if constexpr (RING) ring.start(p, ahead);
     W ka[KEEP ? J : 1][H], kc[KEEP ? J : 1][H], kw[KEEP ? J : 1][H], kb[KEEP ? J : 1][H];
     const float *gate = nullptr, *weight = nullptr, *shift = nullptr;
@@ -261,14 +295,14 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
             // Centres s on its mean for layer norm, and the inverse deviation of what is left.
             auto moments = [&](int kind, int at, float& mean) {
                 mean = 0.f;
-                if (kind == NA_NORM_LAYER) {
+                if (!LEAN && kind == NA_NORM_LAYER) {
                     W t = 0;
 #pragma unroll
                     for (int j = 0; j < J; ++j)
 #pragma unroll
                         for (int e = 0; e < H; ++e) t = A::add(t, s[j][e]);
                     float sum[1] = {A::sum(t)};
-                    team_sum<1, BLOCK>(sum, p.team, slots[turn][at]);
+                    row_sum<1, BLOCK>(sum, p.team, slots[turn][at]);
                     mean = sum[0] * p.inv_c;
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
@@ -283,7 +317,7 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
 #pragma unroll
                     for (int e = 0; e < H; ++e) t = A::fma(s[j][e], s[j][e], t);
                 float sum[1] = {A::sum(t)};
-                team_sum<1, BLOCK>(sum, p.team, slots[turn][at + 1]);
+                row_sum<1, BLOCK>(sum, p.team, slots[turn][at + 1]);
                 return rsqrtf(fmaf(sum[0], p.inv_c, p.eps));
             };
             if (post) {
@@ -304,7 +338,7 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
                 A::from(f, x);
 #pragma unroll
                 for (int e = 0; e < H; ++e)
-                    s[j][e] = A::fma(A::mul(s[j][e], A::both(r)), ka[i][e], A::fma(x[e], A::both(p.residual), kc[i][e]));
+                    s[j][e] = A::fma(A::mul(s[j][e], A::both(r)), ka[i][e], LEAN ? A::mul(x[e], A::both(p.residual)) : A::fma(x[e], A::both(p.residual), kc[i][e]));
                 if (live && p.s && at < p.C) {
                     A::to(s[j], f);
                     store_chunk<T, V>(p.s, row * p.C + at, f);
@@ -324,7 +358,7 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
                 float f[V];
                 W h[H];
 #pragma unroll
-                for (int e = 0; e < H; ++e) h[e] = A::fma(A::mul(s[j][e], A::both(r)), kw[i][e], kb[i][e]);
+                for (int e = 0; e < H; ++e) h[e] = LEAN ? A::mul(A::mul(s[j][e], A::both(r)), kw[i][e]) : A::fma(A::mul(s[j][e], A::both(r)), kw[i][e], kb[i][e]);
                 if (live && at < p.C) {
                     A::to(h, f);
                     store_chunk<T, V>(p.h, row * p.C + at, f);
@@ -390,11 +424,11 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
     constexpr int H = A::H;
     constexpr bool KEEP = J * V <= 8;
     extern __shared__ __align__(128) unsigned char smem[];   // rings; then, of warp teams, the sums: [warp][C]
-    __shared__ float slots[2][2][2][32];   // taken in turn by the rows: a row's sums may be one
+    __shared__ __align__(16) float slots[2][2][2][16];   // taken in turn by the rows: a row's sums may be one
     constexpr int UNITS = BLOCK ? 1 : kAddThreads / 32;
     __shared__ uint64_t full[UNITS][kAddStages];
     const uint32_t row_bytes = p.C * static_cast<uint32_t>(sizeof(T));
-    const size_t ring_bytes = RING ? static_cast<size_t>(p.stages) * 4 * p.tile * row_bytes : 0;
+    const size_t ring_bytes = RING ? static_cast<size_t>(kAddStages) * 4 * p.tile * row_bytes : 0;
     float* cols = reinterpret_cast<float*>(smem + UNITS * ring_bytes);
     const int lane = threadIdx.x & 31, l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1)), unit = BLOCK ? 0 : threadIdx.x >> 5;
     const int mine = BLOCK ? 0 : lane / p.team, teams = BLOCK ? 1 : 32 / p.team;   // of the unit
@@ -412,6 +446,10 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
         for (int i = 0; i < 4; ++i) t[i] = there && from[i] ? from[i][next.row + lane] : 0.f;
         next.next();
     };
+    if constexpr (BLOCK) {
+        for (int i = threadIdx.x; i < static_cast<int>(sizeof slots / sizeof(float)); i += blockDim.x) (&slots[0][0][0][0])[i] = 0.f;
+        __syncthreads();
+    }
     read_stats(ahead_stats);
     if constexpr (RING) ring.start(p, ahead);
     W ka[KEEP ? J : 1][H], kw[KEEP ? J : 1][H];
@@ -511,11 +549,11 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
                     float k0 = 0.f, k1;
                     if constexpr (LEAN) {
                         float s[1] = {A::sum(s1)};
-                        team_sum<1, BLOCK>(s, p.team, slots[turn][0]);
+                        row_sum<1, BLOCK>(s, p.team, slots[turn][0]);
                         k1 = -norm_rstd * (s[0] * p.inv_c);
                     } else {
                         float s[2] = {A::sum(s0), A::sum(s1)};
-                        team_sum<2, BLOCK>(s, p.team, slots[turn][0]);
+                        row_sum<2, BLOCK>(s, p.team, slots[turn][0]);
                         if (p.norm == NA_NORM_LAYER) k0 = -norm_rstd * (s[0] * p.inv_c);
                         k1 = -norm_rstd * (s[1] * p.inv_c);
                     }
@@ -554,11 +592,11 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
                 if (post) {
                     if constexpr (LEAN) {
                         float s[1] = {A::sum(s1)};
-                        team_sum<1, BLOCK>(s, p.team, slots[turn][1]);
+                        row_sum<1, BLOCK>(s, p.team, slots[turn][1]);
                         k1 = -rstd * (s[0] * p.inv_c);
                     } else {
                         float s[2] = {A::sum(s0), A::sum(s1)};
-                        team_sum<2, BLOCK>(s, p.team, slots[turn][1]);
+                        row_sum<2, BLOCK>(s, p.team, slots[turn][1]);
                         if (p.post == NA_NORM_LAYER) k0 = -rstd * (s[0] * p.inv_c);
                         k1 = -rstd * (s[1] * p.inv_c);
                     }
@@ -664,11 +702,11 @@ __global__ void __launch_bounds__(kSumThreads) add_sum_kernel(const SumParams p)
 // How a problem is laid out: chunk width, chunks per thread, threads per row, blocks, parts of a group, rows of a tile.
 struct AddPlan {
     bool vec, block, ring;
-    int j, team, blocks, per_group, tile, stages;
+    int j, team, blocks, per_group, tile;
     size_t ring_bytes;
 };
 
-AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd) {
+AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd, bool lean = false) {
     AddPlan n{};
     const int V = C % (16 / es) == 0 ? 16 / es : 1;
     n.vec = V > 1;
@@ -685,7 +723,7 @@ AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd
         if (!n.vec) n.j = 4;
         teams = 32 / n.team;
         units = kAddThreads / 32;
-        per_sm = bwd ? 2 : (n.vec ? add_fwd_blocks(n.j * V) : 4);
+        per_sm = bwd ? 2 : (n.vec ? add_fwd_blocks(n.j * V, lean) : 4);
     } else {
         n.j = V == 8 ? 1 : (V == 4 ? 2 : 4);
         while (n.j * kAddBlock < chunks) n.j *= n.vec ? 2 : 4;
@@ -696,17 +734,16 @@ AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd
     const int arrays = bwd ? 4 : 2, row = C * es;
     const size_t sums = bwd && !n.block ? static_cast<size_t>(kAddThreads / 32) * C * 4 : 0;
     if (n.vec) {
-        // As many rows of a unit as `per_sm` blocks have room for, of at most kAddTileBytes an array, in three stages or two.  A pass of
-        // a warp's teams is at most 1 KB an array (2 KB forward): two stages of it, the sums and what else a block holds always fit.
-        const size_t room = ((224 * 1024) / per_sm - sums - 4 * 1024) / units, pass = static_cast<size_t>(teams) * row * arrays;
-        n.stages = room >= kAddStages * pass ? kAddStages : 2;
-        if (room >= n.stages * pass) {
+        // As many rows of a unit as `per_sm` blocks have room for, of at most kAddTileBytes an array.  A pass of a warp's teams is at most
+        // 1 KB an array (2 KB forward): two stages of it, the sums and what else a block holds always fit.
+        const size_t room = ((224 * 1024) / per_sm - sums - 4 * 1024) / units, pass = static_cast<size_t>(kAddStages) * teams * row * arrays;
+        if (room >= pass) {
             n.ring = true;
-            int passes = std::max(1, std::min({static_cast<int>(room / (n.stages * pass)), kAddTileBytes / (teams * row), kAddTileRows / teams}));
+            int passes = std::max(1, std::min({static_cast<int>(room / pass), kAddTileBytes / (teams * row), kAddTileRows / teams}));
             // fewer rows a tile where the grid is small
-            while (passes > 1 && groups * group_rows < static_cast<long long>(teams) * passes * units * kSms * per_sm * n.stages) --passes;
+            while (passes > 1 && groups * group_rows < static_cast<long long>(teams) * passes * units * kSms * per_sm * kAddStages) --passes;
             n.tile = teams * passes;
-            n.ring_bytes = static_cast<size_t>(n.stages) * arrays * n.tile * row * units;
+            n.ring_bytes = passes * pass * units;
         }
     }
     const long long tiles = (group_rows + n.tile - 1) / n.tile, most = static_cast<long long>(kSms) * per_sm;
@@ -716,6 +753,8 @@ AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd
     n.blocks = static_cast<int>(std::min(groups * n.per_group, most));
     return n;
 }
+
+bool lean_forward(const AddParams& p) { return p.norm != NA_NORM_LAYER && p.post != NA_NORM_LAYER && !p.b && !p.post_b; }
 
 template <typename Kernel>
 na_status start_add(Kernel* kernel, const AddParams& p, const AddPlan& n, size_t smem, cudaStream_t s) {
@@ -733,7 +772,9 @@ na_status run_add(const AddParams& p, const AddPlan& n, cudaStream_t s) {
             if (lean) return start_add(add_bwd_kernel<T, V, J, BLOCK, RING, true>, p, n, smem, s);
         return start_add(add_bwd_kernel<T, V, J, BLOCK, RING, false>, p, n, smem, s);
     } else {
-        return start_add(add_fwd_kernel<T, V, J, BLOCK, RING>, p, n, n.ring_bytes, s);
+        if constexpr (V > 1)
+            if (lean_forward(p)) return start_add(add_fwd_kernel<T, V, J, BLOCK, RING, true>, p, n, n.ring_bytes, s);
+        return start_add(add_fwd_kernel<T, V, J, BLOCK, RING, false>, p, n, n.ring_bytes, s);
     }
 }
 
@@ -849,11 +890,10 @@ na_status na_addnorm(const void* x, const void* y, void* s, void* h, const float
     p.rows = rows;
     p.group_rows = rows / groups;
     p.groups = static_cast<int>(groups);
-    const AddPlan n = plan_add(p.group_rows, groups, C, elem_bytes(dtype), false);
+    const AddPlan n = plan_add(p.group_rows, groups, C, elem_bytes(dtype), false, lean_forward(p));
     p.team = n.team;
     p.per_group = n.per_group;
     p.tile = n.tile;
-    p.stages = n.stages;
     p.wait_ns = wait_limit_ns();
     p.withhold = wait_withhold();
     if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
@@ -935,7 +975,6 @@ na_status na_addnorm_bwd(const void* dh, const void* ds, const void* s, const vo
     p.team = n.team;
     p.per_group = n.per_group;
     p.tile = n.tile;
-    p.stages = n.stages;
     p.wait_ns = wait_limit_ns();
     p.withhold = wait_withhold();
     if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
