@@ -798,43 +798,53 @@ def na_diff_softmax_bwd(x1, x2, lam, dy, dx1, dx2, dlam, kernel, p: float = 0.0,
 # After the attention: the residual add between norms, the gated feed-forward product
 # ---------------------------------------------------------------------------------------------
 
-_NORMS = {"none": 0, "layer": 1, "rms": 2}
+_NORMS = {(a, b): (i, j) for i, a in enumerate(("none", "layer", "rms")) for j, b in enumerate(("none", "layer", "rms"))}
 
 
 def _norms(norm, post):
-    if norm not in _NORMS or post not in _NORMS:
+    kinds = _NORMS.get((norm, post))
+    if kinds is None:
         raise ValueError("norm and post must be 'none', 'layer' or 'rms'")
-    return _NORMS[norm], _NORMS[post]
+    return kinds
 
 
-def _groups(shape, C, **named):
+def _alike(shape, dtype, names, tensors):
+    """Contiguous tensors of one shape and type, or None.  (The checks of the calls below stand in few loops: a call of a
+    Python function costs as much as three of them.)"""
+    for i, t in enumerate(tensors):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            _check(t, shape, dtype, names[i])
+
+
+def _groups(shape, C, names, tensors):
     """Number of vectors of fp32 tensors [C], or [.., C] with leading axes of the rows (a vector for each); all alike."""
-    lead = None
-    for name, t in named.items():
+    first = None
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        own = t.shape[:-1]
-        _like(t, shape[:len(own)] + (C,), torch.float32, name)
-        if len(own) >= len(shape):
-            raise ValueError(f"{name} has more axes than the rows")
-        if lead is None:
-            lead = own
-        elif lead != own:
-            raise ValueError(f"{name} must have the shape of {next(iter(named))}")
-    return 1 if not lead else math.prod(lead)
+        own = t.shape
+        if first is None:
+            n = len(own)
+            if n > len(shape) or n == 0:
+                raise ValueError(f"{names[i]} must be [C], or have leading axes of the rows")
+            first = (C,) if n == 1 else shape[:n - 1] + (C,)
+        if t.dtype is not torch.float32 or own != first or not t.is_contiguous():
+            _check(t, tuple(first), torch.float32, names[i])
+    return 1 if first is None or n == 1 else math.prod(first[:-1])
 
 
-def _moments(shape, kind, name, mean, rstd, needed):
-    """The statistics of a norm: both for layer norm, rstd alone for root mean square."""
-    if kind == 0 and (mean is not None or rstd is not None):
-        raise ValueError(f"no {name}norm, no statistics of it")
-    if kind == 2 and mean is not None:
-        raise ValueError(f"a root mean square norm has no {name}mean")
-    if (kind and needed and rstd is None) or (kind == 1 and (mean is None) != (rstd is None)):
-        raise ValueError(f"{name}mean and {name}rstd go together" if kind == 1 else f"{name}rstd is needed")
-    for what, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _like(t, shape[:-1], torch.float32, name + what)
+def _moments(shape, kinds, tensors, needed):
+    """The statistics (mean, rstd, post_mean, post_rstd): both of a layer norm, rstd alone of a root mean square norm."""
+    mean, rstd, post_mean, post_rstd = tensors
+    for kind, m, r in ((kinds[0], mean, rstd), (kinds[1], post_mean, post_rstd)):
+        if kind == 1:
+            if (m is None) != (r is None) or (needed and r is None):
+                raise ValueError("the mean and rstd of a layer norm go together")
+        elif m is not None:
+            raise ValueError("only a layer norm has a mean")
+        elif (r is None and needed) if kind else r is not None:
+            raise ValueError("rstd of a root mean square norm is needed" if kind else "no norm, no statistics of it")
+    _alike(shape[:-1], torch.float32, ("mean", "rstd", "post_mean", "post_rstd"), tensors)
 
 
 def na_addnorm(x, y, s, h, w=None, b=None, gate=None, post_w=None, post_b=None, norm: str = "layer", post: str = "none",
@@ -847,25 +857,29 @@ def na_addnorm(x, y, s, h, w=None, b=None, gate=None, post_w=None, post_b=None, 
     (nothing but h is wanted); s and h may each be x or y.  mean, rstd, post_mean, post_rstd: fp32 x.shape[:-1] for
     the backward, or None; root mean square norms have no mean."""
     shape, rows, C = _rows(x)
-    for name, t in (("x", x), ("y", y), ("s", s), ("h", h)):
-        if t is not None:
-            _like(t, shape, x.dtype, name)
-    kind, post_kind = _norms(norm, post)
-    if (h is None) != (kind == 0):
+    _alike(shape, x.dtype, ("x", "y", "s", "h"), (x, y, s, h))
+    kinds = _norms(norm, post)
+    if (h is None) != (norm == "none"):
         raise ValueError("h goes with a norm")
     if s is None and h is None:
         raise ValueError("s is needed without a norm")
-    if (kind == 0 and not (w is None and b is None)) or (post_kind == 0 and not (post_w is None and post_b is None)):
+    if (h is None and (w is not None or b is not None)) or (post == "none" and (post_w is not None or post_b is not None)):
         raise ValueError("weights of a norm that is none")
-    _vectors(C, post_w=post_w, post_b=post_b)
-    w_groups, gate_groups = _groups(shape, C, w=w, b=b), _groups(shape, C, gate=gate)
-    _moments(shape, kind, "", mean, rstd, False)
-    _moments(shape, post_kind, "post_", post_mean, post_rstd, False)
-    raw = _launch_stream(stream, x, y, s, h, w, b, gate, post_w, post_b, mean, rstd, post_mean, post_rstd)
-    st = load().na_addnorm(x.data_ptr(), y.data_ptr(), _ptr(s), _ptr(h), _ptr(w), _ptr(b), _ptr(gate), _ptr(post_w), _ptr(post_b),
-                           _ptr(mean), _ptr(rstd), _ptr(post_mean), _ptr(post_rstd), rows, C, w_groups, gate_groups, kind,
-                           post_kind, scale, residual, eps, _code(x), raw)
-    _ok(st, "na_addnorm")
+    w_groups = gate_groups = 1
+    if w is not None or b is not None:
+        w_groups = _groups(shape, C, ("w", "b"), (w, b))
+    if gate is not None:
+        gate_groups = _groups(shape, C, ("gate",), (gate,))
+    if post_w is not None or post_b is not None:
+        _alike((C,), torch.float32, ("post_w", "post_b"), (post_w, post_b))
+    statistics = (mean, rstd, post_mean, post_rstd)
+    _moments(shape, kinds, statistics, False)
+    tensors = (x, y, s, h, w, b, gate, post_w, post_b) + statistics
+    raw = _launch_stream(stream, *tensors)
+    st = load().na_addnorm(*[None if t is None else t.data_ptr() for t in tensors], rows, C, w_groups, gate_groups, *kinds, scale, residual,
+                           eps, _code(x), raw)
+    if st:
+        _ok(st, "na_addnorm")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -884,34 +898,38 @@ def na_addnorm_bwd(dh, ds, s, y, dx, dy, w=None, gate=None, post_w=None, post_b=
     reaches s from elsewhere (or None), s, y and the forward's statistics.  Without a norm dh and s are None.  dx may be
     dh, ds or s, dy may be dh, ds, s or y, but not dx."""
     shape, rows, C = _rows(y)
-    dtype = y.dtype
-    for name, t in (("dh", dh), ("ds", ds), ("s", s), ("y", y), ("dx", dx), ("dy", dy)):
-        if t is not None:
-            _like(t, shape, dtype, name)
-    kind, post_kind = _norms(norm, post)
-    if (dh is None) != (kind == 0) or (s is None) != (kind == 0):
+    rowwise = (dh, ds, s, y, dx, dy)
+    _alike(shape, y.dtype, ("dh", "ds", "s", "y", "dx", "dy"), rowwise)
+    kinds = _norms(norm, post)
+    normed = norm != "none"
+    if (dh is not None) != normed or (s is not None) != normed:
         raise ValueError("dh and s go with a norm")
-    if ds is None and kind == 0:
-        raise ValueError("ds is needed without a norm")
-    if (kind == 0 and not (w is None and dw is None and db is None)) or (
-            post_kind == 0 and not (post_w is None and post_b is None and dpost_w is None and dpost_b is None)):
+    if dx is None or dy is None or (ds is None and not normed):
+        raise ValueError("dx and dy are written, and ds is needed without a norm")
+    if not normed and not (w is dw is db is None):
+        raise ValueError("weights of a norm that is none")
+    if post == "none" and not (post_w is post_b is dpost_w is dpost_b is None):
         raise ValueError("weights of a norm that is none")
     if gate is None and dgate is not None:
         raise ValueError("dgate goes with gate")
-    _vectors(C, post_w=post_w, post_b=post_b, dpost_w=dpost_w, dpost_b=dpost_b)
-    w_groups, gate_groups = _groups(shape, C, w=w, dw=dw, db=db), _groups(shape, C, gate=gate, dgate=dgate)
-    _moments(shape, kind, "", mean, rstd, True)
-    _moments(shape, post_kind, "post_", post_mean, post_rstd, True)
-    raw = _launch_stream(stream, dh, ds, s, y, dx, dy, w, gate, post_w, post_b, mean, rstd, post_mean, post_rstd, dw, db, dgate,
-                         dpost_w, dpost_b, workspace)
+    w_groups = gate_groups = 1
+    if not (w is dw is db is None):
+        w_groups = _groups(shape, C, ("w", "dw", "db"), (w, dw, db))
+    if gate is not None:
+        gate_groups = _groups(shape, C, ("gate", "dgate"), (gate, dgate))
+    if post != "none":
+        _alike((C,), torch.float32, ("post_w", "post_b", "dpost_w", "dpost_b"), (post_w, post_b, dpost_w, dpost_b))
+    statistics = (mean, rstd, post_mean, post_rstd)
+    _moments(shape, kinds, statistics, True)
+    tensors = (dh, ds, s, y, w, gate, post_w, post_b) + statistics + (dx, dy, dw, db, dgate, dpost_w, dpost_b)
+    raw = _launch_stream(stream, *tensors, workspace)
     code = _code(y)
     ws, ws_ptr, ws_bytes = (None, None, 0) if dw is db is dgate is dpost_w is dpost_b is None else _workspace(
         workspace, stream, lambda: _add_need(rows, C, w_groups, gate_groups, code), y.device)
-    st = load().na_addnorm_bwd(_ptr(dh), _ptr(ds), _ptr(s), y.data_ptr(), _ptr(w), _ptr(gate), _ptr(post_w), _ptr(post_b), _ptr(mean),
-                               _ptr(rstd), _ptr(post_mean), _ptr(post_rstd), dx.data_ptr(), dy.data_ptr(), _ptr(dw), _ptr(db),
-                               _ptr(dgate), _ptr(dpost_w), _ptr(dpost_b), rows, C, w_groups, gate_groups, kind, post_kind, scale,
+    st = load().na_addnorm_bwd(*[None if t is None else t.data_ptr() for t in tensors], rows, C, w_groups, gate_groups, *kinds, scale,
                                residual, code, ws_ptr, ws_bytes, raw)
-    _ok(st, "na_addnorm_bwd")
+    if st:
+        _ok(st, "na_addnorm_bwd")
 
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
@@ -920,19 +938,15 @@ _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 def _glu(x, wg, wu, h, name, bg, bu, act):
     """Checks of what both directions take; rows, D, F and the activation's code."""
     shape, rows, D = _rows(x)
-    if wg.dim() != 2:
-        raise ValueError("wg must be [F, D]")
-    F = wg.shape[0]
+    F = wg.shape[0] if wg.dim() == 2 else 0
     if F < 1 or F > _INT_MAX:
-        raise ValueError("wg must have rows, at most 2^31 - 1")
+        raise ValueError("wg must be [F, D], F at least 1 and at most 2^31 - 1")
     dtype = x.dtype
-    _like(x, shape, dtype, "x")
-    _like(wg, (F, D), dtype, "wg")
-    _like(wu, (F, D), dtype, "wu")
-    _like(h, shape[:-1] + (F,), dtype, name)
-    for what, t in (("bg", bg), ("bu", bu)):
-        if t is not None:
-            _like(t, (F,), dtype, what)
+    _alike(shape, dtype, ("x",), (x,))
+    _alike((F, D), dtype, ("wg", "wu"), (wg, wu))
+    _alike(shape[:-1] + (F,), dtype, (name,), (h,))
+    if bg is not None or bu is not None:
+        _alike((F,), dtype, ("bg", "bu"), (bg, bu))
     code = _ACTS.get(act)
     if code is None:
         raise ValueError("act must be 'silu', 'gelu', 'gelu_tanh', 'relu' or 'sigmoid'")
@@ -943,9 +957,11 @@ def na_glu(x, wg, wu, h, bg=None, bu=None, act: str = "silu", stream=None):
     """h = act(x wg^T + bg) * (x wu^T + bu) for x [.., D], wg and wu [F, D], bg and bu [F] or None, h [.., F], all of one type.
     act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid"."""
     rows, D, F, code = _glu(x, wg, wu, h, "h", bg, bu, act)
-    raw = _launch_stream(stream, x, wg, wu, h, bg, bu)
-    st = load().na_glu(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), _ptr(bg), _ptr(bu), h.data_ptr(), rows, D, F, code, _code(x), raw)
-    _ok(st, "na_glu")
+    tensors = (x, wg, wu, bg, bu, h)
+    raw = _launch_stream(stream, *tensors)
+    st = load().na_glu(*[None if t is None else t.data_ptr() for t in tensors], rows, D, F, code, _code(x), raw)
+    if st:
+        _ok(st, "na_glu")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -968,12 +984,17 @@ def na_glu_bwd(dh, x, wg, wu, dx=None, dwg=None, dwu=None, bg=None, bu=None, dbg
         raise ValueError("dbg goes with bg, dbu with bu")
     if dx is dwg is dbg is dbu is None:
         raise ValueError("no gradient is wanted")
-    for name, t, like in (("dx", dx, x), ("dwg", dwg, wg), ("dwu", dwu, wu), ("dbg", dbg, bg), ("dbu", dbu, bu)):
-        if t is not None:
-            _like(t, like.shape, x.dtype, name)
-    raw = _launch_stream(stream, dh, x, wg, wu, bg, bu, dx, dwg, dwu, dbg, dbu, workspace)
-    dtype = _code(x)
-    ws, ws_ptr, ws_bytes = _workspace(workspace, stream, lambda: _glu_need(rows, D, F, dtype), x.device)
-    st = load().na_glu_bwd(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), _ptr(bg), _ptr(bu), _ptr(dx), _ptr(dwg), _ptr(dwu),
-                           _ptr(dbg), _ptr(dbu), rows, D, F, code, dtype, ws_ptr, ws_bytes, raw)
-    _ok(st, "na_glu_bwd")
+    dtype = x.dtype
+    if dx is not None:
+        _alike(x.shape, dtype, ("dx",), (dx,))
+    if dwg is not None:
+        _alike(wg.shape, dtype, ("dwg", "dwu"), (dwg, dwu))
+    if dbg is not None or dbu is not None:
+        _alike((F,), dtype, ("dbg", "dbu"), (dbg, dbu))
+    tensors = (dh, x, wg, wu, bg, bu, dx, dwg, dwu, dbg, dbu)
+    raw = _launch_stream(stream, *tensors, workspace)
+    kind = _code(x)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, stream, lambda: _glu_need(rows, D, F, kind), x.device)
+    st = load().na_glu_bwd(*[None if t is None else t.data_ptr() for t in tensors], rows, D, F, code, kind, ws_ptr, ws_bytes, raw)
+    if st:
+        _ok(st, "na_glu_bwd")

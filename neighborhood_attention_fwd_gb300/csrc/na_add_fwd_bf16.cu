@@ -1,0 +1,8 @@
+// Residual add between norms, forward, bf16 (see na_add_impl.cuh).
+#include "na_add_impl.cuh"
+
+namespace na {
+namespace add {
+template na_status launch_add<__nv_bfloat16, false>(const AddParams&, const AddPlan&, cudaStream_t);
+}  // namespace add
+}  // namespace na

@@ -118,6 +118,65 @@ __device__ __forceinline__ void activate(float v, float& a, float& slope) {
     }
 }
 
+// act and its derivative of eight values, with the approximations.  The sigmoid that three of the activations are made of takes one
+// reciprocal for two values, 1 / p = q / (p q): reciprocals run at half the rate of exponentials and would be half of the time.
+// p q stays below 2^126 while both exponents are at most 62 (values above -43); chunks with others take one each.
+template <int ACT>
+__device__ __forceinline__ void activate8(const float (&v)[8], float (&a)[8], float (&slope)[8]) {
+    if constexpr (ACT == NA_ACT_RELU || ACT == NA_ACT_GELU) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) activate<ACT, true>(v[k], a[k], slope[k]);
+        return;
+    }
+    // exponents: the sigmoid's argument is -t / log2 e
+    constexpr float L = 1.4426950408889634f, K = 2.f * 0.79788456080286536f;
+    float t[8], top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        using namespace dev;
+        if constexpr (ACT == NA_ACT_GELU_TANH) {
+            const uint64_t x = pack2(v[k], v[k + 1]);
+            float q0, q1;
+            split2(mul2(x, x), q0, q1);
+            const uint64_t q = pack2(fminf(q0, 10000.f), fminf(q1, 10000.f));   // beyond |v| = 100 it is 0 or 1
+            split2(mul2(x, fma2(q, pack2(-L * K * 0.044715f, -L * K * 0.044715f), pack2(-L * K, -L * K))), t[k], t[k + 1]);
+        } else {
+            split2(mul2(pack2(v[k], v[k + 1]), pack2(-L, -L)), t[k], t[k + 1]);
+        }
+        top = fmaxf(top, fmaxf(t[k], t[k + 1]));
+    }
+    if (__any_sync(0xffffffffu, !(top <= 62.f))) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) activate<ACT, true>(v[k], a[k], slope[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        using namespace dev;
+        const float e0 = fast_exp2(t[k]), e1 = fast_exp2(t[k + 1]);
+        const uint64_t e = pack2(e0, e1), one = pack2(1.f, 1.f), p = add2(e, one);
+        float p0, p1;
+        split2(p, p0, p1);
+        const float r = inverse<true>(p0 * p1);
+        const uint64_t y = mul2(pack2(r, r), pack2(p1, p0)), x = pack2(v[k], v[k + 1]);
+        if constexpr (ACT == NA_ACT_SIGMOID) {
+            // y (1 - y) without cancellation: 1 - y = e y
+            split2(y, a[k], a[k + 1]);
+            split2(mul2(mul2(y, y), e), slope[k], slope[k + 1]);
+        } else {
+            const uint64_t s = mul2(x, y), rest = mul2(e, y);   // 1 - y = e y
+            split2(s, a[k], a[k + 1]);
+            if constexpr (ACT == NA_ACT_GELU_TANH) {
+                const uint64_t q = mul2(x, x);   // |v| < 43 here, or the rest is zero
+                const uint64_t rise = fma2(q, pack2(3.f * K * 0.044715f, 3.f * K * 0.044715f), pack2(K, K));
+                split2(fma2(mul2(s, rest), rise, y), slope[k], slope[k + 1]);
+            } else {
+                split2(fma2(s, rest, y), slope[k], slope[k + 1]);
+            }
+        }
+    }
+}
+
 // Calls f<ACT>() for a run-time activation.
 template <typename Call>
 __device__ __forceinline__ void with_act(int act, Call&& call) {

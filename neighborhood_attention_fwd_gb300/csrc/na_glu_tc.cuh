@@ -470,46 +470,46 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                     release(buf);
                     continue;
                 }
-                uint32_t du[16];
+                // eight columns at a time, the next ones on their way
+                uint32_t du[16], rg[2][8], ru[2][8];
+                tmem_ld8(taddr, rg[0]);
+                tmem_ld8(taddr + nf, ru[0]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t rg[16], ru[16];
-                    tmem_ld16(taddr + c * 16, rg);
-                    tmem_ld16(taddr + nf + c * 16, ru);
-                    tmem_ld_wait_all();
-                    reg_fence16(rg);
-                    reg_fence16(ru);
-                    if (c == 1) release(buf);
-                    float g[16], u[16];
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait2(rg[c & 1], ru[c & 1]);
+                    if (c < 3) {
+                        tmem_ld8(taddr + (c + 1) * 8, rg[(c + 1) & 1]);
+                        tmem_ld8(taddr + nf + (c + 1) * 8, ru[(c + 1) & 1]);
+                    } else {
+                        release(buf);
+                    }
+                    float g[8], u[8], a[8], slope[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        g[k] = __uint_as_float(rg[k]);
-                        u[k] = __uint_as_float(ru[k]);
+                    for (int k = 0; k < 8; ++k) {
+                        g[k] = __uint_as_float(rg[c & 1][k]);
+                        u[k] = __uint_as_float(ru[c & 1][k]);
                     }
                     if (biased) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            g[k] += bias[c * 16 + k];
-                            u[k] += bias[32 + c * 16 + k];
+                        for (int k = 0; k < 8; ++k) {
+                            g[k] += bias[c * 8 + k];
+                            u[k] += bias[32 + c * 8 + k];
                         }
                     }
-                    uint32_t v[8];
+                    activate8<ACT>(g, a, slope);
+                    uint32_t v[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float a0, a1, s0, s1;
-                        activate<ACT, true>(g[2 * k], a0, s0);
-                        activate<ACT, true>(g[2 * k + 1], a1, s1);
+                    for (int k = 0; k < 4; ++k) {
                         if constexpr (WHICH == kForward) {
-                            v[k] = Elem<T>::pair(a0 * u[2 * k], a1 * u[2 * k + 1]);
+                            v[k] = Elem<T>::pair(a[2 * k] * u[2 * k], a[2 * k + 1] * u[2 * k + 1]);
                         } else {
                             float d0, d1;
-                            Elem<T>::two(dh[8 * c + k], d0, d1);
-                            v[k] = Elem<T>::pair(d0 * u[2 * k] * s0, d1 * u[2 * k + 1] * s1);
-                            du[8 * c + k] = Elem<T>::pair(d0 * a0, d1 * a1);
+                            Elem<T>::two(dh[4 * c + k], d0, d1);
+                            v[k] = Elem<T>::pair(d0 * u[2 * k] * slope[2 * k], d1 * u[2 * k + 1] * slope[2 * k + 1]);
+                            du[4 * c + k] = Elem<T>::pair(d0 * a[2 * k], d1 * a[2 * k + 1]);
                         }
                     }
-                    st_shared_v4(row + ((2 * c) ^ sw) * 16, v[0], v[1], v[2], v[3]);
-                    st_shared_v4(row + ((2 * c + 1) ^ sw) * 16, v[4], v[5], v[6], v[7]);
+                    st_shared_v4(row + (c ^ sw) * 16, v[0], v[1], v[2], v[3]);
                 }
                 if constexpr (WHICH == kForward) {
                     if (p.wide) by_tma(&p.out[0], m0, f0);
