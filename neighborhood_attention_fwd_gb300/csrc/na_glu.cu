@@ -8,9 +8,6 @@
 // Nothing is kept from the forward: the backward makes g and u again (4 T D F of its 12 T D F operations), so training holds
 // no array of T F elements between the passes.  dg and du go through the workspace in the tensors' type: the rounding is
 // the one that h itself has, and a sum over them averages it out.
-//
-// What bounds it: products.  fp32 runs on FMA units, in pairs (fma.rn.f32x2), no TF32: tiles of 128 x 128, 8 x 8 per
-// thread, operands widened and laid out [k][row] in shared memory, two stages of 16 steps of k.
 #include <algorithm>
 
 #include "na_block.cuh"
@@ -23,210 +20,6 @@ using namespace glu;
 
 namespace {
 
-constexpr int kTile = 128, kDepth = 16, kGluThreads = 256;
-constexpr int kPitch = kTile + 4;   // of an operand's row in shared memory
-
-// One operand of a product: rows (of the result's rows or columns) by k.  Element (r, k) is at base[r * ld + k], or with
-// ALONG_ROWS at base[k * ld + r].
-template <typename T>
-struct Operand {
-    const T* base;
-    long long ld;
-    long long rows, depth;   // zeros past them
-    bool wide;               // rows of memory start at 16 bytes
-};
-
-// A thread's eight elements of a 128 x 16 piece: from row r, steps k .. k + 7, or with ALONG_ROWS from step k, rows r .. r + 7.
-template <typename T, bool ALONG_ROWS>
-__device__ __forceinline__ void fetch(const Operand<T>& o, long long r, long long k, float (&f)[8]) {
-    constexpr int EPC = Elem<T>::EPC;
-    const bool in = r < o.rows && k < o.depth;
-    const long long left = ALONG_ROWS ? o.rows - r : o.depth - k;   // elements there along memory
-    const T* at = o.base + (ALONG_ROWS ? k * o.ld + r : r * o.ld + k);
-    if (in && o.wide && left >= 8) {
-#pragma unroll
-        for (int c = 0; c < 8 / EPC; ++c) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(at) + c);
-            float g[EPC];
-            Elem<T>::unpack(raw, g);
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) f[c * EPC + e] = g[e];
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = in && e < left ? Elem<T>::get(at[e]) : 0.f;
-}
-
-template <bool ALONG_ROWS>
-__device__ __forceinline__ void place(float (*sm)[kPitch], int t, const float (&f)[8]) {
-    if (ALONG_ROWS) {
-        float* to = &sm[t >> 4][(t & 15) * 8];
-        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sm[(t >> 7) * 8 + e][t & 127] = f[e];
-    }
-}
-
-// Products on CUDA cores.  A block makes 128 x 128 elements (kForward, kSlopes: 128 rows x 64 columns of g and the same of u);
-// rows along blockIdx.x, columns along blockIdx.y, kWeights: dWg, dWu and the runs of tokens along blockIdx.z.
-template <typename T, int WHICH>
-__global__ void __launch_bounds__(kGluThreads, 2) glu_fma_kernel(const GluParams p) {
-    constexpr bool PAIR = WHICH == kForward || WHICH == kSlopes;
-    constexpr bool A_ROWS = WHICH == kWeights, B_ROWS = !PAIR;
-    __shared__ __align__(16) float sa[2][kDepth][kPitch], sb[2][kDepth][kPitch];
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    const long long m0 = static_cast<long long>(blockIdx.x) * kTile, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? kTile / 2 : kTile);
-    const int half = WHICH == kWeights ? blockIdx.z & 1 : 0, split = WHICH == kWeights ? blockIdx.z >> 1 : 0;
-    const T *x = static_cast<const T*>(p.x), *wg = static_cast<const T*>(p.wg), *wu = static_cast<const T*>(p.wu);
-    const T *dg = static_cast<const T*>(p.dg), *du = static_cast<const T*>(p.du);
-    const bool wide = p.D % Elem<T>::EPC == 0;
-    // pieces of 16 steps of k; kTokens has two runs of them, dg Wg and du Wu
-    const long long k0 = split * p.run;
-    const long long depth = PAIR ? p.D : (WHICH == kTokens ? p.F : min(p.run, p.T - k0));
-    const long long pieces = (depth + kDepth - 1) / kDepth, total = WHICH == kTokens ? 2 * pieces : pieces;
-    // where this thread fetches within a piece
-    const int ra = A_ROWS ? (t & 15) * 8 : t & 127, ka = A_ROWS ? t >> 4 : (t >> 7) * 8;
-    const int rb = B_ROWS ? (t & 15) * 8 : t & 127, kb = B_ROWS ? t >> 4 : (t >> 7) * 8;
-    float fa[8], fb[8];
-    auto load = [&](long long i) {
-        const bool second = WHICH == kTokens && i >= pieces;
-        const long long k = (second ? i - pieces : i) * kDepth;
-        Operand<T> a, b;
-        if (PAIR) {
-            a = {x, p.D, p.T, p.D, wide};
-            b = {rb < kTile / 2 ? wg : wu, p.D, p.F, p.D, wide};
-            fetch<T, false>(a, m0 + ra, k + ka, fa);
-            fetch<T, false>(b, n0 + (rb & (kTile / 2 - 1)), k + kb, fb);
-        } else if (WHICH == kTokens) {
-            a = {second ? du : dg, p.pitch, p.T, p.F, true};
-            b = {second ? wu : wg, p.D, p.D, p.F, wide};
-            fetch<T, false>(a, m0 + ra, k + ka, fa);
-            fetch<T, true>(b, n0 + rb, k + kb, fb);
-        } else {
-            a = {half ? du : dg, p.pitch, p.F, k0 + depth, true};
-            b = {x, p.D, p.D, k0 + depth, wide};
-            fetch<T, true>(a, m0 + ra, k0 + k + ka, fa);
-            fetch<T, true>(b, n0 + rb, k0 + k + kb, fb);
-        }
-    };
-    uint64_t acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
-    load(0);
-    for (long long i = 0; i < total; ++i) {
-        const int st = static_cast<int>(i & 1);
-        place<A_ROWS>(sa[st], t, fa);
-        place<B_ROWS>(sb[st], t, fb);
-        __syncthreads();   // also: the stage filled next was last read before this barrier
-        if (i + 1 < total) load(i + 1);
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4*>(&sa[st][k][ty * 4]), a1 = *reinterpret_cast<const float4*>(&sa[st][k][64 + ty * 4]);
-            const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][tx * 4]), b1 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][64 + tx * 4]);
-            const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const uint64_t b[4] = {b0.x, b0.y, b1.x, b1.y};
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const uint64_t aa = pack2(a[r], a[r]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[r][c] = fma2(aa, b[c], acc[r][c]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const long long row = m0 + (r < 4 ? ty * 4 + r : 64 + ty * 4 + r - 4);
-        float v[8];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) split2(acc[r][c], v[2 * c], v[2 * c + 1]);
-        if constexpr (PAIR) {
-            if (row >= p.T) continue;
-            with_act(p.act, [&](auto tag) {
-                constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const long long f = n0 + tx * 4 + c;
-                    if (f >= p.F) break;
-                    const float g = v[c] + (p.bg ? Elem<T>::get(static_cast<const T*>(p.bg)[f]) : 0.f);
-                    const float u = v[4 + c] + (p.bu ? Elem<T>::get(static_cast<const T*>(p.bu)[f]) : 0.f);
-                    float a, slope;
-                    activate<ACT, false>(g, a, slope);
-                    if constexpr (WHICH == kForward) {
-                        static_cast<T*>(p.h)[row * p.F + f] = Elem<T>::put(a * u);
-                    } else {
-                        const float dh = Elem<T>::get(static_cast<const T*>(p.dh)[row * p.F + f]);
-                        static_cast<T*>(p.dg)[row * p.pitch + f] = Elem<T>::put(dh * u * slope);
-                        static_cast<T*>(p.du)[row * p.pitch + f] = Elem<T>::put(dh * a);
-                    }
-                }
-            });
-        } else {
-            if (row >= (WHICH == kTokens ? p.T : p.F)) continue;
-            const long long size = static_cast<long long>(p.F) * p.D;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const long long col = n0 + (c < 4 ? tx * 4 + c : 64 + tx * 4 + c - 4);
-                if (col >= p.D) continue;
-                const long long at = row * p.D + col;
-                if (WHICH == kTokens) static_cast<T*>(p.dx)[at] = Elem<T>::put(v[c]);
-                else if (p.splits > 1) p.partial[(2LL * split + half) * size + at] = v[c];
-                else static_cast<T*>(half ? p.dwu : p.dwg)[at] = Elem<T>::put(v[c]);
-            }
-        }
-    }
-}
-
-// out[i] = sums over the runs of partial[run][n], in order: the first `cut` elements to out0, the others to out1; either may
-// be null.  V elements at a time (n and cut are multiples of V).
-template <typename T, int V>
-__global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int runs, long long n, long long cut, T* out0, T* out1) {
-    for (long long i = (blockIdx.x * 256LL + threadIdx.x) * V; i < n; i += gridDim.x * 256LL * V) {
-        T* out = i < cut ? (out0 ? out0 + i : nullptr) : (out1 ? out1 + (i - cut) : nullptr);
-        if (!out) continue;
-        float s[V] = {};
-#pragma unroll 4
-        for (int r = 0; r < runs; ++r) {
-            if constexpr (V == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(partial + r * n + i);
-                s[0] += t.x, s[1] += t.y, s[2] += t.z, s[3] += t.w;
-            } else {
-                s[0] += partial[r * n + i];
-            }
-        }
-        if constexpr (V == 4 && sizeof(T) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pair(s[0], s[1]), Elem<T>::pair(s[2], s[3]));
-        else
-#pragma unroll
-            for (int e = 0; e < V; ++e) out[e] = Elem<T>::put(s[e]);
-    }
-}
-
-// Column sums of dg and du over runs of tokens: partial[run][2][F].  A warp takes 32 columns, a block's warps every eighth row.
-template <typename T>
-__global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* du, long long T_, int F, long long pitch, long long run, float* partial) {
-    __shared__ float sums[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    const T* from = blockIdx.z ? du : dg;
-    const long long first = blockIdx.y * run, end = min(first + run, T_);
-    float s = 0.f;
-    if (c < F)
-#pragma unroll 8
-        for (long long r = first + warp; r < end; r += 8) s += Elem<T>::get(from[r * pitch + c]);
-    sums[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < F) {
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][lane];
-        partial[(blockIdx.y * 2LL + blockIdx.z) * F + c] = s;
-    }
-}
-
 constexpr int kGluMaxWidth = 1 << 20;              // of D and F
 constexpr long long kGluMaxRows = (1LL << 31) - 1;
 
@@ -238,7 +31,6 @@ struct TilePlan {
     unsigned last_nf, span, groups;   // forward, slopes
 };
 
-unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
 
 // Nanoseconds of a step of 64 along the summed axis of a tile, for pairs of blocks and for one, and of what a tile takes besides.
 constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000;
@@ -374,19 +166,6 @@ na_status glu_sizes(long long rows, int D, int F, na_dtype dtype) {
 
 bool known_act(na_glu_act a) { return a >= NA_ACT_SILU && a <= NA_ACT_SIGMOID; }
 
-template <typename T>
-na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
-    auto blocks = [](long long n, int tile) { return static_cast<unsigned>((n + tile - 1) / tile); };
-    const unsigned rows = blocks(p.T, kTile);
-    switch (which) {
-        case kForward: glu_fma_kernel<T, kForward><<<dim3(rows, blocks(p.F, kTile / 2)), kGluThreads, 0, s>>>(p); break;
-        case kSlopes: glu_fma_kernel<T, kSlopes><<<dim3(rows, blocks(p.F, kTile / 2)), kGluThreads, 0, s>>>(p); break;
-        case kTokens: glu_fma_kernel<T, kTokens><<<dim3(rows, blocks(p.D, kTile)), kGluThreads, 0, s>>>(p); break;
-        case kWeights: glu_fma_kernel<T, kWeights><<<dim3(blocks(p.F, kTile), blocks(p.D, kTile), 2 * p.splits), kGluThreads, 0, s>>>(p); break;
-    }
-    return launch_result();
-}
-
 // A product on tensor cores: its tensor maps, boxes of 64 elements by as many rows as one copy brings (na_glu_tc.cuh).
 na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na_dtype dtype, cudaStream_t s) {
     GluTcParams q{};
@@ -464,19 +243,10 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     }
 }
 
-na_status launch_fma(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
+na_status fma_product(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
     if (dtype == NA_BF16) return launch_fma<__nv_bfloat16>(p, which, s);
     if (dtype == NA_FP16) return launch_fma<__half>(p, which, s);
     return launch_fma<float>(p, which, s);
-}
-
-template <typename T>
-na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s) {
-    const bool wide = n % 4 == 0 && cut % 4 == 0;
-    const unsigned blocks = static_cast<unsigned>(std::min((n / (wide ? 4 : 1) + 255) / 256, 8LL * kSms));
-    if (wide) glu_sum_kernel<T, 4><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
-    else glu_sum_kernel<T, 1><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
-    return launch_result();
 }
 
 na_status sum_runs(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, na_dtype dtype, cudaStream_t s) {
@@ -485,18 +255,11 @@ na_status sum_runs(const float* partial, int runs, long long n, long long cut, v
     return launch_sum<float>(partial, runs, n, cut, out0, out1, s);
 }
 
-template <typename T>
-na_status launch_columns(const GluParams& p, const GluPlan& n, float* partial, cudaStream_t s) {
-    glu_column_kernel<T><<<dim3((p.F + 31) / 32, n.runs, 2), 256, 0, s>>>(static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T, p.F,
-                                                                         p.pitch, n.column_run, partial);
-    return launch_result();
-}
-
 na_status column_sums(const GluParams& p, const GluPlan& n, float* partial, void* dbg, void* dbu, na_dtype dtype, cudaStream_t s) {
     na_status st;
-    if (dtype == NA_BF16) st = launch_columns<__nv_bfloat16>(p, n, partial, s);
-    else if (dtype == NA_FP16) st = launch_columns<__half>(p, n, partial, s);
-    else st = launch_columns<float>(p, n, partial, s);
+    if (dtype == NA_BF16) st = launch_columns<__nv_bfloat16>(p, n.runs, n.column_run, partial, s);
+    else if (dtype == NA_FP16) st = launch_columns<__half>(p, n.runs, n.column_run, partial, s);
+    else st = launch_columns<float>(p, n.runs, n.column_run, partial, s);
     return st == NA_OK ? sum_runs(partial, n.runs, 2LL * p.F, p.F, dbg, dbu, dtype, s) : st;
 }
 
@@ -527,7 +290,7 @@ na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, 
     p.F = F;
     p.act = act;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return on_tensor_cores(D, dtype) ? launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s) : launch_fma(p, kForward, dtype, s);
+    return on_tensor_cores(D, dtype) ? launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s) : fma_product(p, kForward, dtype, s);
 }
 
 size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype) {
@@ -594,14 +357,14 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.splits = n.splits;
     p.run = n.run;
     const long long size = static_cast<long long>(F) * D;
-    st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, D, F), dtype, s) : launch_fma(p, kSlopes, dtype, s);
+    st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, D, F), dtype, s) : fma_product(p, kSlopes, dtype, s);
     if (st == NA_OK && dx) {
-        st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : launch_fma(p, kTokens, dtype, s);
+        st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, dtype, s);
         if (st == NA_OK && n.tensor && n.tokens.splits > 1)
             st = sum_runs(p.partial, n.tokens.splits, rows * D, rows * D, dx, nullptr, dtype, s);
     }
     if (st == NA_OK && dwg) {
-        st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : launch_fma(p, kWeights, dtype, s);
+        st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, dtype, s);
         const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.splits;
         if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, dwg, dwu, dtype, s);
     }

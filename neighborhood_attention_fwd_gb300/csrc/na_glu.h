@@ -193,6 +193,19 @@ __device__ __forceinline__ void with_act(int act, Call&& call) {
 template <int WHICH>
 constexpr int kPairRows = WHICH == kForward ? 6 : 5;
 
+inline unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
+
+constexpr int kTile = 128;   // of the CUDA-core kernels
+
+// Launchers of the CUDA-core kernels, of the sums over runs (out0 the first `cut` of n elements, out1 the others; either may be
+// null) and of the column sums of dg and du over runs of `run` tokens, to partial[run][2][F] (na_glu_fma.cuh).
+template <typename T>
+na_status launch_fma(const GluParams& p, Product which, cudaStream_t s);
+template <typename T>
+na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s);
+template <typename T>
+na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s);
+
 // Launchers of the tensor-core kernels (na_glu_tc.cuh).  pairs: tiles of 256 x 256 on pairs of blocks, else of 128 x 128;
 // tokens: 16, 64 or 128, the most that a product of few tokens holds.
 template <int WHICH, typename T>
