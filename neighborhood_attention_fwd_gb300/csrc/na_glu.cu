@@ -43,17 +43,19 @@ TilePlan plan_tiles(Product which, long long T, int D, int F) {
     const bool pair = which == kForward || which == kSlopes;
     TilePlan best{};
     if (pair && T <= 128) {
-        // As many blocks to a tile's sum as make the fewest steps one after another, with two blocks to a multiprocessor and
-        // about eight steps' time for a block to start and end.
+        // As many blocks to a tile's sum as make it shortest, two blocks to a multiprocessor: a step of 64 takes about 0.12 us, a
+        // block 8 steps' time to start and end, a cluster of 2 another 7, of 4 another 24 (1 token, 2736 x 1024: 5.7, 5.5 and 7.1 us;
+        // of 8 17.7).
         best.few = T <= 16 ? 16 : (T <= 64 ? 64 : 128);
         best.rows = up(F, 64);
         best.cols = 1;
         best.steps = up(D, 64);
+        const long long extra[3] = {0, 7, 24};
         long long least = 0;
-        for (unsigned s = 1; s <= 8 && s <= best.steps; s *= 2) {
+        for (unsigned i = 0, s = 1; i < 3 && s <= best.steps; ++i, s *= 2) {
             const unsigned run = up(best.steps, s);
             if (up(best.steps, run) != s) continue;   // every block has steps
-            const long long time = static_cast<long long>(up(static_cast<long long>(best.rows) * s, 2 * kSms)) * (run + 8);
+            const long long time = static_cast<long long>(up(static_cast<long long>(best.rows) * s, 2 * kSms)) * (run + 8) + extra[i];
             if (s == 1 || time < least) {
                 least = time;
                 best.run = run;

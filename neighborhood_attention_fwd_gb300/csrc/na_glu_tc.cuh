@@ -774,13 +774,25 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
     const int f0 = static_cast<int>(blockIdx.x / p.splits * 64);
     const unsigned first = rank * p.run, last = min(p.steps, first + p.run);
     const WaitGuard guard{p.err, p.wait_ns};
-    if (threadIdx.x == 0) {
+    // one step's copies: both weights' rows and the tokens'
+    auto load = [&](unsigned k, unsigned s, bool withhold) {
+        const uint32_t to = smem + s * S::STAGE, bar = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(&full[s], S::STAGE);
+        if (withhold) return;   // test hook: the first copy never lands
+        load_box<1>(to, &p.b[0], bar, k * 64, f0);
+        load_box<1>(to + 8192, &p.b[1], bar, k * 64, f0);
+        load_box<1>(to + S::A_BYTES, &p.a[0], bar, k * 64, 0);
+    };
+    const unsigned ahead = min(last - first, static_cast<unsigned>(S::STAGES));
+    if (warp == 0 && elect_one()) {
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(&done, 1);
         fence_barrier_init();
+        // the first stages need nobody else: their copies are on their way while the block sets up
+        for (unsigned n = 0; n < ahead; ++n) load(first + n, n, n == 0 && p.withhold && blockIdx.x == 0);
     }
     if (warp == 1) tmem_take<1>(&tmem_base, S::COLS);
     tc_fence_before();
@@ -790,20 +802,10 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
     bool ok = true;
     if (warp == 0) {
         const bool leader = elect_one();
-        bool withhold = p.withhold && blockIdx.x == 0;
-        for (unsigned k = first; k < last; ++k) {
-            const unsigned n = k - first, s = n % S::STAGES;
+        for (unsigned n = ahead; n < last - first; ++n) {
+            const unsigned s = n % S::STAGES;
             if (!(ok = warp_wait(&empty[s], (n / S::STAGES & 1u) ^ 1u, guard, kSiteEmpty))) break;
-            const uint32_t to = smem + s * S::STAGE, bar = smem_u32(&full[s]);
-            if (leader) {
-                mbar_arrive_expect_tx(&full[s], S::STAGE);
-                if (!withhold) {   // test hook: the first copy never lands
-                    load_box<1>(to, &p.b[0], bar, k * 64, f0);
-                    load_box<1>(to + 8192, &p.b[1], bar, k * 64, f0);
-                    load_box<1>(to + S::A_BYTES, &p.a[0], bar, k * 64, 0);
-                }
-            }
-            withhold = false;
+            if (leader) load(first + n, s, false);
         }
         if (!ok) settle();
     } else if (warp == 1) {
