@@ -152,8 +152,9 @@ GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
         n.splits = static_cast<int>((T + n.run - 1) / n.run);
         if (n.splits > 1) floats = static_cast<size_t>(n.splits) * 2 * F * D;
     }
-    const long long columns = 2LL * ((F + 31) / 32);
-    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (8 * kSms + columns - 1) / columns)), 1024LL);
+    // column sums: four blocks a multiprocessor, at least 64 tokens each, at most 8192 in one sum
+    const long long columns = 2LL * up(F, 32 * chunk);
+    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (4 * kSms + columns - 1) / columns)), 1024LL);
     n.column_run = (T + runs - 1) / runs;
     n.runs = static_cast<int>((T + n.column_run - 1) / n.column_run);
     n.partial = up256(std::max(floats, static_cast<size_t>(n.runs) * 2 * F) * sizeof(float));

@@ -213,25 +213,33 @@ __global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int 
     }
 }
 
-// Column sums of dg and du over runs of tokens: partial[run][2][F].  A warp takes 32 columns, a block's warps every eighth row.
+// Column sums of dg and du over runs of tokens: partial[run][2][F].  A lane takes a chunk of 16 bytes of every eighth row (rows
+// are padded to whole chunks).
 template <typename T>
 __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* du, long long T_, int F, long long pitch, long long run, float* partial) {
-    __shared__ float sums[8][32];
+    constexpr int V = Elem<T>::EPC;
+    __shared__ float sums[8][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const int first_col = blockIdx.x * 32 * V, c = first_col + lane * V;
     const T* from = blockIdx.z ? du : dg;
     const long long first = blockIdx.y * run, end = min(first + run, T_);
-    float s = 0.f;
-    if (c < F)
-#pragma unroll 8
-        for (long long r = first + warp; r < end; r += 8) s += Elem<T>::get(from[r * pitch + c]);
-    sums[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < F) {
-        s = 0.f;
+    float s[V] = {};
+    if (c < pitch)
+#pragma unroll 4
+        for (long long r = first + warp; r < end; r += 8) {
+            float f[V];
+            Elem<T>::unpack(ld_stream(from + r * pitch + c), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][lane];
-        partial[(blockIdx.y * 2LL + blockIdx.z) * F + c] = s;
+            for (int e = 0; e < V; ++e) s[e] += f[e];
+        }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[warp][lane * V + e] = s[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V && first_col + i < F; i += 256) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += sums[w][i];
+        partial[(blockIdx.y * 2LL + blockIdx.z) * F + first_col + i] = t;
     }
 }
 
@@ -270,7 +278,7 @@ na_status launch_sum(const float* partial, int runs, long long n, long long cut,
 
 template <typename T>
 na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s) {
-    glu_column_kernel<T><<<dim3((p.F + 31) / 32, runs, 2), 256, 0, s>>>(static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T, p.F,
+    glu_column_kernel<T><<<dim3(up(p.F, 32 * Elem<T>::EPC), runs, 2), 256, 0, s>>>(static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T, p.F,
                                                                          p.pitch, run, partial);
     return launch_result();
 }
