@@ -27,17 +27,36 @@ constexpr long long kGluMaxRows = (1LL << 31) - 1;
 struct TilePlan {
     bool pairs;              // tiles of 256 x 256 on pairs of blocks, else of 128 x 128
     int few;                 // 16, 64, 128: the kernel of few tokens
-    unsigned rows, cols, steps, run, splits;
+    unsigned rows, cols, steps, run, splits, ways;
     unsigned last_nf, span, groups;   // forward, slopes
+    unsigned workers;                 // tokens and weights in one launch: pairs of blocks for the tokens, 0: apart
+    double time;                      // estimated nanoseconds
 };
 
 
 // Nanoseconds of a step of 64 along the summed axis of a tile, for pairs of blocks and for one, and of what a tile takes besides.
 constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000;
+// Bytes that one product leaves in L2 for the next.
+constexpr double kFitsL2 = 80e6;
 // The same where the rows' operand stays for several columns of tiles.
 constexpr long long kPairStay = 230, kOneStay = 160;
-// Steps summed in one accumulator at most (16384 products: the tensor cores cut their sums, a bias that grows with the steps).
-constexpr unsigned kMostSteps = 256;
+// Steps of 64 products summed in one accumulator at most.  The tensor cores cut their sums instead of rounding them: sums of
+// 43691 products of one sign came out 2.5e-4 of their value too small; 24576 are 1.4e-4, about half of fp16's rounding.
+constexpr unsigned kMostSteps = 384;
+
+// Cuts the steps into `ways` parts side by side of at most kMostSteps each, and turns of them; false if a part would be empty.
+bool cut_steps(TilePlan& t, unsigned ways) {
+    const unsigned most = up(t.steps, ways), least = t.steps / ways;   // steps of a way
+    if (least == 0) return false;
+    for (unsigned turns = up(most, kMostSteps); turns <= most; ++turns) {
+        t.ways = ways;
+        t.run = up(most, turns);
+        const unsigned n = up(most, t.run);
+        t.splits = ways * n;
+        if ((n - 1) * t.run < least) return true;
+    }
+    return false;
+}
 
 TilePlan plan_tiles(Product which, long long T, int D, int F) {
     const bool pair = which == kForward || which == kSlopes;
@@ -99,21 +118,51 @@ TilePlan plan_tiles(Product which, long long T, int D, int F) {
         t.steps = which == kWeights ? up(T, 64) : 2 * up(F, 64);
         const long long tiles = static_cast<long long>(t.rows) * t.cols;
         const double size = which == kWeights ? 2.0 * F * D : static_cast<double>(T) * D;
-        const unsigned fewest = up(t.steps, kMostSteps), most = std::max(fewest, std::min(64u, t.steps / 4));
-        for (unsigned s = fewest; s <= most; ++s) {
-            const unsigned run = up(t.steps, s), splits = up(t.steps, run);
-            const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-            // sums of several splits: written and read again by another kernel
-            const double time = waves * (run * (pairs ? kPairStep : kOneStep) + kTileTime) + (splits > 1 ? 3000 + 8.0 * size * splits / 5000 : 0);
+        const double arrays = 4.0 * T * F, memory = arrays > kFitsL2 ? arrays / 6000 : 0;
+        for (unsigned ways = 1; ways <= std::max(1u, std::min(64u, t.steps / 4)); ++ways) {
+            if (!cut_steps(t, ways)) continue;
+            const double waves = static_cast<double>((tiles * t.splits + slots - 1) / slots);
+            // no faster than dg and du come from memory; sums of several splits are written and read again by another kernel
+            const double time = std::max(waves * (t.run * (pairs ? kPairStep : kOneStep) + kTileTime), memory) +
+                                (t.splits > 1 ? 3000 + 8.0 * size * t.splits / 5000 : 0);
             if (best.splits == 0 || time < least) {
                 least = time;
                 best = t;
-                best.run = run;
-                best.splits = splits;
+                best.time = time;
             }
         }
     }
     return best;
+}
+
+// Tokens and weights in one launch where that is estimated shorter: of the splits that leave the tokens half of the pairs of blocks
+// at least, those with which both sides end soonest.
+void plan_both(long long T, int D, int F, TilePlan& tokens, TilePlan& weights) {
+    const unsigned slots = kSms / 2, steps_t = 2 * up(F, 64), steps_w = up(T, 64);
+    const unsigned tiles_w = 2 * up(F, 256) * up(D, 256);
+    if (4.0 * T * F <= kFitsL2 || tiles_w > slots / 2) return;
+    const long long tiles_t = static_cast<long long>(up(T, 256)) * up(D, 256);
+    TilePlan t{}, w{};
+    t.pairs = w.pairs = true;
+    t.rows = up(T, 256);
+    w.rows = 2 * up(F, 256);
+    t.cols = w.cols = up(D, 256);
+    t.steps = steps_t;
+    w.steps = steps_w;
+    if (!cut_steps(t, 1) || t.splits > 1) return;
+    double least = tokens.time + weights.time;
+    for (unsigned ways = 1; ways * tiles_w <= slots - 16; ++ways) {
+        if (!cut_steps(w, ways)) continue;
+        t.workers = slots - ways * tiles_w;
+        const double first = static_cast<double>(up(tiles_t, t.workers)) * (steps_t * kPairStep + kTileTime);
+        const double second = static_cast<double>(up(steps_w, ways)) * kPairStep + static_cast<double>(w.splits / ways) * kTileTime;
+        const double time = std::max(first, second) + 3000 + 16.0 * F * D * w.splits / 5000;
+        if (time < least) {
+            least = time;
+            tokens = t;
+            weights = w;
+        }
+    }
 }
 
 // How a problem is laid out: the workspace's arrays, and how the weights' gradients are cut.
@@ -141,6 +190,7 @@ GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
     if (n.tensor) {
         n.tokens = plan_tiles(kTokens, T, D, F);
         n.weights = plan_tiles(kWeights, T, D, F);
+        plan_both(T, D, F, n.tokens, n.weights);
         if (n.tokens.splits > 1) floats = static_cast<size_t>(n.tokens.splits) * T * D;
         if (n.weights.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights.splits) * 2 * F * D);
     } else {
@@ -169,8 +219,9 @@ na_status glu_sizes(long long rows, int D, int F, na_dtype dtype) {
 
 bool known_act(na_glu_act a) { return a >= NA_ACT_SILU && a <= NA_ACT_SIGMOID; }
 
-// A product on tensor cores: its tensor maps, boxes of 64 elements by as many rows as one copy brings (na_glu_tc.cuh).
-na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na_dtype dtype, cudaStream_t s) {
+// A product on tensor cores: its tensor maps, boxes of 64 (or 32) elements by as many rows as one copy brings (na_glu_tc.cuh).
+// n: its plan, of kBoth the tokens'; w: of kBoth the weights'.
+na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na_dtype dtype, cudaStream_t s, const TilePlan* w = nullptr) {
     GluTcParams q{};
     const bool pair = which == kForward || which == kSlopes;
     const uint64_t D = p.D, F = p.F, T = p.T, pitch = 2 * static_cast<uint64_t>(p.pitch);
@@ -179,34 +230,44 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
         const uint64_t sizes[2] = {inner, rows};
         if (st == NA_OK) st = encode_box(&m, base, dtype, sizes, row_bytes, wide, box);
     };
-    const uint32_t a_rows = which == kWeights ? 64 : (n.few ? n.few : 128), b_rows = pair && n.pairs ? 128 : 64;
+    q.wide = p.F % 8 == 0;
     if (pair) {
-        map(q.a[0], p.x, D, T, 2 * D, a_rows);
-    } else {
-        map(q.a[0], p.dg, F, T, pitch, a_rows);
-        map(q.a[1], p.du, F, T, pitch, a_rows);
-    }
-    if (which == kWeights) {
-        map(q.b[0], p.x, D, T, 2 * D, b_rows);
-    } else {
+        const uint32_t b_rows = n.pairs ? 128 : 64;
+        map(q.a[0], p.x, D, T, 2 * D, n.few ? n.few : 128);
         map(q.b[0], p.wg, D, F, 2 * D, b_rows);
         map(q.b[1], p.wu, D, F, 2 * D, b_rows);
-        if (pair && !n.few) {
+        if (!n.few) {   // results and dh: boxes of 32 by 32
             map(q.b[2], p.wg, D, F, 2 * D, n.last_nf);
             map(q.b[3], p.wu, D, F, 2 * D, n.last_nf);
+            if (which == kSlopes) {
+                if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32, 32);
+                map(q.out[0], p.dg, F, T, pitch, 32, 32);
+                map(q.out[1], p.du, F, T, pitch, 32, 32);
+            } else if (q.wide) {
+                map(q.out[0], p.h, F, T, 2 * F, 32, 32);
+            }
         }
-    }
-    q.wide = p.F % 8 == 0;
-    if (pair && !n.few) {   // results and dh: boxes of 32 by 32
-        if (which == kSlopes) {
-            if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32, 32);
-            map(q.out[0], p.dg, F, T, pitch, 32, 32);
-            map(q.out[1], p.du, F, T, pitch, 32, 32);
-        } else if (q.wide) {
-            map(q.out[0], p.h, F, T, 2 * F, 32, 32);
+        q.rows = n.rows;
+        q.cols = n.cols;
+        q.steps = n.steps;
+        q.run = n.run;
+        q.splits = n.splits;
+        q.last_nf = n.last_nf;
+        q.span = n.span;
+        q.groups = n.groups;
+    } else {
+        map(q.a[0], p.dg, F, T, pitch, 64);
+        map(q.a[1], p.du, F, T, pitch, 64);
+        if (which != kWeights) {
+            map(q.b[0], p.wg, D, F, 2 * D, 64);
+            map(q.b[1], p.wu, D, F, 2 * D, 64);
         }
+        if (which != kTokens) map(q.b[2], p.x, D, T, 2 * D, 64);
+        const TilePlan& weights = w ? *w : n;
+        q.job[0] = {n.rows, n.cols, n.splits, n.ways, n.run, n.steps};
+        q.job[1] = {weights.rows, weights.cols, weights.splits, weights.ways, weights.run, weights.steps};
+        q.token_workers = n.workers;
     }
-    q.split = !pair && n.splits > 1;
     if (st != NA_OK) return st;
     q.bg = p.bg;
     q.bu = p.bu;
@@ -223,14 +284,6 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     q.D = p.D;
     q.F = p.F;
     q.act = p.act;
-    q.rows = n.rows;
-    q.cols = n.cols;
-    q.steps = n.steps;
-    q.run = n.run;
-    q.splits = n.splits;
-    q.last_nf = n.last_nf;
-    q.span = n.span;
-    q.groups = n.groups;
     q.wait_ns = wait_limit_ns();
     q.withhold = wait_withhold();
     const bool f16 = dtype == NA_FP16;
@@ -242,7 +295,8 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
             if (n.few) return f16 ? launch_few<kSlopes, __half>(q, n.few, s) : launch_few<kSlopes, __nv_bfloat16>(q, n.few, s);
             return f16 ? launch_tiles<kSlopes, __half>(q, n.pairs, s) : launch_tiles<kSlopes, __nv_bfloat16>(q, n.pairs, s);
         case kTokens: return f16 ? launch_tiles<kTokens, __half>(q, n.pairs, s) : launch_tiles<kTokens, __nv_bfloat16>(q, n.pairs, s);
-        default: return f16 ? launch_tiles<kWeights, __half>(q, n.pairs, s) : launch_tiles<kWeights, __nv_bfloat16>(q, n.pairs, s);
+        case kWeights: return f16 ? launch_tiles<kWeights, __half>(q, n.pairs, s) : launch_tiles<kWeights, __nv_bfloat16>(q, n.pairs, s);
+        default: return f16 ? launch_tiles<kBoth, __half>(q, true, s) : launch_tiles<kBoth, __nv_bfloat16>(q, true, s);
     }
 }
 
@@ -361,13 +415,15 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.run = n.run;
     const long long size = static_cast<long long>(F) * D;
     st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, D, F), dtype, s) : fma_product(p, kSlopes, dtype, s);
+    const bool both = dx && dwg && n.tensor && n.tokens.workers;
+    if (st == NA_OK && both) st = launch_tensor(p, kBoth, n.tokens, dtype, s, &n.weights);
     if (st == NA_OK && dx) {
-        st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, dtype, s);
+        if (!both) st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, dtype, s);
         if (st == NA_OK && n.tensor && n.tokens.splits > 1)
             st = sum_runs(p.partial, n.tokens.splits, rows * D, rows * D, dx, nullptr, dtype, s);
     }
     if (st == NA_OK && dwg) {
-        st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, dtype, s);
+        if (!both) st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, dtype, s);
         const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.splits;
         if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, dwg, dwu, dtype, s);
     }

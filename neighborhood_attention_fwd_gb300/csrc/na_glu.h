@@ -13,7 +13,8 @@ namespace glu {
 
 // The products.  kForward: h from x and both weights.  kSlopes: the same product again, and dg, du from it and dh.
 // kTokens: dx = dg Wg + du Wu.  kWeights: dWg = dg^T x, dWu = du^T x.
-enum Product { kForward = 0, kSlopes = 1, kTokens = 2, kWeights = 3 };
+// kBoth: these two in one launch.
+enum Product { kForward = 0, kSlopes = 1, kTokens = 2, kWeights = 3, kBoth = 4 };
 
 struct GluParams {
     const void* x;        // [T, D]
@@ -36,10 +37,16 @@ struct GluParams {
     long long run;        // tokens of a run (a multiple of 64)
 };
 
+// The tiles of kTokens or kWeights: rows (kWeights: of dWg and dWu together) x cols.  Each is the sum of `splits` parts of the
+// `steps` steps of 64 along the summed axis: part w + ways t takes the steps w + ways (t run + j), j < run; none is empty.
+struct GluJob {
+    unsigned rows, cols, splits, ways, run, steps;
+};
+
 // Parameters of the tensor-core kernels.
 struct GluTcParams {
     CUtensorMap a[2];     // rows' operand: x; dg, du
-    CUtensorMap b[4];     // columns' operand: Wg, Wu (and again in boxes for a row's last tile); x
+    CUtensorMap b[4];     // columns' operand: Wg, Wu and (forward, slopes) again in boxes for a row's last tile; [2]: x (weights)
     CUtensorMap in;       // slopes: dh
     CUtensorMap out[2];   // forward: h; slopes: dg, du
     const void* bg;
@@ -55,12 +62,13 @@ struct GluTcParams {
     long long pitch;      // of dg and du
     int T, D, F, act;
     uint32_t wide;        // rows of h and dh are whole 16-byte chunks
-    uint32_t split;       // results are sums of splits, to partial
-    unsigned rows, cols;  // tiles (weights: rows of dWg and dWu together)
+    GluJob job[2];        // tokens, weights
+    unsigned token_workers;   // both: pairs of blocks that make dx
+    unsigned rows, cols;  // forward, slopes: tiles
     unsigned last_nf;     // forward, slopes: columns of g (and of u) of a row's last tile
     unsigned span, groups;   // forward, slopes: columns of tiles that a block takes in a row, and such runs of a row
-    unsigned splits;
-    unsigned steps, run;  // steps of 64 along the summed axis, and of one split
+    unsigned splits;      // few tokens: blocks to a tile's sum
+    unsigned steps, run;  // forward, slopes: steps of 64 along the summed axis; few tokens: of one block
     unsigned* err;
     unsigned long long wait_ns;
     uint32_t withhold;

@@ -537,8 +537,12 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tokens and weights: plain products, 256 x 256 on pairs of blocks or 128 x 128, the summed axis cut into splits where there
-// are few tiles (their fp32 sums are added by another kernel).
+// Tokens and weights: plain products, 256 x 256 on pairs of blocks or 128 x 128.  Where there are few tiles, or the summed axis is
+// long, it is cut into splits (their fp32 sums are added by another kernel): `ways` of them side by side, each taking every
+// ways-th step, for `run` steps, then the next ones.
+// Both products read all of dg and du.  Where these do not fit L2, one launch makes both side by side: some blocks go down the rows
+// of dx, the others down the tokens of the weights' sums at the same pace, so that what one side reads the other finds in L2
+// (3D tokens: 137 + 136 us one after the other, both bound by memory).
 // ---------------------------------------------------------------------------------------------
 
 template <int CG>
@@ -552,77 +556,60 @@ struct TileShape {
     static_assert(BYTES <= 227 * 1024 - 512, "more than a block's shared memory");
 };
 
-struct Tile {
-    unsigned row, col, first, last, split;   // steps [first, last)
+template <int STAGES>
+struct TileBarriers {
+    uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2];
 };
-__device__ __forceinline__ Tile tile_of(const GluTcParams& p, unsigned i) {
-    const unsigned per = p.rows * p.cols, split = i / per;
-    const Place at = place_of(i - split * per, p.rows, p.cols);
-    const unsigned first = split * p.run;
-    return {at.row, at.col, first, min(p.steps, first + p.run), split};
+
+struct Tile {
+    unsigned row, col, split, first, end;   // steps first, first + ways, .. below end
+};
+__device__ __forceinline__ Tile tile_of(const GluJob& job, unsigned i) {
+    const unsigned per = job.rows * job.cols, split = i / per, turn = split / job.ways;
+    const Place at = place_of(i - split * per, job.rows, job.cols);
+    const unsigned first = turn * job.run * job.ways + split - turn * job.ways;
+    return {at.row, at.col, split, first, min(job.steps, first + job.run * job.ways)};
 }
 
+// A block's part in one of the products: worker `mine` of `all`.
 template <int WHICH, int CG, typename T>
-__global__ void __launch_bounds__(TileShape<CG>::THREADS, 1) glu_tile_kernel(const __grid_constant__ GluTcParams p) {
+__device__ __forceinline__ void tile_work(const GluTcParams& p, unsigned mine, unsigned all, uint32_t smem, TileBarriers<TileShape<CG>::STAGES>& bars,
+                                          uint32_t tmem, uint32_t rank) {
     using S = TileShape<CG>;
     constexpr bool WEIGHTS = WHICH == kWeights;
-    extern __shared__ uint8_t raw_smem[];
-    __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2];
-    __shared__ uint32_t tmem_base;
-    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const GluJob& job = p.job[WEIGHTS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-    const unsigned mine = blockIdx.x / CG, all = gridDim.x / CG, tiles = p.rows * p.cols * p.splits;
+    const unsigned tiles = job.rows * job.cols * job.splits;
     const WaitGuard guard{p.err, p.wait_ns};
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], CG * S::WARPS);
-        }
-        fence_barrier_init();
-    }
-    if (warp == 2) tmem_take<CG>(&tmem_base, 2 * S::N);
-    tc_fence_before();
-    __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base;
-
+    // dg and du, Wg and Wu are halves: of the summed axis (tokens), of the rows of tiles (weights)
     if (warp == 0) {
         // copies
-        const uint32_t full_at = CG == 2 ? peer_address(smem_u32(full), 0) : smem_u32(full);   // the leading block's barriers
+        const uint32_t full_at = CG == 2 ? peer_address(smem_u32(bars.full), 0) : smem_u32(bars.full);   // the leading block's barriers
         int s = 0;
         uint32_t parity = 1;
         const bool leader = elect_one();
         bool ok = true, withhold = p.withhold && blockIdx.x == 0;
         for (unsigned i = mine; ok && i < tiles; i += all) {
-            const Tile t = tile_of(p, i);
-            for (unsigned k = t.first; k < t.last; ++k) {
-                ok = warp_wait(&empty[s], parity, guard, kSiteEmpty);
-                if (!ok) break;
-                const uint32_t to = smem + s * S::STAGE;
-                const uint32_t bar = full_at + s * 8;
+            const Tile t = tile_of(job, i);
+            for (unsigned k = t.first; k < t.end; k += job.ways) {
+                if (!(ok = warp_wait(&bars.empty[s], parity, guard, kSiteEmpty))) break;
+                const uint32_t to = smem + s * S::STAGE, bar = full_at + s * 8;
+                const unsigned half = WEIGHTS ? t.row >= job.rows / 2 : k >= job.steps / 2;
+                const unsigned row = (WEIGHTS ? t.row - half * (job.rows / 2) : t.row) * S::M + rank * 128, col = t.col * S::N + rank * 128;
+                const unsigned at = (WEIGHTS ? k : k - half * (job.steps / 2)) * 64;
                 if (leader) {
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * S::STAGE);
-                    if (withhold) {
-                        // test hook: the first copy never lands
-                    } else if constexpr (WHICH == kTokens) {
-                        const unsigned half = k >= p.steps / 2, at = (k - half * (p.steps / 2)) * 64;
-                        load_box<CG>(to, &p.a[half], bar, at, t.row * S::M + rank * 128);
-    #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[half], bar, t.col * S::N + rank * 128 + j * 64, at);
-                    } else {
-                        const unsigned half = t.row >= p.rows / 2, row = (t.row - half * (p.rows / 2)) * S::M + rank * 128;
-    #pragma unroll
-                        for (int j = 0; j < 2; ++j) load_box<CG>(to + j * 8192, &p.a[half], bar, row + j * 64, k * 64);
-    #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[0], bar, t.col * S::N + rank * 128 + j * 64, k * 64);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], CG * S::STAGE);
+                    if (!withhold) {   // test hook: the first copy never lands
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if constexpr (WEIGHTS) {
+                                load_box<CG>(to + j * 8192, &p.a[half], bar, row + j * 64, at);
+                                load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[2], bar, col + j * 64, at);
+                            } else {
+                                load_box<CG>(to + j * 8192, &p.a[half], bar, at, row + j * 64);
+                                load_box<CG>(to + S::A_BYTES + j * 8192, &p.b[half], bar, col + j * 64, at);
+                            }
+                        }
                     }
                 }
                 withhold = false;
@@ -645,99 +632,128 @@ __global__ void __launch_bounds__(TileShape<CG>::THREADS, 1) glu_tile_kernel(con
         const bool leader = elect_one();
         bool ok = true;
         for (unsigned i = mine; ok && i < tiles; i += all, ++n) {
-            const Tile t = tile_of(p, i);
+            const Tile t = tile_of(job, i);
             const uint32_t buf = n & 1u, acc = tmem + buf * S::N;
-            ok = warp_wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP);
-            if (!ok) break;
+            if (!(ok = warp_wait(&bars.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, guard, kSiteP))) break;
             tc_fence_after();
-            for (unsigned k = t.first; k < t.last; ++k) {
-                ok = warp_wait(&full[s], parity, guard, kSiteKV);
-                if (!ok) break;
+            for (unsigned k = t.first; k < t.end; k += job.ways) {
+                if (!(ok = warp_wait(&bars.full[s], parity, guard, kSiteKV))) break;
                 tc_fence_after();
                 const uint32_t at = smem + s * S::STAGE;
                 if (leader) {
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
                         mma<CG>(acc, da + ((at + j * KA) >> 4), db + ((at + S::A_BYTES + j * KB) >> 4), idesc, k > t.first || j > 0);
-                    commit<CG>(&empty[s]);
+                    commit<CG>(&bars.empty[s]);
                 }
                 if (++s == S::STAGES) {
                     s = 0;
                     parity ^= 1u;
                 }
             }
-            if (ok && leader) commit<CG>(&acc_full[buf]);
+            if (ok && leader) commit<CG>(&bars.acc_full[buf]);
         }
         if (!ok) settle();
     } else if (warp >= 4) {
-        // results: warp e takes rows 32 (e & 3) .. of the block and the (e / 4)-th run of columns
+        // results: warp e takes rows 32 (e & 3) .. of the block and the (e / 4)-th half of its columns
         const int e = warp - 4, quarter = e & 3, part = e >> 2;
         const uint32_t staging = smem + S::STAGING + e * 4096;
+        const uint32_t row = staging + lane * 128, sw = lane & 7;   // rows of 128 bytes in 128-byte swizzle
+        const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(bars.acc_empty), 0) : 0u;
+        const bool split = job.splits > 1;
         uint32_t n = 0;
-        const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(acc_empty), 0) : 0u;
-        auto release = [&](uint32_t buf) {   // this warp has read its accumulators
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2) arrive_remote(acc_at + buf * 8);
-                else mbar_arrive(&acc_empty[buf]);
+        for (unsigned i = mine; i < tiles; i += all, ++n) {
+            const Tile t = tile_of(job, i);
+            const uint32_t buf = n & 1u, taddr = tmem + buf * S::N + (static_cast<uint32_t>(quarter * 32) << 16) + part * S::OUT;
+            const unsigned half = WEIGHTS && t.row >= job.rows / 2;
+            const int m0 = static_cast<int>((t.row - half * (job.rows / 2)) * S::M + rank * 128 + quarter * 32), last_row = WEIGHTS ? p.F : p.T;
+            const int c0 = static_cast<int>(t.col * S::N + part * S::OUT);
+            float* sums = p.partial + static_cast<long long>(WEIGHTS ? t.split * 2 + half : t.split) * last_row * p.D;
+            T* result = static_cast<T*>(!WEIGHTS ? p.dx : half ? p.dwu : p.dwg);
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal))) {
+                settle();
+                break;
             }
-        };
-                    const uint32_t row = staging + lane * 128, sw = lane & 7;   // rows of 128 bytes in 128-byte swizzle
-                    for (unsigned i = mine; i < tiles; i += all, ++n) {
-                        const Tile t = tile_of(p, i);
-                        const uint32_t buf = n & 1u;
-                        const int m0 = static_cast<int>((WEIGHTS && t.row >= p.rows / 2 ? t.row - p.rows / 2 : t.row) * S::M + rank * 128 + quarter * 32);
-                        const uint32_t taddr = tmem + buf * S::N + (static_cast<uint32_t>(quarter * 32) << 16);
-                                        const int c0 = static_cast<int>(t.col * S::N + part * S::OUT);
-                                        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (n >> 1) & 1u, guard, kSiteFinal))) {
-                                            settle();
-                                            break;
-                                        }
-                                        tc_fence_after();
-                                        const unsigned half = WEIGHTS && t.row >= p.rows / 2;
-                        const int last_row = WEIGHTS ? p.F : p.T;
-                        float* sums = p.partial + static_cast<long long>(WEIGHTS ? t.split * 2 + half : t.split) * last_row * p.D;
-                        T* result = static_cast<T*>(WHICH == kTokens ? p.dx : half ? p.dwu : p.dwg);
-                        uint32_t v[2][16];
-                        tmem_ld16(taddr + part * S::OUT, v[0]);
-                        constexpr int PIECES = S::OUT / 16;
-        #pragma unroll
-                        for (int c = 0; c < PIECES; ++c) {
-                            const int per = p.split ? 2 : 4, at = c % per;   // the staging holds 64 columns of 2 bytes or 32 of 4
-                            tmem_ld_wait_all();
-                            reg_fence16(v[c & 1]);
-                            if (c + 1 < PIECES) tmem_ld16(taddr + part * S::OUT + (c + 1) * 16, v[(c + 1) & 1]);
-                            else release(buf);
-                            if (p.split) {
-        #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    st_shared_v4(row + ((4 * at + j) ^ sw) * 16, v[c & 1][4 * j], v[c & 1][4 * j + 1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]);
-                            } else {
-                                uint32_t w[8];
-        #pragma unroll
-                                for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pair(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
-                                st_shared_v4(row + ((2 * at) ^ sw) * 16, w[0], w[1], w[2], w[3]);
-                                st_shared_v4(row + ((2 * at + 1) ^ sw) * 16, w[4], w[5], w[6], w[7]);
-                            }
-                            if (at == per - 1) {   // out by rows: eight lanes a row
-                                __syncwarp();
-                                const int r = lane >> 3, col = c0 + (c / per) * per * 16 + (lane & 7) * (p.split ? 4 : 8);
-        #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint4 w = ld_shared_v4(staging + (r + 4 * j) * 128 + (((lane & 7) ^ ((r + 4 * j) & 7)) << 4));
-                                    const long long to = static_cast<long long>(m0 + r + 4 * j) * p.D + col;
-                                    if (m0 + r + 4 * j < last_row && col < p.D) {
-                                        if (p.split) st_stream(sums + to, w);
-                                        else st_stream(result + to, w);
-                                    }
-                                }
-                                __syncwarp();
-                            }
+            tc_fence_after();
+            uint32_t v[2][16];
+            tmem_ld16(taddr, v[0]);
+            constexpr int PIECES = S::OUT / 16;
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c) {
+                const int per = split ? 2 : 4, at = c % per;   // the staging holds 64 columns of 2 bytes or 32 of 4
+                tmem_ld_wait_all();
+                reg_fence16(v[c & 1]);
+                if (c + 1 < PIECES) {
+                    tmem_ld16(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                } else {   // this warp has read its accumulators
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2) arrive_remote(acc_at + buf * 8);
+                        else mbar_arrive(&bars.acc_empty[buf]);
+                    }
+                }
+                if (split) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        st_shared_v4(row + ((4 * at + j) ^ sw) * 16, v[c & 1][4 * j], v[c & 1][4 * j + 1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]);
+                } else {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pair(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
+                    st_shared_v4(row + ((2 * at) ^ sw) * 16, w[0], w[1], w[2], w[3]);
+                    st_shared_v4(row + ((2 * at + 1) ^ sw) * 16, w[4], w[5], w[6], w[7]);
+                }
+                if (at == per - 1) {   // out by rows: eight lanes a row
+                    __syncwarp();
+                    const int r = lane >> 3, col = c0 + (c / per) * per * 16 + (lane & 7) * (split ? 4 : 8);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 w = ld_shared_v4(staging + (r + 4 * j) * 128 + (((lane & 7) ^ ((r + 4 * j) & 7)) << 4));
+                        const long long to = static_cast<long long>(m0 + r + 4 * j) * p.D + col;
+                        if (m0 + r + 4 * j < last_row && col < p.D) {
+                            if (split) st_stream(sums + to, w);
+                            else st_stream(result + to, w);
                         }
                     }
+                    __syncwarp();
+                }
+            }
+        }
         tc_fence_before();
     }
+}
+
+template <int WHICH, int CG, typename T>
+__global__ void __launch_bounds__(TileShape<CG>::THREADS, 1) glu_tile_kernel(const __grid_constant__ GluTcParams p) {
+    using S = TileShape<CG>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ TileBarriers<S::STAGES> bars;
+    __shared__ uint32_t tmem_base;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const unsigned mine = blockIdx.x / CG, all = gridDim.x / CG;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&bars.full[s], 1);
+            mbar_init(&bars.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], CG * S::WARPS);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_take<CG>(&tmem_base, 2 * S::N);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    if constexpr (WHICH != kBoth) tile_work<WHICH, CG, T>(p, mine, all, smem, bars, tmem, rank);
+    else if (mine < p.token_workers) tile_work<kTokens, CG, T>(p, mine, p.token_workers, smem, bars, tmem, rank);
+    else tile_work<kWeights, CG, T>(p, mine - p.token_workers, all - p.token_workers, smem, bars, tmem, rank);
     __syncwarp();
     if constexpr (CG == 2) cluster_sync();
     else __syncthreads();
@@ -947,7 +963,9 @@ na_status launch_tiles(const GluTcParams& p, unsigned tiles, cudaStream_t s) {
 
 template <int WHICH, typename T>
 na_status launch_tiles(const GluTcParams& p, bool pairs, cudaStream_t s) {
-    const unsigned tiles = WHICH == kForward || WHICH == kSlopes ? p.rows * p.groups : p.rows * p.cols * p.splits;
+    if constexpr (WHICH == kBoth) return launch_tiles<kBoth, 2, T>(p, kSms / 2, s);
+    const GluJob& job = p.job[WHICH == kWeights];
+    const unsigned tiles = WHICH == kForward || WHICH == kSlopes ? p.rows * p.groups : job.rows * job.cols * job.splits;
     return pairs ? launch_tiles<WHICH, 2, T>(p, tiles, s) : launch_tiles<WHICH, 1, T>(p, tiles, s);
 }
 
