@@ -808,34 +808,44 @@ def _norms(norm, post):
     return kinds
 
 
-def _alike(shape, dtype, names, tensors):
-    """Contiguous tensors of one shape and type, or None.  (The checks of the calls below stand in few loops: a call of a
-    Python function costs as much as three of them.)"""
-    for i, t in enumerate(tensors):
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
-            _check(t, shape, dtype, names[i])
+def _here(stream, t):
+    """The current CUDA device, which t must be on, and the raw stream of a call."""
+    here = t.get_device()
+    if here < 0 or here != torch._C._cuda_getDevice():
+        _launch_stream(stream, t)   # raises
+    return here, torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
+
+
+def _gather(pointers, here, shape, dtype, names, tensors):
+    """Appends the pointers of contiguous tensors of one shape and type on the device `here` (null for None).  All checks of
+    a tensor stand in this loop: in a call of their own they would cost several times what they do."""
+    for t in tensors:
+        if t is None:
+            pointers.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != here or not t.is_contiguous():
+            name = names.split()[[u is t for u in tensors].index(True)]
+            _check(t, tuple(shape), dtype, name)
+            raise ValueError(f"{name} on {t.device}, but the current device is cuda:{here}")
+        pointers.append(t.data_ptr())
 
 
 def _groups(shape, C, names, tensors):
-    """Number of vectors of fp32 tensors [C], or [.., C] with leading axes of the rows (a vector for each); all alike."""
-    first = None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        own = t.shape
-        if first is None:
-            n = len(own)
-            if n > len(shape) or n == 0:
-                raise ValueError(f"{names[i]} must be [C], or have leading axes of the rows")
-            first = (C,) if n == 1 else shape[:n - 1] + (C,)
-        if t.dtype is not torch.float32 or own != first or not t.is_contiguous():
-            _check(t, tuple(first), torch.float32, names[i])
-    return 1 if first is None or n == 1 else math.prod(first[:-1])
+    """Shape and number of vectors, [C] or [.., C] with leading axes of the rows (a vector for each), by the first one given."""
+    for t in tensors:
+        if t is not None:
+            n = t.dim() - 1
+            if n == 0:
+                return (C,), 1
+            if not 0 < n < len(shape):
+                raise ValueError(f"{names} must be [C], or have leading axes of the rows")
+            lead = shape[:n]
+            return lead + (C,), math.prod(lead)
+    return None, 1
 
 
-def _moments(shape, kinds, tensors, needed):
-    """The statistics (mean, rstd, post_mean, post_rstd): both of a layer norm, rstd alone of a root mean square norm."""
-    mean, rstd, post_mean, post_rstd = tensors
+def _moments(kinds, mean, rstd, post_mean, post_rstd, needed):
+    """The statistics go together: both of a layer norm, rstd alone of a root mean square norm."""
     for kind, m, r in ((kinds[0], mean, rstd), (kinds[1], post_mean, post_rstd)):
         if kind == 1:
             if (m is None) != (r is None) or (needed and r is None):
@@ -844,7 +854,6 @@ def _moments(shape, kinds, tensors, needed):
             raise ValueError("only a layer norm has a mean")
         elif (r is None and needed) if kind else r is not None:
             raise ValueError("rstd of a root mean square norm is needed" if kind else "no norm, no statistics of it")
-    _alike(shape[:-1], torch.float32, ("mean", "rstd", "post_mean", "post_rstd"), tensors)
 
 
 def na_addnorm(x, y, s, h, w=None, b=None, gate=None, post_w=None, post_b=None, norm: str = "layer", post: str = "none",
@@ -857,27 +866,24 @@ def na_addnorm(x, y, s, h, w=None, b=None, gate=None, post_w=None, post_b=None, 
     (nothing but h is wanted); s and h may each be x or y.  mean, rstd, post_mean, post_rstd: fp32 x.shape[:-1] for
     the backward, or None; root mean square norms have no mean."""
     shape, rows, C = _rows(x)
-    _alike(shape, x.dtype, ("x", "y", "s", "h"), (x, y, s, h))
     kinds = _norms(norm, post)
-    if (h is None) != (norm == "none"):
+    if (h is None) != (kinds[0] == 0):
         raise ValueError("h goes with a norm")
     if s is None and h is None:
         raise ValueError("s is needed without a norm")
-    if (h is None and (w is not None or b is not None)) or (post == "none" and (post_w is not None or post_b is not None)):
+    if (h is None and not (w is b is None)) or (kinds[1] == 0 and not (post_w is post_b is None)):
         raise ValueError("weights of a norm that is none")
-    w_groups = gate_groups = 1
-    if w is not None or b is not None:
-        w_groups = _groups(shape, C, ("w", "b"), (w, b))
-    if gate is not None:
-        gate_groups = _groups(shape, C, ("gate",), (gate,))
-    if post_w is not None or post_b is not None:
-        _alike((C,), torch.float32, ("post_w", "post_b"), (post_w, post_b))
-    statistics = (mean, rstd, post_mean, post_rstd)
-    _moments(shape, kinds, statistics, False)
-    tensors = (x, y, s, h, w, b, gate, post_w, post_b) + statistics
-    raw = _launch_stream(stream, *tensors)
-    st = load().na_addnorm(*[None if t is None else t.data_ptr() for t in tensors], rows, C, w_groups, gate_groups, *kinds, scale, residual,
-                           eps, _code(x), raw)
+    _moments(kinds, mean, rstd, post_mean, post_rstd, False)
+    w_shape, w_groups = _groups(shape, C, "w and b", (w, b))
+    gate_shape, gate_groups = _groups(shape, C, "gate", (gate,))
+    here, raw = _here(stream, x)
+    f32, pointers = torch.float32, []
+    _gather(pointers, here, shape, x.dtype, "x y s h", (x, y, s, h))
+    _gather(pointers, here, w_shape, f32, "w b", (w, b))
+    _gather(pointers, here, gate_shape, f32, "gate", (gate,))
+    _gather(pointers, here, (C,), f32, "post_w post_b", (post_w, post_b))
+    _gather(pointers, here, shape[:-1], f32, "mean rstd post_mean post_rstd", (mean, rstd, post_mean, post_rstd))
+    st = load().na_addnorm(*pointers, rows, C, w_groups, gate_groups, *kinds, scale, residual, eps, _code(x), raw)
     if st:
         _ok(st, "na_addnorm")
 
@@ -898,36 +904,34 @@ def na_addnorm_bwd(dh, ds, s, y, dx, dy, w=None, gate=None, post_w=None, post_b=
     reaches s from elsewhere (or None), s, y and the forward's statistics.  Without a norm dh and s are None.  dx may be
     dh, ds or s, dy may be dh, ds, s or y, but not dx."""
     shape, rows, C = _rows(y)
-    rowwise = (dh, ds, s, y, dx, dy)
-    _alike(shape, y.dtype, ("dh", "ds", "s", "y", "dx", "dy"), rowwise)
     kinds = _norms(norm, post)
-    normed = norm != "none"
+    normed = kinds[0] != 0
     if (dh is not None) != normed or (s is not None) != normed:
         raise ValueError("dh and s go with a norm")
     if dx is None or dy is None or (ds is None and not normed):
         raise ValueError("dx and dy are written, and ds is needed without a norm")
-    if not normed and not (w is dw is db is None):
-        raise ValueError("weights of a norm that is none")
-    if post == "none" and not (post_w is post_b is dpost_w is dpost_b is None):
+    if (not normed and not (w is dw is db is None)) or (kinds[1] == 0 and not (post_w is post_b is dpost_w is dpost_b is None)):
         raise ValueError("weights of a norm that is none")
     if gate is None and dgate is not None:
         raise ValueError("dgate goes with gate")
-    w_groups = gate_groups = 1
-    if not (w is dw is db is None):
-        w_groups = _groups(shape, C, ("w", "dw", "db"), (w, dw, db))
-    if gate is not None:
-        gate_groups = _groups(shape, C, ("gate", "dgate"), (gate, dgate))
-    if post != "none":
-        _alike((C,), torch.float32, ("post_w", "post_b", "dpost_w", "dpost_b"), (post_w, post_b, dpost_w, dpost_b))
-    statistics = (mean, rstd, post_mean, post_rstd)
-    _moments(shape, kinds, statistics, True)
-    tensors = (dh, ds, s, y, w, gate, post_w, post_b) + statistics + (dx, dy, dw, db, dgate, dpost_w, dpost_b)
-    raw = _launch_stream(stream, *tensors, workspace)
+    _moments(kinds, mean, rstd, post_mean, post_rstd, True)
+    w_shape, w_groups = _groups(shape, C, "w, dw and db", (w, dw, db))
+    gate_shape, gate_groups = _groups(shape, C, "gate", (gate,))
+    here, raw = _here(stream, y)
+    f32, dtype, p, q = torch.float32, y.dtype, [], []
+    _gather(p, here, shape, dtype, "dh ds s y dx dy", (dh, ds, s, y, dx, dy))
+    _gather(q, here, w_shape, f32, "w dw db", (w, dw, db))
+    _gather(q, here, gate_shape, f32, "gate dgate", (gate, dgate))
+    _gather(q, here, (C,), f32, "post_w post_b dpost_w dpost_b", (post_w, post_b, dpost_w, dpost_b))
+    _gather(q, here, shape[:-1], f32, "mean rstd post_mean post_rstd", (mean, rstd, post_mean, post_rstd))
     code = _code(y)
-    ws, ws_ptr, ws_bytes = (None, None, 0) if dw is db is dgate is dpost_w is dpost_b is None else _workspace(
-        workspace, stream, lambda: _add_need(rows, C, w_groups, gate_groups, code), y.device)
-    st = load().na_addnorm_bwd(*[None if t is None else t.data_ptr() for t in tensors], rows, C, w_groups, gate_groups, *kinds, scale,
-                               residual, code, ws_ptr, ws_bytes, raw)
+    ws_ptr, ws_bytes = None, 0
+    if not (dw is db is dgate is dpost_w is dpost_b is None):
+        if workspace is not None and workspace.get_device() != here:
+            raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{here}")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, stream, lambda: _add_need(rows, C, w_groups, gate_groups, code), y.device)
+    st = load().na_addnorm_bwd(p[0], p[1], p[2], p[3], q[0], q[3], q[5], q[6], q[9], q[10], q[11], q[12], p[4], p[5], q[1], q[2], q[4], q[7], q[8],
+                               rows, C, w_groups, gate_groups, *kinds, scale, residual, code, ws_ptr, ws_bytes, raw)
     if st:
         _ok(st, "na_addnorm_bwd")
 
@@ -935,31 +939,29 @@ def na_addnorm_bwd(dh, ds, s, y, dx, dy, w=None, gate=None, post_w=None, post_b=
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
 
-def _glu(x, wg, wu, h, name, bg, bu, act):
-    """Checks of what both directions take; rows, D, F and the activation's code."""
+def _glu(x, wg, wu, h, name, bg, bu, act, stream):
+    """Checks of what both directions take; the pointers, rows, D, F, the activation's code, the device and the stream."""
     shape, rows, D = _rows(x)
     F = wg.shape[0] if wg.dim() == 2 else 0
     if F < 1 or F > _INT_MAX:
         raise ValueError("wg must be [F, D], F at least 1 and at most 2^31 - 1")
-    dtype = x.dtype
-    _alike(shape, dtype, ("x",), (x,))
-    _alike((F, D), dtype, ("wg", "wu"), (wg, wu))
-    _alike(shape[:-1] + (F,), dtype, (name,), (h,))
-    if bg is not None or bu is not None:
-        _alike((F,), dtype, ("bg", "bu"), (bg, bu))
     code = _ACTS.get(act)
     if code is None:
         raise ValueError("act must be 'silu', 'gelu', 'gelu_tanh', 'relu' or 'sigmoid'")
-    return rows, D, F, code
+    here, raw = _here(stream, x)
+    dtype, p = x.dtype, []
+    _gather(p, here, shape, dtype, "x", (x,))
+    _gather(p, here, (F, D), dtype, "wg wu", (wg, wu))
+    _gather(p, here, (F,), dtype, "bg bu", (bg, bu))
+    _gather(p, here, shape[:-1] + (F,), dtype, name, (h,))
+    return p, rows, D, F, code, here, raw
 
 
 def na_glu(x, wg, wu, h, bg=None, bu=None, act: str = "silu", stream=None):
     """h = act(x wg^T + bg) * (x wu^T + bu) for x [.., D], wg and wu [F, D], bg and bu [F] or None, h [.., F], all of one type.
     act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid"."""
-    rows, D, F, code = _glu(x, wg, wu, h, "h", bg, bu, act)
-    tensors = (x, wg, wu, bg, bu, h)
-    raw = _launch_stream(stream, *tensors)
-    st = load().na_glu(*[None if t is None else t.data_ptr() for t in tensors], rows, D, F, code, _code(x), raw)
+    p, rows, D, F, code, _, raw = _glu(x, wg, wu, h, "h", bg, bu, act, stream)
+    st = load().na_glu(*p, rows, D, F, code, _code(x), raw)
     if st:
         _ok(st, "na_glu")
 
@@ -977,24 +979,21 @@ def na_glu_bwd(dh, x, wg, wu, dx=None, dwg=None, dwu=None, bg=None, bu=None, dbg
                workspace=None, stream=None):
     """Gradients of na_glu from dh and its inputs, each laid out as its tensor and left out where None (dwg and dwu go
     together).  Nothing of the forward is kept: the products are made again."""
-    rows, D, F, code = _glu(x, wg, wu, dh, "dh", bg, bu, act)
     if (dwg is None) != (dwu is None):
         raise ValueError("dwg and dwu go together")
     if (bg is None and dbg is not None) or (bu is None and dbu is not None):
         raise ValueError("dbg goes with bg, dbu with bu")
     if dx is dwg is dbg is dbu is None:
         raise ValueError("no gradient is wanted")
-    dtype = x.dtype
-    if dx is not None:
-        _alike(x.shape, dtype, ("dx",), (dx,))
-    if dwg is not None:
-        _alike(wg.shape, dtype, ("dwg", "dwu"), (dwg, dwu))
-    if dbg is not None or dbu is not None:
-        _alike((F,), dtype, ("dbg", "dbu"), (dbg, dbu))
-    tensors = (dh, x, wg, wu, bg, bu, dx, dwg, dwu, dbg, dbu)
-    raw = _launch_stream(stream, *tensors, workspace)
+    p, rows, D, F, code, here, raw = _glu(x, wg, wu, dh, "dh", bg, bu, act, stream)
+    dtype, q = x.dtype, []
+    _gather(q, here, x.shape, dtype, "dx", (dx,))
+    _gather(q, here, (F, D), dtype, "dwg dwu", (dwg, dwu))
+    _gather(q, here, (F,), dtype, "dbg dbu", (dbg, dbu))
+    if workspace is not None and workspace.get_device() != here:
+        raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{here}")
     kind = _code(x)
     ws, ws_ptr, ws_bytes = _workspace(workspace, stream, lambda: _glu_need(rows, D, F, kind), x.device)
-    st = load().na_glu_bwd(*[None if t is None else t.data_ptr() for t in tensors], rows, D, F, code, kind, ws_ptr, ws_bytes, raw)
+    st = load().na_glu_bwd(p[5], *p[:5], *q, rows, D, F, code, kind, ws_ptr, ws_bytes, raw)
     if st:
         _ok(st, "na_glu_bwd")
