@@ -438,13 +438,15 @@ typedef enum {
 /*
  * The gated feed-forward product: h = act(x Wg^T + bg) * (x Wu^T + bu) for `rows` tokens, both products, the activation
  * and the gating in one kernel.  x: [rows, D], wg, wu: [F, D] (halves of one [2 F, D] array will do), bg, bu: [F] or null
- * (zeros), h: [rows, F], all of the tensors' type.  Sums in fp32, h rounded once.  2-byte tensors with D a multiple of 8
- * run on tensor cores, others on FMA units.  rows < 2^31, D and F up to 2^20 (else NA_ERR_UNSUPPORTED).
+ * (zeros), h: [rows, F], all of the tensors' type.  Sums in fp32, h rounded once.  2-byte tensors run on tensor
+ * cores (where D is no multiple of 8, from some size on, on copies of x, wg and wu allocated on the stream), fp32 on FMA
+ * units.  rows < 2^31, D and F up to 2^20 (else NA_ERR_UNSUPPORTED).
  */
 na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* h, int64_t rows, int D,
                  int F, na_glu_act act, na_dtype dtype, void* stream);
 
-/* Bytes of device workspace na_glu_bwd needs (0 on invalid arguments): dg, du (below) and sums over runs of tokens. */
+/* Bytes of device workspace na_glu_bwd needs (0 on invalid arguments): dg, du (below), sums over runs of tokens, and
+ * the copies of rows that are not whole 16-byte chunks. */
 size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype);
 
 /*

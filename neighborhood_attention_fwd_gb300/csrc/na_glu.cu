@@ -168,6 +168,8 @@ void plan_both(long long T, int D, int F, TilePlan& tokens, TilePlan& weights) {
 // How a problem is laid out: the workspace's arrays, and how the weights' gradients are cut.
 struct GluPlan {
     bool tensor;                     // tensor cores
+    int width;                       // channels of the products, as tensor_width
+    size_t tokens_copy, weights_copy;   // bytes of x or dx, of Wg, Wu, dWg or dWu in that width; 0 where it is D
     long long pitch;                 // of a row of dg and du
     size_t array;                    // bytes of one of them
     int splits, runs;                // CUDA cores: runs of tokens of dWg and dWu; of dbg and dbu
@@ -178,12 +180,26 @@ struct GluPlan {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-bool on_tensor_cores(int D, na_dtype dtype) { return dtype != NA_FP32 && D % 8 == 0; }
+// Channels that the tensor cores work on: D, or for 2-byte rows that are not whole 16-byte chunks D with zeros up to the next chunk,
+// in copies, from 5e7 operations on (bf16, forward and gradients, FMA units -> copies: 100 x 499 x 501 25 -> 24 us, 97 -> 55; 300 x
+// 999 x 1001 145 -> 27, 455 -> 59; 2000 x 1001 x 3001 543 -> 50, 1876 -> 138).  0: none, the product runs on FMA units.
+int tensor_width(long long T, int D, int F, na_dtype dtype) {
+    if (dtype == NA_FP32) return 0;
+    if (D % 8 == 0) return D;
+    return 4.0 * T * D * F >= 5e7 ? (D + 7) / 8 * 8 : 0;
+}
 
 GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
     GluPlan n{};
     const int es = elem_bytes(dtype), chunk = 16 / es;
-    n.tensor = on_tensor_cores(D, dtype);
+    const int width = tensor_width(T, D, F, dtype);
+    n.tensor = width > 0;
+    n.width = n.tensor ? width : D;
+    if (n.width != D) {
+        n.tokens_copy = up256(static_cast<size_t>(T) * n.width * es);
+        n.weights_copy = up256(static_cast<size_t>(F) * n.width * es);
+    }
+    D = n.width;
     n.pitch = (static_cast<long long>(F) + chunk - 1) / chunk * chunk;
     n.array = up256(static_cast<size_t>(T) * n.pitch * es);
     size_t floats = 0;
@@ -211,10 +227,49 @@ GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
     return n;
 }
 
+size_t glu_workspace(const GluPlan& n) { return 2 * n.array + n.partial + 2 * n.tokens_copy + 4 * n.weights_copy; }
+
 na_status glu_sizes(long long rows, int D, int F, na_dtype dtype) {
     if (rows < 1 || D < 1 || F < 1 || !known_dtype(dtype)) return NA_ERR_INVALID_ARG;
     if (D > kGluMaxWidth || F > kGluMaxWidth || rows > kGluMaxRows || rows > (1LL << 40) / D || rows > (1LL << 40) / F) return NA_ERR_UNSUPPORTED;
     return NA_OK;
+}
+
+// Rows of D 2-byte elements to rows of W, a multiple of 8, with zeros past D, or back.  A thread has a 16-byte chunk of the W.
+template <bool WIDEN>
+__global__ void __launch_bounds__(256) glu_copy_kernel(const GluCopies c) {
+    const int i = blockIdx.y, per = c.W / 8;
+    const long long chunks = c.rows[i] * per;
+    for (long long k = blockIdx.x * 256LL + threadIdx.x; k < chunks; k += gridDim.x * 256LL) {
+        const long long row = k / per;
+        const int col = static_cast<int>(k - row * per) * 8;
+        if constexpr (WIDEN) {
+            const uint16_t* from = static_cast<const uint16_t*>(c.from[i]) + row * c.D;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int a = col + 2 * e;
+                w[e] = (a < c.D ? from[a] : 0u) | (a + 1 < c.D ? static_cast<uint32_t>(from[a + 1]) << 16 : 0u);
+            }
+            static_cast<uint4*>(c.to[i])[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            const uint4 v = static_cast<const uint4*>(c.from[i])[k];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint16_t* to = static_cast<uint16_t*>(c.to[i]) + row * c.D;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e < c.D) to[col + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+        }
+    }
+}
+
+na_status launch_copies(const GluCopies& c, bool widen, cudaStream_t s) {
+    const long long most = std::max(c.rows[0], std::max(c.rows[1], c.rows[2])) * (c.W / 8);
+    if (most == 0) return NA_OK;
+    const dim3 grid(static_cast<unsigned>(std::min((most + 255) / 256, 8LL * kSms)), 3);
+    if (widen) glu_copy_kernel<true><<<grid, 256, 0, s>>>(c);
+    else glu_copy_kernel<false><<<grid, 256, 0, s>>>(c);
+    return launch_result();
 }
 
 bool known_act(na_glu_act a) { return a >= NA_ACT_SILU && a <= NA_ACT_SIGMOID; }
@@ -347,14 +402,28 @@ na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, 
     p.F = F;
     p.act = act;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return on_tensor_cores(D, dtype) ? launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s) : fma_product(p, kForward, dtype, s);
+    const int width = tensor_width(rows, D, F, dtype);
+    if (width == 0) return fma_product(p, kForward, dtype, s);
+    if (width == D) return launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s);
+    const size_t tokens = up256(static_cast<size_t>(rows) * width * es), weights = up256(static_cast<size_t>(F) * width * es);
+    void* ws = nullptr;
+    if (cudaMallocAsync(&ws, tokens + 2 * weights, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+    char* at = static_cast<char*>(ws);
+    const GluCopies copies{{x, wg, wu}, {at, at + tokens, at + tokens + weights}, {rows, F, F}, D, width};
+    st = launch_copies(copies, true, s);
+    p.x = copies.to[0];
+    p.wg = copies.to[1];
+    p.wu = copies.to[2];
+    p.D = width;
+    if (st == NA_OK) st = launch_tensor(p, kForward, plan_tiles(kForward, rows, width, F), dtype, s);
+    if (cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
+    return st;
 }
 
 size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype) {
     using namespace na;
     if (glu_sizes(rows, D, F, dtype) != NA_OK) return 0;
-    const GluPlan n = plan_glu(rows, D, F, dtype);
-    return 2 * n.array + n.partial;
+    return glu_workspace(plan_glu(rows, D, F, dtype));
 }
 
 na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* dx,
@@ -379,7 +448,7 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
             if (spans_overlap(out[i], out[k])) return NA_ERR_INVALID_ARG;
     }
     const GluPlan n = plan_glu(rows, D, F, dtype);
-    const size_t need = 2 * n.array + n.partial;
+    const size_t need = glu_workspace(n);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = workspace;
     if (ws) {
@@ -408,25 +477,41 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n.array);
     p.T = rows;
     p.pitch = n.pitch;
-    p.D = D;
+    p.D = n.width;
     p.F = F;
     p.act = act;
     p.splits = n.splits;
     p.run = n.run;
-    const long long size = static_cast<long long>(F) * D;
-    st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, D, F), dtype, s) : fma_product(p, kSlopes, dtype, s);
+    const bool copied = n.width != D;
+    if (copied) {   // the products' own tensors, in whole chunks
+        char* at = static_cast<char*>(ws) + 2 * n.array + n.partial;
+        const GluCopies in_copies{{x, wg, wu}, {at, at + n.tokens_copy, at + n.tokens_copy + n.weights_copy}, {rows, F, F}, D, n.width};
+        st = launch_copies(in_copies, true, s);
+        p.x = in_copies.to[0];
+        p.wg = in_copies.to[1];
+        p.wu = in_copies.to[2];
+        at += n.tokens_copy + 2 * n.weights_copy;
+        if (dx) p.dx = at;
+        if (dwg) {
+            p.dwg = at + n.tokens_copy;
+            p.dwu = at + n.tokens_copy + n.weights_copy;
+        }
+    }
+    const long long size = static_cast<long long>(F) * n.width, tokens_size = rows * n.width;
+    if (st == NA_OK) st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, n.width, F), dtype, s) : fma_product(p, kSlopes, dtype, s);
     const bool both = dx && dwg && n.tensor && n.tokens.workers;
     if (st == NA_OK && both) st = launch_tensor(p, kBoth, n.tokens, dtype, s, &n.weights);
     if (st == NA_OK && dx) {
         if (!both) st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, dtype, s);
         if (st == NA_OK && n.tensor && n.tokens.splits > 1)
-            st = sum_runs(p.partial, n.tokens.splits, rows * D, rows * D, dx, nullptr, dtype, s);
+            st = sum_runs(p.partial, n.tokens.splits, tokens_size, tokens_size, p.dx, nullptr, dtype, s);
     }
     if (st == NA_OK && dwg) {
         if (!both) st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, dtype, s);
         const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.splits;
-        if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, dwg, dwu, dtype, s);
+        if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, p.dwg, p.dwu, dtype, s);
     }
+    if (st == NA_OK && copied) st = launch_copies({{p.dx, p.dwg, p.dwu}, {dx, dwg, dwu}, {dx ? rows : 0, dwg ? F : 0, dwg ? F : 0}, D, n.width}, false, s);
     if (st == NA_OK && (dbg || dbu)) st = column_sums(p, n, p.partial, dbg, dbu, dtype, s);
     if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
     return st;

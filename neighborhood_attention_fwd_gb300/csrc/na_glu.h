@@ -126,30 +126,27 @@ __device__ __forceinline__ void activate(float v, float& a, float& slope) {
     }
 }
 
-// act and its derivative of eight values, with the approximations.  The sigmoid that three of the activations are made of takes one
-// reciprocal for two values, 1 / p = q / (p q): reciprocals run at half the rate of exponentials and would be half of the time.
-// p q stays below 2^126 while both exponents are at most 62 (values above -43); chunks with others take one each.
+// act and its derivative of eight values, with the approximations, in pairs of fp32 operations.  Each value has a reciprocal of
+// its own: one for two, 1 / p = q / (p q), is no faster here (its exponentials and products are not what bounds the kernels), and
+// a value's bits would depend on its neighbour's.
 template <int ACT>
 __device__ __forceinline__ void activate8(const float (&v)[8], float (&a)[8], float (&slope)[8]) {
+    using namespace dev;
+    constexpr float L = 1.4426950408889634f, K = 2.f * 0.79788456080286536f;
+    const uint64_t one = pack2(1.f, 1.f);
     if constexpr (ACT == NA_ACT_RELU) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) activate<ACT, true>(v[k], a[k], slope[k]);
-        return;
-    }
-    if constexpr (ACT == NA_ACT_GELU) {
+    } else if constexpr (ACT == NA_ACT_GELU) {
         // Phi(-|v|) = exp(-v^2 / 2) t Q(t) / 2, t = 1 / (1 + p |v| / sqrt 2): the form of Abramowitz and Stegun 7.1.26, with
         // p = 0.52 and a Q of degree 6 fitted to the relative error of erfc over [0, 14] (2^-19.6; 2^-17 with the roundings).
-        using namespace dev;
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             const uint64_t x = pack2(v[k], v[k + 1]);
-            float q0, q1, z0, z1, e0, e1, phi0, phi1;
-            split2(mul2(mul2(x, x), pack2(-0.72134752044448170f, -0.72134752044448170f)), q0, q1);   // log2 of exp(-v^2 / 2)
-            e0 = fast_exp2(q0);
-            e1 = fast_exp2(q1);
-            split2(fma2(pack2(fminf(fabsf(v[k]), 100.f), fminf(fabsf(v[k + 1]), 100.f)), pack2(0.36769554f, 0.36769554f), pack2(1.f, 1.f)), z0, z1);
-            const float r = inverse<true>(z0 * z1);
-            const uint64_t t = mul2(pack2(r, r), pack2(z1, z0)), e = pack2(e0, e1);
+            float q0, q1, z0, z1, phi0, phi1;
+            split2(mul2(mul2(x, x), pack2(-0.5f * L, -0.5f * L)), q0, q1);   // log2 of exp(-v^2 / 2)
+            split2(fma2(pack2(fminf(fabsf(v[k]), 100.f), fminf(fabsf(v[k + 1]), 100.f)), pack2(0.36769554f, 0.36769554f), one), z0, z1);
+            const uint64_t t = pack2(inverse<true>(z0), inverse<true>(z1)), e = pack2(fast_exp2(q0), fast_exp2(q1));
             auto coefficient = [](float c) { return pack2(0.5f * c, 0.5f * c); };
             uint64_t q = fma2(t, coefficient(0.09600309f), coefficient(-0.3451418f));
             q = fma2(t, q, coefficient(0.3083583f));
@@ -158,58 +155,45 @@ __device__ __forceinline__ void activate8(const float (&v)[8], float (&a)[8], fl
             q = fma2(t, q, coefficient(0.29128924f));
             q = fma2(t, q, coefficient(0.29346788f));
             split2(mul2(mul2(e, t), q), phi0, phi1);
-            phi0 = v[k] < 0.f ? phi0 : 1.f - phi0;
-            phi1 = v[k + 1] < 0.f ? phi1 : 1.f - phi1;
-            const uint64_t phi = pack2(phi0, phi1);
+            const uint64_t phi = pack2(v[k] < 0.f ? phi0 : 1.f - phi0, v[k + 1] < 0.f ? phi1 : 1.f - phi1);
             split2(mul2(x, phi), a[k], a[k + 1]);
             split2(fma2(mul2(x, e), pack2(0.39894228f, 0.39894228f), phi), slope[k], slope[k + 1]);
         }
-        return;
-    }
-    // exponents: the sigmoid's argument is -t / log2 e
-    constexpr float L = 1.4426950408889634f, K = 2.f * 0.79788456080286536f;
-    float t[8], top = 0.f;
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-        using namespace dev;
-        if constexpr (ACT == NA_ACT_GELU_TANH) {
+        for (int k = 0; k < 8; k += 2) {
             const uint64_t x = pack2(v[k], v[k + 1]);
-            float q0, q1;
-            split2(mul2(x, x), q0, q1);
-            const uint64_t q = pack2(fminf(q0, 10000.f), fminf(q1, 10000.f));   // beyond |v| = 100 it is 0 or 1
-            split2(mul2(x, fma2(q, pack2(-L * K * 0.044715f, -L * K * 0.044715f), pack2(-L * K, -L * K))), t[k], t[k + 1]);
-        } else {
-            split2(mul2(pack2(v[k], v[k + 1]), pack2(-L, -L)), t[k], t[k + 1]);
-        }
-        top = fmaxf(top, fmaxf(t[k], t[k + 1]));
-    }
-    if (__any_sync(0xffffffffu, !(top <= 62.f))) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) activate<ACT, true>(v[k], a[k], slope[k]);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-        using namespace dev;
-        const float e0 = fast_exp2(t[k]), e1 = fast_exp2(t[k + 1]);
-        const uint64_t e = pack2(e0, e1), one = pack2(1.f, 1.f), p = add2(e, one);
-        float p0, p1;
-        split2(p, p0, p1);
-        const float r = inverse<true>(p0 * p1);
-        const uint64_t y = mul2(pack2(r, r), pack2(p1, p0)), x = pack2(v[k], v[k + 1]);
-        if constexpr (ACT == NA_ACT_SIGMOID) {
-            // y (1 - y) without cancellation: 1 - y = e y
-            split2(y, a[k], a[k + 1]);
-            split2(mul2(mul2(y, y), e), slope[k], slope[k + 1]);
-        } else {
-            const uint64_t s = mul2(x, y), rest = mul2(e, y);   // 1 - y = e y
-            split2(s, a[k], a[k + 1]);
+            uint64_t q = 0, t;   // v^2; the exponent of exp(-..) of the sigmoid's argument
             if constexpr (ACT == NA_ACT_GELU_TANH) {
-                const uint64_t q = mul2(x, x);   // |v| < 43 here, or the rest is zero
-                const uint64_t rise = fma2(q, pack2(3.f * K * 0.044715f, 3.f * K * 0.044715f), pack2(K, K));
-                split2(fma2(mul2(s, rest), rise, y), slope[k], slope[k + 1]);
+                float q0, q1;
+                split2(mul2(x, x), q0, q1);
+                q = pack2(fminf(q0, 10000.f), fminf(q1, 10000.f));   // beyond |v| = 100 the sigmoid is 0 or 1
+                t = mul2(x, fma2(q, pack2(-L * K * 0.044715f, -L * K * 0.044715f), pack2(-L * K, -L * K)));
             } else {
-                split2(fma2(s, rest, y), slope[k], slope[k + 1]);
+                t = mul2(x, pack2(-L, -L));
+            }
+            float t0, t1, p0, p1;
+            split2(t, t0, t1);
+            const float e0 = fast_exp2(t0), e1 = fast_exp2(t1);
+            split2(add2(pack2(e0, e1), one), p0, p1);
+            const float y0 = inverse<true>(p0), y1 = inverse<true>(p1);
+            const uint64_t y = pack2(y0, y1), rest = fma2(y, pack2(-1.f, -1.f), one);
+            if constexpr (ACT == NA_ACT_SIGMOID) {
+                a[k] = y0;
+                a[k + 1] = y1;
+                float r0, r1;   // 1 - y without cancellation on either side
+                split2(rest, r0, r1);
+                slope[k] = y0 * (v[k] > 0.f ? e0 * y0 : r0);
+                slope[k + 1] = y1 * (v[k + 1] > 0.f ? e1 * y1 : r1);
+            } else {
+                const uint64_t s = mul2(x, y);
+                split2(s, a[k], a[k + 1]);
+                if constexpr (ACT == NA_ACT_GELU_TANH) {
+                    const uint64_t rise = fma2(q, pack2(3.f * K * 0.044715f, 3.f * K * 0.044715f), pack2(K, K));
+                    split2(fma2(mul2(s, rest), rise, y), slope[k], slope[k + 1]);
+                } else {
+                    split2(fma2(s, rest, y), slope[k], slope[k + 1]);
+                }
             }
         }
     }
@@ -235,6 +219,13 @@ inline unsigned up(long long n, long long by) { return static_cast<unsigned>((n 
 
 constexpr int kTile = 128;   // of the CUDA-core kernels
 
+// Up to three matrices of 2-byte elements, rows of D elements in one place and of W >= D, whole chunks, in the other.
+struct GluCopies {
+    const void* from[3];
+    void* to[3];
+    long long rows[3];   // 0: none
+    int D, W;
+};
 // Launchers of the CUDA-core kernels, of the sums over runs (out0 the first `cut` of n elements, out1 the others; either may be
 // null) and of the column sums of dg and du over runs of `run` tokens, to partial[run][2][F] (na_glu_fma.cuh).
 template <typename T>

@@ -454,10 +454,9 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 }
                 if (biased) {
                     __syncwarp();
-                    if (f0 + lane < p.F) {
-                        bias[lane] = p.bg ? widen<T>(p.bg, f0 + lane) : 0.f;
-                        bias[32 + lane] = p.bu ? widen<T>(p.bu, f0 + lane) : 0.f;
-                    }
+                    const bool in = f0 + lane < p.F;
+                    bias[lane] = in && p.bg ? widen<T>(p.bg, f0 + lane) : 0.f;
+                    bias[32 + lane] = in && p.bu ? widen<T>(p.bu, f0 + lane) : 0.f;
                 }
                 if (lane == 0) tma_store_wait_read();   // the results before have left the staging
                 __syncwarp();

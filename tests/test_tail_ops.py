@@ -263,6 +263,7 @@ GLU = [
     ("bf16", 40000, 264, 88, "sigmoid", False),
     # rows that are not whole 16-byte chunks
     ("bf16", 1, 1, 1, "silu", True), ("bf16", 37, 99, 50, "silu", True), ("fp16", 200, 130, 131, "gelu", False),
+    ("bf16", 1300, 257, 700, "silu", True), ("fp16", 900, 1001, 260, "gelu", True), ("bf16", 3, 9001, 8000, "relu", False),
 ]
 
 
@@ -385,6 +386,38 @@ def test_glu_rows_do_not_depend_on_their_neighbours(dtype, cuda_lib):
     out = torch.full((T + 64, F), 3.0, dtype=TYPES[dtype], device="cuda")
     na.na_glu(pad[32:32 + T], wg, wu, out[32:32 + T])
     assert torch.equal(out[32:32 + T], ref) and (out[:32] == 3).all() and (out[32 + T:] == 3).all()
+    status_ok(na)
+
+
+@pytest.mark.parametrize("T", [3, 200, 5200])
+@pytest.mark.parametrize("how", ot.ACTS)
+def test_glu_columns_do_not_depend_on_their_neighbours(how, T, cuda_lib):
+    """Bit for bit: weights and biases that are not finite, or far from zero, change their own column alone."""
+    na = cuda_lib
+    D, F = 72, 333
+    x, wg, wu, bg, bu, dh = (dev(a) for a in glu_inputs("bf16", T, D, F, True))
+    ill = [v.clone() for v in (wg, wu, bg, bu)]
+    ill[0][20, 3], ill[0][37, 0], ill[1][50, 9], ill[2][99], ill[3][130] = float("nan"), float("inf"), float("nan"), float("nan"), float("inf")
+    ill[2][201], ill[2][300], ill[2][301], ill[2][332] = -60.0, -1e30, 1e30, float("nan")
+    cols = torch.ones(F, dtype=torch.bool, device="cuda")
+    cols[[20, 37, 50, 99, 130, 201, 300, 301, 332]] = False
+
+    def run(wg, wu, bg, bu):
+        h, g = torch.empty(T, F, dtype=x.dtype, device="cuda"), [torch.empty_like(v) for v in (wg, wu, bg, bu)]
+        na.na_glu(x, wg, wu, h, bg, bu, act=how)
+        na.na_glu_bwd(dh, x, wg, wu, None, g[0], g[1], bg, bu, g[2], g[3], act=how)
+        return [h.T] + g
+
+    good, bad = run(wg, wu, bg, bu), run(*ill)
+    for a, b in zip(good, bad):
+        assert torch.isfinite(a).all() and torch.equal(a[cols], b[cols])
+    # a far bias gives its own value: act(-60) and its limit
+    G = f64(x) @ f64(wg[201]) - 60.0
+    ref = ot.act(G, how) * (f64(x) @ f64(wu[201]) + f64(bu[201]))
+    slack = 2.0 ** -14 * np.abs(ref) + 2.0 ** -50 * 60 * (how in ("gelu", "gelu_tanh", "silu", "sigmoid"))
+    if how in ("silu", "sigmoid"):   # the only ones that are not zero there; g is off by its sum's error, and so is its exponential
+        slack = slack + np.abs(ref) * 4 * D * E * (60 + (np.abs(f64(x)) @ np.abs(f64(wg[201]))))
+    close("far", bad[0][201], ref, slack, torch.bfloat16)
     status_ok(na)
 
 
