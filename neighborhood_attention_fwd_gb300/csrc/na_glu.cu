@@ -24,7 +24,7 @@ constexpr int kGluMaxWidth = 1 << 20;              // of D and F
 constexpr long long kGluMaxRows = (1LL << 31) - 1;
 
 // How a product is cut on tensor cores.
-struct TilePlan {
+struct GluTiles {
     bool pairs;              // tiles of 256 x 256 on pairs of blocks, else of 128 x 128
     int few;                 // 16, 64, 128: the kernel of few tokens
     unsigned rows, cols, steps, run, splits, ways;
@@ -45,7 +45,7 @@ constexpr long long kPairStay = 230, kOneStay = 160;
 constexpr unsigned kMostSteps = 384;
 
 // Cuts the steps into `ways` parts side by side of at most kMostSteps each, and turns of them; false if a part would be empty.
-bool cut_steps(TilePlan& t, unsigned ways) {
+bool cut_steps(GluTiles& t, unsigned ways) {
     const unsigned most = up(t.steps, ways), least = t.steps / ways;   // steps of a way
     if (least == 0) return false;
     for (unsigned turns = up(most, kMostSteps); turns <= most; ++turns) {
@@ -58,9 +58,9 @@ bool cut_steps(TilePlan& t, unsigned ways) {
     return false;
 }
 
-TilePlan plan_tiles(Product which, long long T, int D, int F) {
+GluTiles plan_tiles(Product which, long long T, int D, int F) {
     const bool pair = which == kForward || which == kSlopes;
-    TilePlan best{};
+    GluTiles best{};
     if (pair && T <= 128) {
         // As many blocks to a tile's sum as make it shortest, two blocks to a multiprocessor: a step of 64 takes about 0.12 us, a
         // block 8 steps' time to start and end, a cluster of 2 another 7, of 4 another 24 (1 token, 2736 x 1024: 5.7, 5.5 and 7.1 us;
@@ -86,7 +86,7 @@ TilePlan plan_tiles(Product which, long long T, int D, int F) {
     double least = 0;
     for (int pairs = 0; pairs < 2; ++pairs) {
         const int m = pairs ? 256 : 128, slots = pairs ? kSms / 2 : kSms;
-        TilePlan t{};
+        GluTiles t{};
         t.pairs = pairs != 0;
         t.splits = 1;
         if (pair) {
@@ -137,12 +137,12 @@ TilePlan plan_tiles(Product which, long long T, int D, int F) {
 
 // Tokens and weights in one launch where that is estimated shorter: of the splits that leave the tokens half of the pairs of blocks
 // at least, those with which both sides end soonest.
-void plan_both(long long T, int D, int F, TilePlan& tokens, TilePlan& weights) {
+void plan_both(long long T, int D, int F, GluTiles& tokens, GluTiles& weights) {
     const unsigned slots = kSms / 2, steps_t = 2 * up(F, 64), steps_w = up(T, 64);
     const unsigned tiles_w = 2 * up(F, 256) * up(D, 256);
     if (4.0 * T * F <= kFitsL2 || tiles_w > slots / 2) return;
     const long long tiles_t = static_cast<long long>(up(T, 256)) * up(D, 256);
-    TilePlan t{}, w{};
+    GluTiles t{}, w{};
     t.pairs = w.pairs = true;
     t.rows = up(T, 256);
     w.rows = 2 * up(F, 256);
@@ -172,11 +172,49 @@ struct GluPlan {
     size_t tokens_copy, weights_copy;   // bytes of x or dx, of Wg, Wu, dWg or dWu in that width; 0 where it is D
     long long pitch;                 // of a row of dg and du
     size_t array;                    // bytes of one of them
-    int splits, runs;                // CUDA cores: runs of tokens of dWg and dWu; of dbg and dbu
-    long long run, column_run;
-    TilePlan tokens, weights;        // tensor cores
+    FmaTile tokens_fma, weights_fma; // CUDA cores
+    int runs;                        // of tokens, of dbg and dbu
+    long long column_run;
+    GluTiles tokens, weights;        // tensor cores
     size_t partial;                  // bytes
 };
+
+// Tiles and splits of a product on CUDA cores.  Cycles of a multiprocessor for a step of a tile: 128 x 128 are bound by FMA, the
+// others by shared memory; one block alone takes about 60 for the latency of its loads.  The summed axis is cut where the
+// tiles leave multiprocessors idle, and to at most 8192 products in one sum.
+FmaTile plan_fma(Product which, long long T, int D, int F) {
+    const bool pair = which == kForward || which == kSlopes;
+    const long long rows = which == kWeights ? F : T, cols = pair ? 2LL * F : D, depth = pair ? D : (which == kWeights ? T : 2LL * up(F, 16) * 16);
+    FmaTile best{};
+    double least = 0;
+    for (int r : {128, 32})
+        for (int c : {128, 32}) {
+            const double cycles = r == 128 ? (c == 128 ? 128 : 40) : (c == 128 ? 48 : 36);
+            const long long tiles = static_cast<long long>(up(rows, r)) * up(cols, c) * (which == kWeights ? 2 : 1);
+            if (up(cols, c) > 65535) continue;   // a launch's columns
+            const long long fewest = pair ? 1 : (depth + 8191) / 8192;
+            const long long most = pair ? 1 : std::max(fewest, std::min({depth / 128, (2 * kSms + tiles - 1) / tiles, 1024LL}));
+            for (long long splits : {fewest, (fewest + most) / 2, most}) {
+                if (splits < 1) continue;
+                const long long blocks = tiles * splits, waves = (blocks + kSms - 1) / kSms;
+                double time = std::max(waves * cycles, 60.0) * (static_cast<double>(depth) / splits + 32) / 1.9;   // nanoseconds
+                if (splits > 1) time += 3000 + 8.0 * rows * D * (which == kWeights ? 2 : 1) * splits / 5000;
+                if (best.rows == 0 || time < least) {
+                    least = time;
+                    best = {r, c, static_cast<int>(splits), 0};
+                }
+            }
+        }
+    if (which == kWeights) {
+        best.run = ((T + best.splits - 1) / best.splits + 15) / 16 * 16;
+        best.splits = static_cast<int>((T + best.run - 1) / best.run);
+    } else if (which == kTokens) {
+        const long long pieces = 2LL * up(F, 16);
+        best.run = (pieces + best.splits - 1) / best.splits;
+        best.splits = static_cast<int>((pieces + best.run - 1) / best.run);
+    }
+    return best;
+}
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -210,13 +248,10 @@ GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
         if (n.tokens.splits > 1) floats = static_cast<size_t>(n.tokens.splits) * T * D;
         if (n.weights.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights.splits) * 2 * F * D);
     } else {
-        // runs of tokens: enough blocks to fill the GPU twice, at least 256 tokens each, at most 8192 in one sum
-        const long long tiles = 2LL * ((F + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
-        long long splits = std::max((T + 8191) / 8192, std::min((T + 255) / 256, (4 * kSms + tiles - 1) / tiles));
-        splits = std::min(splits, 1024LL);
-        n.run = ((T + splits - 1) / splits + 63) / 64 * 64;
-        n.splits = static_cast<int>((T + n.run - 1) / n.run);
-        if (n.splits > 1) floats = static_cast<size_t>(n.splits) * 2 * F * D;
+        n.tokens_fma = plan_fma(kTokens, T, D, F);
+        n.weights_fma = plan_fma(kWeights, T, D, F);
+        if (n.tokens_fma.splits > 1) floats = static_cast<size_t>(n.tokens_fma.splits) * T * D;
+        if (n.weights_fma.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights_fma.splits) * 2 * F * D);
     }
     // column sums: four blocks a multiprocessor, at least 64 tokens each, at most 8192 in one sum
     const long long columns = 2LL * up(F, 32 * chunk);
@@ -276,7 +311,7 @@ bool known_act(na_glu_act a) { return a >= NA_ACT_SILU && a <= NA_ACT_SIGMOID; }
 
 // A product on tensor cores: its tensor maps, boxes of 64 (or 32) elements by as many rows as one copy brings (na_glu_tc.cuh).
 // n: its plan, of kBoth the tokens'; w: of kBoth the weights'.
-na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na_dtype dtype, cudaStream_t s, const TilePlan* w = nullptr) {
+na_status launch_tensor(const GluParams& p, Product which, const GluTiles& n, na_dtype dtype, cudaStream_t s, const GluTiles* w = nullptr) {
     GluTcParams q{};
     const bool pair = which == kForward || which == kSlopes;
     const uint64_t D = p.D, F = p.F, T = p.T, pitch = 2 * static_cast<uint64_t>(p.pitch);
@@ -296,6 +331,7 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
             map(q.b[3], p.wu, D, F, 2 * D, n.last_nf);
             if (which == kSlopes) {
                 if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32, 32);
+                else map(q.in, p.dg, F, T, pitch, 32, 32);
                 map(q.out[0], p.dg, F, T, pitch, 32, 32);
                 map(q.out[1], p.du, F, T, pitch, 32, 32);
             } else if (q.wide) {
@@ -318,7 +354,7 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
             map(q.b[1], p.wu, D, F, 2 * D, 64);
         }
         if (which != kTokens) map(q.b[2], p.x, D, T, 2 * D, 64);
-        const TilePlan& weights = w ? *w : n;
+        const GluTiles& weights = w ? *w : n;
         q.job[0] = {n.rows, n.cols, n.splits, n.ways, n.run, n.steps};
         q.job[1] = {weights.rows, weights.cols, weights.splits, weights.ways, weights.run, weights.steps};
         q.token_workers = n.workers;
@@ -355,10 +391,12 @@ na_status launch_tensor(const GluParams& p, Product which, const TilePlan& n, na
     }
 }
 
-na_status fma_product(const GluParams& p, Product which, na_dtype dtype, cudaStream_t s) {
-    if (dtype == NA_BF16) return launch_fma<__nv_bfloat16>(p, which, s);
-    if (dtype == NA_FP16) return launch_fma<__half>(p, which, s);
-    return launch_fma<float>(p, which, s);
+na_status fma_product(GluParams p, Product which, const FmaTile& tile, na_dtype dtype, cudaStream_t s) {
+    p.splits = tile.splits;
+    p.run = tile.run;
+    if (dtype == NA_BF16) return launch_fma<__nv_bfloat16>(p, which, tile, s);
+    if (dtype == NA_FP16) return launch_fma<__half>(p, which, tile, s);
+    return launch_fma<float>(p, which, tile, s);
 }
 
 na_status sum_runs(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, na_dtype dtype, cudaStream_t s) {
@@ -403,7 +441,7 @@ na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, 
     p.act = act;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int width = tensor_width(rows, D, F, dtype);
-    if (width == 0) return fma_product(p, kForward, dtype, s);
+    if (width == 0) return fma_product(p, kForward, plan_fma(kForward, rows, D, F), dtype, s);
     if (width == D) return launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s);
     const size_t tokens = up256(static_cast<size_t>(rows) * width * es), weights = up256(static_cast<size_t>(F) * width * es);
     void* ws = nullptr;
@@ -480,8 +518,6 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.D = n.width;
     p.F = F;
     p.act = act;
-    p.splits = n.splits;
-    p.run = n.run;
     const bool copied = n.width != D;
     if (copied) {   // the products' own tensors, in whole chunks
         char* at = static_cast<char*>(ws) + 2 * n.array + n.partial;
@@ -498,17 +534,25 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
         }
     }
     const long long size = static_cast<long long>(F) * n.width, tokens_size = rows * n.width;
-    if (st == NA_OK) st = n.tensor ? launch_tensor(p, kSlopes, plan_tiles(kSlopes, rows, n.width, F), dtype, s) : fma_product(p, kSlopes, dtype, s);
+    if (n.tensor) {
+        const GluTiles slopes = plan_tiles(kSlopes, rows, n.width, F);
+        // rows of dh that are not whole chunks go to dg's place first
+        if (st == NA_OK && !slopes.few && F % 8 != 0) st = launch_copies({{dh, nullptr, nullptr}, {p.dg, nullptr, nullptr}, {rows, 0, 0}, F, static_cast<int>(n.pitch)}, true, s);
+        if (st == NA_OK) st = launch_tensor(p, kSlopes, slopes, dtype, s);
+    } else {
+        st = fma_product(p, kSlopes, plan_fma(kSlopes, rows, D, F), dtype, s);
+    }
     const bool both = dx && dwg && n.tensor && n.tokens.workers;
     if (st == NA_OK && both) st = launch_tensor(p, kBoth, n.tokens, dtype, s, &n.weights);
     if (st == NA_OK && dx) {
-        if (!both) st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, dtype, s);
-        if (st == NA_OK && n.tensor && n.tokens.splits > 1)
-            st = sum_runs(p.partial, n.tokens.splits, tokens_size, tokens_size, p.dx, nullptr, dtype, s);
+        if (!both) st = n.tensor ? launch_tensor(p, kTokens, n.tokens, dtype, s) : fma_product(p, kTokens, n.tokens_fma, dtype, s);
+        const int splits = n.tensor ? static_cast<int>(n.tokens.splits) : n.tokens_fma.splits;
+        if (st == NA_OK && splits > 1)
+            st = sum_runs(p.partial, splits, tokens_size, tokens_size, p.dx, nullptr, dtype, s);
     }
     if (st == NA_OK && dwg) {
-        if (!both) st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, dtype, s);
-        const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.splits;
+        if (!both) st = n.tensor ? launch_tensor(p, kWeights, n.weights, dtype, s) : fma_product(p, kWeights, n.weights_fma, dtype, s);
+        const int splits = n.tensor ? static_cast<int>(n.weights.splits) : n.weights_fma.splits;
         if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, p.dwg, p.dwu, dtype, s);
     }
     if (st == NA_OK && copied) st = launch_copies({{p.dx, p.dwg, p.dwu}, {dx, dwg, dwu}, {dx ? rows : 0, dwg ? F : 0, dwg ? F : 0}, D, n.width}, false, s);

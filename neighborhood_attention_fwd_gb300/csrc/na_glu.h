@@ -33,8 +33,8 @@ struct GluParams {
     long long T, pitch;   // pitch: F rounded up to whole 16-byte chunks
     int D, F;
     int act;              // na_glu_act
-    int splits;           // kWeights: runs of tokens summed apart
-    long long run;        // tokens of a run (a multiple of 64)
+    int splits;           // CUDA cores: as FmaTile
+    long long run;
 };
 
 // The tiles of kTokens or kWeights: rows (kWeights: of dWg and dWu together) x cols.  Each is the sum of `splits` parts of the
@@ -47,7 +47,7 @@ struct GluJob {
 struct GluTcParams {
     CUtensorMap a[2];     // rows' operand: x; dg, du
     CUtensorMap b[4];     // columns' operand: Wg, Wu and (forward, slopes) again in boxes for a row's last tile; [2]: x (weights)
-    CUtensorMap in;       // slopes: dh
+    CUtensorMap in;       // slopes: dh (where its rows are not whole chunks a copy in dg's place: a warp's box of it is read before dg is written)
     CUtensorMap out[2];   // forward: h; slopes: dg, du
     const void* bg;
     const void* bu;
@@ -61,7 +61,7 @@ struct GluTcParams {
     float* partial;
     long long pitch;      // of dg and du
     int T, D, F, act;
-    uint32_t wide;        // rows of h and dh are whole 16-byte chunks
+    uint32_t wide;        // rows of h are whole 16-byte chunks
     GluJob job[2];        // tokens, weights
     unsigned token_workers;   // both: pairs of blocks that make dx
     unsigned rows, cols;  // forward, slopes: tiles
@@ -217,7 +217,12 @@ constexpr int kPairRows = WHICH == kForward ? 6 : 5;
 
 inline unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
 
-constexpr int kTile = 128;   // of the CUDA-core kernels
+// How a product is cut on CUDA cores: tiles of 128 or 32 rows and columns, splits of the summed axis (run: kWeights: tokens of one,
+// kTokens: pieces of 16 columns of dg, then du).
+struct FmaTile {
+    int rows, cols, splits;
+    long long run;
+};
 
 // Up to three matrices of 2-byte elements, rows of D elements in one place and of W >= D, whole chunks, in the other.
 struct GluCopies {
@@ -229,7 +234,7 @@ struct GluCopies {
 // Launchers of the CUDA-core kernels, of the sums over runs (out0 the first `cut` of n elements, out1 the others; either may be
 // null) and of the column sums of dg and du over runs of `run` tokens, to partial[run][2][F] (na_glu_fma.cuh).
 template <typename T>
-na_status launch_fma(const GluParams& p, Product which, cudaStream_t s);
+na_status launch_fma(const GluParams& p, Product which, const FmaTile& tile, cudaStream_t s);
 template <typename T>
 na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s);
 template <typename T>

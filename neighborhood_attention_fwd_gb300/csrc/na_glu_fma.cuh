@@ -15,7 +15,7 @@ namespace glu {
 
 using namespace dev;
 
-constexpr int kSmallTile = 32, kDepth = 16, kGluThreads = 256;
+constexpr int kDepth = 16, kGluThreads = 256;
 
 // One operand of a product: rows (of the result's rows or columns) by k.  Element (r, k) is at base[r * ld + k], or with
 // ALONG_ROWS at base[k * ld + r].
@@ -68,39 +68,39 @@ __device__ __forceinline__ void place(float (*sm)[TS + 4], int t, const float (&
     }
 }
 
-// Products on CUDA cores.  A block makes TS x TS elements (kForward, kSlopes: TS rows x TS / 2 columns of g and the same of u);
-// rows along blockIdx.x, columns along blockIdx.y, kWeights: dWg, dWu and the runs of tokens along blockIdx.z.  A thread's
-// elements are two runs of G rows by two of G columns, half a tile apart, so that g and u of an element are its own.
-// TS = 32 is for products of few tiles, where the blocks there are, not their rate, count (253 x 255 from 96, fp32: 18.9 -> 7.7 us).
-template <typename T, int WHICH, int TS>
-__global__ void __launch_bounds__(kGluThreads, TS == kTile ? 2 : 4) glu_fma_kernel(const GluParams p) {
+// Products on CUDA cores.  A block makes TR x TC elements (kForward, kSlopes: TR rows x TC / 2 columns of g and the same of u);
+// rows along blockIdx.x, columns along blockIdx.y; along blockIdx.z the splits of the summed axis, kWeights: of dWg and dWu each.
+// A thread's elements are two runs of GR rows by two of GC columns, half a tile apart, so that g and u of an element are its own.
+template <typename T, int WHICH, int TR, int TC>
+__global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_kernel(const GluParams p) {
     constexpr bool PAIR = WHICH == kForward || WHICH == kSlopes;
     constexpr bool A_ROWS = WHICH == kWeights, B_ROWS = !PAIR;
-    constexpr int G = TS / 32, R = 2 * G, N = TS / 16;
-    __shared__ __align__(16) float sa[2][kDepth][TS + 4], sb[2][kDepth][TS + 4];
+    constexpr int GR = TR / 32, GC = TC / 32, R = 2 * GR, NA = TR / 16, NB = TC / 16;
+    __shared__ __align__(16) float sa[2][kDepth][TR + 4], sb[2][kDepth][TC + 4];
     const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    const long long m0 = static_cast<long long>(blockIdx.x) * TS, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? TS / 2 : TS);
-    const int half = WHICH == kWeights ? blockIdx.z & 1 : 0, split = WHICH == kWeights ? blockIdx.z >> 1 : 0;
+    const long long m0 = static_cast<long long>(blockIdx.x) * TR, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? TC / 2 : TC);
+    const int half = WHICH == kWeights ? blockIdx.z & 1 : 0, split = WHICH == kWeights ? blockIdx.z >> 1 : blockIdx.z;
     const T *x = static_cast<const T*>(p.x), *wg = static_cast<const T*>(p.wg), *wu = static_cast<const T*>(p.wu);
     const T *dg = static_cast<const T*>(p.dg), *du = static_cast<const T*>(p.du);
     const bool wide = p.D % Elem<T>::EPC == 0;
-    // pieces of 16 steps of k; kTokens has two runs of them, dg Wg and du Wu
-    const long long k0 = split * p.run;
+    // pieces of 16 steps of k: of kWeights a run of tokens; kTokens has two runs of columns of them, dg Wg and du Wu, cut together
+    const long long k0 = WHICH == kWeights ? split * p.run : 0;
     const long long depth = PAIR ? p.D : (WHICH == kTokens ? p.F : min(p.run, p.T - k0));
-    const long long pieces = (depth + kDepth - 1) / kDepth, total = WHICH == kTokens ? 2 * pieces : pieces;
+    const long long pieces = (depth + kDepth - 1) / kDepth;
+    const long long first = WHICH == kTokens ? split * p.run : 0, last = WHICH == kTokens ? min(2 * pieces, first + p.run) : pieces;
     // where this thread fetches within a piece
-    const int ra = A_ROWS ? (t & 15) * N : t % TS, ka = A_ROWS ? t >> 4 : t / TS * N;
-    const int rb = B_ROWS ? (t & 15) * N : t % TS, kb = B_ROWS ? t >> 4 : t / TS * N;
-    float fa[N], fb[N];
+    const int ra = A_ROWS ? (t & 15) * NA : t % TR, ka = A_ROWS ? t >> 4 : t / TR * NA;
+    const int rb = B_ROWS ? (t & 15) * NB : t % TC, kb = B_ROWS ? t >> 4 : t / TC * NB;
+    float fa[NA], fb[NB];
     auto load = [&](long long i) {
         const bool second = WHICH == kTokens && i >= pieces;
         const long long k = (second ? i - pieces : i) * kDepth;
         Operand<T> a, b;
         if (PAIR) {
             a = {x, p.D, p.T, p.D, wide};
-            b = {rb < TS / 2 ? wg : wu, p.D, p.F, p.D, wide};
+            b = {rb < TC / 2 ? wg : wu, p.D, p.F, p.D, wide};
             fetch<T, false>(a, m0 + ra, k + ka, fa);
-            fetch<T, false>(b, n0 + (rb & (TS / 2 - 1)), k + kb, fb);
+            fetch<T, false>(b, n0 + (rb & (TC / 2 - 1)), k + kb, fb);
         } else if (WHICH == kTokens) {
             a = {second ? du : dg, p.pitch, p.T, p.F, true};
             b = {second ? wu : wg, p.D, p.D, p.F, wide};
@@ -113,55 +113,58 @@ __global__ void __launch_bounds__(kGluThreads, TS == kTile ? 2 : 4) glu_fma_kern
             fetch<T, true>(b, n0 + rb, k0 + k + kb, fb);
         }
     };
-    uint64_t acc[R][G];   // pairs of columns
+    uint64_t acc[R][GC];   // pairs of columns
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < G; ++j) acc[i][j] = 0;
-    load(0);
-    for (long long i = 0; i < total; ++i) {
+        for (int j = 0; j < GC; ++j) acc[i][j] = 0;
+    load(first);
+    for (long long i = first; i < last; ++i) {
         const int st = static_cast<int>(i & 1);
-        place<A_ROWS, TS>(sa[st], t, fa);
-        place<B_ROWS, TS>(sb[st], t, fb);
+        place<A_ROWS, TR>(sa[st], t, fa);
+        place<B_ROWS, TC>(sb[st], t, fb);
         __syncthreads();   // also: the stage filled next was last read before this barrier
-        if (i + 1 < total) load(i + 1);
+        if (i + 1 < last) load(i + 1);
 #pragma unroll
         for (int k = 0; k < kDepth; ++k) {
             float a[R];
-            uint64_t b[G];
-            if constexpr (G == 4) {
+            uint64_t b[GC];
+            if constexpr (GR == 4) {
                 const float4 a0 = *reinterpret_cast<const float4*>(&sa[st][k][ty * 4]), a1 = *reinterpret_cast<const float4*>(&sa[st][k][64 + ty * 4]);
-                const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][tx * 4]), b1 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][64 + tx * 4]);
                 a[0] = a0.x, a[1] = a0.y, a[2] = a0.z, a[3] = a0.w, a[4] = a1.x, a[5] = a1.y, a[6] = a1.z, a[7] = a1.w;
-                b[0] = b0.x, b[1] = b0.y, b[2] = b1.x, b[3] = b1.y;
             } else {
                 a[0] = sa[st][k][ty], a[1] = sa[st][k][16 + ty];
+            }
+            if constexpr (GC == 4) {
+                const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][tx * 4]), b1 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][64 + tx * 4]);
+                b[0] = b0.x, b[1] = b0.y, b[2] = b1.x, b[3] = b1.y;
+            } else {
                 b[0] = pack2(sb[st][k][tx], sb[st][k][16 + tx]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint64_t aa = pack2(a[r], a[r]);
 #pragma unroll
-                for (int c = 0; c < G; ++c) acc[r][c] = fma2(aa, b[c], acc[r][c]);
+                for (int c = 0; c < GC; ++c) acc[r][c] = fma2(aa, b[c], acc[r][c]);
             }
         }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const long long row = m0 + (r < G ? ty * G + r : TS / 2 + ty * G + r - G);
-        float v[2 * G];   // the first run of columns, then the second
+        const long long row = m0 + (r < GR ? ty * GR + r : TR / 2 + ty * GR + r - GR);
+        float v[2 * GC];   // the first run of columns, then the second
 #pragma unroll
-        for (int c = 0; c < G; ++c) split2(acc[r][c], v[2 * c], v[2 * c + 1]);
+        for (int c = 0; c < GC; ++c) split2(acc[r][c], v[2 * c], v[2 * c + 1]);
         if constexpr (PAIR) {
             if (row >= p.T) continue;
             with_act(p.act, [&](auto tag) {
                 constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-                for (int c = 0; c < G; ++c) {
-                    const long long f = n0 + tx * G + c;
+                for (int c = 0; c < GC; ++c) {
+                    const long long f = n0 + tx * GC + c;
                     if (f >= p.F) break;
                     const float g = v[c] + (p.bg ? Elem<T>::get(static_cast<const T*>(p.bg)[f]) : 0.f);
-                    const float u = v[G + c] + (p.bu ? Elem<T>::get(static_cast<const T*>(p.bu)[f]) : 0.f);
+                    const float u = v[GC + c] + (p.bu ? Elem<T>::get(static_cast<const T*>(p.bu)[f]) : 0.f);
                     float a, slope;
                     activate<ACT, false>(g, a, slope);
                     if constexpr (WHICH == kForward) {
@@ -174,16 +177,17 @@ __global__ void __launch_bounds__(kGluThreads, TS == kTile ? 2 : 4) glu_fma_kern
                 }
             });
         } else {
-            if (row >= (WHICH == kTokens ? p.T : p.F)) continue;
-            const long long size = static_cast<long long>(p.F) * p.D;
+            const long long rows = WHICH == kTokens ? p.T : p.F;
+            if (row >= rows) continue;
+            float* sums = p.partial + (WHICH == kTokens ? static_cast<long long>(split) : 2LL * split + half) * rows * p.D;
+            T* out = static_cast<T*>(WHICH == kTokens ? p.dx : half ? p.dwu : p.dwg);
 #pragma unroll
-            for (int c = 0; c < 2 * G; ++c) {
-                const long long col = n0 + (c < G ? tx * G + c : TS / 2 + tx * G + c - G);
+            for (int c = 0; c < 2 * GC; ++c) {
+                const long long col = n0 + (c < GC ? tx * GC + c : TC / 2 + tx * GC + c - GC);
                 if (col >= p.D) continue;
                 const long long at = row * p.D + col;
-                if (WHICH == kTokens) static_cast<T*>(p.dx)[at] = Elem<T>::put(v[c]);
-                else if (p.splits > 1) p.partial[(2LL * split + half) * size + at] = v[c];
-                else static_cast<T*>(half ? p.dwu : p.dwg)[at] = Elem<T>::put(v[c]);
+                if (p.splits > 1) sums[at] = v[c];
+                else out[at] = Elem<T>::put(v[c]);
             }
         }
     }
@@ -243,28 +247,22 @@ __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* d
     }
 }
 
-template <typename T, int TS>
+template <typename T, int TR, int TC>
 na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
-    const unsigned rows = up(p.T, TS);
+    const unsigned splits = p.splits;
     switch (which) {
-        case kForward: glu_fma_kernel<T, kForward, TS><<<dim3(rows, up(p.F, TS / 2)), kGluThreads, 0, s>>>(p); break;
-        case kSlopes: glu_fma_kernel<T, kSlopes, TS><<<dim3(rows, up(p.F, TS / 2)), kGluThreads, 0, s>>>(p); break;
-        case kTokens: glu_fma_kernel<T, kTokens, TS><<<dim3(rows, up(p.D, TS)), kGluThreads, 0, s>>>(p); break;
-        case kWeights: glu_fma_kernel<T, kWeights, TS><<<dim3(up(p.F, TS), up(p.D, TS), 2 * p.splits), kGluThreads, 0, s>>>(p); break;
+        case kForward: glu_fma_kernel<T, kForward, TR, TC><<<dim3(up(p.T, TR), up(p.F, TC / 2)), kGluThreads, 0, s>>>(p); break;
+        case kSlopes: glu_fma_kernel<T, kSlopes, TR, TC><<<dim3(up(p.T, TR), up(p.F, TC / 2)), kGluThreads, 0, s>>>(p); break;
+        case kTokens: glu_fma_kernel<T, kTokens, TR, TC><<<dim3(up(p.T, TR), up(p.D, TC), splits), kGluThreads, 0, s>>>(p); break;
+        default: glu_fma_kernel<T, kWeights, TR, TC><<<dim3(up(p.F, TR), up(p.D, TC), 2 * splits), kGluThreads, 0, s>>>(p); break;
     }
     return launch_result();
 }
 
-// Small tiles where all of them, at 48 cycles of shared memory a step and multiprocessor, are done before one wave of large ones
-// at 128 cycles of FMA.
 template <typename T>
-na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
-    const bool pair = which == kForward || which == kSlopes;
-    const long long rows = which == kWeights ? p.F : p.T, cols = pair ? 2LL * p.F : p.D, depths = which == kWeights ? 2LL * p.splits : 1;
-    const long long large = static_cast<long long>(up(rows, kTile)) * up(cols, kTile) * depths;
-    const long long small = static_cast<long long>(up(rows, kSmallTile)) * up(cols, kSmallTile) * depths;
-    const bool few = (small + kSms - 1) / kSms * 48 < (large + kSms - 1) / kSms * 128;
-    return few ? launch_fma<T, kSmallTile>(p, which, s) : launch_fma<T, kTile>(p, which, s);
+na_status launch_fma(const GluParams& p, Product which, const FmaTile& tile, cudaStream_t s) {
+    if (tile.rows == 128) return tile.cols == 128 ? launch_fma<T, 128, 128>(p, which, s) : launch_fma<T, 128, 32>(p, which, s);
+    return tile.cols == 128 ? launch_fma<T, 32, 128>(p, which, s) : launch_fma<T, 32, 32>(p, which, s);
 }
 
 template <typename T>

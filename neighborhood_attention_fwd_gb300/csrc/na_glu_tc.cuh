@@ -387,16 +387,23 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 load_box<1>(dh_at, &p.in, smem_u32(&dh_full[e]), col_of(w), row_of(w));
             }
         };
-        // element by element, where rows are not whole chunks
+        // where rows are not whole chunks: two rows at a time, a lane two columns, as a word if rows are whole words
         auto by_elements = [&](int m0, int f0) {
             __syncwarp();
-            uint16_t* out = static_cast<uint16_t*>(p.h);
-            for (int r = lane >> 4; r < 32 && m0 + r < p.T; r += 2) {
-                const int f = f0 + 2 * (lane & 15);
-                const uint32_t w = ld_shared_b32(word_at(staging, r, lane & 15));
+            const int r0 = lane >> 4, c = 2 * (lane & 15), n = min(32, p.T - m0);
+            const bool first = f0 + c < p.F, second = f0 + c + 1 < p.F, words = p.F % 2 == 0;
+            uint16_t* out = static_cast<uint16_t*>(p.h) + static_cast<long long>(m0 + r0) * p.F + f0 + c;
+            const long long step = 2LL * p.F;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (f + j < p.F) out[static_cast<long long>(m0 + r) * p.F + f + j] = static_cast<uint16_t>(w >> (16 * j));
+            for (int r = 0; r < 32; r += 2, out += step) {
+                const uint32_t w = ld_shared_b32(word_at(staging, r + r0, lane & 15));
+                if (r + r0 >= n) continue;
+                if (words) {
+                    if (first) *reinterpret_cast<uint32_t*>(out) = w;
+                } else {
+                    if (first) out[0] = static_cast<uint16_t>(w);
+                    if (second) out[1] = static_cast<uint16_t>(w >> 16);
+                }
             }
             __syncwarp();
         };
@@ -414,8 +421,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
         auto results = [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
             PairWalk<CG> w(p);
-            if constexpr (WHICH == kSlopes)
-                if (p.wide) fetch(w);
+            if constexpr (WHICH == kSlopes) fetch(w);
             for (uint32_t n = 0; w.more(); ++n) {
                 const uint32_t buf = n & 1u;
                 const int m0 = row_of(w), f0 = col_of(w);
@@ -425,22 +431,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 w.next();
                 uint32_t dh[16];
                 if constexpr (WHICH == kSlopes) {
-                    if (!p.wide) {
-                        __syncwarp();
-                        if (there) {
-                            const uint16_t* from = static_cast<const uint16_t*>(p.dh);
-                            for (int r = lane >> 4; r < 32; r += 2) {
-                                const int f = f0 + 2 * (lane & 15);
-                                uint32_t v = 0;
-#pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    if (m0 + r < p.T && f + j < p.F)
-                                        v |= static_cast<uint32_t>(from[static_cast<long long>(m0 + r) * p.F + f + j]) << (16 * j);
-                                st_shared_b32(word_at(dh_at, r, lane & 15), v);
-                            }
-                        }
-                        __syncwarp();
-                    } else if (!__all_sync(0xffffffffu, mbar_wait(&dh_full[e], n & 1u, guard, kSiteQ))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&dh_full[e], n & 1u, guard, kSiteQ))) {
                         settle();
                         break;
                     }
@@ -450,7 +441,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                         dh[4 * j] = v.x, dh[4 * j + 1] = v.y, dh[4 * j + 2] = v.z, dh[4 * j + 3] = v.w;
                     }
                     __syncwarp();
-                    if (p.wide) fetch(w);
+                    fetch(w);
                 }
                 if (biased) {
                     __syncwarp();
