@@ -59,6 +59,9 @@ struct AddPlan {
     size_t ring_bytes;
 };
 
+// Bytes of a tile in a ring: rows that are not whole chunks are copied with up to 15 bytes on both sides.
+__host__ __device__ constexpr uint32_t ring_pitch(uint32_t bytes, bool whole) { return whole ? bytes : (bytes + 30u) & ~15u; }
+
 inline bool lean_forward(const AddParams& p) { return p.norm != NA_NORM_LAYER && p.post != NA_NORM_LAYER && !p.b && !p.post_b; }
 
 template <typename T, bool BWD>

@@ -55,10 +55,11 @@ struct Walk {
     __device__ __forceinline__ const float* at(const float* v, long long step) const { return v ? v + group * step : nullptr; }
 };
 
-// A unit's rows of several arrays through a ring of tiles in shared memory (cp.async.bulk; rows are whole chunks, so a tile is one
-// run of bytes of each array): registers alone do not keep enough loads under way beside the sums.  The unit's first thread
-// fills a stage again once the unit has read it.
-template <int N, bool BLOCK>
+// A unit's rows of several arrays through a ring of tiles in shared memory (cp.async.bulk): registers alone do not keep enough
+// loads under way beside the sums.  A tile is one run of bytes of each array.  Rows that are not whole chunks start anywhere: then
+// the run is widened to 16 bytes on both sides (what it brings of other rows is not read), and the tensor's last bytes, which it
+// must not pass, are copied one by one.  The unit's first thread fills a stage again once the unit has read it.
+template <int N, bool BLOCK, bool WHOLE>
 struct Ring {
     uint64_t* full;                // shared: a barrier a stage
     unsigned char* smem;           // [stage][array][tile]
@@ -73,19 +74,32 @@ struct Ring {
         if (BLOCK) __syncthreads();
         else __syncwarp();
     }
+    __device__ __forceinline__ uint32_t pitch(const AddParams& p) const { return ring_pitch(p.tile * row_bytes, WHOLE); }
     __device__ __forceinline__ void load(const AddParams& p, Walk& w, int stage) {   // the tile at w, if there is one
         w.settle();
         if (!w.parts()) return;
-        const uint32_t bytes = row_bytes * w.rows();
-        unsigned char* to = smem + static_cast<size_t>(stage) * N * p.tile * row_bytes;
+        unsigned char* to = smem + static_cast<size_t>(stage) * N * pitch(p);
+        uint32_t bytes = row_bytes * w.rows();
+        long long start = w.row * row_bytes;
+        if (!WHOLE) {
+            const long long end = start + bytes, stop = min((end + 15) & ~15ll, (p.rows * row_bytes) & ~15ll);
+            start &= ~15ll;
+            for (long long o = stop; o < end; o += 2)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (from[i])
+                        *reinterpret_cast<uint16_t*>(to + static_cast<size_t>(i) * pitch(p) + (o - start)) =
+                            *reinterpret_cast<const uint16_t*>(static_cast<const char*>(from[i]) + o);
+            bytes = static_cast<uint32_t>(stop - start);
+        }
         int arrays = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) arrays += from[i] != nullptr;
         mbar_arrive_expect_tx(&full[stage], arrays * bytes);
-        if (!(p.withhold && blockIdx.x == 0 && issued == 0))   // test hook: the first copy never lands
+        if (!(p.withhold && blockIdx.x == 0 && issued == 0) && (WHOLE || bytes))   // test hook: the first copy never lands
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (from[i]) bulk_load(to + static_cast<size_t>(i) * p.tile * row_bytes, static_cast<const char*>(from[i]) + w.row * row_bytes, bytes, &full[stage]);
+                if (from[i]) bulk_load(to + static_cast<size_t>(i) * pitch(p), static_cast<const char*>(from[i]) + start, bytes, &full[stage]);
         ++issued;
         w.next();
     }
@@ -105,8 +119,9 @@ struct Ring {
     __device__ __forceinline__ void wait(const AddParams& p, int step) {
         if (!mbar_wait(&full[s], parity, WaitGuard{p.err, p.wait_ns}, kSiteNorm) && lost < 0) lost = step;
     }
-    __device__ __forceinline__ const unsigned char* at(const AddParams& p, int array, int row) const {
-        return smem + static_cast<uint32_t>((s * N + array) * p.tile + row) * row_bytes;
+    __device__ __forceinline__ const unsigned char* at(const AddParams& p, const Walk& w, int array, int row) const {   // of the tile at w
+        if (WHOLE) return smem + static_cast<uint32_t>((s * N + array) * p.tile + row) * row_bytes;
+        return smem + (s * N + array) * pitch(p) + (static_cast<uint32_t>(w.row * row_bytes) & 15u) + static_cast<uint32_t>(row) * row_bytes;
     }
     __device__ __forceinline__ void done(const AddParams& p, Walk& ahead) {   // the unit has read the tile
         sync();
@@ -151,9 +166,10 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int team, float (*slot)[1
 
 // A chunk of a row, of the ring or of memory; zeros where it is not there.
 template <typename T, int V, bool RING>
-__device__ __forceinline__ void take(Chunk<T, V>& c, bool there, const unsigned char* tile, const void* base, long long at, int col) {
-    if constexpr (RING) c.raw = *reinterpret_cast<const uint4*>(tile + col * sizeof(T));
-    else c.load(base, at + col);
+__device__ __forceinline__ void take(Chunk<T, V>& c, bool there, const unsigned char* row, const void* from, long long base, int at) {
+    if constexpr (!RING) c.load(from, base + at);
+    else if constexpr (V == 1) c.raw = *reinterpret_cast<const T*>(row + at * sizeof(T));
+    else c.raw = *reinterpret_cast<const uint4*>(row + at * sizeof(T));
     if (!there) c = Chunk<T, V>{};
 }
 
@@ -174,8 +190,8 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
     auto inside = [&](int j) { return (l + p.team * j) * V < p.C; };
     Walk w(p, unit, UNITS), ahead(w);
     const uint32_t row_bytes = p.C * static_cast<uint32_t>(sizeof(T));
-    Ring<2, BLOCK> ring{full[unit], smem + static_cast<size_t>(unit) * kAddStages * 2 * p.tile * row_bytes, {p.y, p.x}, row_bytes,
-                        BLOCK ? threadIdx.x == 0 : (threadIdx.x & 31) == 0};
+    Ring<2, BLOCK, (V > 1)> ring{full[unit], smem + static_cast<size_t>(unit) * kAddStages * 2 * ring_pitch(p.tile * row_bytes, V > 1), {p.y, p.x}, row_bytes,
+                                 BLOCK ? threadIdx.x == 0 : (threadIdx.x & 31) == 0};
     if constexpr (BLOCK) {
         for (int i = threadIdx.x; i < static_cast<int>(sizeof slots / sizeof(float)); i += blockDim.x) (&slots[0][0][0][0])[i] = 0.f;
         __syncthreads();
@@ -224,8 +240,8 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK || !RIN
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int at = min((l + p.team * j) * V, p.C - V);
-                take<T, V, RING>(ry[j], inside(j), RING ? ring.at(p, 0, ri) : nullptr, p.y, row * p.C, at);
-                take<T, V, RING>(rx[j], inside(j), RING ? ring.at(p, 1, ri) : nullptr, p.x, row * p.C, at);
+                take<T, V, RING>(ry[j], inside(j), RING ? ring.at(p, w, 0, ri) : nullptr, p.y, row * p.C, at);
+                take<T, V, RING>(rx[j], inside(j), RING ? ring.at(p, w, 1, ri) : nullptr, p.x, row * p.C, at);
             }
             W s[J][H];
             float r = 1.f;
@@ -371,14 +387,14 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
     constexpr int UNITS = BLOCK ? 1 : kAddThreads / 32;
     __shared__ uint64_t full[UNITS][kAddStages];
     const uint32_t row_bytes = p.C * static_cast<uint32_t>(sizeof(T));
-    const size_t ring_bytes = RING ? static_cast<size_t>(kAddStages) * 4 * p.tile * row_bytes : 0;
+    const size_t ring_bytes = RING ? static_cast<size_t>(kAddStages) * 4 * ring_pitch(p.tile * row_bytes, V > 1) : 0;
     float* cols = reinterpret_cast<float*>(smem + UNITS * ring_bytes);
     const int lane = threadIdx.x & 31, l = BLOCK ? threadIdx.x : (threadIdx.x & (p.team - 1)), unit = BLOCK ? 0 : threadIdx.x >> 5;
     const int mine = BLOCK ? 0 : lane / p.team, teams = BLOCK ? 1 : 32 / p.team;   // of the unit
     const bool post = p.post != NA_NORM_NONE, norm = p.norm != NA_NORM_NONE;
     auto inside = [&](int j) { return (l + p.team * j) * V < p.C; };
     Walk w(p, unit, UNITS), ahead(w), next(w);
-    Ring<4, BLOCK> ring{full[unit], smem + unit * ring_bytes, {p.dh, p.s_in, p.ds, p.y}, row_bytes, BLOCK ? threadIdx.x == 0 : lane == 0};
+    Ring<4, BLOCK, (V > 1)> ring{full[unit], smem + unit * ring_bytes, {p.dh, p.s_in, p.ds, p.y}, row_bytes, BLOCK ? threadIdx.x == 0 : lane == 0};
     // a tile's statistics, a tile ahead: lane r holds those of row r
     float ahead_stats[4];
     auto read_stats = [&](float (&t)[4]) {
@@ -446,7 +462,7 @@ __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2
                 auto read = [&](int array, int j, W (&v)[H]) {
                     float f[V];
                     Chunk<T, V> c;
-                    if constexpr (RING) c.raw = *reinterpret_cast<const uint4*>(ring.at(p, array, ri) + min((l + p.team * j) * V, p.C - V) * sizeof(T));
+                    if constexpr (RING) take<T, V, true>(c, true, ring.at(p, w, array, ri), nullptr, 0, min((l + p.team * j) * V, p.C - V));
                     else c = raw[array][j];
                     if (!live || !inside(j)) c = Chunk<T, V>{};
                     c.get(f);
@@ -592,23 +608,34 @@ na_status run_add(const AddParams& p, const AddPlan& n, cudaStream_t s) {
     }
 }
 
+template <typename T, int V, int J, bool BWD>
+na_status run_block(const AddParams& p, const AddPlan& n, cudaStream_t s) {
+    return n.ring ? run_add<T, V, J, true, BWD, true>(p, n, s) : run_add<T, V, J, true, BWD, false>(p, n, s);
+}
+
 template <typename T, bool BWD>
 na_status launch_add(const AddParams& p, const AddPlan& n, cudaStream_t s) {
     constexpr int V = Elem<T>::EPC;
-    if (n.vec && !n.block) {
+    if (!n.block) {
         if (!n.ring) return NA_ERR_UNSUPPORTED;   // never: see plan_add
+        if (!n.vec) {
+            return n.j == 4 ? run_add<T, 1, 4, false, BWD, true>(p, n, s) : run_add<T, 1, 8, false, BWD, true>(p, n, s);
+        }
         if (n.j == 1) return run_add<T, V, 1, false, BWD, true>(p, n, s);
-        if (n.j == 2) return run_add<T, V, 2, false, BWD, true>(p, n, s);
+        if constexpr (V == 4 || !BWD)
+            if (n.j == 2) return run_add<T, V, 2, false, BWD, true>(p, n, s);
         if constexpr (V == 4 && !BWD) return run_add<T, V, 4, false, BWD, true>(p, n, s);
-    } else if (n.vec) {
-        if constexpr (V == 8)
-            if (n.j == 1) return n.ring ? run_add<T, V, 1, true, BWD, true>(p, n, s) : run_add<T, V, 1, true, BWD, false>(p, n, s);
-        if (n.j == 2) return n.ring ? run_add<T, V, 2, true, BWD, true>(p, n, s) : run_add<T, V, 2, true, BWD, false>(p, n, s);
-        if constexpr (V == 4) return n.ring ? run_add<T, V, 4, true, BWD, true>(p, n, s) : run_add<T, V, 4, true, BWD, false>(p, n, s);
-    } else if (!n.block) {
-        return run_add<T, 1, 4, false, BWD, false>(p, n, s);
+        return NA_ERR_UNSUPPORTED;   // never: see plan_add
     }
-    return n.j == 4 ? run_add<T, 1, 4, true, BWD, false>(p, n, s) : run_add<T, 1, 16, true, BWD, false>(p, n, s);
+    if (!n.vec) {
+        if (n.j == 4) return run_block<T, 1, 4, BWD>(p, n, s);
+        return n.j == 8 ? run_block<T, 1, 8, BWD>(p, n, s) : run_block<T, 1, 16, BWD>(p, n, s);
+    }
+    if constexpr (V == 8)
+        if (n.j == 1) return run_block<T, V, 1, BWD>(p, n, s);
+    if (n.j == 2) return run_block<T, V, 2, BWD>(p, n, s);
+    if constexpr (V == 4) return run_block<T, V, 4, BWD>(p, n, s);
+    return NA_ERR_UNSUPPORTED;   // never: see plan_add
 }
 
 }  // namespace add

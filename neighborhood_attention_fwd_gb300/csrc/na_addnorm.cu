@@ -98,40 +98,48 @@ AddPlan plan_add(long long group_rows, long long groups, int C, int es, bool bwd
     const int V = C % (16 / es) == 0 ? 16 / es : 1;
     n.vec = V > 1;
     const int chunks = C / V;
-    // chunks per thread of a warp team, at most; longer rows are a block's
-    const int warp_j = V == 8 || (bwd && V == 4) ? 2 : 4;
+    // chunks per thread of a warp team, at most (the backward holds 8 channels to a thread, the forward 16); longer rows are a block's
+    const int warp_j = V == 1 ? 8 : (bwd ? 8 / V : 16 / V);
     n.block = chunks > 32 * warp_j;
     int teams = 1, per_sm, units = 1;
     if (!n.block) {
-        n.team = 1;
-        while (n.team < chunks && n.team < 32) n.team *= 2;
         n.j = 1;
-        while (n.j * n.team < chunks) n.j *= 2;
-        if (!n.vec) n.j = 4;
+        if (n.vec) {
+            while (n.j * 32 < chunks) n.j *= 2;
+        } else {
+            n.j = chunks > 128 ? 8 : 4;
+        }
+        n.team = 1;
+        while (n.team * n.j < chunks) n.team *= 2;
         teams = 32 / n.team;
         units = kAddThreads / 32;
-        per_sm = bwd ? 2 : (n.vec ? add_fwd_blocks(n.j * V, lean) : 4);
+        per_sm = bwd ? 2 : add_fwd_blocks(n.j * V, lean && n.vec);
     } else {
         n.j = V == 8 ? 1 : (V == 4 ? 2 : 4);
-        while (n.j * kAddBlock < chunks) n.j *= n.vec ? 2 : 4;
+        while (n.j * kAddBlock < chunks) n.j *= 2;
         n.team = ((chunks + n.j - 1) / n.j + 31) / 32 * 32;
         per_sm = std::max(1, std::min(16, (bwd ? 512 : 1024) / n.team));
     }
     n.tile = teams;
     const int arrays = bwd ? 4 : 2, row = C * es;
     const size_t sums = bwd && !n.block ? static_cast<size_t>(kAddThreads / 32) * C * 4 : 0;
-    if (n.vec) {
-        // As many rows of a unit as `per_sm` blocks have room for, of at most kAddTileBytes an array.  A pass of a warp's teams is at most
-        // 1 KB an array (2 KB forward): two stages of it, the sums and what else a block holds always fit.
-        const size_t room = ((224 * 1024) / per_sm - sums - 4 * 1024) / units, pass = static_cast<size_t>(kAddStages) * teams * row * arrays;
-        if (room >= pass) {
-            n.ring = true;
-            int passes = std::max(1, std::min({static_cast<int>(room / pass), kAddTileBytes / (teams * row), kAddTileRows / teams}));
-            // fewer rows a tile where the grid is small
-            while (passes > 1 && groups * group_rows < static_cast<long long>(teams) * passes * units * kSms * per_sm * kAddStages) --passes;
-            n.tile = teams * passes;
-            n.ring_bytes = passes * pass * units;
-        }
+    // As many rows of a unit as `per_sm` blocks have room for, of at most kAddTileBytes an array.  A pass of a warp's teams is at most
+    // 1 KB an array (2 KB forward): two stages of it, the sums and what else a block holds always fit.
+    const size_t room = ((224 * 1024) / per_sm - sums - 4 * 1024) / units;
+    auto stages = [&](int passes) { return static_cast<size_t>(kAddStages) * arrays * ring_pitch(teams * passes * row, n.vec); };
+    // A ring costs its filling: blocks that have one row each take it straight from memory (333 rows of 1024, 2 bytes, forward: 3.4 ->
+    // 3.1 us), rows that are not whole chunks, copied with their edges, up to 16 each (backward, 2 bytes, 1001
+    // wide, 2000 rows: 18.5 us, with the ring 22.0; 20000 rows: 128, with the ring 91).
+    const bool few = n.block && groups * group_rows <= static_cast<long long>(kSms) * per_sm * (n.vec || n.j == 16 ? 1 : 16);
+    if (room >= stages(1) && !few) {
+        n.ring = true;
+        int passes = std::max(1, std::min(kAddTileBytes / (teams * row), kAddTileRows / teams));
+        // fewer rows a tile where there is no room, or where the grid is small
+        while (passes > 1 && (stages(passes) > room ||
+                              groups * group_rows < static_cast<long long>(teams) * passes * units * kSms * per_sm * kAddStages))
+            --passes;
+        n.tile = teams * passes;
+        n.ring_bytes = stages(passes) * units;
     }
     const long long tiles = (group_rows + n.tile - 1) / n.tile, most = static_cast<long long>(kSms) * per_sm;
     // in the backward a part's sums cost about as much as a few rows of its own

@@ -66,6 +66,13 @@ ADD = [
     ("bf16", (1, 5000), 96, "rms", "rms", "channel", "channel", False, False, 1.0, 1.0),
     ("fp32", (2, 2500), 72, "layer", "layer", "batch", "batch", True, True, 1.0, 1.0),
     ("fp16", (1, 3001), 520, "layer", "none", "channel", "channel", True, False, 1.0, 1.0),
+    # rows that are not whole 16-byte chunks, over several tiles
+    ("bf16", (2, 2501), 11, "layer", "layer", "batch", "batch", True, True, 1.0, 1.0),
+    ("fp32", (1, 3), 1, "none", "none", "channel", None, False, False, 1.0, 1.0),
+    ("fp16", (3, 1001), 53, "rms", "layer", "channel", "batch", True, True, 1.0, 1.0),
+    ("fp32", (1, 777), 165, "layer", "rms", "channel", "channel", True, False, 0.5, 1.0),
+    ("bf16", (300, 1), 259, "rms", "none", "batch", "batch", True, False, 1.0, 1.0),
+    ("bf16", (1, 401), 2803, "layer", "none", "channel", "channel", True, False, 1.0, 1.0),
 ]
 
 
