@@ -439,8 +439,9 @@ typedef enum {
  * The gated feed-forward product: h = act(x Wg^T + bg) * (x Wu^T + bu) for `rows` tokens, both products, the activation
  * and the gating in one kernel.  x: [rows, D], wg, wu: [F, D] (halves of one [2 F, D] array will do), bg, bu: [F] or null
  * (zeros), h: [rows, F], all of the tensors' type.  Sums in fp32, h rounded once.  2-byte tensors run on tensor
- * cores (where D is no multiple of 8, from some size on, on copies of x, wg and wu allocated on the stream), fp32 on FMA
- * units.  rows < 2^31, D and F up to 2^20 (else NA_ERR_UNSUPPORTED).
+ * cores (where D is no multiple of 8, from some size on, on copies of x, wg and wu allocated on the stream; where it is small
+ * or above 2^16 (fp16) or 2^18, on FMA units), fp32 on FMA units.  rows up to 2^31 - 256, D and F up to 2^20 (else
+ * NA_ERR_UNSUPPORTED).
  */
 na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* h, int64_t rows, int D,
                  int F, na_glu_act act, na_dtype dtype, void* stream);

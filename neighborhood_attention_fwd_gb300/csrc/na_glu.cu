@@ -1,6 +1,6 @@
-// na_glu.cu -- the gated feed-forward product h = act(x Wg^T + bg) * (x Wu^T + bu) and its gradients: host side, the
-// CUDA-core kernels (fp32 tensors, and 2-byte ones whose rows are not whole 16-byte chunks) and the sums that follow the
-// products.  The tensor-core kernels are in na_glu_tc.cu.
+// na_glu.cu -- the gated feed-forward product h = act(x Wg^T + bg) * (x Wu^T + bu) and its gradients: host side, plans and
+// copies.  The tensor-core kernels are in na_glu_tc.cuh; those on FMA units (fp32 tensors, and small 2-byte ones whose rows
+// are not whole 16-byte chunks) and the sums that follow the products in na_glu_fma.cuh.
 //
 //   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u
 //   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg, dbu = column sums of dg, du
@@ -21,7 +21,7 @@ using namespace glu;
 namespace {
 
 constexpr int kGluMaxWidth = 1 << 20;              // of D and F
-constexpr long long kGluMaxRows = (1LL << 31) - 1;
+constexpr long long kGluMaxRows = (1LL << 31) - 256;   // a tile's rows are counted in 31 bits
 
 // How a product is cut on tensor cores.
 struct GluTiles {
@@ -221,9 +221,11 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Channels that the tensor cores work on: D, or for 2-byte rows that are not whole 16-byte chunks D with zeros up to the next chunk,
 // in copies, from 5e7 operations on (bf16, forward and gradients, FMA units -> copies: 100 x 499 x 501 25 -> 24 us, 97 -> 55; 300 x
-// 999 x 1001 145 -> 27, 455 -> 59; 2000 x 1001 x 3001 543 -> 50, 1876 -> 138).  0: none, the product runs on FMA units.
+// 999 x 1001 145 -> 27, 455 -> 59; 2000 x 1001 x 3001 543 -> 50, 1876 -> 138).  0: none, the product runs on FMA units, as fp32
+// does, and sums over more channels than an accumulator of the tensor cores takes within the type's rounding (kMostSteps; 2^16 of one
+// sign come out 3.7e-4 too small, and fp16 rounds by 4.9e-4).
 int tensor_width(long long T, int D, int F, na_dtype dtype) {
-    if (dtype == NA_FP32) return 0;
+    if (dtype == NA_FP32 || D > (dtype == NA_FP16 ? 1 << 16 : 1 << 18)) return 0;
     if (D % 8 == 0) return D;
     return 4.0 * T * D * F >= 5e7 ? (D + 7) / 8 * 8 : 0;
 }

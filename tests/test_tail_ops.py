@@ -271,6 +271,8 @@ GLU = [
     # rows that are not whole 16-byte chunks
     ("bf16", 1, 1, 1, "silu", True), ("bf16", 37, 99, 50, "silu", True), ("fp16", 200, 130, 131, "gelu", False),
     ("bf16", 1300, 257, 700, "silu", True), ("fp16", 900, 1001, 260, "gelu", True), ("bf16", 3, 9001, 8000, "relu", False),
+    # long sums
+    ("fp16", 2, 65544, 9, "silu", True), ("fp16", 5, 65528, 24, "gelu", False), ("bf16", 130, 70000, 40, "sigmoid", True),
 ]
 
 
@@ -532,3 +534,117 @@ def test_calls_on_several_streams_at_once(cuda_lib):
     status_ok(na)
     for b in sets:
         assert all(torch.equal(p, q) for p, q in zip(b, ref))
+
+
+def spread(dtype, *shape):
+    """Values over [-1, 1] without a buffer of another type beside them."""
+    return torch.empty(shape, dtype=TYPES[dtype], device="cuda").uniform_(-1, 1)
+
+
+@pytest.mark.parametrize("dtype,T,D,F", [("bf16", 600_000, 16, 7500), ("bf16", 600_001, 16, 7501), ("fp32", 70_000, 4, 62_000)])
+def test_glu_of_more_than_32_bits_of_elements(dtype, T, D, F, cuda_lib):
+    """T F above 2^32: the rows at both sides of that element and the last ones, and the columns of the weights' gradients
+    that the last tokens alone reach."""
+    na = cuda_lib
+    assert T * F > 1 << 32
+    x, wg, wu = spread(dtype, T, D), spread(dtype, F, D), spread(dtype, F, D)
+    h, dx = torch.empty(T, F, dtype=TYPES[dtype], device="cuda"), torch.empty_like(x)
+    na.na_glu(x, wg, wu, h)
+    edge = (1 << 32) // F
+    rows = torch.cat([torch.arange(2), torch.arange(edge - 2, edge + 3), torch.arange(T - 5, T)]).cuda()
+    X, WG, WU = f64(x[rows]), f64(wg), f64(wu)
+    ref, g, u = ot.glu(X, WG, WU, None, None, "silu")
+    depth = 2 * (D + 16) * E
+    eg, eu = (depth * (np.abs(X) @ np.abs(W).T) for W in (WG, WU))
+    a, sl = ot.act(g, "silu"), ot.slope(g, "silu")
+    ea, esl = act_error(g, "silu", dtype)
+    ea, esl = ea + 1.2 * eg, esl + 0.8 * eg
+    close("h", h[rows], ref, ea * np.abs(u) + np.abs(a) * eu + ea * eu + 2 * E * np.abs(ref), TYPES[dtype])
+    # dh in h's place; only the rows looked at reach the weights
+    h.zero_()
+    h[rows] = spread(dtype, len(rows), F)
+    DH = f64(h[rows])
+    dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+    na.na_glu_bwd(h, x, wg, wu, dx, dwg, dwu)
+    status_ok(na)
+    rdx, rdwg, rdwu, _, _ = ot.glu_bwd(DH, X, WG, WU, None, None, "silu")
+    info = torch.finfo(TYPES[dtype])
+    small = info.smallest_normal * info.eps / 2
+    round_ = lambda v, e: info.eps / 2 * (np.abs(v) + e) + e + small
+    dg, du = DH * u * sl, DH * a
+    edg = round_(dg, np.abs(DH) * (np.abs(u) * esl + np.abs(sl) * eu + esl * eu) + 4 * E * np.abs(dg))
+    edu = round_(du, np.abs(DH) * ea + 2 * E * np.abs(du))
+    dg, du = np.abs(dg) + edg, np.abs(du) + edu
+    close("dx", dx[rows], rdx, edg @ np.abs(WG) + edu @ np.abs(WU) + 2 * (2 * F + 16) * E * (dg @ np.abs(WG) + du @ np.abs(WU)), TYPES[dtype])
+    for name, got, want, e, v in (("dwg", dwg, rdwg, edg, dg), ("dwu", dwu, rdwu, edu, du)):
+        close(name, got, want, e.T @ np.abs(X) + 2 * (len(rows) + 16) * E * (v.T @ np.abs(X)), TYPES[dtype])
+    other = torch.ones(T, dtype=torch.bool, device="cuda")
+    other[rows] = False
+    assert not dx[other].any()
+
+
+@pytest.mark.parametrize("C", [4096, 4001])
+def test_addnorm_of_more_than_32_bits_of_elements(C, cuda_lib):
+    """The rows at both sides of element 2^32 and the last ones are what a call of these rows alone gives."""
+    na = cuda_lib
+    rows = (1 << 32) // C + 1000
+    x, y = spread("bf16", rows, C), spread("bf16", rows, C)
+    w = torch.rand(C, device="cuda") + 0.5
+    s, h = torch.empty_like(x), torch.empty_like(x)
+    st = {k: torch.empty(rows, device="cuda") for k in ("mean", "rstd", "post_rstd")}
+    how = dict(norm="layer", post="rms", w=w, gate=w, post_w=w)
+    na.na_addnorm(x, y, s, h, **how, **st)
+    few = torch.cat([torch.arange(3), torch.arange(rows - 1010, rows - 990), torch.arange(rows - 3, rows)]).cuda()
+    pick = lambda t: t[few].clone()
+    s1, h1 = torch.empty_like(pick(s)), torch.empty_like(pick(s))
+    st1 = {k: torch.empty(len(few), device="cuda") for k in st}
+    na.na_addnorm(pick(x), pick(y), s1, h1, **how, **st1)
+    assert torch.equal(s[few], s1) and torch.equal(h[few], h1) and all(torch.equal(st[k][few], st1[k]) for k in st)
+    dx, dy = x, torch.empty_like(x)
+    na.na_addnorm_bwd(h, None, s, y, dx, dy, **how, **st)
+    dx1, dy1 = torch.empty_like(s1), torch.empty_like(s1)
+    na.na_addnorm_bwd(h1, None, s1, pick(y), dx1, dy1, **how, **st1)
+    assert torch.equal(dx[few], dx1) and torch.equal(dy[few], dy1)
+    status_ok(na)
+
+
+@pytest.mark.parametrize("T,D,F", [(300, 257, 331), (9, 1000, 700), (200, 96, 255)])
+def test_captured_calls_without_a_workspace(T, D, F, cuda_lib):
+    """Two graphs, which allocate for themselves, replayed in turn and at once with other inputs in place: what eager calls give."""
+    na = cuda_lib
+    sets, graphs = [], []
+    for i in range(2):
+        x, wg, wu, bg, bu, dh = (dev(a) for a in glu_inputs("bf16", T, D, F, True, seed=30 + i))
+        gate, rstd = torch.rand(D, device="cuda"), torch.rand(T, device="cuda") + 0.5
+        out = [torch.empty_like(t) for t in (dh, x, wg, wu, bg, bu, x, x, gate)]
+
+        def calls(o, x=x, wg=wg, wu=wu, bg=bg, bu=bu, dh=dh, gate=gate, rstd=rstd):
+            na.na_glu(x, wg, wu, o[0], bg, bu)
+            na.na_glu_bwd(dh, x, wg, wu, o[1], o[2], o[3], bg, bu, o[4], o[5])
+            na.na_addnorm_bwd(x, None, x, o[1], o[6], o[7], gate=gate, norm="rms", rstd=rstd, dgate=o[8])
+
+        calls(out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls(out)
+        sets.append((x, dh, out, calls))
+        graphs.append(g)
+    for turn in range(3):
+        for k, (x, dh, out, calls) in enumerate(sets):
+            x.copy_(randn((T, D), "bf16", 50 + 2 * turn + k))
+            dh.copy_(randn((T, F), "bf16", 60 + 2 * turn + k))
+            for o in out:
+                o.fill_(3.0)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s if turn else torch.cuda.current_stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        status_ok(na)
+        for x, dh, out, calls in sets:
+            want = [torch.empty_like(o) for o in out]
+            calls(want)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
