@@ -180,7 +180,7 @@ struct GluPlan {
 };
 
 // Tiles and splits of a product on CUDA cores.  Cycles of a multiprocessor for a step of a tile: 128 x 128 are bound by FMA, the
-// others by shared memory; one block alone waits 60 to 95 for its loads.  The summed axis is cut where the
+// others by shared memory; one block alone takes 40 (32 x 32) to 115 for the latency of its loads.  The summed axis is cut where the
 // tiles leave multiprocessors idle, and to at most 8192 products in one sum.
 FmaTile plan_fma(Product which, long long T, int D, int F) {
     const bool pair = which == kForward || which == kSlopes;
@@ -198,7 +198,7 @@ FmaTile plan_fma(Product which, long long T, int D, int F) {
                 if (splits < 1) continue;
                 const long long blocks = tiles * splits, waves = (blocks + kSms - 1) / kSms;
                 // nanoseconds; alone on its multiprocessor a block waits for its operands
-                double time = std::max(waves * cycles, r + c > 64 ? 95.0 : 60.0) * (static_cast<double>(depth) / splits + 32) / 1.9;
+                double time = std::max(waves * cycles, r + c > 64 ? 115.0 : 40.0) * (static_cast<double>(depth) / splits + 32) / 1.9;
                 if (splits > 1) time += 3000 + 8.0 * rows * D * (which == kWeights ? 2 : 1) * splits / 5000;
                 if (best.rows == 0 || time < least) {
                     least = time;

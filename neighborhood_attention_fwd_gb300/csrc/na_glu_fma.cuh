@@ -1,7 +1,9 @@
 // na_glu_fma.cuh -- the gated feed-forward product on CUDA cores, and the sums that follow the products (see na_glu.cu).
 //
-// What bounds it: products.  fp32 runs on FMA units, in pairs (fma.rn.f32x2), no TF32: tiles of 128 x 128, 8 x 8 per
-// thread, operands widened and laid out [k][row] in shared memory, two stages of 16 steps of k.
+// What bounds it: products.  fp32 runs on FMA units, in pairs (fma.rn.f32x2), no TF32; operands are widened and laid out
+// [k][row] in shared memory, two stages of 16 steps of k.  Tiles of 128 x 128, 8 x 8 per thread, run at 45 TFLOP/s (20000 x 512
+// x 1376, forward: 1.24 ms); 32 in place of 128 on either side where a problem has few tiles or short sides.  Those are bound
+// by the latency of a step's loads, so that they keep two or four pieces on their way in registers (32 x 512 x 512: 32 -> 14 us).
 #pragma once
 
 #include <algorithm>
@@ -27,44 +29,57 @@ struct Operand {
     bool wide;               // rows of memory start at 16 bytes
 };
 
-// A thread's N elements of a piece: from row r, steps k .. k + N - 1, or with ALONG_ROWS from step k, rows r .. r + N - 1.
+// A thread's N elements of a piece: from row r, steps k .. k + N - 1, or with ALONG_ROWS from step k, rows r .. r + N - 1.  They are
+// widened when they are placed: until then nothing waits for them.
 template <typename T, bool ALONG_ROWS, int N>
-__device__ __forceinline__ void fetch(const Operand<T>& o, long long r, long long k, float (&f)[N]) {
-    constexpr int EPC = Elem<T>::EPC;
+__device__ __forceinline__ void fetch(const Operand<T>& o, long long r, long long k, T (&f)[N]) {
     const bool in = r < o.rows && k < o.depth;
     const long long left = ALONG_ROWS ? o.rows - r : o.depth - k;   // elements there along memory
     const T* at = o.base + (ALONG_ROWS ? k * o.ld + r : r * o.ld + k);
-    if constexpr (N == 8) {
-        if (in && o.wide && left >= 8) {
+    constexpr int RUN = N * sizeof(T) < 16 ? N : 16 / sizeof(T);   // elements of one load
+    if (in && o.wide && left >= N) {
+        struct alignas(RUN * sizeof(T)) Run { T v[RUN]; };
 #pragma unroll
-            for (int c = 0; c < 8 / EPC; ++c) {
-                const uint4 raw = __ldg(reinterpret_cast<const uint4*>(at) + c);
-                float g[EPC];
-                Elem<T>::unpack(raw, g);
+        for (int c = 0; c < N / RUN; ++c) {
+            Run run;
+            if constexpr (sizeof run == 16) *reinterpret_cast<uint4*>(&run) = __ldg(reinterpret_cast<const uint4*>(at) + c);
+            else run = reinterpret_cast<const Run*>(at)[c];
 #pragma unroll
-                for (int e = 0; e < EPC; ++e) f[c * EPC + e] = g[e];
-            }
-            return;
+            for (int e = 0; e < RUN; ++e) f[c * RUN + e] = run.v[e];
         }
+        return;
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = in && e < left ? Elem<T>::get(at[e]) : 0.f;
+    for (int e = 0; e < N; ++e) f[e] = in && e < left ? at[e] : Elem<T>::put(0.f);
 }
 
-template <bool ALONG_ROWS, int TS, int N>
-__device__ __forceinline__ void place(float (*sm)[TS + 4], int t, const float (&f)[N]) {
-    if constexpr (!ALONG_ROWS) {
+// Where thread t fetches in a piece of TS rows by kDepth steps: N = TS / 16 elements along memory.  128 rows: eight steps are a
+// sector of a row of theirs; 32: eight threads take the 16 steps of a row.
+template <bool ALONG_ROWS, int TS>
+__device__ __forceinline__ int row_of(int t) { return ALONG_ROWS ? (t & 15) * (TS / 16) : (TS == 128 ? t % TS : t >> 3); }
+template <bool ALONG_ROWS, int TS>
+__device__ __forceinline__ int step_of(int t) { return ALONG_ROWS ? t >> 4 : (TS == 128 ? t / TS * 8 : (t & 7) * 2); }
+
+// A piece in shared memory: [step][row], of 32 rows those 16 apart, a thread's two, side by side.
+template <bool ALONG_ROWS, int TS, int N, typename T>
+__device__ __forceinline__ void place(float (*sm)[TS + 4], int t, const T (&raw)[N]) {
+    float f[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) sm[t / TS * N + e][t % TS] = f[e];
-    } else {
-        float* to = &sm[t >> 4][(t & 15) * N];
-        if constexpr (N == 8) {
-            *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
+    for (int e = 0; e < N; ++e) f[e] = Elem<T>::get(raw[e]);
+    const int r = row_of<ALONG_ROWS, TS>(t), k = step_of<ALONG_ROWS, TS>(t);
+    if constexpr (TS == 32) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) to[e] = f[e];
+        for (int e = 0; e < N; ++e) {
+            const int row = ALONG_ROWS ? r + e : r;
+            sm[ALONG_ROWS ? k : k + e][(row & 15) * 2 + (row >> 4)] = f[e];
         }
+    } else if constexpr (!ALONG_ROWS) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) sm[k + e][r] = f[e];
+    } else {
+        float* to = &sm[k][r];
+        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -89,10 +104,11 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
     const long long pieces = (depth + kDepth - 1) / kDepth;
     const long long first = WHICH == kTokens ? split * p.run : 0, last = WHICH == kTokens ? min(2 * pieces, first + p.run) : pieces;
     // where this thread fetches within a piece
-    const int ra = A_ROWS ? (t & 15) * NA : t % TR, ka = A_ROWS ? t >> 4 : t / TR * NA;
-    const int rb = B_ROWS ? (t & 15) * NB : t % TC, kb = B_ROWS ? t >> 4 : t / TC * NB;
-    float fa[NA], fb[NB];
-    auto load = [&](long long i) {
+    const int ra = row_of<A_ROWS, TR>(t), ka = step_of<A_ROWS, TR>(t), rb = row_of<B_ROWS, TC>(t), kb = step_of<B_ROWS, TC>(t);
+    // pieces on their way in registers; small tiles take less time than a load, and have the registers for more of them
+    constexpr int AHEAD = TR + TC == 256 ? 1 : (TR + TC == 64 ? 4 : 2);
+    T pa[AHEAD][NA], pb[AHEAD][NB];
+    auto load = [&](long long i, T (&fa)[NA], T (&fb)[NB]) {
         const bool second = WHICH == kTokens && i >= pieces;
         const long long k = (second ? i - pieces : i) * kDepth;
         Operand<T> a, b;
@@ -118,13 +134,15 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < GC; ++j) acc[i][j] = 0;
-    load(first);
-    for (long long i = first; i < last; ++i) {
-        const int st = static_cast<int>(i & 1);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+        if (first + q < last) load(first + q, pa[q], pb[q]);
+    int st = 0;
+    auto piece = [&](long long i, T (&fa)[NA], T (&fb)[NB]) {
         place<A_ROWS, TR>(sa[st], t, fa);
         place<B_ROWS, TC>(sb[st], t, fb);
         __syncthreads();   // also: the stage filled next was last read before this barrier
-        if (i + 1 < last) load(i + 1);
+        if (i + AHEAD < last) load(i + AHEAD, fa, fb);
 #pragma unroll
         for (int k = 0; k < kDepth; ++k) {
             float a[R];
@@ -133,13 +151,14 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
                 const float4 a0 = *reinterpret_cast<const float4*>(&sa[st][k][ty * 4]), a1 = *reinterpret_cast<const float4*>(&sa[st][k][64 + ty * 4]);
                 a[0] = a0.x, a[1] = a0.y, a[2] = a0.z, a[3] = a0.w, a[4] = a1.x, a[5] = a1.y, a[6] = a1.z, a[7] = a1.w;
             } else {
-                a[0] = sa[st][k][ty], a[1] = sa[st][k][16 + ty];
+                const float2 a0 = *reinterpret_cast<const float2*>(&sa[st][k][ty * 2]);
+                a[0] = a0.x, a[1] = a0.y;
             }
             if constexpr (GC == 4) {
                 const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][tx * 4]), b1 = *reinterpret_cast<const ulonglong2*>(&sb[st][k][64 + tx * 4]);
                 b[0] = b0.x, b[1] = b0.y, b[2] = b1.x, b[3] = b1.y;
             } else {
-                b[0] = pack2(sb[st][k][tx], sb[st][k][16 + tx]);
+                b[0] = *reinterpret_cast<const uint64_t*>(&sb[st][k][tx * 2]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -148,7 +167,12 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
                 for (int c = 0; c < GC; ++c) acc[r][c] = fma2(aa, b[c], acc[r][c]);
             }
         }
-    }
+        st ^= 1;
+    };
+    for (long long i = first; i < last; i += AHEAD)
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+            if (i + q < last) piece(i + q, pa[q], pb[q]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const long long row = m0 + (r < GR ? ty * GR + r : TR / 2 + ty * GR + r - GR);
