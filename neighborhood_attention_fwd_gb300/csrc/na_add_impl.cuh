@@ -378,6 +378,7 @@ __device__ __forceinline__ void store_sums(const AddParams& p, int part, int slo
 // bound rows of 2-byte channels.
 template <typename T, int V, int J, bool BLOCK, bool RING, bool LEAN>
 __global__ void __launch_bounds__(BLOCK ? kAddBlock : kAddThreads, BLOCK ? 1 : 2) add_bwd_kernel(const AddParams p) {
+    next_may_start();
     using A = Cols<V>;
     using W = typename A::W;
     constexpr int H = A::H;

@@ -44,6 +44,7 @@ struct SumParams {
 
 constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) add_sum_kernel(const SumParams p) {
+    after_previous();
     __shared__ float part[4][kSumThreads / 32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 8 + (lane & 7);
@@ -374,8 +375,7 @@ na_status na_addnorm_bwd(const void* dh, const void* ds, const void* s, const vo
         q.scale = scale;
         q.all = ((dw || db) && !q.w_many) || (dgate && !q.gate_many) || dpost_w || dpost_b;
         const bool many = ((dw || db) && q.w_many) || (dgate && q.gate_many);
-        add_sum_kernel<<<dim3((C + 7) / 8, q.all + (many ? p.groups : 0)), kSumThreads, 0, cs>>>(q);
-        st = launch_result();
+        st = launch_after(add_sum_kernel, dim3((C + 7) / 8, q.all + (many ? p.groups : 0)), kSumThreads, cs, q);
     }
     if (owned && cudaFreeAsync(ws, cs) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
     return st;

@@ -74,6 +74,27 @@ constexpr int kSms = 152;   // multiprocessors of a GB300: grids are sized for t
 
 inline na_status launch_result() { return cudaGetLastError() == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 
+// Launches a kernel that begins with after_previous() behind one of the same call: it is set up while that one ends.
+template <typename... P, typename... A>
+na_status launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.stream = s;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess ? NA_OK : NA_ERR_CUDA;
+}
+
+// Waits until the kernel before has ended and its results are there; returns at once in a kernel that is launched plainly.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on in every block the kernel behind may be set up.  Behind the block's own allocation of TMEM: blocks of the next kernel
+// on the same multiprocessor must not hold what this one still has to get.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------------------------
 // Device: 16-byte accesses.  The operators read and write every byte once, so they leave L1 alone.
 // Not the read-only path: an output may be the input's tensor.

@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
 // be null.  V elements at a time (n and cut are multiples of V).
 template <typename T, int V>
 __global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int runs, long long n, long long cut, T* out0, T* out1) {
+    after_previous();
+    next_may_start();
     for (long long i = (blockIdx.x * 256LL + threadIdx.x) * V; i < n; i += gridDim.x * 256LL * V) {
         T* out = i < cut ? (out0 ? out0 + i : nullptr) : (out1 ? out1 + (i - cut) : nullptr);
         if (!out) continue;
@@ -245,6 +247,8 @@ __global__ void __launch_bounds__(256) glu_sum_kernel(const float* partial, int 
 // are padded to whole chunks).
 template <typename T>
 __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* du, long long T_, int F, long long pitch, long long run, float* partial) {
+    after_previous();
+    next_may_start();
     constexpr int V = Elem<T>::EPC;
     __shared__ float sums[8][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -293,16 +297,13 @@ template <typename T>
 na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s) {
     const bool wide = n % 4 == 0 && cut % 4 == 0;
     const unsigned blocks = static_cast<unsigned>(std::min((n / (wide ? 4 : 1) + 255) / 256, 8LL * kSms));
-    if (wide) glu_sum_kernel<T, 4><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
-    else glu_sum_kernel<T, 1><<<blocks, 256, 0, s>>>(partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
-    return launch_result();
+    return launch_after(wide ? glu_sum_kernel<T, 4> : glu_sum_kernel<T, 1>, dim3(blocks), 256, s, partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
 }
 
 template <typename T>
 na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s) {
-    glu_column_kernel<T><<<dim3(up(p.F, 32 * Elem<T>::EPC), runs, 2), 256, 0, s>>>(static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T, p.F,
-                                                                         p.pitch, run, partial);
-    return launch_result();
+    return launch_after(glu_column_kernel<T>, dim3(up(p.F, 32 * Elem<T>::EPC), runs, 2), 256, s, static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T,
+                        p.F, p.pitch, run, partial);
 }
 
 }  // namespace glu

@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    if constexpr (WHICH == kSlopes) next_may_start();
 
     if (warp == 0) {
         // copies
@@ -741,6 +742,8 @@ __global__ void __launch_bounds__(TileShape<CG>::THREADS, 1) glu_tile_kernel(con
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    after_previous();
+    next_may_start();
     if constexpr (WHICH != kBoth) tile_work<WHICH, CG, T>(p, mine, all, smem, bars, tmem, rank);
     else if (mine < p.token_workers) tile_work<kTokens, CG, T>(p, mine, p.token_workers, smem, bars, tmem, rank);
     else tile_work<kWeights, CG, T>(p, mine - p.token_workers, all - p.token_workers, smem, bars, tmem, rank);
@@ -926,19 +929,26 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
 // ---------------------------------------------------------------------------------------------
 
 template <typename Kernel>
-na_status launch_glu(Kernel* kernel, const GluTcParams& p, unsigned blocks, int cluster, int threads, uint32_t bytes, cudaStream_t s) {
+na_status launch_glu(Kernel* kernel, const GluTcParams& p, unsigned blocks, int cluster, int threads, uint32_t bytes, cudaStream_t s, bool after = false) {
     if (!allow_shared(reinterpret_cast<const void*>(kernel))) return NA_ERR_CUDA;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(blocks);
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = bytes;
     c.stream = s;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = cluster;
-    a.val.clusterDim.y = a.val.clusterDim.z = 1;
-    c.attrs = &a;
-    c.numAttrs = cluster > 1 ? 1 : 0;
+    cudaLaunchAttribute a[2]{};
+    c.attrs = a;
+    if (cluster > 1) {
+        a[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        a[c.numAttrs].val.clusterDim.x = cluster;
+        a[c.numAttrs].val.clusterDim.y = a[c.numAttrs].val.clusterDim.z = 1;
+        ++c.numAttrs;
+    }
+    if (after) {   // behind another kernel of the call
+        a[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        a[c.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++c.numAttrs;
+    }
     return cudaLaunchKernelEx(&c, kernel, p) == cudaSuccess ? NA_OK : NA_ERR_CUDA;
 }
 
@@ -948,7 +958,7 @@ na_status launch_tiles(const GluTcParams& p, unsigned tiles, cudaStream_t s) {
     if constexpr (WHICH == kForward || WHICH == kSlopes)
         return launch_glu(glu_pair_kernel<WHICH, CG, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
     else
-        return launch_glu(glu_tile_kernel<WHICH, CG, T>, p, blocks, CG, TileShape<CG>::THREADS, TileShape<CG>::BYTES, s);
+        return launch_glu(glu_tile_kernel<WHICH, CG, T>, p, blocks, CG, TileShape<CG>::THREADS, TileShape<CG>::BYTES, s, true);
 }
 
 template <int WHICH, typename T>
