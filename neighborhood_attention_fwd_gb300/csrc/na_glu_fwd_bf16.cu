@@ -3,7 +3,7 @@
 
 namespace na {
 namespace glu {
-template na_status launch_tiles<kForward, __nv_bfloat16>(const GluTcParams&, bool, cudaStream_t);
+template na_status launch_tiles<kForward, __nv_bfloat16>(const GluTcParams&, int, cudaStream_t);
 template na_status launch_few<kForward, __nv_bfloat16>(const GluTcParams&, int, cudaStream_t);
 }  // namespace glu
 }  // namespace na

@@ -3,8 +3,8 @@
 
 namespace na {
 namespace glu {
-template na_status launch_tiles<kTokens, __nv_bfloat16>(const GluTcParams&, bool, cudaStream_t);
-template na_status launch_tiles<kWeights, __nv_bfloat16>(const GluTcParams&, bool, cudaStream_t);
-template na_status launch_tiles<kBoth, __nv_bfloat16>(const GluTcParams&, bool, cudaStream_t);
+template na_status launch_tiles<kTokens, __nv_bfloat16>(const GluTcParams&, int, cudaStream_t);
+template na_status launch_tiles<kWeights, __nv_bfloat16>(const GluTcParams&, int, cudaStream_t);
+template na_status launch_tiles<kBoth, __nv_bfloat16>(const GluTcParams&, int, cudaStream_t);
 }  // namespace glu
 }  // namespace na

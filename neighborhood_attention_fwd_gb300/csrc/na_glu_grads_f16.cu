@@ -3,8 +3,8 @@
 
 namespace na {
 namespace glu {
-template na_status launch_tiles<kTokens, __half>(const GluTcParams&, bool, cudaStream_t);
-template na_status launch_tiles<kWeights, __half>(const GluTcParams&, bool, cudaStream_t);
-template na_status launch_tiles<kBoth, __half>(const GluTcParams&, bool, cudaStream_t);
+template na_status launch_tiles<kTokens, __half>(const GluTcParams&, int, cudaStream_t);
+template na_status launch_tiles<kWeights, __half>(const GluTcParams&, int, cudaStream_t);
+template na_status launch_tiles<kBoth, __half>(const GluTcParams&, int, cudaStream_t);
 }  // namespace glu
 }  // namespace na

@@ -3,7 +3,7 @@
 
 namespace na {
 namespace glu {
-template na_status launch_tiles<kSlopes, __half>(const GluTcParams&, bool, cudaStream_t);
+template na_status launch_tiles<kSlopes, __half>(const GluTcParams&, int, cudaStream_t);
 template na_status launch_few<kSlopes, __half>(const GluTcParams&, int, cudaStream_t);
 }  // namespace glu
 }  // namespace na

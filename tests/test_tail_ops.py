@@ -268,6 +268,8 @@ GLU = [
     # enough tiles for pairs of blocks, forward and for every gradient
     ("bf16", 5200, 136, 1000, "silu", True), ("fp16", 5001, 72, 2001, "relu", True), ("fp16", 2900, 1032, 1304, "silu", False),
     ("bf16", 40000, 264, 88, "sigmoid", False),
+    # pairs of pairs, the last one's second beyond the tokens
+    ("fp16", 5200, 1000, 1001, "gelu", False), ("bf16", 2900, 1096, 1304, "relu", True),
     # rows that are not whole 16-byte chunks
     ("bf16", 1, 1, 1, "silu", True), ("bf16", 37, 99, 50, "silu", True), ("fp16", 200, 130, 131, "gelu", False),
     ("bf16", 1300, 257, 700, "silu", True), ("fp16", 900, 1001, 260, "gelu", True), ("bf16", 3, 9001, 8000, "relu", False),

@@ -24,8 +24,8 @@ def bf(shape, seed):
     return torch.randn(shape, generator=g).bfloat16().cuda()
 
 
-# tokens, D, F: few tokens alone and in a cluster, single blocks, pairs of blocks
-@pytest.mark.parametrize("T,D,F", [(3, 64, 200), (100, 2048, 96), (300, 200, 400), (5200, 136, 1000)])
+# tokens, D, F: few tokens alone and in a cluster, single blocks, pairs of blocks, pairs of pairs
+@pytest.mark.parametrize("T,D,F", [(3, 64, 200), (100, 2048, 96), (300, 200, 400), (5200, 136, 1000), (5200, 1000, 1000)])
 def test_the_gated_product(cuda_lib, T, D, F):
     na = cuda_lib
     x, wg, wu, dh = bf((T, D), 1), bf((F, D), 2), bf((F, D), 3), bf((T, F), 4)
