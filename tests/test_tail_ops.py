@@ -73,6 +73,9 @@ ADD = [
     ("fp32", (1, 777), 165, "layer", "rms", "channel", "channel", True, False, 0.5, 1.0),
     ("bf16", (300, 1), 259, "rms", "none", "batch", "batch", True, False, 1.0, 1.0),
     ("bf16", (1, 401), 2803, "layer", "none", "channel", "channel", True, False, 1.0, 1.0),
+    ("bf16", (1, 5000), 2601, "rms", "layer", "channel", "channel", True, True, 1.0, 1.0),
+    ("fp16", (1, 400), 8191, "layer", "layer", "channel", "channel", True, True, 1.0, 1.0),
+    ("fp32", (2, 5500), 1001, "layer", "rms", "batch", "channel", True, False, 1.0, 1.0),
 ]
 
 

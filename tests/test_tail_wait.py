@@ -45,7 +45,7 @@ def test_the_gated_product(cuda_lib, T, D, F):
     assert all(torch.equal(a, b) for a, b in zip((h, dx, dwg, dwu), ref))
 
 
-@pytest.mark.parametrize("rows,C", [(50, 32), (4000, 256), (700, 2048)])
+@pytest.mark.parametrize("rows,C", [(50, 32), (4000, 256), (700, 2048), (4001, 53), (12000, 1001)])
 def test_the_add_with_its_norms(cuda_lib, rows, C):
     na = cuda_lib
     x, y, dh = bf((rows, C), 1), bf((rows, C), 2), bf((rows, C), 3)
