@@ -26,7 +26,6 @@ constexpr long long kGluMaxRows = (1LL << 31) - 256;   // a tile's rows are coun
 // How a product is cut on tensor cores.
 struct GluTiles {
     bool pairs;              // tiles of 256 x 256 on pairs of blocks, else of 128 x 128
-    bool quads;              // forward, slopes: two pairs, one above the other, that share the columns' operand
     int few;                 // 16, 64, 128: the kernel of few tokens
     unsigned rows, cols, steps, run, splits, ways;
     unsigned last_nf, span, groups;   // forward, slopes
@@ -36,7 +35,7 @@ struct GluTiles {
 
 
 // Nanoseconds of a step of 64 along the summed axis of a tile, for pairs of blocks and for one, and of what a tile takes besides.
-constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000, kQuadStep = 255;
+constexpr long long kPairStep = 280, kOneStep = 190, kTileTime = 1000;
 // Bytes that one product leaves in L2 for the next.
 constexpr double kFitsL2 = 80e6;
 // The same where the rows' operand stays for several columns of tiles.
@@ -85,31 +84,25 @@ GluTiles plan_tiles(Product which, long long T, int D, int F) {
         return best;
     }
     double least = 0;
-    for (int blocks : {1, 2, 4}) {
-        const bool pairs = blocks > 1, quads = blocks == 4;
-        // Two pairs together take a quarter less out of L2, and there is room for 36 clusters of four, 72 pairs instead of 76.  Long sums
-        // gain (4095 x 4096 x 11008: 467 -> 451 us, 2001 x 1536 x 4096: 43 -> 40), those of fewer than 16 steps lose (65536 x 512 x
-        // 1376, dg and du: 308 -> 322).  Their rows are counted in 31 bits.
-        if (quads && (!pair || D <= 960 || T > 1LL << 30)) continue;
-        const int m = pairs ? 256 : 128, slots = quads ? static_cast<int>(kQuads) : kSms / blocks;
+    for (bool pairs : {false, true}) {
+        const int m = pairs ? 256 : 128, slots = pairs ? kSms / 2 : kSms;
         GluTiles t{};
         t.pairs = pairs;
-        t.quads = quads;
         t.splits = 1;
         if (pair) {
             // a row's last tile is only as wide as it has to be: a product of pairs takes 32 columns (16 of g) at a time, of one
             // block 16
-            t.rows = up(T, quads ? 512 : m);
+            t.rows = up(T, m);
             t.cols = up(F, m / 2);
             t.last_nf = up(F - (t.cols - 1) * (m / 2), pairs ? 16 : 8) * (pairs ? 16 : 8);
             t.steps = t.run = up(D, 64);
             const unsigned stay = which == kForward ? kPairRows<kForward> : kPairRows<kSlopes>;
             for (unsigned span = 1; span <= t.cols; ++span) {
-                if (span > 1 && (quads || t.steps > stay || span > 64)) break;
+                if (span > 1 && (t.steps > stay || span > 64)) break;
                 const unsigned groups = up(t.cols, span);
                 if (span > 1 && up(t.cols, span - 1) == groups) continue;   // no fewer items than with the shorter run
                 const double waves = static_cast<double>((static_cast<long long>(t.rows) * groups + slots - 1) / slots);
-                const long long step = span > 1 ? (pairs ? kPairStay : kOneStay) : (quads ? kQuadStep : pairs ? kPairStep : kOneStep);
+                const long long step = span > 1 ? (pairs ? kPairStay : kOneStay) : (pairs ? kPairStep : kOneStep);
                 const double time = waves * std::min<double>(span, static_cast<double>(F) / (m / 2)) * t.steps * step + kTileTime;
                 if (best.groups == 0 || time < least) {
                     least = time;
@@ -332,13 +325,13 @@ na_status launch_tensor(const GluParams& p, Product which, const GluTiles& n, na
     };
     q.wide = p.F % 8 == 0;
     if (pair) {
-        const uint32_t b_rows = n.pairs && !n.quads ? 128 : 64, last_rows = n.quads ? n.last_nf / 2 : n.last_nf;
+        const uint32_t b_rows = n.pairs ? 128 : 64;
         map(q.a[0], p.x, D, T, 2 * D, n.few ? n.few : 128);
         map(q.b[0], p.wg, D, F, 2 * D, b_rows);
         map(q.b[1], p.wu, D, F, 2 * D, b_rows);
         if (!n.few) {   // results and dh: boxes of 32 by 32
-            map(q.b[2], p.wg, D, F, 2 * D, last_rows);
-            map(q.b[3], p.wu, D, F, 2 * D, last_rows);
+            map(q.b[2], p.wg, D, F, 2 * D, n.last_nf);
+            map(q.b[3], p.wu, D, F, 2 * D, n.last_nf);
             if (which == kSlopes) {
                 if (q.wide) map(q.in, p.dh, F, T, 2 * F, 32, 32);
                 else map(q.in, p.dg, F, T, pitch, 32, 32);
@@ -388,7 +381,7 @@ na_status launch_tensor(const GluParams& p, Product which, const GluTiles& n, na
     q.wait_ns = wait_limit_ns();
     q.withhold = wait_withhold();
     const bool f16 = dtype == NA_FP16;
-    const int blocks = n.quads ? 4 : n.pairs ? 2 : 1;
+    const int blocks = n.pairs ? 2 : 1;
     switch (which) {
         case kForward:
             if (n.few) return f16 ? launch_few<kForward, __half>(q, n.few, s) : launch_few<kForward, __nv_bfloat16>(q, n.few, s);

@@ -214,7 +214,6 @@ __device__ __forceinline__ void with_act(int act, Call&& call) {
 // Steps of the rows' operand that a block of the forward or of the slopes holds.
 template <int WHICH>
 constexpr int kPairRows = WHICH == kForward ? 6 : 5;
-constexpr unsigned kQuads = 36;   // clusters of four blocks that there is room for at once (of two: 76)
 
 inline unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
 
@@ -241,10 +240,10 @@ na_status launch_sum(const float* partial, int runs, long long n, long long cut,
 template <typename T>
 na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s);
 
-// Launchers of the tensor-core kernels (na_glu_tc.cuh).  pairs: tiles of 256 x 256 on pairs of blocks, else of 128 x 128;
-// tokens: 16, 64 or 128, the most that a product of few tokens holds.
+// Launchers of the tensor-core kernels (na_glu_tc.cuh).  blocks: of a tile, 2 (256 x 256) or 1 (128 x 128); tokens: 16, 64 or
+// 128, the most that a product of few tokens holds.
 template <int WHICH, typename T>
-na_status launch_tiles(const GluTcParams& p, int blocks, cudaStream_t s);   // blocks: of a tile; 4: two pairs (forward, slopes)
+na_status launch_tiles(const GluTcParams& p, int blocks, cudaStream_t s);
 template <int WHICH, typename T>
 na_status launch_few(const GluTcParams& p, int tokens, cudaStream_t s);
 

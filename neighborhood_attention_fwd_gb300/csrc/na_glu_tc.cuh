@@ -107,15 +107,15 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
             : "memory");
     }
 }
-// Arrive on `bar` (of both blocks of a pair; of the cluster's blocks in `to`) when every product issued so far has completed.
+// Arrive on `bar` (of both blocks of a pair) when every product issued so far has completed.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t to = 3) {
+__device__ __forceinline__ void commit(uint64_t* bar) {
     if constexpr (CG == 1) {
         umma_commit(bar);
     } else {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                          smem_u32(bar)),
-                     "h"(static_cast<uint16_t>(to))
+                     "h"(static_cast<uint16_t>(3))
                      : "memory");
     }
 }
@@ -133,14 +133,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
             "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
             : "memory");
     }
-}
-
-// The same box into the same place of every block of the cluster in `to`; in each pair the bytes count on its block like `bar`'s.
-__device__ __forceinline__ void load_box_to(uint32_t to, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(static_cast<uint16_t>(to))
-        : "memory");
 }
 
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
@@ -214,10 +206,9 @@ __device__ __forceinline__ Place place_of(unsigned i, unsigned rows, unsigned co
 // Forward and slopes.  A tile: 128 CG rows of tokens, 64 CG columns of g and the same of u, fewer of them in the last of a row.  The
 // rows' and the columns' operand have rings of their own: where all of a row of tiles' operand (its steps of 64) fits its ring,
 // it is brought once for the `span` columns of tiles that a block takes in a row, which halves what comes out of L2, the bound
-// of short sums (1024^2 tokens, 256 -> 688, 2-byte: 535 us, 13 TB/s).  For long sums two pairs make a cluster of four with one
-// column of tiles: each brings half of the columns' operand to both (multicast), a slot is free when both have read it.  They run
-// at 1640 TFLOP/s (4095 tokens, 4096 -> 11008: 451 us), what a plain library product reaches at the power limit.  The epilogue has
-// sixteen (eight) warps, each for 32 rows by 32 columns.
+// of short sums (1024^2 tokens, 256 -> 688, 2-byte: 535 us, 13 TB/s).  Long sums run at 1580 TFLOP/s (4095 tokens, 4096 -> 11008:
+// 467 us).  The epilogue has sixteen (eight) warps, each for 32 rows by 32 columns.  Every block copies what it and its pair
+// read itself: the library also runs as one of several ranks, each on a GPU of its own, and no load of it goes to several blocks.
 // ---------------------------------------------------------------------------------------------
 
 template <int WHICH, int CG>
@@ -235,39 +226,37 @@ struct PairShape {
     static_assert(BYTES <= 227 * 1024 - 512, "more than a block's shared memory");
 };
 
-// The tiles of a block, in order.  QUAD: two pairs of blocks take tiles one above the other.
-template <int CG, bool QUAD>
+// The tiles of a block, in order.
+template <int CG>
 struct PairWalk {
-    static constexpr unsigned BLOCKS = QUAD ? 4 : CG;
     const GluTcParams& p;
     unsigned item, items, row, col, end;   // tile (row, col); the item ends before column `end`
-    __device__ __forceinline__ explicit PairWalk(const GluTcParams& q) : p(q), item(blockIdx.x / BLOCKS), items(q.rows * q.groups) { open(); }
+    __device__ __forceinline__ explicit PairWalk(const GluTcParams& q) : p(q), item(blockIdx.x / CG), items(q.rows * q.groups) { open(); }
     __device__ __forceinline__ void open() {
         if (item >= items) return;
         const Place at = place_of(item, p.rows, p.groups);
-        row = QUAD ? 2 * at.row + (blockIdx.x >> 1 & 1) : at.row;
+        row = at.row;
         col = at.col * p.span;
         end = min(p.cols, col + p.span);
     }
     __device__ __forceinline__ bool more() const { return item < items; }
     __device__ __forceinline__ void next() {
         if (++col < end) return;
-        item += gridDim.x / BLOCKS;
+        item += gridDim.x / CG;
         open();
     }
 };
 
-template <int WHICH, int CG, bool QUAD, typename T>
+template <int WHICH, int CG, typename T>
 __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_kernel(const __grid_constant__ GluTcParams p) {
     using S = PairShape<WHICH, CG>;
-    using Walk = PairWalk<CG, QUAD>;
+    using Walk = PairWalk<CG>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ uint64_t rows_full[S::ROWS], rows_empty[S::ROWS], cols_full[S::COLS], cols_empty[S::COLS], acc_full[2], acc_empty[2], dh_full[S::WARPS];
     __shared__ uint32_t tmem_base;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the block in its pair; the pair's leading block and the pair in the cluster
-    const uint32_t place = CG == 2 ? cluster_rank() : 0u, rank = place & 1u, lead = QUAD ? place & 2u : 0u, pair = lead >> 1;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;   // the block in its pair
     const WaitGuard guard{p.err, p.wait_ns};
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::ROWS; ++s) {
@@ -276,7 +265,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
         }
         for (int s = 0; s < S::COLS; ++s) {
             mbar_init(&cols_full[s], 1);
-            mbar_init(&cols_empty[s], QUAD ? 2 : 1);
+            mbar_init(&cols_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -295,8 +284,8 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
 
     if (warp == 0) {
         // copies
-        const uint32_t rows_at = CG == 2 ? peer_address(smem_u32(rows_full), lead) : smem_u32(rows_full);   // the leading block's barriers
-        const uint32_t cols_at = CG == 2 ? peer_address(smem_u32(cols_full), lead) : smem_u32(cols_full);
+        const uint32_t rows_at = CG == 2 ? peer_address(smem_u32(rows_full), 0) : smem_u32(rows_full);   // the leading block's barriers
+        const uint32_t cols_at = CG == 2 ? peer_address(smem_u32(cols_full), 0) : smem_u32(cols_full);
         uint32_t sa = 0, pa = 1, sb = 0, pb = 1;
         const bool leader = elect_one();
         bool ok = true, withhold = p.withhold && blockIdx.x == 0, fresh = true;
@@ -320,9 +309,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 const uint32_t to = smem + (S::ROWS + sb) * S::SLOT, bar = cols_at + sb * 8;
                 if (leader) {
                     if (rank == 0) mbar_arrive_expect_tx(&cols_full[sb], 2 * nf * 128);   // of both blocks
-                    if constexpr (QUAD) {   // half of it from this pair, half from the other
-                        load_box_to(5u << rank, to + pair * nf * 64, &p.b[at + rank], bar, k * 64, w.col * S::NF + pair * nf / 2);
-                    } else if constexpr (CG == 2) {
+                    if constexpr (CG == 2) {
                         load_box<CG>(to, &p.b[at + rank], bar, k * 64, w.col * S::NF);
                     } else {
                         load_box<CG>(to, &p.b[at], bar, k * 64, w.col * S::NF);
@@ -361,8 +348,8 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 if (leader) {
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j) mma<CG>(acc, desc + ((at + j * 32) >> 4), desc + ((bt + j * 32) >> 4), idesc, k > 0 || j > 0);
-                    commit<CG>(&cols_empty[sb], QUAD ? 15u : 3u);
-                    if (last) commit<CG>(&rows_empty[sa], 3u << lead);
+                    commit<CG>(&cols_empty[sb]);
+                    if (last) commit<CG>(&rows_empty[sa]);
                 }
                 if (++sa == S::ROWS) {
                     sa = 0;
@@ -373,7 +360,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                     pb ^= 1u;
                 }
             }
-            if (ok && leader) commit<CG>(&acc_full[buf], 3u << lead);
+            if (ok && leader) commit<CG>(&acc_full[buf]);
             const unsigned item = w.item;
             w.next();
             fresh = w.item != item;
@@ -388,7 +375,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
         const int e = warp - 4, quarter = e & 3, part = e >> 2;
         const uint32_t staging = smem + S::STAGING + e * S::WARP_STAGING, dh_at = staging + 2048;
         float* bias = reinterpret_cast<float*>(raw_smem + (smem - smem_u32(raw_smem)) + S::BIAS) + e * 64;
-        const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(acc_empty), lead) : 0u;
+        const uint32_t acc_at = CG == 2 ? peer_address(smem_u32(acc_empty), 0) : 0u;
         auto release = [&](uint32_t buf) {   // this warp has read its accumulators
             tc_fence_before();
             __syncwarp();
@@ -973,7 +960,7 @@ template <int WHICH, int CG, typename T>
 na_status launch_tiles(const GluTcParams& p, unsigned tiles, cudaStream_t s) {
     const unsigned blocks = CG * std::min<unsigned>(tiles, kSms / CG);
     if constexpr (WHICH == kForward || WHICH == kSlopes)
-        return launch_glu(glu_pair_kernel<WHICH, CG, false, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
+        return launch_glu(glu_pair_kernel<WHICH, CG, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
     else
         return launch_glu(glu_tile_kernel<WHICH, CG, T>, p, blocks, CG, TileShape<CG>::THREADS, TileShape<CG>::BYTES, s, true);
 }
@@ -984,8 +971,6 @@ na_status launch_tiles(const GluTcParams& p, int blocks, cudaStream_t s) {
         return launch_tiles<kBoth, 2, T>(p, static_cast<unsigned>(kSms / 2), s);
     } else if constexpr (WHICH == kForward || WHICH == kSlopes) {
         const unsigned items = p.rows * p.groups;
-        if (blocks == 4)
-            return launch_glu(glu_pair_kernel<WHICH, 2, true, T>, p, 4 * std::min(items, kQuads), 4, PairShape<WHICH, 2>::THREADS, PairShape<WHICH, 2>::BYTES, s);
         return blocks == 2 ? launch_tiles<WHICH, 2, T>(p, items, s) : launch_tiles<WHICH, 1, T>(p, items, s);
     } else {
         const GluJob& job = p.job[WHICH == kWeights];
