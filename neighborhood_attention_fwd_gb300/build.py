@@ -19,7 +19,8 @@ SOURCES += [f"na_glu_fma_{t}.cu" for t in ("bf16", "f16", "f32")]
 SOURCES += [f"na_glu_{part}_{t}.cu" for part in ("fwd", "slopes", "grads") for t in ("bf16", "f16")]
 SOURCES += [f"na_win_{form}_{way}_{t}.cu" for form in ("soft", "diff") for way in ("fwd", "bwd") for t in ("bf16", "f16", "f32")]
 HEADERS = ["na_internal.h", "na_device.cuh", "na_tc_impl.cuh", "na_elem.cuh", "na_block.cuh",
-           "na_win.h", "na_win_impl.cuh", "na_rows.cuh", "na_add.h", "na_add_impl.cuh", "na_glu.h", "na_glu_tc.cuh", "na_glu_fma.cuh"]
+           "na_win.h", "na_win_impl.cuh", "na_rows.cuh", "na_add.h", "na_add_impl.cuh", "na_machine.h",
+           "na_glu_plan.h", "na_glu.h", "na_glu_tc.cuh", "na_glu_fma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]
 

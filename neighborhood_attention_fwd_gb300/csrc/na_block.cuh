@@ -11,6 +11,7 @@
 #include "../../include/na.h"
 #include "na_elem.cuh"
 #include "na_internal.h"
+#include "na_machine.h"
 
 namespace na {
 
@@ -69,8 +70,6 @@ inline na_status grid_tokens(int B, int ndim, const int* spatial, int heads, lon
     if (tokens > (1LL << 40) / heads || tokens * heads > (1LL << 40) / width) return NA_ERR_UNSUPPORTED;
     return NA_OK;
 }
-
-constexpr int kSms = 152;   // multiprocessors of a GB300: grids are sized for them
 
 inline na_status launch_result() { return cudaGetLastError() == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 

@@ -7,14 +7,10 @@
 
 #include "../../include/na.h"
 #include "na_device.cuh"
+#include "na_glu_plan.h"
 
 namespace na {
 namespace glu {
-
-// The products.  kForward: h from x and both weights.  kSlopes: the same product again, and dg, du from it and dh.
-// kTokens: dx = dg Wg + du Wu.  kWeights: dWg = dg^T x, dWu = du^T x.
-// kBoth: these two in one launch.
-enum Product { kForward = 0, kSlopes = 1, kTokens = 2, kWeights = 3, kBoth = 4 };
 
 struct GluParams {
     const void* x;        // [T, D]
@@ -210,19 +206,6 @@ __device__ __forceinline__ void with_act(int act, Call&& call) {
         default: call(ActTag<NA_ACT_SILU>{}); break;
     }
 }
-
-// Steps of the rows' operand that a block of the forward or of the slopes holds.
-template <int WHICH>
-constexpr int kPairRows = WHICH == kForward ? 6 : 5;
-
-inline unsigned up(long long n, long long by) { return static_cast<unsigned>((n + by - 1) / by); }
-
-// How a product is cut on CUDA cores: tiles of 128 or 32 rows and columns, splits of the summed axis (run: kWeights: tokens of one,
-// kTokens: pieces of 16 columns of dg, then du).
-struct FmaTile {
-    int rows, cols, splits;
-    long long run;
-};
 
 // Up to three matrices of 2-byte elements, rows of D elements in one place and of W >= D, whole chunks, in the other.
 struct GluCopies {

@@ -298,21 +298,22 @@ __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* d
 }
 
 template <typename T, int TR, int TC>
-na_status launch_fma(const GluParams& p, Product which, cudaStream_t s) {
-    const unsigned splits = p.splits;
+na_status launch_fma(const GluParams& p, Product which, dim3 grid, cudaStream_t s) {
     switch (which) {
-        case kForward: glu_fma_kernel<T, kForward, TR, TC><<<dim3(up(p.T, TR), up(p.F, TC / 2)), kGluThreads, 0, s>>>(p); break;
-        case kSlopes: glu_fma_kernel<T, kSlopes, TR, TC><<<dim3(up(p.T, TR), up(p.F, TC / 2)), kGluThreads, 0, s>>>(p); break;
-        case kTokens: glu_fma_kernel<T, kTokens, TR, TC><<<dim3(up(p.T, TR), up(p.D, TC), splits), kGluThreads, 0, s>>>(p); break;
-        default: glu_fma_kernel<T, kWeights, TR, TC><<<dim3(up(p.F, TR), up(p.D, TC), 2 * splits), kGluThreads, 0, s>>>(p); break;
+        case kForward: glu_fma_kernel<T, kForward, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
+        case kSlopes: glu_fma_kernel<T, kSlopes, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
+        case kTokens: glu_fma_kernel<T, kTokens, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
+        default: glu_fma_kernel<T, kWeights, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
     }
     return launch_result();
 }
 
 template <typename T>
 na_status launch_fma(const GluParams& p, Product which, const FmaTile& tile, cudaStream_t s) {
-    if (tile.rows == 128) return tile.cols == 128 ? launch_fma<T, 128, 128>(p, which, s) : launch_fma<T, 128, 32>(p, which, s);
-    return tile.cols == 128 ? launch_fma<T, 32, 128>(p, which, s) : launch_fma<T, 32, 32>(p, which, s);
+    const FmaGrid n = fma_grid(which, p.T, p.D, p.F, tile);
+    const dim3 grid(n.x, n.y, n.z);
+    if (tile.rows == 128) return tile.cols == 128 ? launch_fma<T, 128, 128>(p, which, grid, s) : launch_fma<T, 128, 32>(p, which, grid, s);
+    return tile.cols == 128 ? launch_fma<T, 32, 128>(p, which, grid, s) : launch_fma<T, 32, 32>(p, which, grid, s);
 }
 
 template <typename T>
