@@ -84,7 +84,8 @@ __device__ __forceinline__ void place(float (*sm)[TS + 4], int t, const T (&raw)
 }
 
 // Products on CUDA cores.  A block makes TR x TC elements (kForward, kSlopes: TR rows x TC / 2 columns of g and the same of u);
-// rows along blockIdx.x, columns along blockIdx.y; along blockIdx.z the splits of the summed axis, kWeights: of dWg and dWu each.
+// rows along blockIdx.x, columns along blockIdx.y; along blockIdx.z the splits of the summed axis, kWeights: of dWg and dWu each
+// (fma_grid).
 // A thread's elements are two runs of GR rows by two of GC columns, half a tile apart, so that g and u of an element are its own.
 template <typename T, int WHICH, int TR, int TC>
 __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_kernel(const GluParams p) {
@@ -93,8 +94,15 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
     constexpr int GR = TR / 32, GC = TC / 32, R = 2 * GR, NA = TR / 16, NB = TC / 16;
     __shared__ __align__(16) float sa[2][kDepth][TR + 4], sb[2][kDepth][TC + 4];
     const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    const long long m0 = static_cast<long long>(blockIdx.x) * TR, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? TC / 2 : TC);
-    const int half = WHICH == kWeights ? blockIdx.z & 1 : 0, split = WHICH == kWeights ? blockIdx.z >> 1 : blockIdx.z;
+    int half = 0, split = blockIdx.z, row_tile = blockIdx.x;
+    if constexpr (WHICH == kWeights) {
+        const int tiles = (p.F + TR - 1) / TR, turn = row_tile / tiles;
+        half = blockIdx.z & 1;
+        split = turn * static_cast<int>(gridDim.z >> 1) + static_cast<int>(blockIdx.z >> 1);
+        row_tile -= turn * tiles;
+        if (split >= p.splits) return;
+    }
+    const long long m0 = static_cast<long long>(row_tile) * TR, n0 = static_cast<long long>(blockIdx.y) * (PAIR ? TC / 2 : TC);
     const T *x = static_cast<const T*>(p.x), *wg = static_cast<const T*>(p.wg), *wu = static_cast<const T*>(p.wu);
     const T *dg = static_cast<const T*>(p.dg), *du = static_cast<const T*>(p.du);
     const bool wide = p.D % Elem<T>::EPC == 0;

@@ -29,14 +29,16 @@ struct FmaTile {
     long long run;
 };
 
-// Blocks of a product on CUDA cores: tiles of rows, tiles of columns, splits (kWeights: of dWg and dWu each).
+// Blocks of a product on CUDA cores: tiles of rows, tiles of columns, splits (kWeights: of dWg and dWu each).  A grid has 65535 places
+// along z: past 32767 splits (over 2^28 tokens) the others follow along x, behind the rows.
+constexpr int kMostZ = 32767;
 struct FmaGrid {
     unsigned x, y, z;
 };
 inline FmaGrid fma_grid(Product which, long long T, int D, int F, const FmaTile& n) {
     if (which == kForward || which == kSlopes) return {up(T, n.rows), up(F, n.cols / 2), 1};
     if (which == kTokens) return {up(T, n.rows), up(D, n.cols), static_cast<unsigned>(n.splits)};
-    return {up(F, n.rows), up(D, n.cols), 2u * n.splits};
+    return {up(F, n.rows) * up(n.splits, kMostZ), up(D, n.cols), 2u * std::min(n.splits, kMostZ)};
 }
 
 constexpr int kGluMaxWidth = 1 << 20;              // of D and F

@@ -1,0 +1,36 @@
+"""GPU tests of the gated feed-forward product over long sums: every step of a sum over tokens counts, whatever the way the
+sum is cut.  dh is zero but for a few tokens at the ends and at both sides of every place where a sum is cut, so that the
+gradients of the weights are sums of few terms with a bound as tight as these."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.tail as ot
+import test_block_ops as tb
+from test_tail_plan import BF16, FP16, FP32, planner  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+TYPES, E, close, f64, status_ok = tb.TYPES, tb.E, tb.close, tb.f64, tb.status_ok
+CODES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
+
+
+def test_more_splits_than_a_grid_has_places(planner, cuda_lib):  # noqa: F811
+    """fp32, over 2^28 tokens: more than 32767 splits of 8192 tokens.  Values are whole numbers and halves: every sum is exact."""
+    na = cuda_lib
+    T, D, F = (1 << 28) + 20000, 1, 1
+    (p,) = planner([(T, D, F, FP32)])
+    run, splits = p["weights"]["run"], p["weights"]["splits"]
+    assert splits > 32767
+    x = torch.full((T, D), 0.5, device="cuda")
+    dh = torch.zeros(T, F, device="cuda")
+    at = sorted({t for s in (0, 1, 16384, 32766, 32767, 32768, splits - 1) for t in (s * run, s * run + 1, s * run - 1) if 0 <= t < T} | {T - 1})
+    at = torch.tensor(at, device="cuda")
+    dh[at, 0] = (1 + torch.arange(len(at), device="cuda")).float()
+    wg, wu = torch.full((F, D), 4.0, device="cuda"), torch.full((F, D), -2.0, device="cuda")
+    bg, bu = torch.zeros(F, device="cuda"), torch.full((F,), 3.0, device="cuda")   # g = 2, u = 2
+    dx, dwg, dwu, dbg, dbu = (torch.full_like(t, 9.0) for t in (x, wg, wu, bg, bu))
+    na.na_glu_bwd(dh, x, wg, wu, dx, dwg, dwu, bg, bu, dbg, dbu, act="relu")
+    status_ok(na)
+    total = float(dh.double().sum())   # dg = dh u = 2 dh, du = dh g = 2 dh
+    assert float(dwg) == float(dwu) == total and float(dbg) == float(dbu) == 2 * total
+    assert torch.equal(dx[at], dh[at] * (2 * 4 - 2 * 2)) and int(torch.count_nonzero(dx)) == len(at)
