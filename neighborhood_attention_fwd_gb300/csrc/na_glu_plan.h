@@ -276,9 +276,10 @@ inline GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
         if (n.tokens_fma.splits > 1) floats = static_cast<size_t>(n.tokens_fma.splits) * T * D;
         if (n.weights_fma.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights_fma.splits) * 2 * F * D);
     }
-    // column sums: four blocks a multiprocessor, at least 64 tokens each, at most 8192 in one sum
+    // column sums: four blocks a multiprocessor, at least 64 tokens each, at most 8192 (of more than 2^28 tokens up to 65536: a
+    // thread of the kernel adds every eighth token, so that no sum takes more than 8192 terms)
     const long long columns = 2LL * up(F, 32 * chunk);
-    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (4 * kSms + columns - 1) / columns)), 1024LL);
+    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (4 * kSms + columns - 1) / columns)), 32768LL);
     n.column_run = (T + runs - 1) / runs;
     n.runs = static_cast<int>((T + n.column_run - 1) / n.column_run);
     n.partial = up256(std::max(floats, static_cast<size_t>(n.runs) * 2 * F) * sizeof(float));

@@ -14,6 +14,24 @@ TYPES, E, close, f64, status_ok = tb.TYPES, tb.E, tb.close, tb.f64, tb.status_ok
 CODES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sums_over_tokens_of_one_value(dtype, cuda_lib):
+    """dbg and dbu over 2^25 tokens of one value, 0.1 in the type.  In one sequence of fp32 additions every term is rounded the same way and
+    the sum is off by percents; here a sum takes at most 8192 terms, then the runs (4096) are added eight warps a block."""
+    na = cuda_lib
+    T, D, F = 1 << 25, 8, 8
+    x = torch.zeros(T, D, dtype=TYPES[dtype], device="cuda")
+    wg, wu = torch.zeros(F, D, dtype=x.dtype, device="cuda"), torch.zeros(F, D, dtype=x.dtype, device="cuda")
+    bg, bu = torch.ones(F, dtype=x.dtype, device="cuda"), torch.ones(F, dtype=x.dtype, device="cuda")
+    dh = torch.full((T, F), 0.1, dtype=x.dtype, device="cuda")
+    dbg, dbu = torch.empty_like(bg), torch.empty_like(bu)
+    na.na_glu_bwd(dh, x, wg, wu, bg=bg, bu=bu, dbg=dbg, dbu=dbu, act="relu")   # g = u = 1: dg = du = dh
+    status_ok(na)
+    want = np.full(F, T * float(dh[0, 0]))
+    close("dbg", dbg, want, (1024 + 8 + 512 + 8) * E * want, TYPES[dtype])   # a thread's 1024 tokens, eight warps, 512 runs of a warp, eight warps
+    assert torch.equal(dbg, dbu)
+
+
 def test_more_splits_than_a_grid_has_places(planner, cuda_lib):  # noqa: F811
     """fp32, over 2^28 tokens: more than 32767 splits of 8192 tokens.  Values are whole numbers and halves: every sum is exact."""
     na = cuda_lib

@@ -98,6 +98,8 @@ def check(size, p):
     assert p["workspace"] >= 2 * p["array"] + p["partial"]
     assert 0 < (p["runs"] - 1) * p["column_run"] + 1 <= T <= p["runs"] * p["column_run"] and p["runs"] <= 65535
     assert p["partial"] >= 4 * p["runs"] * 2 * F
+    # no sum of the columns takes more than 8192 terms: a thread adds every eighth token of a run, then the runs are added
+    assert up(p["column_run"], 8) <= 8192 and p["runs"] <= 32768 and (T > 2 ** 28 or p["column_run"] <= 8192)
     for name, size_ in (("tokens", T * D), ("weights", 2 * F * D)):
         if p[name]["splits"] > 1:
             assert p["partial"] >= 4 * p[name]["splits"] * size_
