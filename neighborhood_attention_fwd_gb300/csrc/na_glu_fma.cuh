@@ -85,9 +85,9 @@ __device__ __forceinline__ void place(float (*sm)[TS + 4], int t, const T (&raw)
 
 // Products on CUDA cores.  A block makes TR x TC elements (kForward, kSlopes: TR rows x TC / 2 columns of g and the same of u);
 // rows along blockIdx.x, columns along blockIdx.y; along blockIdx.z the splits of the summed axis, kWeights: of dWg and dWu each
-// (fma_grid).
+// (fma_grid).  LONG (kForward, kSlopes): sums over more than kMostProducts channels, which are added up in runs of that many.
 // A thread's elements are two runs of GR rows by two of GC columns, half a tile apart, so that g and u of an element are its own.
-template <typename T, int WHICH, int TR, int TC>
+template <typename T, int WHICH, int TR, int TC, bool LONG>
 __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_kernel(const GluParams p) {
     constexpr bool PAIR = WHICH == kForward || WHICH == kSlopes;
     constexpr bool A_ROWS = WHICH == kWeights, B_ROWS = !PAIR;
@@ -137,11 +137,23 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
             fetch<T, true>(b, n0 + rb, k0 + k + kb, fb);
         }
     };
-    uint64_t acc[R][GC];   // pairs of columns
+    uint64_t acc[R][GC], total[LONG ? R : 1][LONG ? GC : 1];   // pairs of columns
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < GC; ++j) acc[i][j] = 0;
+        for (int j = 0; j < GC; ++j) {
+            acc[i][j] = 0;
+            if constexpr (LONG) total[i][j] = 0;
+        }
+    auto add_up = [&]() {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < GC; ++j) {
+                total[i][j] = add2(total[i][j], acc[i][j]);
+                acc[i][j] = 0;
+            }
+    };
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q)
         if (first + q < last) load(first + q, pa[q], pb[q]);
@@ -177,10 +189,21 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
         }
         st ^= 1;
     };
-    for (long long i = first; i < last; i += AHEAD)
+    static_assert(kMostProducts % (kDepth * AHEAD) == 0, "a run ends between turns of the loop");
+    for (long long i = first; i < last; i += AHEAD) {
 #pragma unroll
         for (int q = 0; q < AHEAD; ++q)
             if (i + q < last) piece(i + q, pa[q], pb[q]);
+        if constexpr (LONG)
+            if ((i + AHEAD) % (kMostProducts / kDepth) == 0) add_up();
+    }
+    if constexpr (LONG) {
+        add_up();
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < GC; ++c) acc[r][c] = total[r][c];
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const long long row = m0 + (r < GR ? ty * GR + r : TR / 2 + ty * GR + r - GR);
@@ -307,11 +330,17 @@ __global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* d
 
 template <typename T, int TR, int TC>
 na_status launch_fma(const GluParams& p, Product which, dim3 grid, cudaStream_t s) {
+    if constexpr (TR == TC)   // as plan_fma
+        if (p.D > kMostProducts && (which == kForward || which == kSlopes)) {
+            if (which == kForward) glu_fma_kernel<T, kForward, TR, TC, true><<<grid, kGluThreads, 0, s>>>(p);
+            else glu_fma_kernel<T, kSlopes, TR, TC, true><<<grid, kGluThreads, 0, s>>>(p);
+            return launch_result();
+        }
     switch (which) {
-        case kForward: glu_fma_kernel<T, kForward, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
-        case kSlopes: glu_fma_kernel<T, kSlopes, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
-        case kTokens: glu_fma_kernel<T, kTokens, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
-        default: glu_fma_kernel<T, kWeights, TR, TC><<<grid, kGluThreads, 0, s>>>(p); break;
+        case kForward: glu_fma_kernel<T, kForward, TR, TC, false><<<grid, kGluThreads, 0, s>>>(p); break;
+        case kSlopes: glu_fma_kernel<T, kSlopes, TR, TC, false><<<grid, kGluThreads, 0, s>>>(p); break;
+        case kTokens: glu_fma_kernel<T, kTokens, TR, TC, false><<<grid, kGluThreads, 0, s>>>(p); break;
+        default: glu_fma_kernel<T, kWeights, TR, TC, false><<<grid, kGluThreads, 0, s>>>(p); break;
     }
     return launch_result();
 }

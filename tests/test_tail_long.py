@@ -32,6 +32,33 @@ def test_sums_over_tokens_of_one_value(dtype, cuda_lib):
     assert torch.equal(dbg, dbu)
 
 
+@pytest.mark.parametrize("dtype,T,D,F,tile", [("fp32", 3, (1 << 18) + 5, 9, 32), ("fp32", 1300, 1 << 18, 700, 128), ("bf16", 2, 1 << 20, 5, 32), ("fp32", 200, 8193, 40, 32)])
+def test_products_over_many_channels_of_one_value(dtype, T, D, F, tile, planner, cuda_lib):  # noqa: F811
+    """g and u over D channels of one product, 0.3 x 0.7 in the type, on FMA units: runs of 8192 are added up, not all in one sequence
+    (which was off by 0.3% at 2^18).  A run's path is 8192 additions, then the runs."""
+    na = cuda_lib
+    (p,) = planner([(T, D, F, CODES[dtype])])
+    assert not p["tensor"] and p["forward"]["rows"] == p["slopes"]["rows"] == tile
+    x = torch.full((T, D), 0.3, dtype=TYPES[dtype], device="cuda")
+    w = torch.full((F, D), 0.7, dtype=TYPES[dtype], device="cuda")
+    w2 = w * (1.0 / 1024)   # exact; h stays in range
+    h = torch.empty(T, F, dtype=x.dtype, device="cuda")
+    na.na_glu(x, w, w2, h, act="relu")
+    g = D * float(x[0, 0]) * float(w[0, 0])
+    u, path = g / 1024, (8192 + 16 + -(-D // 8192)) * E
+    want = np.full((T, F), g * u)
+    close("h", h, want, (2 * path + path * path + 2 * E) * want, TYPES[dtype])
+    # the gradients' g and u: with dh of one, dbu sums act(g) over the tokens, dbg sums u
+    bg, bu = torch.zeros(F, dtype=x.dtype, device="cuda"), torch.zeros(F, dtype=x.dtype, device="cuda")
+    dbg, dbu = torch.empty_like(bg), torch.empty_like(bu)
+    na.na_glu_bwd(torch.ones_like(h), x, w, w2, bg=bg, bu=bu, dbg=dbg, dbu=dbu, act="relu")
+    status_ok(na)
+    step = torch.finfo(x.dtype).eps / 2   # dg and du are rounded to the type
+    for name, got, one in (("dbg", dbg, u), ("dbu", dbu, g)):
+        want = np.full(F, T * one)
+        close(name, got, want, (path + (T + 16) * E + step * (1 + path)) * want, TYPES[dtype])
+
+
 def test_more_splits_than_a_grid_has_places(planner, cuda_lib):  # noqa: F811
     """fp32, over 2^28 tokens: more than 32767 splits of 8192 tokens.  Values are whole numbers and halves: every sum is exact."""
     na = cuda_lib

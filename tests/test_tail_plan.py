@@ -111,6 +111,9 @@ def check(size, p):
         for name, n in (("tokens", pieces), ("weights", T)):
             t = p[name]
             assert (t["splits"] - 1) * t["run"] < n <= t["splits"] * t["run"], name
+            assert t["run"] * (16 if name == "tokens" else 1) <= 8192   # products in one sum
+        for name in ("forward", "slopes"):   # more than 8192 channels: kernels that add up runs of them
+            assert D <= 8192 or p[name]["rows"] == p[name]["cols"]
         x, _, z = p["weights"]["grid"]
         tiles = up(F, p["weights"]["rows"])
         assert x % tiles == 0 and z % 2 == 0 and (x // tiles) * (z // 2) >= p["weights"]["splits"]   # places of the splits
