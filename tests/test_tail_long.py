@@ -79,3 +79,113 @@ def test_more_splits_than_a_grid_has_places(planner, cuda_lib):  # noqa: F811
     total = float(dh.double().sum())   # dg = dh u = 2 dh, du = dh g = 2 dh
     assert float(dwg) == float(dwu) == total and float(dbg) == float(dbu) == 2 * total
     assert torch.equal(dx[at], dh[at] * (2 * 4 - 2 * 2)) and int(torch.count_nonzero(dx)) == len(at)
+
+
+def cut_tokens(p, T):
+    """Tokens on both sides of every kind of place where the sums over tokens are cut: steps, parts side by side, turns of them, ends."""
+    w = p["weights"]
+    if p["tensor"]:
+        edges = {0, 1, w["ways"] - 1, w["ways"], w["ways"] + 1, w["steps"] - 1, w["steps"]}
+        edges |= {t * w["run"] * w["ways"] + d for t in range(w["splits"] // w["ways"] + 1) for d in (-1, 0, 1, w["ways"] - 1)}
+        edges = {64 * e for e in edges}
+    else:
+        edges = {s * w["run"] for s in (0, 1, 2, w["splits"] // 2, w["splits"] - 1, w["splits"])} | {16, T // 16 * 16}
+    edges |= {s * p["column_run"] for s in (0, 1, p["runs"] - 1, p["runs"])}
+    return sorted({t + d for t in edges for d in (-1, 0) if 0 <= t + d < T} | {0, T - 1})
+
+
+LONG = [
+    # dtype, T, D, F, one launch for dx and the weights' sums
+    ("bf16", 40001, 72, 700, True), ("fp16", 70003, 136, 520, True), ("bf16", 262147, 256, 688, True), ("fp16", 60000, 40, 1000, True),
+    ("bf16", 60001, 99, 1000, True), ("fp16", 70003, 264, 520, False), ("bf16", 300001, 520, 100, False), ("bf16", 40000, 264, 88, False), ("fp16", 20000, 32, 24, False), ("bf16", 5001, 72, 2001, False), ("fp16", 100003, 8, 8, False),
+    ("bf16", 30000, 1032, 1304, False), ("bf16", 9000, 1001, 260, False), ("fp32", 9000, 8, 12, False), ("fp32", 70001, 40, 30, False), ("fp32", 20001, 260, 130, False),
+]
+
+
+@pytest.mark.parametrize("dtype,T,D,F,both", LONG)
+def test_every_token_counts(dtype, T, D, F, both, planner, cuda_lib):  # noqa: F811
+    na = cuda_lib
+    (p,) = planner([(T, D, F, CODES[dtype])])
+    assert both == bool(p["tensor"] and p["tokens"]["workers"])
+    type_ = TYPES[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    spread = lambda *s: torch.empty(s, dtype=type_, device="cuda").uniform_(-1, 1, generator=gen)
+    x, wg, wu, bg, bu = spread(T, D), spread(F, D) * (D ** -0.5), spread(F, D) * (D ** -0.5), spread(F), spread(F)
+    wg, wu = wg * 2, wu * 2
+    full = spread(T, F)
+    at = torch.tensor(cut_tokens(p, T), device="cuda")
+    dh = torch.zeros_like(full)
+    dh[at] = full[at]
+    dx, rest = torch.full_like(x, 9.0), [torch.full_like(t, 9.0) for t in (wg, wu, bg, bu)]
+    na.na_glu_bwd(dh, x, wg, wu, dx, rest[0], rest[1], bg, bu, rest[2], rest[3])
+    status_ok(na)
+    X, WG, WU, BG, BU, DH = (f64(t) for t in (x[at], wg, wu, bg, bu, dh[at]))
+    ref = ot.glu_bwd(DH, X, WG, WU, BG, BU, "silu")
+    _, g, u = ot.glu(X, WG, WU, BG, BU, "silu")
+    depth = 2 * (D + 16) * E
+    eg, eu = (depth * (np.abs(X) @ np.abs(W).T + np.abs(b)) for W, b in ((WG, BG), (WU, BU)))
+    a, sl = ot.act(g, "silu"), ot.slope(g, "silu")
+    r = 32 * E if dtype == "fp32" else 2.0 ** -17
+    ea, esl = r * np.abs(a) + 1.2 * eg, r * (1 + np.abs(g)) + 0.8 * eg
+    info = torch.finfo(type_)
+    round_ = lambda v, e: info.eps / 2 * (np.abs(v) + e) + e + info.smallest_normal * info.eps / 2
+    dg, du = DH * u * sl, DH * a
+    edg = round_(dg, np.abs(DH) * (np.abs(u) * esl + np.abs(sl) * eu + esl * eu) + 4 * E * np.abs(dg))
+    edu = round_(du, np.abs(DH) * ea + 2 * E * np.abs(du))
+    dg, du = np.abs(dg) + edg, np.abs(du) + edu
+    n = 2 * (len(at) + 16) * E   # the other terms are zeros
+    slack = [edg @ np.abs(WG) + edu @ np.abs(WU) + 2 * (2 * F + 16) * E * (dg @ np.abs(WG) + du @ np.abs(WU)),
+             edg.T @ np.abs(X) + n * (dg.T @ np.abs(X)), edu.T @ np.abs(X) + n * (du.T @ np.abs(X)), edg.sum(0) + n * dg.sum(0), edu.sum(0) + n * du.sum(0)]
+    for name, got, want, e in zip(("dx", "dwg", "dwu", "dbg", "dbu"), [dx[at]] + rest, ref, slack):
+        close(name, got, want, e, type_)
+    dx[at] = 0
+    assert not dx.any()
+    # a token that were left out would show: the oracle without any one of them is outside the bounds
+    for k in range(len(at)):
+        missing = np.abs((DH[k] * u[k] * sl[k])[:, None] * X[k])
+        assert (missing > slack[1] + info.eps * np.abs(ref[1])).any(), int(at[k])
+    # dh of all tokens: dx of rows at both sides of tiles, and each gradient alone gives the same bits
+    na.na_glu_bwd(full, x, wg, wu, dx, rest[0], rest[1], bg, bu, rest[2], rest[3])
+    rows = torch.tensor(sorted({t + d for t in range(0, T, max(256, T // 2048 * 256)) for d in (-1, 0, 1, 127, 128) if 0 <= t + d < T} | set(range(T - 3, T)))[:400], device="cuda")
+    X, DH = f64(x[rows]), f64(full[rows])
+    want, _, _, _, _ = ot.glu_bwd(DH, X, WG, WU, BG, BU, "silu")
+    _, g, u = ot.glu(X, WG, WU, BG, BU, "silu")
+    eg, eu = (depth * (np.abs(X) @ np.abs(W).T + np.abs(b)) for W, b in ((WG, BG), (WU, BU)))
+    a, sl = ot.act(g, "silu"), ot.slope(g, "silu")
+    ea, esl = r * np.abs(a) + 1.2 * eg, r * (1 + np.abs(g)) + 0.8 * eg
+    dg, du = DH * u * sl, DH * a
+    edg = round_(dg, np.abs(DH) * (np.abs(u) * esl + np.abs(sl) * eu + esl * eu) + 4 * E * np.abs(dg))
+    edu = round_(du, np.abs(DH) * ea + 2 * E * np.abs(du))
+    dg, du = np.abs(dg) + edg, np.abs(du) + edu
+    close("dx", dx[rows], want, edg @ np.abs(WG) + edu @ np.abs(WU) + 2 * (2 * F + 16) * E * (dg @ np.abs(WG) + du @ np.abs(WU)), type_)
+    alone = [torch.full_like(t, 5.0) for t in [dx] + rest]
+    na.na_glu_bwd(full, x, wg, wu, alone[0], None, None, bg, bu)
+    na.na_glu_bwd(full, x, wg, wu, None, alone[1], alone[2], bg, bu)
+    na.na_glu_bwd(full, x, wg, wu, None, None, None, bg, bu, alone[3])
+    na.na_glu_bwd(full, x, wg, wu, None, None, None, bg, bu, None, alone[4])
+    status_ok(na)
+    assert all(torch.equal(one, all_) for one, all_ in zip(alone, [dx] + rest))
+
+
+def test_the_shared_launch_gives_up_a_copy_that_never_lands(planner, cuda_lib):  # noqa: F811
+    """As test_tail_wait.py, at a size whose dx and weights' sums share a launch."""
+    na = cuda_lib
+    T, D, F = 40001, 72, 700
+    (p,) = planner([(T, D, F, BF16)])
+    assert p["tokens"]["workers"]
+    x, wg, wu, dh = (tb.randn(s, "bf16", i).cuda() for i, s in enumerate(((T, D), (F, D), (F, D), (T, F))))
+    out = [torch.empty_like(t) for t in (x, wg, wu)]
+    run = lambda: na.na_glu_bwd(dh, x, wg, wu, *out)
+    run()
+    status_ok(na)
+    ref = [t.clone() for t in out]
+    na.na_debug_wait_hook(2_000_000, True)
+    try:
+        run()
+        st, raw = na.na_device_status()
+    finally:
+        na.na_debug_wait_hook(0, False)
+    assert st == 5 and raw & 0xF000 == 0x5000, (st, hex(raw))
+    run()
+    status_ok(na)
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
