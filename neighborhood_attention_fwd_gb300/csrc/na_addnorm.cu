@@ -348,7 +348,7 @@ na_status na_addnorm_bwd(const void* dh, const void* ds, const void* s, const vo
     }
     if (n.ring && (st = device_status_word(&p.err)) != NA_OK) return st;
     if (p.sums && !ws) {
-        if (cudaMallocAsync(&ws, need, cs) != cudaSuccess) return NA_ERR_WORKSPACE;
+        if (!taken(cudaMallocAsync(&ws, need, cs))) return NA_ERR_WORKSPACE;
         owned = true;
     }
     p.partial = static_cast<float*>(ws);

@@ -568,10 +568,8 @@ bool allow_shared(const void* kernel) {
     std::lock_guard<std::mutex> lk(mu);
     if (done.count({kernel, dev})) return true;
     cudaFuncAttributes a{};
-    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess ||
-        cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(a.sharedSizeBytes)) !=
-            cudaSuccess)
+    if (!taken(cudaFuncGetAttributes(&a, kernel)) || !taken(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) ||
+        !taken(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(a.sharedSizeBytes))))
         return false;
     try {
         done.insert({kernel, dev});
@@ -754,7 +752,7 @@ na_status na_bwd(const void* q, const void* k, const void* v, const void* o, con
         if (workspace_bytes < need) return NA_ERR_WORKSPACE;
         if (!aligned16(ws)) return NA_ERR_ALIGNMENT;
     } else {
-        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+        if (!na::taken(cudaMallocAsync(&ws, need, s))) return NA_ERR_WORKSPACE;
         owned = true;
     }
     float* delta = static_cast<float*>(ws);
@@ -1028,7 +1026,7 @@ na_status na_rpb_grad(const void* dattn, float* drpb, int B, int ndim, const int
         if (workspace_bytes < need) return NA_ERR_WORKSPACE;
         if (!aligned16(ws)) return NA_ERR_ALIGNMENT;
     } else {
-        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+        if (!na::taken(cudaMallocAsync(&ws, need, s))) return NA_ERR_WORKSPACE;
         owned = true;
     }
     p.a = dattn;

@@ -85,7 +85,7 @@ na_status launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_
     a.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &a;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess ? NA_OK : NA_ERR_CUDA;
+    return taken(cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...)) ? NA_OK : NA_ERR_CUDA;
 }
 
 // Waits until the kernel before has ended and its results are there; returns at once in a kernel that is launched plainly.

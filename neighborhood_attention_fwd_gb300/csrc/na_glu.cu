@@ -202,7 +202,7 @@ na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, 
     if (width == D) return launch_tensor(p, kForward, plan_tiles(kForward, rows, D, F), dtype, s);
     const size_t tokens = up256(static_cast<size_t>(rows) * width * es), weights = up256(static_cast<size_t>(F) * width * es);
     void* ws = nullptr;
-    if (cudaMallocAsync(&ws, tokens + 2 * weights, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+    if (!taken(cudaMallocAsync(&ws, tokens + 2 * weights, s))) return NA_ERR_WORKSPACE;
     char* at = static_cast<char*>(ws);
     const GluCopies copies{{x, wg, wu}, {at, at + tokens, at + tokens + weights}, {rows, F, F}, D, width};
     st = launch_copies(copies, true, s);
@@ -254,7 +254,7 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
             if (spans_overlap(sws, q)) return NA_ERR_INVALID_ARG;
         for (const Span& q : out)
             if (spans_overlap(sws, q)) return NA_ERR_INVALID_ARG;
-    } else if (cudaMallocAsync(&ws, need, s) != cudaSuccess) {
+    } else if (!taken(cudaMallocAsync(&ws, need, s))) {
         return NA_ERR_WORKSPACE;
     }
     GluParams p{};

@@ -953,7 +953,7 @@ na_status launch_glu(Kernel* kernel, const GluTcParams& p, unsigned blocks, int 
         a[c.numAttrs].val.programmaticStreamSerializationAllowed = 1;
         ++c.numAttrs;
     }
-    return cudaLaunchKernelEx(&c, kernel, p) == cudaSuccess ? NA_OK : NA_ERR_CUDA;
+    return taken(cudaLaunchKernelEx(&c, kernel, p)) ? NA_OK : NA_ERR_CUDA;
 }
 
 template <int WHICH, int CG, typename T>

@@ -9,8 +9,17 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 namespace na {
+
+// True where a runtime call succeeded.  A call that was refused (no memory, say) leaves its error behind, which the next launch
+// would find and report as its own: it is taken back here.
+inline bool taken(cudaError_t e) {
+    if (e == cudaSuccess) return true;
+    (void)cudaGetLastError();
+    return false;
+}
 
 // Division of 32-bit unsigned values by a divisor fixed for a launch, by multiplication (Granlund
 // and Montgomery, "Division by invariant integers using multiplication", 1994): with s = ceil(log2 d)

@@ -838,7 +838,7 @@ na_status na_layernorm_bwd(const void* dy, const void* x, const float* w, const 
         return dtype == NA_FP16 ? launch_few<__half>(p, n, s) : launch_few<float>(p, n, s);
     }
     if (dw && !ws) {
-        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return NA_ERR_WORKSPACE;
+        if (!taken(cudaMallocAsync(&ws, need, s))) return NA_ERR_WORKSPACE;
         owned = true;
     }
     p.partial = static_cast<float*>(ws);

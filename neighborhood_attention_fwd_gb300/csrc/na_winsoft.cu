@@ -288,7 +288,7 @@ na_status na_diff_softmax_bwd(const void* x1, const void* x2, const float* lam, 
     }
     if ((st = device_status_word(&w.err)) != NA_OK) return st;
     if (!lam_per_row && !ws) {
-        if (cudaMallocAsync(&ws, diff_workspace(w), s) != cudaSuccess) return NA_ERR_WORKSPACE;
+        if (!taken(cudaMallocAsync(&ws, diff_workspace(w), s))) return NA_ERR_WORKSPACE;
         owned = true;
     }
     w.x1 = x1;
