@@ -392,7 +392,7 @@ typedef enum {
  *   s = residual * x + scale * gate * (post(y) * post_w + post_b),   h = norm(s) * w + b.
  * x: the stream, y: the block's output, s: the stream after it, h: what the next block reads.  post and norm are kinds
  * of norm; without one, y is taken as it is, and h is null.  h is made from the fp32 values that s rounds.
- * Vectors are fp32 whatever the tensors' type, each may be null (weights and gates of one, shifts of zero; null where its
+ * Vectors are fp32 whatever the tensors' type, contiguous and 16-byte aligned, each may be null (weights and gates of one, shifts of zero; null where its
  * norm is none): post_w, post_b [C]; gate [gate_groups, C]; w, b [w_groups, C].  The rows are cut into that many runs of
  * equal length (a batch entry each, say), run i taking vector i; groups of 1 serve all rows.  w_groups and gate_groups
  * divide rows and are equal where both exceed 1 (else NA_ERR_INVALID_ARG), at most 32768 (else NA_ERR_UNSUPPORTED).
@@ -437,11 +437,12 @@ typedef enum {
 
 /*
  * The gated feed-forward product: h = act(x Wg^T + bg) * (x Wu^T + bu) for `rows` tokens, both products, the activation
- * and the gating in one kernel.  x: [rows, D], wg, wu: [F, D] (halves of one [2 F, D] array will do), bg, bu: [F] or null
+ * and the gating in one kernel.  x: [rows, D], wg, wu: [F, D] (halves of one [2 F, D] array will do where
+ * F * D elements are whole 16 bytes: wu starts on 16 bytes too), bg, bu: [F] or null
  * (zeros), h: [rows, F], all of the tensors' type.  Sums in fp32, h rounded once.  2-byte tensors run on tensor
- * cores (where D is no multiple of 8, from some size on, on copies of x, wg and wu allocated on the stream; where it is small
- * or above 2^16 (fp16) or 2^18, on FMA units), fp32 on FMA units.  rows up to 2^31 - 256, D and F up to 2^20 (else
- * NA_ERR_UNSUPPORTED).
+ * cores (where D is no multiple of 8, from some size on, on copies of x, wg and wu that every call allocates on the stream and
+ * makes anew; where it is small or above 2^16 (fp16) or 2^18, on FMA units), fp32 on FMA units.  rows up to 2^31 - 256, D and F
+ * up to 2^20, rows * D and rows * F up to 2^40 (else NA_ERR_UNSUPPORTED).
  */
 na_status na_glu(const void* x, const void* wg, const void* wu, const void* bg, const void* bu, void* h, int64_t rows, int D,
                  int F, na_glu_act act, na_dtype dtype, void* stream);
@@ -452,7 +453,8 @@ size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype);
 
 /*
  * Gradients of na_glu from dh and its inputs; nothing of the forward is kept, g = x Wg^T + bg and u = x Wu^T + bu are made
- * again.  With dg = dh * u * act'(g) and du = dh * act(g), each rounded to the tensors' type:
+ * again.  With dg = dh * u * act'(g) and du = dh * act(g), each rounded to the tensors' type (fp16: infinite past 65504, in steps
+ * of 2^-24 below 2^-14; scale dh so that they stay between):
  *   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg = sum over tokens of dg,  dbu = sum over tokens of du,
  * laid out and typed as their tensors, overwritten.  dx may be null, dwg and dwu both null, dbg and dbu each (and must
  * be where the bias is).  Workspace: null (allocated on the stream), or na_glu_bwd_workspace_size bytes.

@@ -6,8 +6,11 @@
 //   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg, dbu = column sums of dg, du
 //
 // Nothing is kept from the forward: the backward makes g and u again (4 T D F of its 12 T D F operations), so training holds
-// no array of T F elements between the passes.  dg and du go through the workspace in the tensors' type: the rounding is
-// the one that h itself has, and a sum over them averages it out.
+// no array of T F elements between the passes.  dg and du go through the workspace in the tensors' type: beside 2-byte x and
+// weights the tensor cores take no wider operands.  A sum over them keeps the relative size of that rounding, and it is as large as
+// the result's own: against 64 bits the gradients are off by 0.00234 (bf16) and 0.00029 (fp16) where fp32 dg and du would leave 0.00166
+// and 0.00021.  Each as the sum of two values of the type would avoid it for 20 instead of 12 T D F operations.  dbg and dbu are sums of
+// the same rounded values: what dwg and dwu are for a channel of ones.
 #include <algorithm>
 
 #include "na_block.cuh"

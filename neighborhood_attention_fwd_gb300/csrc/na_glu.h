@@ -1,5 +1,5 @@
-// na_glu.h -- the gated feed-forward product's parameters, shared by its host code and CUDA-core kernels (na_glu.cu) and its
-// tensor-core kernels (na_glu_tc.cu).
+// na_glu.h -- the gated feed-forward product's parameters and activations, shared by its host code (na_glu.cu), its CUDA-core kernels
+// (na_glu_fma.cuh) and its tensor-core kernels (na_glu_tc.cuh).
 #pragma once
 
 #include <cuda.h>
@@ -71,7 +71,9 @@ struct GluTcParams {
 };
 
 // act(v) and its derivative.  FAST: exponentials and reciprocals of the hardware's approximations (results below 2^-126 are
-// zeros), off by less than 2^-17 of their value in the range that 2-byte results have; else the full ones of fp32.
+// zeros).  An exponential's error grows with its argument: act(v) is off by less than 2^-17 of its value down to values of 2^-46, by
+// less than 2^-15.5 below (GELU's tanh form, whose argument is a cubic; the others 2^-16.9).  Else the full ones of fp32, zeros where
+// the exponential's inverse leaves fp32 (below 2^-121).
 template <int ACT>   // an activation as a type
 struct ActTag {
     static constexpr int value = ACT;
@@ -135,7 +137,7 @@ __device__ __forceinline__ void activate8(const float (&v)[8], float (&a)[8], fl
         for (int k = 0; k < 8; ++k) activate<ACT, true>(v[k], a[k], slope[k]);
     } else if constexpr (ACT == NA_ACT_GELU) {
         // Phi(-|v|) = exp(-v^2 / 2) t Q(t) / 2, t = 1 / (1 + p |v| / sqrt 2): the form of Abramowitz and Stegun 7.1.26, with
-        // p = 0.52 and a Q of degree 6 fitted to the relative error of erfc over [0, 14] (2^-19.6; 2^-17 with the roundings).
+        // p = 0.52 and a Q of degree 6 fitted to the relative error of erfc over [0, 14] (2^-19.6; with the roundings as above).
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             const uint64_t x = pack2(v[k], v[k + 1]);

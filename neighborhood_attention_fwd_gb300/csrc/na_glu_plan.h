@@ -158,8 +158,9 @@ inline GluTiles plan_tiles(Product which, long long T, int D, int F) {
     return best;
 }
 
-// Tokens and weights in one launch where that is estimated shorter: of the splits that leave the tokens half of the pairs of blocks
-// at least, those with which both sides end soonest.
+// Tokens and weights in one launch where that is estimated shorter: of the splits that leave the tokens 16 of the pairs of blocks at
+// least, those with which both sides end soonest.  A call that wants one of the two alone keeps this cut, and so its bits (dx or dwg, dwu
+// alone of 262144 x 256 x 688 take 374 and 376 us, both 478).
 inline void plan_both(long long T, int D, int F, GluTiles& tokens, GluTiles& weights) {
     const unsigned slots = kSms / 2, steps_t = 2 * up(F, 64), steps_w = up(T, 64);
     const unsigned tiles_w = 2 * up(F, 256) * up(D, 256);
