@@ -455,7 +455,8 @@ size_t na_glu_bwd_workspace_size(int64_t rows, int D, int F, na_dtype dtype);
  * Gradients of na_glu from dh and its inputs; nothing of the forward is kept, g = x Wg^T + bg and u = x Wu^T + bu are made
  * again.  With dg = dh * u * act'(g) and du = dh * act(g), each rounded to the tensors' type (fp16: infinite past 65504, in steps
  * of 2^-24 below 2^-14; scale dh so that they stay between):
- *   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg = sum over tokens of dg,  dbu = sum over tokens of du,
+ *   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x;
+ * dbg and dbu are the sums over tokens of dg and du in fp32, before that rounding.  All are
  * laid out and typed as their tensors, overwritten.  dx may be null, dwg and dwu both null, dbg and dbu each (and must
  * be where the bias is).  Workspace: null (allocated on the stream), or na_glu_bwd_workspace_size bytes.
  */

@@ -9,8 +9,8 @@
 // no array of T F elements between the passes.  dg and du go through the workspace in the tensors' type: beside 2-byte x and
 // weights the tensor cores take no wider operands.  A sum over them keeps the relative size of that rounding, and it is as large as
 // the result's own: against 64 bits the gradients are off by 0.00234 (bf16) and 0.00029 (fp16) where fp32 dg and du would leave 0.00166
-// and 0.00021.  Each as the sum of two values of the type would avoid it for 20 instead of 12 T D F operations.  dbg and dbu are sums of
-// the same rounded values: what dwg and dwu are for a channel of ones.
+// and 0.00021.  Each as the sum of two values of the type would avoid it for 20 instead of 12 T D F operations.  dbg and dbu need no
+// operands: they are sums of the fp32 values, made over a tile's rows as the tile is and then added up.
 #include <algorithm>
 
 #include "na_block.cuh"
@@ -129,6 +129,8 @@ na_status launch_tensor(const GluParams& p, Product which, const GluTiles& n, na
     q.dwg = p.dwg;
     q.dwu = p.dwu;
     q.partial = p.partial;
+    q.sums = p.sums;
+    q.sum_pitch = p.sum_pitch;
     q.pitch = p.pitch;
     q.T = static_cast<int>(p.T);
     q.D = p.D;
@@ -165,12 +167,37 @@ na_status sum_runs(const float* partial, int runs, long long n, long long cut, v
     return launch_sum<float>(partial, runs, n, cut, out0, out1, s);
 }
 
-na_status column_sums(const GluParams& p, const GluPlan& n, float* partial, void* dbg, void* dbu, na_dtype dtype, cudaStream_t s) {
-    na_status st;
-    if (dtype == NA_BF16) st = launch_columns<__nv_bfloat16>(p, n.runs, n.column_run, partial, s);
-    else if (dtype == NA_FP16) st = launch_columns<__half>(p, n.runs, n.column_run, partial, s);
-    else st = launch_columns<float>(p, n.runs, n.column_run, partial, s);
-    return st == NA_OK ? sum_runs(partial, n.runs, 2LL * p.F, p.F, dbg, dbu, dtype, s) : st;
+// Sums of the tiles' rows of sums over runs of them: partial[run][2][F].  A lane takes a chunk of 16 bytes of every eighth row.
+__global__ void __launch_bounds__(256) glu_column_kernel(const float* tiles, long long rows, int F, int pitch, long long run, float* partial) {
+    after_previous();
+    next_may_start();
+    __shared__ __align__(16) float sums[8][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first_col = blockIdx.x * 128, c = first_col + lane * 4;
+    const float* from = tiles + static_cast<long long>(blockIdx.z) * pitch + c;
+    const long long first = blockIdx.y * run, end = min(first + run, rows);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < pitch)
+#pragma unroll 4
+        for (long long r = first + warp; r < end; r += 8) {
+            const float4 f = *reinterpret_cast<const float4*>(from + r * 2 * pitch);
+            s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+        }
+    *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = s;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i >= 128 || first_col + i >= F) return;
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][i];
+    partial[(blockIdx.y * 2LL + blockIdx.z) * F + first_col + i] = t;
+}
+
+// dbg and dbu from the sums that the slopes' kernel has made.
+na_status column_sums(const GluParams& p, const GluPlan& n, void* dbg, void* dbu, na_dtype dtype, cudaStream_t s) {
+    float* runs = p.sums + n.sums / sizeof(float);
+    const na_status st = launch_after(glu_column_kernel, dim3(up(p.F, 128), n.runs, 2), 256, s, p.sums, n.sum_rows, p.F, n.sum_pitch, n.column_run, runs);
+    return st == NA_OK ? sum_runs(runs, n.runs, 2LL * p.F, p.F, dbg, dbu, dtype, s) : st;
 }
 
 }  // namespace
@@ -273,6 +300,8 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     p.dg = ws;
     p.du = static_cast<char*>(ws) + n.array;
     p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n.array);
+    if (dbg || dbu) p.sums = p.partial;   // added up before anything else is put there
+    p.sum_pitch = n.sum_pitch;
     p.T = rows;
     p.pitch = n.pitch;
     p.D = n.width;
@@ -295,13 +324,13 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
     }
     const long long size = static_cast<long long>(F) * n.width, tokens_size = rows * n.width;
     if (n.tensor) {
-        const GluTiles slopes = plan_tiles(kSlopes, rows, n.width, F);
         // rows of dh that are not whole chunks go to dg's place first
-        if (st == NA_OK && !slopes.few && F % 8 != 0) st = launch_copies({{dh, nullptr, nullptr}, {p.dg, nullptr, nullptr}, {rows, 0, 0}, F, static_cast<int>(n.pitch)}, true, s);
-        if (st == NA_OK) st = launch_tensor(p, kSlopes, slopes, dtype, s);
+        if (st == NA_OK && !n.slopes.few && F % 8 != 0) st = launch_copies({{dh, nullptr, nullptr}, {p.dg, nullptr, nullptr}, {rows, 0, 0}, F, static_cast<int>(n.pitch)}, true, s);
+        if (st == NA_OK) st = launch_tensor(p, kSlopes, n.slopes, dtype, s);
     } else {
-        st = fma_product(p, kSlopes, plan_fma(kSlopes, rows, D, F), dtype, s);
+        st = fma_product(p, kSlopes, n.slopes_fma, dtype, s);
     }
+    if (st == NA_OK && p.sums) st = column_sums(p, n, dbg, dbu, dtype, s);
     const bool both = dx && dwg && n.tensor && n.tokens.workers;
     if (st == NA_OK && both) st = launch_tensor(p, kBoth, n.tokens, dtype, s, &n.weights);
     if (st == NA_OK && dx) {
@@ -316,7 +345,6 @@ na_status na_glu_bwd(const void* dh, const void* x, const void* wg, const void* 
         if (st == NA_OK && splits > 1) st = sum_runs(p.partial, splits, 2 * size, size, p.dwg, p.dwu, dtype, s);
     }
     if (st == NA_OK && copied) st = launch_copies({{p.dx, p.dwg, p.dwu}, {dx, dwg, dwu}, {dx ? rows : 0, dwg ? F : 0, dwg ? F : 0}, D, n.width}, false, s);
-    if (st == NA_OK && (dbg || dbu)) st = column_sums(p, n, p.partial, dbg, dbu, dtype, s);
     if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess && st == NA_OK) st = NA_ERR_CUDA;
     return st;
 }

@@ -26,6 +26,8 @@ struct GluParams {
     void* dwg;            // [F, D]
     void* dwu;
     float* partial;       // sums of several splits: [split][2][F][D] of kWeights, [split][T][D] of kTokens
+    float* sums;          // kSlopes: sums of dg and du over the rows of a tile, [tile][2][sum_pitch]; null: not wanted
+    int sum_pitch;
     long long T, pitch;   // pitch: F rounded up to whole 16-byte chunks
     int D, F;
     int act;              // na_glu_act
@@ -55,8 +57,9 @@ struct GluTcParams {
     void* dwg;
     void* dwu;
     float* partial;
+    float* sums;          // slopes: as in GluParams, of 32 tokens, or of all few ones; null: not wanted
     long long pitch;      // of dg and du
-    int T, D, F, act;
+    int T, D, F, act, sum_pitch;
     uint32_t wide;        // rows of h are whole 16-byte chunks
     GluJob job[2];        // tokens, weights
     unsigned token_workers;   // both: pairs of blocks that make dx
@@ -217,13 +220,11 @@ struct GluCopies {
     int D, W;
 };
 // Launchers of the CUDA-core kernels, of the sums over runs (out0 the first `cut` of n elements, out1 the others; either may be
-// null) and of the column sums of dg and du over runs of `run` tokens, to partial[run][2][F] (na_glu_fma.cuh).
+// null) (na_glu_fma.cuh).
 template <typename T>
 na_status launch_fma(const GluParams& p, Product which, const FmaTile& tile, cudaStream_t s);
 template <typename T>
 na_status launch_sum(const float* partial, int runs, long long n, long long cut, void* out0, void* out1, cudaStream_t s);
-template <typename T>
-na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s);
 
 // Launchers of the tensor-core kernels (na_glu_tc.cuh).  blocks: of a tile, 2 (256 x 256) or 1 (128 x 128); tokens: 16, 64 or
 // 128, the most that a product of few tokens holds.

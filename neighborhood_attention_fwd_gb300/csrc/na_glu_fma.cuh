@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
 #pragma unroll
             for (int c = 0; c < GC; ++c) acc[r][c] = total[r][c];
     }
+    float sum_g[WHICH == kSlopes ? GC : 1] = {}, sum_u[WHICH == kSlopes ? GC : 1] = {};   // of dg and du over this thread's rows
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const long long row = m0 + (r < GR ? ty * GR + r : TR / 2 + ty * GR + r - GR);
@@ -226,8 +227,11 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
                         static_cast<T*>(p.h)[row * p.F + f] = Elem<T>::put(a * u);
                     } else {
                         const float dh = Elem<T>::get(static_cast<const T*>(p.dh)[row * p.F + f]);
-                        static_cast<T*>(p.dg)[row * p.pitch + f] = Elem<T>::put(dh * u * slope);
-                        static_cast<T*>(p.du)[row * p.pitch + f] = Elem<T>::put(dh * a);
+                        const float dg = dh * u * slope, du = dh * a;
+                        static_cast<T*>(p.dg)[row * p.pitch + f] = Elem<T>::put(dg);
+                        static_cast<T*>(p.du)[row * p.pitch + f] = Elem<T>::put(du);
+                        sum_g[c] += dg;
+                        sum_u[c] += du;
                     }
                 }
             });
@@ -244,6 +248,30 @@ __global__ void __launch_bounds__(kGluThreads, TR + TC == 256 ? 2 : 4) glu_fma_k
                 if (p.splits > 1) sums[at] = v[c];
                 else out[at] = Elem<T>::put(v[c]);
             }
+        }
+    }
+    if constexpr (WHICH == kSlopes) {
+        if (!p.sums) return;
+        // over the block's rows: the two of a warp, then the warps through shared memory
+        float (*part)[2][TC / 2] = reinterpret_cast<float (*)[2][TC / 2]>(&sa[0][0][0]);
+        static_assert(sizeof(float) * 8 * TC <= sizeof(sa), "the warps' sums take the rows' operand's place");
+        __syncthreads();   // which has been read
+#pragma unroll
+        for (int c = 0; c < GC; ++c) {
+            sum_g[c] += __shfl_xor_sync(0xffffffffu, sum_g[c], 16);
+            sum_u[c] += __shfl_xor_sync(0xffffffffu, sum_u[c], 16);
+            if ((t & 16) == 0) {
+                part[t >> 5][0][tx * GC + c] = sum_g[c];
+                part[t >> 5][1][tx * GC + c] = sum_u[c];
+            }
+        }
+        __syncthreads();
+        const int which = t / (TC / 2), col = t % (TC / 2);
+        if (which < 2 && n0 + col < p.F) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kGluThreads / 32; ++w) s += part[w][which][col];
+            p.sums[(static_cast<long long>(row_tile) * 2 + which) * p.sum_pitch + n0 + col] = s;
         }
     }
 }
@@ -296,38 +324,6 @@ __global__ void __launch_bounds__(256) glu_sum_runs_kernel(const float* partial,
     out[i < cut ? i : i - cut] = Elem<T>::put(t);
 }
 
-// Column sums of dg and du over runs of tokens: partial[run][2][F].  A lane takes a chunk of 16 bytes of every eighth row (rows
-// are padded to whole chunks).
-template <typename T>
-__global__ void __launch_bounds__(256) glu_column_kernel(const T* dg, const T* du, long long T_, int F, long long pitch, long long run, float* partial) {
-    after_previous();
-    next_may_start();
-    constexpr int V = Elem<T>::EPC;
-    __shared__ float sums[8][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first_col = blockIdx.x * 32 * V, c = first_col + lane * V;
-    const T* from = blockIdx.z ? du : dg;
-    const long long first = blockIdx.y * run, end = min(first + run, T_);
-    float s[V] = {};
-    if (c < pitch)
-#pragma unroll 4
-        for (long long r = first + warp; r < end; r += 8) {
-            float f[V];
-            Elem<T>::unpack(ld_stream(from + r * pitch + c), f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[e] += f[e];
-        }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sums[warp][lane * V + e] = s[e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * V && first_col + i < F; i += 256) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) t += sums[w][i];
-        partial[(blockIdx.y * 2LL + blockIdx.z) * F + first_col + i] = t;
-    }
-}
-
 template <typename T, int TR, int TC>
 na_status launch_fma(const GluParams& p, Product which, dim3 grid, cudaStream_t s) {
     if constexpr (TR == TC)   // as plan_fma
@@ -360,12 +356,6 @@ na_status launch_sum(const float* partial, int runs, long long n, long long cut,
     if (blocks < kSms / 2 && runs >= 8)
         return launch_after(glu_sum_runs_kernel<T>, dim3(static_cast<unsigned>((n + 31) / 32)), 256, s, partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
     return launch_after(wide ? glu_sum_kernel<T, 4> : glu_sum_kernel<T, 1>, dim3(blocks), 256, s, partial, runs, n, cut, static_cast<T*>(out0), static_cast<T*>(out1));
-}
-
-template <typename T>
-na_status launch_columns(const GluParams& p, int runs, long long run, float* partial, cudaStream_t s) {
-    return launch_after(glu_column_kernel<T>, dim3(up(p.F, 32 * Elem<T>::EPC), runs, 2), 256, s, static_cast<const T*>(p.dg), static_cast<const T*>(p.du), p.T,
-                        p.F, p.pitch, run, partial);
 }
 
 }  // namespace glu

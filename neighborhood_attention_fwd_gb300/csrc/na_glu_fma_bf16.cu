@@ -5,6 +5,5 @@ namespace na {
 namespace glu {
 template na_status launch_fma<__nv_bfloat16>(const GluParams&, Product, const FmaTile&, cudaStream_t);
 template na_status launch_sum<__nv_bfloat16>(const float*, int, long long, long long, void*, void*, cudaStream_t);
-template na_status launch_columns<__nv_bfloat16>(const GluParams&, int, long long, float*, cudaStream_t);
 }  // namespace glu
 }  // namespace na

@@ -5,6 +5,5 @@ namespace na {
 namespace glu {
 template na_status launch_fma<__half>(const GluParams&, Product, const FmaTile&, cudaStream_t);
 template na_status launch_sum<__half>(const float*, int, long long, long long, void*, void*, cudaStream_t);
-template na_status launch_columns<__half>(const GluParams&, int, long long, float*, cudaStream_t);
 }  // namespace glu
 }  // namespace na

@@ -5,6 +5,5 @@ namespace na {
 namespace glu {
 template na_status launch_fma<float>(const GluParams&, Product, const FmaTile&, cudaStream_t);
 template na_status launch_sum<float>(const float*, int, long long, long long, void*, void*, cudaStream_t);
-template na_status launch_columns<float>(const GluParams&, int, long long, float*, cudaStream_t);
 }  // namespace glu
 }  // namespace na

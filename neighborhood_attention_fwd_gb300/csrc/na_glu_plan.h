@@ -196,10 +196,13 @@ struct GluPlan {
     size_t tokens_copy, weights_copy;   // bytes of x or dx, of Wg, Wu, dWg or dWu in that width; 0 where it is D
     long long pitch;                 // of a row of dg and du
     size_t array;                    // bytes of one of them
-    FmaTile tokens_fma, weights_fma; // CUDA cores
-    int runs;                        // of tokens, of dbg and dbu
+    FmaTile slopes_fma, tokens_fma, weights_fma;   // CUDA cores
+    GluTiles slopes, tokens, weights;              // tensor cores
+    long long sum_rows;              // dbg and dbu: sums of dg and du over the rows of a tile, [sum_rows][2][sum_pitch]
+    int sum_pitch;                   // F up to whole 16-byte chunks
+    int runs;                        // of those rows
     long long column_run;
-    GluTiles tokens, weights;        // tensor cores
+    size_t sums;                     // bytes of the sums of tiles, at the start of the partial ones
     size_t partial;                  // bytes
 };
 
@@ -271,24 +274,30 @@ inline GluPlan plan_glu(long long T, int D, int F, na_dtype dtype) {
     n.array = up256(static_cast<size_t>(T) * n.pitch * es);
     size_t floats = 0;
     if (n.tensor) {
+        n.slopes = plan_tiles(kSlopes, T, D, F);
         n.tokens = plan_tiles(kTokens, T, D, F);
         n.weights = plan_tiles(kWeights, T, D, F);
         plan_both(T, D, F, n.tokens, n.weights);
         if (n.tokens.splits > 1) floats = static_cast<size_t>(n.tokens.splits) * T * D;
         if (n.weights.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights.splits) * 2 * F * D);
     } else {
+        n.slopes_fma = plan_fma(kSlopes, T, D, F);
         n.tokens_fma = plan_fma(kTokens, T, D, F);
         n.weights_fma = plan_fma(kWeights, T, D, F);
         if (n.tokens_fma.splits > 1) floats = static_cast<size_t>(n.tokens_fma.splits) * T * D;
         if (n.weights_fma.splits > 1) floats = std::max(floats, static_cast<size_t>(n.weights_fma.splits) * 2 * F * D);
     }
-    // column sums: four blocks a multiprocessor, at least 64 tokens each, at most 8192 (of more than 2^28 tokens up to 65536: a
-    // thread of the kernel adds every eighth token, so that no sum takes more than 8192 terms)
-    const long long columns = 2LL * up(F, 32 * chunk);
-    const long long runs = std::min(std::max((T + 8191) / 8192, std::min((T + 63) / 64, (4 * kSms + columns - 1) / columns)), 32768LL);
-    n.column_run = (T + runs - 1) / runs;
-    n.runs = static_cast<int>((T + n.column_run - 1) / n.column_run);
-    n.partial = up256(std::max(floats, static_cast<size_t>(n.runs) * 2 * F) * sizeof(float));
+    // sums of dg and du: over the rows of a tile as it is made (all of few tokens; else a warp's 32 on tensor cores, a block's on CUDA
+    // cores), then runs of those rows: four blocks a multiprocessor, at least 64 rows each, at most 8192, of which a thread adds every
+    // eighth
+    n.sum_rows = n.tensor ? (n.slopes.few ? 1 : up(T, 32)) : up(T, n.slopes_fma.rows);
+    n.sum_pitch = (F + 3) / 4 * 4;
+    const long long columns = 2LL * up(F, 128);
+    const long long runs = std::max((n.sum_rows + 8191) / 8192, std::min((n.sum_rows + 63) / 64, (4 * kSms + columns - 1) / columns));
+    n.column_run = (n.sum_rows + runs - 1) / runs;
+    n.runs = static_cast<int>((n.sum_rows + n.column_run - 1) / n.column_run);
+    n.sums = up256(static_cast<size_t>(n.sum_rows) * 2 * n.sum_pitch * sizeof(float));
+    n.partial = std::max(up256(floats * sizeof(float)), n.sums + up256(static_cast<size_t>(n.runs) * 2 * F * sizeof(float)));
     return n;
 }
 

@@ -180,6 +180,22 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return v;
 }
 
+// The sums over a warp's lanes of eight columns, of column lane / 4 to each lane: lanes hand one another the half of the columns that
+// is not theirs (nine shuffles for 40).
+__device__ __forceinline__ float columns_sum(float (&v)[8], int lane) {
+#pragma unroll
+    for (int half = 4; half >= 1; half /= 2) {
+        const bool upper = lane & 4 * half;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const float away = upper ? v[k] : v[k + half];
+            v[k] = (upper ? v[k + half] : v[k]) + __shfl_xor_sync(0xffffffffu, away, 4 * half);
+        }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
 // After a wait that ran out: time for what is in flight into this block's memory to land.
 __device__ __forceinline__ void settle() {
     const unsigned long long t0 = globaltimer();
@@ -247,7 +263,8 @@ struct PairWalk {
     }
 };
 
-template <int WHICH, int CG, typename T>
+// SUMS: also the sums of dg and du over a warp's 32 rows.
+template <int WHICH, int CG, bool SUMS, typename T>
 __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_kernel(const __grid_constant__ GluTcParams p) {
     using S = PairShape<WHICH, CG>;
     using Walk = PairWalk<CG>;
@@ -467,6 +484,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                 }
                 // eight columns at a time, the next ones on their way
                 uint32_t du[16], rg[2][8], ru[2][8];
+                float sum_g = 0.f, sum_u = 0.f;   // of column 8 (lane % 4) + lane / 4
                 tmem_ld8(taddr, rg[0]);
                 tmem_ld8(taddr + nf, ru[0]);
 #pragma unroll
@@ -493,6 +511,7 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                     }
                     activate8<ACT>(g, a, slope);
                     uint32_t v[4];
+                    float dg8[SUMS ? 8 : 1], du8[SUMS ? 8 : 1];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if constexpr (WHICH == kForward) {
@@ -500,8 +519,22 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                         } else {
                             float d0, d1;
                             Elem<T>::two(dh[4 * c + k], d0, d1);
-                            v[k] = Elem<T>::pair(d0 * u[2 * k] * slope[2 * k], d1 * u[2 * k + 1] * slope[2 * k + 1]);
-                            du[4 * c + k] = Elem<T>::pair(d0 * a[2 * k], d1 * a[2 * k + 1]);
+                            const float dg0 = d0 * u[2 * k] * slope[2 * k], dg1 = d1 * u[2 * k + 1] * slope[2 * k + 1];
+                            const float du0 = d0 * a[2 * k], du1 = d1 * a[2 * k + 1];
+                            v[k] = Elem<T>::pair(dg0, dg1);
+                            du[4 * c + k] = Elem<T>::pair(du0, du1);
+                            if constexpr (SUMS) {   // rows past the last token are not there: a bias may make them infinite
+                                const bool in = m0 + lane < p.T;
+                                dg8[2 * k] = in ? dg0 : 0.f, dg8[2 * k + 1] = in ? dg1 : 0.f;
+                                du8[2 * k] = in ? du0 : 0.f, du8[2 * k + 1] = in ? du1 : 0.f;
+                            }
+                        }
+                    }
+                    if constexpr (SUMS) {
+                        const float tg = columns_sum(dg8, lane), tu = columns_sum(du8, lane);
+                        if ((lane & 3) == c) {
+                            sum_g = tg;
+                            sum_u = tu;
                         }
                     }
                     st_shared_v4(row + (c ^ sw) * 16, v[0], v[1], v[2], v[3]);
@@ -510,6 +543,14 @@ __global__ void __launch_bounds__(PairShape<WHICH, CG>::THREADS, 1) glu_pair_ker
                     if (p.wide) by_tma(&p.out[0], m0, f0);
                     else by_elements(m0, f0);
                 } else {
+                    if constexpr (SUMS) {
+                        const int f = f0 + (lane & 3) * 8 + (lane >> 2);
+                        float* to = p.sums + static_cast<long long>(m0 / 32) * 2 * p.sum_pitch + f;
+                        if (f < p.F) {
+                            to[0] = sum_g;
+                            to[p.sum_pitch] = sum_u;
+                        }
+                    }
                     // dg, then du through the same staging
                     by_tma(&p.out[0], m0, f0);
                     if (lane == 0) tma_store_wait_read();
@@ -894,6 +935,7 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
         }
         named_bar_sync(1, 128);
         if (gate) {
+            float sum_g = 0.f, sum_u = 0.f;   // of dg and du over the tokens
 #pragma unroll 1
             for (int c = 0; c < NTOK; c += 16) {
                 if (c >= p.T) break;
@@ -912,12 +954,20 @@ __global__ void __launch_bounds__(192) glu_few_kernel(const __grid_constant__ Gl
                             static_cast<T*>(p.h)[t * p.F + f] = Elem<T>::put(a * u);
                         } else {
                             const float dh = widen<T>(p.dh, t * p.F + f);
-                            static_cast<T*>(p.dg)[t * p.pitch + f] = Elem<T>::put(dh * u * slope);
-                            static_cast<T*>(p.du)[t * p.pitch + f] = Elem<T>::put(dh * a);
+                            const float dg = dh * u * slope, du = dh * a;
+                            static_cast<T*>(p.dg)[t * p.pitch + f] = Elem<T>::put(dg);
+                            static_cast<T*>(p.du)[t * p.pitch + f] = Elem<T>::put(du);
+                            sum_g += dg;
+                            sum_u += du;
                         }
                     }
                 });
             }
+            if constexpr (WHICH == kSlopes)
+                if (p.sums && f < p.F && ok) {
+                    p.sums[f] = sum_g;
+                    p.sums[p.sum_pitch + f] = sum_u;
+                }
         }
         tc_fence_before();
     }
@@ -959,8 +1009,10 @@ na_status launch_glu(Kernel* kernel, const GluTcParams& p, unsigned blocks, int 
 template <int WHICH, int CG, typename T>
 na_status launch_tiles(const GluTcParams& p, unsigned tiles, cudaStream_t s) {
     const unsigned blocks = CG * std::min<unsigned>(tiles, kSms / CG);
+    if constexpr (WHICH == kSlopes)
+        if (p.sums) return launch_glu(glu_pair_kernel<WHICH, CG, true, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
     if constexpr (WHICH == kForward || WHICH == kSlopes)
-        return launch_glu(glu_pair_kernel<WHICH, CG, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
+        return launch_glu(glu_pair_kernel<WHICH, CG, false, T>, p, blocks, CG, PairShape<WHICH, CG>::THREADS, PairShape<WHICH, CG>::BYTES, s);
     else
         return launch_glu(glu_tile_kernel<WHICH, CG, T>, p, blocks, CG, TileShape<CG>::THREADS, TileShape<CG>::BYTES, s, true);
 }

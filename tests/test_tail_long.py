@@ -17,7 +17,7 @@ CODES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_sums_over_tokens_of_one_value(dtype, cuda_lib):
     """dbg and dbu over 2^25 tokens of one value, 0.1 in the type.  In one sequence of fp32 additions every term is rounded the same way and
-    the sum is off by percents; here a sum takes at most 8192 terms, then the runs (4096) are added eight warps a block."""
+    the sum is off by percents; here a tile's tokens are added first (at most 32 in one sequence), then runs of tiles, then the runs."""
     na = cuda_lib
     T, D, F = 1 << 25, 8, 8
     x = torch.zeros(T, D, dtype=TYPES[dtype], device="cuda")
@@ -28,7 +28,7 @@ def test_sums_over_tokens_of_one_value(dtype, cuda_lib):
     na.na_glu_bwd(dh, x, wg, wu, bg=bg, bu=bu, dbg=dbg, dbu=dbu, act="relu")   # g = u = 1: dg = du = dh
     status_ok(na)
     want = np.full(F, T * float(dh[0, 0]))
-    close("dbg", dbg, want, (1024 + 8 + 512 + 8) * E * want, TYPES[dtype])   # a thread's 1024 tokens, eight warps, 512 runs of a warp, eight warps
+    close("dbg", dbg, want, (32 + 432 + 8 + 38 + 8) * E * want, TYPES[dtype])   # a tile, a thread's 432 tiles, eight warps, 38 runs of a warp, eight warps
     assert torch.equal(dbg, dbu)
 
 
@@ -90,7 +90,8 @@ def cut_tokens(p, T):
         edges = {64 * e for e in edges}
     else:
         edges = {s * w["run"] for s in (0, 1, 2, w["splits"] // 2, w["splits"] - 1, w["splits"])} | {16, T // 16 * 16}
-    edges |= {s * p["column_run"] for s in (0, 1, p["runs"] - 1, p["runs"])}
+    rows = -(-T // p["sum_rows"]) if p["sum_rows"] == 1 else 32 if p["tensor"] else p["slopes"]["rows"]
+    edges |= {s * p["column_run"] * rows for s in (0, 1, p["runs"] - 1, p["runs"])} | {rows, (p["sum_rows"] - 1) * rows}
     return sorted({t + d for t in edges for d in (-1, 0) if 0 <= t + d < T} | {0, T - 1})
 
 

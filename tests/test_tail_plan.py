@@ -32,16 +32,16 @@ int main() {
     while (std::scanf("%lld %d %d %d", &T, &D, &F, &type) == 4) {
         const na_dtype dt = static_cast<na_dtype>(type);
         const GluPlan n = plan_glu(T, D, F, dt);
-        std::printf("{\"tensor\": %d, \"width\": %d, \"pitch\": %lld, \"array\": %zu, \"runs\": %d, \"column_run\": %lld, \"partial\": %zu, \"workspace\": %zu", n.tensor, n.width, n.pitch,
-                    n.array, n.runs, n.column_run, n.partial, glu_workspace(n));
+        std::printf("{\"tensor\": %d, \"width\": %d, \"pitch\": %lld, \"array\": %zu, \"sum_rows\": %lld, \"sum_pitch\": %d, \"sums\": %zu, \"runs\": %d, \"column_run\": %lld, \"partial\": %zu, \"workspace\": %zu",
+                    n.tensor, n.width, n.pitch, n.array, n.sum_rows, n.sum_pitch, n.sums, n.runs, n.column_run, n.partial, glu_workspace(n));
         if (n.tensor) {
             tiles("forward", plan_tiles(kForward, T, n.width, F));
-            tiles("slopes", plan_tiles(kSlopes, T, n.width, F));
+            tiles("slopes", n.slopes);
             tiles("tokens", n.tokens);
             tiles("weights", n.weights);
         } else {
             fma("forward", kForward, T, D, F, plan_fma(kForward, T, D, F));
-            fma("slopes", kSlopes, T, D, F, plan_fma(kSlopes, T, D, F));
+            fma("slopes", kSlopes, T, D, F, n.slopes_fma);
             fma("tokens", kTokens, T, D, F, n.tokens_fma);
             fma("weights", kWeights, T, D, F, n.weights_fma);
         }
@@ -96,10 +96,11 @@ def check(size, p):
     chunk = 16 // es
     assert p["pitch"] == up(F, chunk) * chunk and p["array"] >= T * p["pitch"] * es
     assert p["workspace"] >= 2 * p["array"] + p["partial"]
-    assert 0 < (p["runs"] - 1) * p["column_run"] + 1 <= T <= p["runs"] * p["column_run"] and p["runs"] <= 65535
-    assert p["partial"] >= 4 * p["runs"] * 2 * F
-    # no sum of the columns takes more than 8192 terms: a thread adds every eighth token of a run, then the runs are added
-    assert up(p["column_run"], 8) <= 8192 and p["runs"] <= 32768 and (T > 2 ** 28 or p["column_run"] <= 8192)
+    # dbg and dbu: rows of sums over a tile's tokens, then runs of those rows, then the runs; no sum takes more than 8192 terms
+    rows = up(T, p["slopes"]["rows"]) if not p["tensor"] else 1 if p["slopes"]["few"] else up(T, 32)
+    assert p["sum_rows"] == rows and p["sum_pitch"] % 4 == 0 and F <= p["sum_pitch"] < F + 4
+    assert 0 < (p["runs"] - 1) * p["column_run"] + 1 <= rows <= p["runs"] * p["column_run"] and p["column_run"] <= 8192 and p["runs"] <= 8192
+    assert p["sums"] % 256 == 0 and p["sums"] >= 4 * rows * 2 * p["sum_pitch"] and p["partial"] >= p["sums"] + 4 * p["runs"] * 2 * F
     for name, size_ in (("tokens", T * D), ("weights", 2 * F * D)):
         if p[name]["splits"] > 1:
             assert p["partial"] >= 4 * p[name]["splits"] * size_
