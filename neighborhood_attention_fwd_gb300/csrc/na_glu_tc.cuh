@@ -222,8 +222,8 @@ __device__ __forceinline__ Place place_of(unsigned i, unsigned rows, unsigned co
 // Forward and slopes.  A tile: 128 CG rows of tokens, 64 CG columns of g and the same of u, fewer of them in the last of a row.  The
 // rows' and the columns' operand have rings of their own: where all of a row of tiles' operand (its steps of 64) fits its ring,
 // it is brought once for the `span` columns of tiles that a block takes in a row, which halves what comes out of L2, the bound
-// of short sums (1024^2 tokens, 256 -> 688, 2-byte: 535 us, 13 TB/s).  Long sums run at 1580 TFLOP/s (4095 tokens, 4096 -> 11008:
-// 467 us).  The epilogue has sixteen (eight) warps, each for 32 rows by 32 columns.  Every block copies what it and its pair
+// of short sums (1024^2 tokens, 256 -> 688, 2-byte: 535 us, 13 TB/s).  Long sums run at 1560 TFLOP/s (4095 tokens, 4096 -> 11008:
+// 472 us).  The epilogue has sixteen (eight) warps, each for 32 rows by 32 columns.  Every block copies what it and its pair
 // read itself: the library also runs as one of several ranks, each on a GPU of its own, and no load of it goes to several blocks.
 // ---------------------------------------------------------------------------------------------
 
